@@ -11,22 +11,29 @@
 points of ``include/attn_sink.h`` one to one: they only turn tensors into
 device pointers and return the library's status.  ``forward``, ``backward``
 and ``attn_sink`` (autograd) are conveniences on top that allocate outputs and
-the workspace with torch and raise on a non-zero status.  Every step of the
+the workspace with torch and raise on a non-zero status.  The entry points of
+``include/attn_sink_step.h`` (``attn_sink_page_plan``, ``attn_sink_qkv_rope``,
+``attn_sink_qkv_rope_bwd``, ``attn_sink_extend`` and their workspace sizes) and
+their conveniences ``page_plan``, ``qkv_rope``, ``qkv_rope_backward``,
+``qkv_rope_autograd`` and ``extend`` come after them.  Every step of the
 computation runs in the library's CUDA kernels; there is no other code path,
 and loading fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
 from .build import LIB_PATH, INCLUDE
 
 c_int, c_float, c_void_p, c_size_t = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+c_longlong = ctypes.c_longlong
 
 ATTN_SINK_OK = 0
 STATUS_NAMES = {0: "ATTN_SINK_OK", 1: "ATTN_SINK_ERR_INVALID_ARG", 2: "ATTN_SINK_ERR_UNSUPPORTED",
@@ -54,6 +61,35 @@ class AttnSinkDecodeParams(ctypes.Structure):
     ]
 
 
+class AttnSinkPlanParams(ctypes.Structure):
+    """Mirror of ``attn_sink_plan_params`` in include/attn_sink_step.h."""
+    _fields_ = [
+        ("batch", c_int), ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int),
+        ("num_free", c_int), ("max_tokens", c_int),
+    ]
+
+
+class AttnSinkRopeParams(ctypes.Structure):
+    """Mirror of ``attn_sink_rope_params`` in include/attn_sink_step.h."""
+    _fields_ = [
+        ("q_stride", c_longlong), ("k_stride", c_longlong), ("v_stride", c_longlong),
+        ("tokens", c_int), ("heads_q", c_int), ("heads_kv", c_int), ("head_dim", c_int),
+        ("rotary_dim", c_int), ("interleaved", c_int), ("num_axes", c_int),
+        ("pair_axis", ctypes.c_ubyte * 32), ("norm", c_int), ("weight_bf16", c_int),
+        ("eps", c_float), ("amplitude", c_float), ("page_size", c_int), ("num_pages", c_int),
+        ("grad_dtype", c_int),
+    ]
+
+
+class AttnSinkExtendParams(ctypes.Structure):
+    """Mirror of ``attn_sink_extend_params`` in include/attn_sink_step.h."""
+    _fields_ = [
+        ("batch", c_int), ("total_q", c_int), ("heads_q", c_int), ("heads_kv", c_int),
+        ("head_dim", c_int), ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int),
+        ("window", c_int), ("softmax_scale", c_float),
+    ]
+
+
 class AttnSinkError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -67,9 +103,9 @@ class AttnSinkError(RuntimeError):
 _LIB = None
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/attn_sink.h declares."""
-    text = open(os.path.join(INCLUDE, "attn_sink.h")).read()
+def header_functions(header: str = "attn_sink.h") -> list[str]:
+    """Names of the functions a header under include/ declares."""
+    text = open(os.path.join(INCLUDE, header)).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"^(?:[A-Za-z_]\w*[\s*]+)+(attn_sink_\w+)\s*\(", text, flags=re.M)
 
@@ -89,7 +125,7 @@ def lib():
 
 def load_library(path: str):
     """A ctypes handle on a build of the library at `path` with the C
-    signatures of include/attn_sink.h attached (the product library, or the
+    signatures of the headers under include/ attached (the product library, or the
     test build that also exports attn_sink_test_withhold)."""
     L = ctypes.CDLL(path)
     P = ctypes.POINTER(AttnSinkParams)
@@ -140,6 +176,21 @@ def load_library(path: str):
     L.attn_sink_kernel_time.argtypes = [c_int, ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_ulonglong)]
     L.attn_sink_kernel_time.restype = c_int
+    L.attn_sink_page_plan.argtypes = [ctypes.POINTER(AttnSinkPlanParams)] + [c_void_p] * 10
+    L.attn_sink_page_plan.restype = c_int
+    PR = ctypes.POINTER(AttnSinkRopeParams)
+    L.attn_sink_qkv_rope.argtypes = [PR] + [c_void_p] * 14
+    L.attn_sink_qkv_rope.restype = c_int
+    L.attn_sink_qkv_rope_bwd_workspace_size.argtypes = [PR]
+    L.attn_sink_qkv_rope_bwd_workspace_size.restype = c_size_t
+    L.attn_sink_qkv_rope_bwd.argtypes = ([PR] + [c_void_p] * 12 + [c_longlong] * 3 +
+                                         [c_void_p] * 3 + [c_size_t, c_void_p])
+    L.attn_sink_qkv_rope_bwd.restype = c_int
+    PE = ctypes.POINTER(AttnSinkExtendParams)
+    L.attn_sink_extend_workspace_size.argtypes = [PE]
+    L.attn_sink_extend_workspace_size.restype = c_size_t
+    L.attn_sink_extend.argtypes = [PE] + [c_void_p] * 10 + [c_size_t, c_void_p]
+    L.attn_sink_extend.restype = c_int
     if hasattr(L, "attn_sink_test_withhold"):
         L.attn_sink_test_withhold.argtypes = [c_int, c_int]
         L.attn_sink_test_withhold.restype = c_int
@@ -506,3 +557,320 @@ def attn_sink(q, k, v, sink, *, causal: bool = True, window: int = 0,
     """Differentiable attention with a learnable per-head sink (bf16 q/k/v)."""
     return AttnSinkFunction.apply(q, k, v, sink, causal, window, softmax_scale, cu_seqlens_q,
                                   cu_seqlens_k, max_seqlen_q, max_seqlen_k)
+
+
+# ----------------------------------------------------------------------------- include/attn_sink_step.h
+def attn_sink_page_plan(params: AttnSinkPlanParams, cached_lens, new_lens, free_pages, block_table,
+                        slots, positions, cu_seqlens, seq_lens, pages_needed, stream=None) -> int:
+    return lib().attn_sink_page_plan(_pref(params), _ptr(cached_lens), _ptr(new_lens),
+                                     _ptr(free_pages), _ptr(block_table), _ptr(slots),
+                                     _ptr(positions), _ptr(cu_seqlens), _ptr(seq_lens),
+                                     _ptr(pages_needed), _stream(stream))
+
+
+def attn_sink_qkv_rope(params: AttnSinkRopeParams, q, k, v, positions, inv_freq, q_weight,
+                       k_weight, slots, q_out, k_out, v_out, k_cache, v_cache,
+                       stream=None) -> int:
+    return lib().attn_sink_qkv_rope(_pref(params), _ptr(q), _ptr(k), _ptr(v), _ptr(positions),
+                                    _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(slots),
+                                    _ptr(q_out), _ptr(k_out), _ptr(v_out), _ptr(k_cache),
+                                    _ptr(v_cache), _stream(stream))
+
+
+def attn_sink_qkv_rope_bwd_workspace_size(params: AttnSinkRopeParams) -> int:
+    return int(lib().attn_sink_qkv_rope_bwd_workspace_size(_pref(params)))
+
+
+def attn_sink_qkv_rope_bwd(params: AttnSinkRopeParams, q, k, positions, inv_freq, q_weight,
+                           k_weight, dq, dk, dv, dq_in, dk_in, dv_in, dq_in_stride: int,
+                           dk_in_stride: int, dv_in_stride: int, dq_weight, dk_weight, workspace,
+                           workspace_bytes: int, stream=None) -> int:
+    return lib().attn_sink_qkv_rope_bwd(_pref(params), _ptr(q), _ptr(k), _ptr(positions),
+                                        _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(dq),
+                                        _ptr(dk), _ptr(dv), _ptr(dq_in), _ptr(dk_in),
+                                        _ptr(dv_in), int(dq_in_stride), int(dk_in_stride),
+                                        int(dv_in_stride), _ptr(dq_weight), _ptr(dk_weight),
+                                        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def attn_sink_extend_workspace_size(params: AttnSinkExtendParams) -> int:
+    return int(lib().attn_sink_extend_workspace_size(_pref(params)))
+
+
+def attn_sink_extend(params: AttnSinkExtendParams, q, k_cache, v_cache, block_table, seq_lens,
+                     cu_seqlens_q, sink, out, lse, workspace, workspace_bytes: int,
+                     stream=None) -> int:
+    return lib().attn_sink_extend(_pref(params), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens_q),
+                                  _ptr(sink), _ptr(out), _ptr(lse), _ptr(workspace),
+                                  int(workspace_bytes), _stream(stream))
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Context in which `device` is current and `stream` (None: the device's
+    current one) is its current stream, so that outputs and workspaces are
+    allocated for the stream that uses them."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors have to be on a CUDA device, not on {device}")
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return _NOTHING
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _want(name, t, dtype, device, shape, contiguous: bool = True):
+    """Check one tensor argument; `shape` holds None where any size will do."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has to be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} has to be contiguous")
+
+
+class PagePlan(NamedTuple):
+    """What a serving step needs to know of its tokens (see page_plan)."""
+    slots: torch.Tensor          # [max_tokens] int64: cache row of each new token, -1: none
+    positions: torch.Tensor      # [max_tokens] int32
+    cu_seqlens_q: torch.Tensor   # [B + 1] int32
+    seq_lens: torch.Tensor       # [B] int32: cached + new
+    pages_needed: torch.Tensor   # [1] int32: entries of free_pages that are now taken
+
+
+def page_plan(cached_lens, new_lens, free_pages, block_table, *, page_size: int, num_pages: int,
+              max_tokens: int, stream=None) -> PagePlan:
+    """Plan a serving step on the GPU (attn_sink_page_plan): sequence b has
+    cached_lens[b] keys and gets new_lens[b] new tokens; new pages are taken from
+    free_pages in order and written into block_table [B, max_pages] in place.
+    Nothing is read back: max_tokens bounds the tokens of the step."""
+    dev = block_table.device
+    b, i32 = cached_lens.shape[0], torch.int32
+    _want("cached_lens", cached_lens, i32, dev, (b,))
+    _want("new_lens", new_lens, i32, dev, (b,))
+    _want("free_pages", free_pages, i32, dev, (None,))
+    _want("block_table", block_table, i32, dev, (b, None))
+    if max_tokens < 0:
+        raise ValueError(f"max_tokens is {max_tokens}")
+    with _on(dev, stream):
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        positions = torch.empty(max_tokens, dtype=i32, device=dev)
+        small = torch.empty(2 * b + 2, dtype=i32, device=dev)
+        cu, lens, needed = small[:b + 1], small[b + 1:2 * b + 1], small[2 * b + 1:]
+        p = AttnSinkPlanParams(b, page_size, num_pages, block_table.shape[1],
+                               free_pages.shape[0], max_tokens)
+        _check(attn_sink_page_plan(p, cached_lens, new_lens, free_pages, block_table, slots,
+                                   positions, cu, lens, needed), "attn_sink_page_plan")
+    return PagePlan(slots, positions, cu, lens, needed)
+
+
+def axis_sections(*sections: int) -> list[int]:
+    """pair_axis of qkv_rope for whole sections of pairs: the first sections[0]
+    pairs turn with axis 0, the next sections[1] with axis 1, and so on."""
+    return [axis for axis, n in enumerate(sections) for _ in range(n)]
+
+
+def make_rope_params(tokens: int, heads_q: int, heads_kv: int, *, rotary_dim: int,
+                     row_stride: int, num_axes: int = 1, pair_axis=None,
+                     interleaved: bool = False, norm: bool = False, weight_bf16: bool = False,
+                     eps: float = 1e-6, amplitude: float = 1.0, page_size: int = 0,
+                     num_pages: int = 0, grad_dtype: int = 0,
+                     head_dim: int = 64) -> AttnSinkRopeParams:
+    """Params of attn_sink_qkv_rope / _bwd for a packed projection whose tokens
+    are row_stride elements apart."""
+    p = AttnSinkRopeParams()
+    p.q_stride = p.k_stride = p.v_stride = row_stride
+    p.tokens, p.heads_q, p.heads_kv, p.head_dim = tokens, heads_q, heads_kv, head_dim
+    p.rotary_dim, p.interleaved, p.num_axes = rotary_dim, int(interleaved), num_axes
+    if pair_axis is not None:
+        ctypes.memmove(p.pair_axis, bytes(pair_axis), len(pair_axis))
+    p.norm, p.weight_bf16, p.eps, p.amplitude = int(norm), int(weight_bf16), eps, amplitude
+    p.page_size, p.num_pages, p.grad_dtype = page_size, num_pages, grad_dtype
+    return p
+
+
+def _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
+                 **kw) -> AttnSinkRopeParams:
+    """Checks of qkv_rope and its backward, and their params."""
+    dev, t, rows = qkv.device, qkv.shape[0], heads_q + 2 * heads_kv
+    _want("qkv", qkv, torch.bfloat16, dev, (None, rows, 64), contiguous=False)
+    stride = qkv.stride(0) if t > 1 else rows * 64
+    if t and (qkv.stride(2) != 1 or qkv.stride(1) != 64 or stride < rows * 64 or stride % 8):
+        raise ValueError("qkv: the heads of a token have to be contiguous and the tokens a "
+                         f"multiple of 8 elements apart (strides {tuple(qkv.stride())})")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _want("positions", positions, torch.int32, dev, (t,) if positions.dim() == 1 else (axes, t))
+    _want("inv_freq", inv_freq, torch.float32, dev, (None,))
+    pairs = inv_freq.shape[0]
+    if pairs > 32:
+        raise ValueError(f"inv_freq has {pairs} entries: a head has 32 pairs")
+    if pair_axis is None:
+        if axes > 1:
+            raise ValueError("positions with several axes need pair_axis")
+    elif len(pair_axis) != pairs or not all(0 <= a < axes for a in pair_axis):
+        raise ValueError(f"pair_axis needs {pairs} entries in [0, {axes}), one per pair")
+    norm = q_weight is not None
+    if norm != (k_weight is not None):
+        raise ValueError("q_weight and k_weight go together")
+    if norm:
+        if q_weight.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"q_weight has to be float32 or bfloat16, not {q_weight.dtype}")
+        _want("q_weight", q_weight, q_weight.dtype, dev, (64,))
+        _want("k_weight", k_weight, q_weight.dtype, dev, (64,))
+    return make_rope_params(t, heads_q, heads_kv, rotary_dim=2 * pairs, row_stride=stride,
+                            num_axes=axes, pair_axis=pair_axis, norm=norm,
+                            weight_bf16=norm and q_weight.dtype == torch.bfloat16, **kw)
+
+
+def qkv_rope(qkv, positions, inv_freq, *, heads_q: int, heads_kv: int, q_weight=None,
+             k_weight=None, eps: float = 1e-6, pair_axis=None, interleaved: bool = False,
+             amplitude: float = 1.0, slots=None, k_cache=None, v_cache=None,
+             keep_kv: bool | None = None, stream=None):
+    """(q, k, v) of a packed projection qkv [T, heads_q + 2 heads_kv, 64] bf16
+    (attn_sink_qkv_rope): q and k normalised per head (with q_weight and k_weight
+    [64], fp32 or bf16; None: no norm) and rotated by positions [T] or [axes, T]
+    int32, inv_freq [rotary_dim / 2] fp32.  Pair i turns with the axis
+    pair_axis[i] (see axis_sections); interleaved pairs are (2i, 2i + 1), the
+    others (i, i + rotary_dim / 2); amplitude multiplies the rotated dimensions.
+    With slots [T] int64, k and v are written to those rows of k_cache and
+    v_cache [pages, page_size, heads_kv, 64], and k and v are None unless
+    keep_kv."""
+    paged = slots is not None
+    p = _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
+                     eps=eps, interleaved=interleaved, amplitude=amplitude,
+                     page_size=k_cache.shape[1] if paged and k_cache is not None else 0,
+                     num_pages=k_cache.shape[0] if paged and k_cache is not None else 0)
+    dev, t, bf16 = qkv.device, qkv.shape[0], torch.bfloat16
+    if paged:
+        if k_cache is None or v_cache is None:
+            raise ValueError("slots need k_cache and v_cache")
+        _want("slots", slots, torch.int64, dev, (t,))
+        _want("k_cache", k_cache, bf16, dev, (None, None, heads_kv, 64))
+        _want("v_cache", v_cache, bf16, dev, tuple(k_cache.shape))
+    elif k_cache is not None or v_cache is not None:
+        raise ValueError("k_cache and v_cache need slots")
+    keep = not paged if keep_kv is None else keep_kv
+    with _on(dev, stream):
+        q = torch.empty((t, heads_q, 64), dtype=bf16, device=dev)
+        k = torch.empty((t, heads_kv, 64), dtype=bf16, device=dev) if keep else None
+        v = torch.empty((t, heads_kv, 64), dtype=bf16, device=dev) if keep else None
+        base = qkv.data_ptr()
+        _check(attn_sink_qkv_rope(p, base, base + 128 * heads_q,
+                                  base + 128 * (heads_q + heads_kv), positions, inv_freq,
+                                  q_weight, k_weight, slots, q, k, v, k_cache, v_cache),
+               "attn_sink_qkv_rope")
+    return q, k, v
+
+
+def qkv_rope_backward(qkv, positions, inv_freq, dq, dk, dv, *, heads_q: int, heads_kv: int,
+                      q_weight=None, k_weight=None, eps: float = 1e-6, pair_axis=None,
+                      interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """(dqkv, dq_weight, dk_weight) of qkv_rope (attn_sink_qkv_rope_bwd): dq
+    [T, heads_q, 64], dk and dv [T, heads_kv, 64], all bf16 or all fp32 (as
+    backward gives them); dqkv [T, heads_q + 2 heads_kv, 64] bf16, the weights'
+    gradients [64] fp32 (None without norm), bitwise reproducible."""
+    kind = dq.dtype
+    if kind not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dq has to be float32 or bfloat16, not {kind}")
+    p = _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
+                     eps=eps, interleaved=interleaved, amplitude=amplitude,
+                     grad_dtype=int(kind == torch.float32))
+    dev, t, rows = qkv.device, qkv.shape[0], heads_q + 2 * heads_kv
+    _want("dq", dq, kind, dev, (t, heads_q, 64))
+    _want("dk", dk, kind, dev, (t, heads_kv, 64))
+    _want("dv", dv, kind, dev, (t, heads_kv, 64))
+    with _on(dev, stream):
+        dqkv = torch.empty((t, rows, 64), dtype=torch.bfloat16, device=dev)
+        dw = ws = None
+        if p.norm:
+            dw = torch.empty((2, 64), dtype=torch.float32, device=dev)
+            ws = torch.empty(attn_sink_qkv_rope_bwd_workspace_size(p), dtype=torch.uint8,
+                             device=dev)
+        src, dst, kq, kk = qkv.data_ptr(), dqkv.data_ptr(), 128 * heads_q, 128 * heads_kv
+        _check(attn_sink_qkv_rope_bwd(p, src, src + kq, positions, inv_freq, q_weight, k_weight,
+                                      dq, dk, dv, dst, dst + kq, dst + kq + kk, rows * 64,
+                                      rows * 64, rows * 64, None if dw is None else dw[0],
+                                      None if dw is None else dw[1], ws,
+                                      0 if ws is None else ws.numel()),
+               "attn_sink_qkv_rope_bwd")
+    return (dqkv, None, None) if dw is None else (dqkv, dw[0], dw[1])
+
+
+class QkvRopeFunction(torch.autograd.Function):
+    """Autograd wrapper of qkv_rope and qkv_rope_backward."""
+
+    @staticmethod
+    def forward(ctx, qkv, q_weight, k_weight, positions, inv_freq, cfg):
+        ctx.save_for_backward(qkv, q_weight, k_weight, positions, inv_freq)
+        ctx.cfg = cfg
+        return qkv_rope(qkv, positions, inv_freq, q_weight=q_weight, k_weight=k_weight, **cfg)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk, dv):
+        qkv, qw, kw, positions, inv_freq = ctx.saved_tensors
+        dqkv, dqw, dkw = qkv_rope_backward(qkv, positions, inv_freq, dq.contiguous(),
+                                           dk.contiguous(), dv.contiguous(), q_weight=qw,
+                                           k_weight=kw, **ctx.cfg)
+        if dqw is not None:
+            dqw, dkw = dqw.to(qw.dtype), dkw.to(kw.dtype)
+        return dqkv, dqw, dkw, None, None, None
+
+
+def qkv_rope_autograd(qkv, positions, inv_freq, *, heads_q: int, heads_kv: int, q_weight=None,
+                      k_weight=None, eps: float = 1e-6, pair_axis=None,
+                      interleaved: bool = False, amplitude: float = 1.0):
+    """qkv_rope with gradients to qkv, q_weight and k_weight (training).  inv_freq
+    is a constant: one that requires a gradient is refused.  To capture a
+    backward pass into a CUDA graph, call qkv_rope_backward itself."""
+    if inv_freq.requires_grad:
+        raise ValueError("inv_freq has no gradient here")
+    cfg = dict(heads_q=heads_q, heads_kv=heads_kv, eps=eps, pair_axis=pair_axis,
+               interleaved=interleaved, amplitude=amplitude)
+    return QkvRopeFunction.apply(qkv, q_weight, k_weight, positions, inv_freq, cfg)
+
+
+def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, window: int = 0,
+           softmax_scale: float | None = None, out=None, lse=None, stream=None):
+    """(out, lse) of several new tokens per sequence over a paged cache
+    (attn_sink_extend): q [T, H_q, 64] packed by cu_seqlens_q [B + 1] int32,
+    caches [pages, page_size, H_kv, 64] that hold the new tokens' keys too,
+    block_table [B, max_pages] int32, seq_lens [B] int32 (cached + new), sink
+    [H_q] fp32.  Rows of out and lse behind cu_seqlens_q[B] are not written:
+    give out and lse to keep what they hold there."""
+    dev, bf16, i32 = q.device, torch.bfloat16, torch.int32
+    b = seq_lens.shape[0]
+    _want("q", q, bf16, dev, (None, None, 64))
+    t, hq = q.shape[0], q.shape[1]
+    _want("k_cache", k_cache, bf16, dev, (None, None, None, 64))
+    _want("v_cache", v_cache, bf16, dev, tuple(k_cache.shape))
+    _want("block_table", block_table, i32, dev, (b, None))
+    _want("seq_lens", seq_lens, i32, dev, (b,))
+    _want("cu_seqlens_q", cu_seqlens_q, i32, dev, (b + 1,))
+    _want("sink", sink, torch.float32, dev, (hq,))
+    if out is not None:
+        _want("out", out, bf16, dev, (t, hq, 64))
+    if lse is not None:
+        _want("lse", lse, torch.float32, dev, (hq, t))
+    p = AttnSinkExtendParams(b, t, hq, k_cache.shape[2], 64, k_cache.shape[1], k_cache.shape[0],
+                             block_table.shape[1], window,
+                             0.125 if softmax_scale is None else softmax_scale)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((t, hq, 64), dtype=bf16, device=dev)
+        if lse is None:
+            lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
+        nbytes = attn_sink_extend_workspace_size(p)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(attn_sink_extend(p, q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink,
+                                out, lse, ws, nbytes), "attn_sink_extend")
+    return out, lse

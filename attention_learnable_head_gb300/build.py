@@ -28,7 +28,7 @@ def _nvcc() -> str:
 def _sources() -> list[str]:
     files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
              if f.endswith((".cu", ".cuh", ".h"))]
-    files.append(os.path.join(INCLUDE, "attn_sink.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("attn_sink.h", "attn_sink_step.h")]
     return files
 
 

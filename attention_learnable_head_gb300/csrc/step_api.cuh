@@ -1,0 +1,437 @@
+// Host side of attn_sink_step.h: validation, tensor maps, workspace carving and
+// launches.  Included by attn_sink_api.cu after attn_sink.h's own entry points:
+// one translation unit, so that both share the device error word, the launch
+// counter and the per-device state.
+#pragma once
+
+namespace {
+
+// ----------------------------------------------------------------------------- plan
+// Tokens a CTA of the plan writes; more CTAs per group only repeat the sums.
+constexpr int kPlanTokensPerCta = 4 * kPlanThreads;
+
+// ----------------------------------------------------------------------------- rope
+int rope_validate(const attn_sink_rope_params* p) {
+  if (p == nullptr) return ATTN_SINK_ERR_INVALID_ARG;
+  if (p->head_dim != kHeadDim) return ATTN_SINK_ERR_UNSUPPORTED;
+  if (p->tokens < 0 || p->heads_q < 1 || p->heads_kv < 1 ||
+      p->heads_q > (1 << 20) || p->heads_kv > (1 << 20))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (p->rotary_dim < 0 || p->rotary_dim > kHeadDim) return ATTN_SINK_ERR_INVALID_ARG;
+  if (p->rotary_dim % 16 != 0) return ATTN_SINK_ERR_UNSUPPORTED;
+  if ((p->interleaved | p->norm | p->weight_bf16) & ~1) return ATTN_SINK_ERR_INVALID_ARG;
+  if (p->num_axes < 1 || p->num_axes > ATTN_SINK_ROPE_MAX_AXES) return ATTN_SINK_ERR_INVALID_ARG;
+  for (int i = 0; i < p->rotary_dim / 2; ++i)
+    if (p->pair_axis[i] >= p->num_axes) return ATTN_SINK_ERR_INVALID_ARG;
+  if (!std::isfinite(p->eps) || p->eps < 0.0f || !std::isfinite(p->amplitude))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  return ATTN_SINK_OK;
+}
+
+// A token stride: whole 16-byte chunks, heads that do not overlap.
+bool rope_stride_ok(long long stride, int heads) {
+  return stride % 8 == 0 && stride >= (long long)heads * kHeadDim && stride < (1ll << 40);
+}
+
+// Warps that share a token's heads, and the grid.  One warp per token where
+// that fills the GPU (the token's angles are computed once); with fewer tokens
+// the heads are spread over more warps, four heads at the least each.
+struct RopeGrid {
+  int parts, ctas;
+};
+RopeGrid rope_grid(const attn_sink_rope_params* p, int sms, int ctas_per_sm) {
+  RopeGrid g;
+  const long long warps = (long long)sms * ctas_per_sm * kRopeWarps;
+  const int most = (p->heads_q + 3) / 4;
+  long long parts = p->tokens > 0 ? warps / p->tokens : 1;
+  g.parts = (int)std::max<long long>(1, std::min<long long>(parts, most));
+  const long long items = (long long)p->tokens * g.parts;
+  g.ctas = (int)std::max<long long>(
+      1, std::min<long long>((items + kRopeWarps - 1) / kRopeWarps, (long long)sms * ctas_per_sm));
+  return g;
+}
+constexpr int kRopeCtas = 6;       // resident CTAs per SM the grids are sized for
+constexpr int kRopeBwdCtas = 4;
+
+RopeParams rope_params(const attn_sink_rope_params* p) {
+  RopeParams rp;
+  std::memset(&rp, 0, sizeof(rp));
+  rp.q_stride = p->q_stride;
+  rp.k_stride = p->k_stride;
+  rp.v_stride = p->v_stride;
+  rp.tokens = p->tokens;
+  rp.heads_q = p->heads_q;
+  rp.heads_kv = p->heads_kv;
+  rp.rotary = p->rotary_dim;
+  rp.weight_bf16 = p->weight_bf16;
+  rp.eps = p->eps;
+  rp.amplitude = p->amplitude;
+  std::memcpy(rp.pair_axis, p->pair_axis, sizeof(rp.pair_axis));
+  return rp;
+}
+
+template <bool kNorm, bool kInter>
+void rope_bwd_launch(const RopeParams& rp, int ctas, bool fp32, cudaStream_t s) {
+  if (fp32)
+    attn_sink_rope_bwd_kernel<kNorm, kInter, true><<<ctas, kRopeThreads, 0, s>>>(rp);
+  else
+    attn_sink_rope_bwd_kernel<kNorm, kInter, false><<<ctas, kRopeThreads, 0, s>>>(rp);
+}
+
+// ----------------------------------------------------------------------------- extend
+struct ExtendLayout {
+  int tokens;        // per tile
+  int n_items, max_parts, target;
+  size_t off_done, off_ml, off_o, total;
+};
+
+// CTAs an SM holds at once (shared memory, TMEM and registers allow two), and
+// key blocks a part has at least (each part stores and joins a 128-row fp32
+// result).
+constexpr int kExtCtasPerSm = 2;
+constexpr int kExtMinBlocks = 4;
+
+int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
+  if (p == nullptr) return ATTN_SINK_ERR_INVALID_ARG;
+  if (p->head_dim != kHeadDim) return ATTN_SINK_ERR_UNSUPPORTED;
+  if (p->batch < 0 || p->total_q < 0 || p->heads_kv < 1 || p->heads_q < 1 ||
+      p->heads_q % p->heads_kv != 0 || p->page_size < 1 || p->num_pages < 0 ||
+      p->max_pages < 0 || !(p->softmax_scale > 0.0f) || !std::isfinite(p->softmax_scale))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if ((long long)p->max_pages * p->page_size > (1ll << 30)) return ATTN_SINK_ERR_INVALID_ARG;
+  const int group = p->heads_q / p->heads_kv;
+  if (group > kExtMaxGroup) return ATTN_SINK_ERR_UNSUPPORTED;
+  L->tokens = kBlockM / group;
+  L->target = kExtCtasPerSm * sms;
+  const long long shares = (L->target + p->heads_kv - 1) / p->heads_kv;
+  // the bounds of attn_sink_extend_plan_kernel
+  const long long items = p->total_q / L->tokens + (long long)p->batch + shares;
+  if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
+  L->n_items = (int)items;
+  L->max_parts = (int)std::min<long long>(items, 2 * shares);
+  const size_t parts = (size_t)L->max_parts * p->heads_kv;
+  size_t off = align256((size_t)L->n_items * sizeof(ExtItem));
+  L->off_done = off;
+  off += align256(parts * sizeof(int));
+  L->off_ml = off;
+  off += align256(parts * kBlockM * sizeof(float2));
+  L->off_o = off;
+  off += align256(parts * kBlockM * kHeadDim * sizeof(float));
+  L->total = off;
+  return ATTN_SINK_OK;
+}
+
+bool g_ext_attr_set[kMaxDevices] = {false};
+
+// The extend kernels' shared memory limit, once per device.
+int extend_attributes() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return ATTN_SINK_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_dev_mutex);
+  if (!g_ext_attr_set[dev]) {
+    if (cudaFuncSetAttribute(attn_sink_extend_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kFwdSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_sink_extend_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kFwdSmemBytes) != cudaSuccess)
+      return ATTN_SINK_ERR_CUDA;
+    g_ext_attr_set[dev] = true;
+  }
+  return ATTN_SINK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_lens,
+                        const int* new_lens, const int* free_pages, int* block_table,
+                        long long* slots, int* positions, int* cu_seqlens, int* seq_lens,
+                        int* pages_needed, void* stream) {
+  NvtxRange range("attn_sink_page_plan");
+  if (params == nullptr || params->batch < 0 || params->page_size < 1 || params->num_pages < 0 ||
+      params->max_pages < 0 || params->num_free < 0 || params->max_tokens < 0 ||
+      (long long)params->max_pages * params->page_size > (1ll << 30))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr || pages_needed == nullptr ||
+      (params->batch > 0 &&
+       (cached_lens == nullptr || new_lens == nullptr || seq_lens == nullptr)) ||
+      (params->batch > 0 && params->max_pages > 0 && block_table == nullptr) ||
+      (params->num_free > 0 && free_pages == nullptr) ||
+      (params->max_tokens > 0 && (slots == nullptr || positions == nullptr)))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return ATTN_SINK_ERR_INVALID_ARG;
+  int sms = 0;
+  int* err = nullptr;
+  int st;
+  if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
+  PlanParams pp;
+  pp.cached = cached_lens;
+  pp.fresh = new_lens;
+  pp.free_pages = free_pages;
+  pp.table = block_table;
+  pp.slots = slots;
+  pp.positions = positions;
+  pp.cu = cu_seqlens;
+  pp.lens = seq_lens;
+  pp.needed = pages_needed;
+  pp.err = err;
+  pp.batch = params->batch;
+  pp.page_size = params->page_size;
+  pp.num_pages = params->num_pages;
+  pp.max_pages = params->max_pages;
+  pp.num_free = params->num_free;
+  pp.max_tokens = params->max_tokens;
+  // groups of sequences x blocks of a group's tokens, two CTAs per SM at most
+  const int groups = std::max(1, (params->batch + kPlanSeqs - 1) / kPlanSeqs);
+  const long long per_group = (params->max_tokens + groups - 1) / groups;
+  const long long blocks = (per_group + kPlanTokensPerCta - 1) / kPlanTokensPerCta;
+  const int y = (int)std::max<long long>(
+      1, std::min<long long>(blocks, std::max(1, 2 * sms / groups)));
+  attn_sink_plan_kernel<<<dim3(groups, y), kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      pp);
+  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+}
+
+int attn_sink_qkv_rope(const attn_sink_rope_params* params, const void* q, const void* k,
+                       const void* v, const int* positions, const float* inv_freq,
+                       const void* q_weight, const void* k_weight, const long long* slots,
+                       void* q_out, void* k_out, void* v_out, void* k_cache, void* v_cache,
+                       void* stream) {
+  NvtxRange range("attn_sink_qkv_rope");
+  int st = rope_validate(params);
+  if (st != ATTN_SINK_OK) return st;
+  if (!rope_stride_ok(params->q_stride, params->heads_q) ||
+      !rope_stride_ok(params->k_stride, params->heads_kv) ||
+      !rope_stride_ok(params->v_stride, params->heads_kv))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (slots != nullptr && (params->page_size < 1 || params->num_pages < 0))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (params->tokens == 0) return ATTN_SINK_OK;
+  const bool to_cache = slots != nullptr && params->num_pages > 0;
+  if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr ||
+      (params->rotary_dim > 0 && (positions == nullptr || inv_freq == nullptr)) ||
+      (params->norm && (q_weight == nullptr || k_weight == nullptr)) ||
+      (to_cache && (k_cache == nullptr || v_cache == nullptr)))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return ATTN_SINK_ERR_INVALID_ARG;
+  int sms = 0;
+  int* err = nullptr;
+  if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
+  RopeParams rp = rope_params(params);
+  rp.q = static_cast<const __nv_bfloat16*>(q);
+  rp.k = static_cast<const __nv_bfloat16*>(k);
+  rp.v = static_cast<const __nv_bfloat16*>(v);
+  rp.positions = positions;
+  rp.inv_freq = inv_freq;
+  rp.q_weight = q_weight;
+  rp.k_weight = k_weight;
+  rp.slots = slots;
+  rp.q_out = static_cast<__nv_bfloat16*>(q_out);
+  rp.k_out = static_cast<__nv_bfloat16*>(k_out);
+  rp.v_out = static_cast<__nv_bfloat16*>(v_out);
+  rp.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  rp.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  rp.cache_rows = slots != nullptr ? (long long)params->num_pages * params->page_size : 0;
+  rp.err = err;
+  const RopeGrid g = rope_grid(params, sms, kRopeCtas);
+  rp.parts = g.parts;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (params->norm && params->interleaved)
+    attn_sink_rope_kernel<true, true><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+  else if (params->norm)
+    attn_sink_rope_kernel<true, false><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+  else if (params->interleaved)
+    attn_sink_rope_kernel<false, true><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+  else
+    attn_sink_rope_kernel<false, false><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+}
+
+size_t attn_sink_qkv_rope_bwd_workspace_size(const attn_sink_rope_params* params) {
+  if (rope_validate(params) != ATTN_SINK_OK || !params->norm || params->tokens == 0) return 0;
+  const RopeGrid g = rope_grid(params, sm_count_or_default(), kRopeBwdCtas);
+  return align256((size_t)g.ctas * 2 * kHeadDim * sizeof(float));
+}
+
+int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, const void* k,
+                           const int* positions, const float* inv_freq, const void* q_weight,
+                           const void* k_weight, const void* dq, const void* dk, const void* dv,
+                           void* dq_in, void* dk_in, void* dv_in, long long dq_in_stride,
+                           long long dk_in_stride, long long dv_in_stride, float* dq_weight,
+                           float* dk_weight, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  NvtxRange range("attn_sink_qkv_rope_bwd");
+  int st = rope_validate(params);
+  if (st != ATTN_SINK_OK) return st;
+  if (params->grad_dtype != 0 && params->grad_dtype != 1) return ATTN_SINK_ERR_INVALID_ARG;
+  if (!rope_stride_ok(dq_in_stride, params->heads_q) ||
+      !rope_stride_ok(dk_in_stride, params->heads_kv) ||
+      (dv != nullptr && !rope_stride_ok(dv_in_stride, params->heads_kv)) ||
+      (params->norm && (!rope_stride_ok(params->q_stride, params->heads_q) ||
+                        !rope_stride_ok(params->k_stride, params->heads_kv))))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (params->norm && (dq_weight == nullptr || dk_weight == nullptr))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (params->tokens == 0) {
+    // no token: the weights' gradients are zero
+    if (params->norm &&
+        (cudaMemsetAsync(dq_weight, 0, kHeadDim * sizeof(float), s) != cudaSuccess ||
+         cudaMemsetAsync(dk_weight, 0, kHeadDim * sizeof(float), s) != cudaSuccess))
+      return ATTN_SINK_ERR_CUDA;
+    return ATTN_SINK_OK;
+  }
+  if (dq == nullptr || dk == nullptr || dq_in == nullptr || dk_in == nullptr ||
+      (dv == nullptr) != (dv_in == nullptr) ||
+      (params->rotary_dim > 0 && (positions == nullptr || inv_freq == nullptr)) ||
+      (params->norm &&
+       (q == nullptr || k == nullptr || q_weight == nullptr || k_weight == nullptr)))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      !aligned16(dq_in) || !aligned16(dk_in) || !aligned16(dv_in))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  int sms = 0;
+  int* err = nullptr;
+  if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
+  const RopeGrid g = rope_grid(params, sms, kRopeBwdCtas);
+  if (params->norm &&
+      (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+       workspace_bytes < align256((size_t)g.ctas * 2 * kHeadDim * sizeof(float))))
+    return ATTN_SINK_ERR_WORKSPACE;
+  RopeParams rp = rope_params(params);
+  rp.q = static_cast<const __nv_bfloat16*>(q);
+  rp.k = static_cast<const __nv_bfloat16*>(k);
+  rp.positions = positions;
+  rp.inv_freq = inv_freq;
+  rp.q_weight = q_weight;
+  rp.k_weight = k_weight;
+  rp.dq = dq;
+  rp.dk = dk;
+  rp.dv = dv;
+  rp.dq_in = static_cast<__nv_bfloat16*>(dq_in);
+  rp.dk_in = static_cast<__nv_bfloat16*>(dk_in);
+  rp.dv_in = static_cast<__nv_bfloat16*>(dv_in);
+  rp.dq_in_stride = dq_in_stride;
+  rp.dk_in_stride = dk_in_stride;
+  rp.dv_in_stride = dv_in_stride;
+  rp.dw_part = static_cast<float*>(workspace);
+  rp.err = err;
+  rp.parts = g.parts;
+  const bool fp32 = params->grad_dtype == 1;
+  if (params->norm && params->interleaved)
+    rope_bwd_launch<true, true>(rp, g.ctas, fp32, s);
+  else if (params->norm)
+    rope_bwd_launch<true, false>(rp, g.ctas, fp32, s);
+  else if (params->interleaved)
+    rope_bwd_launch<false, true>(rp, g.ctas, fp32, s);
+  else
+    rope_bwd_launch<false, false>(rp, g.ctas, fp32, s);
+  if (!launched()) return ATTN_SINK_ERR_CUDA;
+  if (params->norm) {
+    attn_sink_rope_dw_kernel<<<1, kRopeSumThreads, 0, s>>>(rp.dw_part, g.ctas, dq_weight,
+                                                           dk_weight);
+    if (!launched()) return ATTN_SINK_ERR_CUDA;
+  }
+  return ATTN_SINK_OK;
+}
+
+size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params) {
+  ExtendLayout L;
+  if (extend_layout(params, sm_count_or_default(), &L) != ATTN_SINK_OK || params->batch == 0 ||
+      params->total_q == 0)
+    return 0;
+  return L.total;
+}
+
+int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const void* k_cache,
+                     const void* v_cache, const int* block_table, const int* seq_lens,
+                     const int* cu_seqlens_q, const float* sink, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange range("attn_sink_extend");
+  ExtendLayout L;
+  int st = extend_layout(params, sm_count_or_default(), &L);
+  if (st != ATTN_SINK_OK) return st;
+  if (params->batch == 0 || params->total_q == 0) return ATTN_SINK_OK;
+  if (q == nullptr || sink == nullptr || out == nullptr || lse == nullptr ||
+      seq_lens == nullptr || cu_seqlens_q == nullptr ||
+      (params->max_pages > 0 && block_table == nullptr) ||
+      (params->num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return ATTN_SINK_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < L.total ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return ATTN_SINK_ERR_WORKSPACE;
+  int sms = 0;
+  int* err = nullptr;
+  if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
+  if ((st = extend_attributes()) != ATTN_SINK_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ExtParams ep;
+  std::memset(&ep, 0, sizeof(ep));
+  ep.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
+  ep.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+  ep.block_table = block_table;
+  ep.seq_lens = seq_lens;
+  ep.cu_q = cu_seqlens_q;
+  ep.sink = sink;
+  ep.out = static_cast<__nv_bfloat16*>(out);
+  ep.lse = lse;
+  ep.items = reinterpret_cast<ExtItem*>(ws);
+  ep.done = reinterpret_cast<int*>(ws + L.off_done);
+  ep.ml_part = reinterpret_cast<float2*>(ws + L.off_ml);
+  ep.o_part = reinterpret_cast<float*>(ws + L.off_o);
+  ep.err = err;
+  ep.batch = params->batch;
+  ep.total_q = params->total_q;
+  ep.heads_q = params->heads_q;
+  ep.heads_kv = params->heads_kv;
+  ep.group = params->heads_q / params->heads_kv;
+  ep.tokens = L.tokens;
+  ep.page_size = params->page_size;
+  ep.num_pages = params->num_pages;
+  ep.max_pages = params->max_pages;
+  ep.window = params->window > 0 ? params->window : 0;
+  ep.n_items = L.n_items;
+  ep.max_parts = L.max_parts;
+  ep.target = L.target;
+  ep.min_blocks = kExtMinBlocks;
+  ep.scale_log2 = params->softmax_scale * kLog2e;
+#ifdef ATTN_SINK_TEST_HOOKS
+  ep.skip_k_tile = g_test_skip_k_tile.load();
+#endif
+  // Page sizes that are a multiple of 8 keys (whole swizzle atoms) are copied by
+  // TMA, in boxes of the largest power of two that divides the page, at most a
+  // block; the rows have to fit a copy's 32-bit coordinates.
+  const long long rows = (long long)params->num_pages * params->page_size;
+  const bool tma = params->page_size % 8 == 0 && rows > 0 && rows < (1ll << 31);
+  ep.box = tma ? std::min(params->page_size & -params->page_size, kBlockN) : 0;
+  if ((st = encode_rows(&ep.tm_q, q, params->total_q, params->heads_q,
+                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.tokens, ep.group)) != ATTN_SINK_OK ||
+      (st = encode_rows(&ep.tm_out, out, params->total_q, params->heads_q,
+                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.tokens, ep.group)) != ATTN_SINK_OK)
+    return st;
+  if (tma &&
+      ((st = encode_rows(&ep.tm_k, k_cache, rows, params->heads_kv,
+                         CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ep.box)) != ATTN_SINK_OK ||
+       (st = encode_rows(&ep.tm_v, v_cache, rows, params->heads_kv,
+                         CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ep.box)) != ATTN_SINK_OK))
+    return st;
+  attn_sink_extend_plan_kernel<<<1, kExtSchedThreads, 0, s>>>(ep);
+  if (!launched()) return ATTN_SINK_ERR_CUDA;
+  const unsigned grid = (unsigned)L.n_items * (unsigned)params->heads_kv;
+  if (tma)
+    attn_sink_extend_kernel<true><<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
+  else
+    attn_sink_extend_kernel<false><<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
+  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+}
+
+}  // extern "C"
