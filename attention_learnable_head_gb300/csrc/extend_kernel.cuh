@@ -15,11 +15,13 @@
 // other page sizes are copied 16 bytes a lane with cp.async.
 //
 // Work items.  A schedule kernel of one CTA lists (sequence, tile, key range)
-// in the workspace.  Sequences whose keys exceed an even share of the launch's
-// work are split over several CTAs per tile, so that a long cache with few new
-// tokens fills the GPU; the CTA of a tile that finishes last joins the parts
-// and adds the sink (counters that the schedule kernel zeroes).  The parts are
-// joined in the order of their keys, whichever CTA does it.
+// in the workspace; the hardware hands them out, each to one CTA per kv head
+// (which go through the same keys at the same time: each reads 128 bytes of a
+// cache row that holds them all).  Tiles with more keys than an even share of
+// the launch's work are split, so that a long cache with few new tokens fills
+// the GPU; the parts leave fp32 sums in the workspace and a third kernel joins
+// them and adds the sink.  The three are chained by programmatic dependent
+// launch.
 //
 // The rest is the forward kernel's pipeline: S = Q K^T into TMEM, online
 // softmax by two warpgroups (one per key half), P to TMEM, O += P V with P
@@ -28,21 +30,30 @@
 // by each CTA; one more rounding of 2^-8 next to that of the bf16 output.  The
 // row sums add the fp32 probabilities.
 #pragma once
+#include <climits>
 #include "fwd_kernel.cuh"
 
 namespace attn_sink {
 
 constexpr int kExtThreads = 320;           // 8 softmax warps, copy warp, MMA warp
 constexpr int kExtMaxGroup = 128;
-constexpr int kExtMaxSplits = 64;
+constexpr int kExtMaxSplits = 64;          // parts of a tile
+constexpr int kExtMinBlocks = 4;           // key blocks of a part
+constexpr int kExtOver = 5;                // what a CTA costs beside its blocks, in blocks
 constexpr int kExtSchedThreads = 1024;
-constexpr uint32_t kExtNone = 0xFFFFFFFFu;
+constexpr int kExtJoinThreads = 256;
 
-struct ExtItem {                           // one CTA's work for each kv head
-  uint32_t seq;                            // kExtNone: unused entry
-  uint32_t tile;
-  uint32_t split;                          // part << 16 | parts of the tile
-  uint32_t first;                          // index of the tile's first partial result
+// One CTA's work for each kv head: a tile, or a range of its key blocks.
+struct ExtItem {
+  int num, blk0, seq, row0;                // blocks (-1: unused entry); first block; sequence;
+  int lo, hi, mlo, mhi;                    // first row of q; keys the tile sees; blocks [mlo, mhi)
+  int rows, at0, split, first;             // that need no mask; rows with a token; key position of
+};                                         // the first token; part << 16 | parts; first partial
+static_assert(sizeof(ExtItem) == 48, "three 16-byte loads");
+
+// A tile whose parts are to be joined.
+struct ExtTileRef {
+  int first, parts, rows, row0;            // first partial result; rows with a token; row of q
 };
 
 struct ExtParams {
@@ -61,14 +72,14 @@ struct ExtParams {
   ExtItem* items;
   float* o_part;           // [partial][kv head][128 rows][64]
   float2* ml_part;         // [partial][kv head][128 rows]: maximum (log2 units), sum
-  int* done;               // [partial][kv head], counted at a tile's first partial
+  ExtTileRef* tiles;       // tiles that are split, for the join
+  int* n_tiles;            // and how many
   int* err;
   int batch, total_q, heads_q, heads_kv, group, tokens;
   int page_size, num_pages, max_pages, window;
   int box;                 // keys of a TMA box (0: cp.async copies)
-  int n_items, max_parts;  // sizes of items, and of the partial results
-  int target;              // CTAs the work is spread over
-  int min_blocks;          // key blocks a part has at least
+  int n_items, max_parts, max_tiles;   // sizes of items, partial results, tiles
+  int slots;               // CTAs the GPU holds at once
   float scale_log2;
 #ifdef ATTN_SINK_TEST_HOOKS
   int skip_k_tile;
@@ -91,116 +102,193 @@ __device__ __forceinline__ ExtSeq ext_seq(const ExtParams& p, int b, bool* bad) 
   return s;
 }
 
-// Keys [lo, hi) that tokens i0 .. i1 of the sequence see.
-__device__ __forceinline__ void ext_keys(const ExtSeq& s, int i0, int i1, int window, int* lo,
-                                         int* hi) {
+// Keys [lo, hi) that tile `t` of the sequence sees, and their blocks.
+struct ExtTile {
+  int lo, hi, blocks;
+};
+__device__ __forceinline__ ExtTile ext_tile(const ExtParams& p, const ExtSeq& s, int t) {
+  const int i0 = t * p.tokens, i1 = min(i0 + p.tokens, s.n) - 1;
   const int off = s.len - s.n;             // key position of token 0
-  *hi = max(0, min(s.len, i1 + off + 1));
-  *lo = window > 0 ? max(0, i0 + off - window + 1) : 0;
+  ExtTile x;
+  x.hi = max(0, min(s.len, i1 + off + 1));
+  x.lo = p.window > 0 ? max(0, i0 + off - p.window + 1) : 0;
+  x.blocks = x.hi > x.lo ? (x.hi + kBlockN - 1) / kBlockN - x.lo / kBlockN : 0;
+  return x;
 }
 
-__device__ __forceinline__ int ext_blocks(int lo, int hi) {
-  return hi > lo ? (hi + kBlockN - 1) / kBlockN - lo / kBlockN : 0;
+// Parts of a tile of `blocks` blocks, of at least c blocks each (rounded up).
+__device__ __forceinline__ int ext_parts(int blocks, int c) {
+  return min(kExtMaxSplits, max(1, (blocks + c - 1) / c));
+}
+
+// Exclusive scan of the block's values; *all receives their sum.
+__device__ __forceinline__ int ext_scan(int x, int* s_warp, int* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int inc = x;
+  #pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  __syncthreads();                         // the last scan's sums have been read
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  // every warp scans the 32 warps' sums
+  int sum = s_warp[lane];
+  #pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += y;
+  }
+  *all = __shfl_sync(0xffffffffu, sum, 31);
+  const int before = __shfl_sync(0xffffffffu, sum, max(warp - 1, 0));
+  return (warp > 0 ? before : 0) + inc - x;
 }
 
 // Lists the work items.  With W the key blocks of all tiles (each taken as long
-// as its sequence's last) times the kv heads, a part has at least c = W / target
-// blocks and a tile ceil(blocks / c) parts: tiles + target / H_kv items at most.
+// as its sequence's last) times the kv heads, a part has at least c blocks and a
+// tile ceil(blocks / c) parts.  Tried are c = all blocks (nothing is split), W /
+// slots and W / (2 slots), slots being the CTAs the GPU holds at once; taken is
+// the one with the least ceil(CTAs / slots) * (c + kExtOver): rounds of CTAs, and
+// what a CTA costs beside its blocks.  That makes tiles + 2 slots / H_kv items at
+// most.
+// A thread takes a sequence (neighbours go to different warps), its warp writes
+// the sequence's items.
 __global__ void __launch_bounds__(kExtSchedThreads, 1)
 attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
-  constexpr int kWarps = kExtSchedThreads / 32;
-  __shared__ long long s_red[kWarps];
-  __shared__ int s_scan[2][kWarps];
+  __shared__ int s_scan[kExtSchedThreads / 32];
+  __shared__ unsigned long long s_work, s_items[3];
+  __shared__ int s_most;
+  grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool bad = false;
-  auto tiles_of = [&](const ExtSeq& s) { return (s.n + p.tokens - 1) / p.tokens; };
-  auto blocks_of = [&](const ExtSeq& s, int tiles) {     // of the last tile
-    int lo, hi;
-    ext_keys(s, (tiles - 1) * p.tokens, s.n - 1, p.window, &lo, &hi);
-    return ext_blocks(lo, hi);
+  ExtSeq s{0, 0, 0};
+  int tiles = 0, blocks = 0;               // of the sequence; of its last tile
+  auto load = [&](int b) {
+    s = ExtSeq{0, 0, 0};
+    tiles = blocks = 0;
+    if (b >= p.batch) return;
+    s = ext_seq(p, b, &bad);
+    tiles = (s.n + p.tokens - 1) / p.tokens;
+    if (tiles > 0) blocks = ext_tile(p, s, tiles - 1).blocks;
   };
-  // total work
-  long long w = 0;
-  for (int b = tid; b < p.batch; b += kExtSchedThreads) {
-    const ExtSeq s = ext_seq(p, b, &bad);
-    const int tiles = tiles_of(s);
-    if (tiles > 0) w += (long long)tiles * blocks_of(s, tiles);
+  if (tid == 0) {
+    s_work = s_items[0] = s_items[1] = s_items[2] = 0;
+    s_most = 0;
+  }
+  __syncthreads();
+  unsigned long long w = 0;
+  int most = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
+    load(b0 + 32 * lane + warp);
+    w += (unsigned long long)tiles * (unsigned)blocks;
+    most = max(most, blocks);
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
   #pragma unroll
   for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  if (lane == 0) s_red[warp] = w;
-  // the tiles' completion counters, and the table's entries behind the last item
-  for (int i = tid; i < p.max_parts * p.heads_kv; i += kExtSchedThreads) p.done[i] = 0;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0 && w > 0) {                                // whole numbers: any order
+    atomicAdd(&s_work, w);
+    atomicMax(&s_most, most);
+  }
   __syncthreads();
-  w = 0;
-  #pragma unroll
-  for (int i = 0; i < kWarps; ++i) w += s_red[i];
-  const long long share = (w * p.heads_kv + p.target - 1) / p.target;
-  const int chunk = (int)min(max((long long)p.min_blocks, share), 1ll << 24);   // > any tile's blocks
-
-  int item0 = 0, part0 = 0;                // of the sequences before this round
-  for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
-    const int b = b0 + tid;
-    ExtSeq s{0, 0, 0};
-    int tiles = 0, parts = 0;
-    if (b < p.batch) {
-      s = ext_seq(p, b, &bad);
-      tiles = tiles_of(s);
-      if (tiles > 0)
-        parts = min(kExtMaxSplits, max(1, (blocks_of(s, tiles) + chunk - 1) / chunk));
-    }
-    const int mine_i = tiles * parts, mine_p = parts > 1 ? tiles * parts : 0;
-    int it = mine_i, ip = mine_p;          // inclusive scans
+  int chunk = 0;
+  {
+    int c[3];
     #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, it, d), c = __shfl_up_sync(0xffffffffu, ip, d);
-      if (lane >= d) {
-        it += a;
-        ip += c;
+    for (int i = 0; i < 3; ++i) {
+      const long long share =
+          i == 0 ? s_most : ((long long)s_work * p.heads_kv + i * p.slots - 1) / (i * p.slots);
+      c[i] = (int)min(max((long long)kExtMinBlocks, share), 1ll << 24);   // > any tile's
+      long long n = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
+        if (p.batch > kExtSchedThreads) load(b0 + 32 * lane + warp);     // else still at hand
+        if (tiles > 0) n += (long long)tiles * ext_parts(blocks, c[i]);
       }
-    }
-    if (lane == 31) {
-      s_scan[0][warp] = it;
-      s_scan[1][warp] = ip;
+      #pragma unroll
+      for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+      if (lane == 0 && n > 0) atomicAdd(&s_items[i], (unsigned long long)n);
     }
     __syncthreads();
-    int bi = item0, bp = part0, all_i = 0, all_p = 0;
+    long long least = LLONG_MAX;
     #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) {
-        bi += s_scan[0][i];
-        bp += s_scan[1][i];
-      }
-      all_i += s_scan[0][i];
-      all_p += s_scan[1][i];
-    }
-    bi += it - mine_i;
-    bp += ip - mine_p;
-    // a warp writes its 32 sequences' items, 32 at a time
-    for (int l = 0; l < 32; ++l) {
-      const int n = __shfl_sync(0xffffffffu, mine_i, l);
-      if (n == 0) continue;
-      const int sp = __shfl_sync(0xffffffffu, parts, l), nt = __shfl_sync(0xffffffffu, tiles, l);
-      const int wi = __shfl_sync(0xffffffffu, bi, l), wp = __shfl_sync(0xffffffffu, bp, l);
-      for (int k = lane; k < n; k += 32) {
-        const int tile = k / sp, part = k - tile * sp;
-        ExtItem e;
-        e.seq = (uint32_t)(b0 + 32 * warp + l);
-        e.tile = (uint32_t)(nt - 1 - tile);            // the longest tiles first
-        e.split = (uint32_t)part << 16 | (uint32_t)sp;
-        e.first = (uint32_t)(wp + tile * sp);
-        // both bounds hold for every cu_seqlens that ascends; one that does not
-        // may list more, which is dropped (and was recorded)
-        if (sp > 1 && wp + tile * sp + sp > p.max_parts) e.seq = kExtNone;
-        if (wi + k < p.n_items) reinterpret_cast<uint4*>(p.items)[wi + k] = *reinterpret_cast<uint4*>(&e);
+    for (int i = 0; i < 3; ++i) {
+      const long long ctas = (long long)s_items[i] * p.heads_kv;
+      const long long cost = (ctas + p.slots - 1) / p.slots * (min(c[i], s_most) + kExtOver);
+      if (cost < least) {
+        least = cost;
+        chunk = c[i];
       }
     }
+  }
+
+  int item0 = 0, part0 = 0, split0 = 0;    // of the sequences before this round
+  for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
+    const int b = b0 + 32 * lane + warp;
+    if (p.batch > kExtSchedThreads) load(b);               // else still at hand
+    const int parts = tiles > 0 ? ext_parts(blocks, chunk) : 0;
+    int all_i, all_p, all_s;
+    const int first_i = item0 + ext_scan(tiles * parts, s_scan, &all_i);
+    const int first_p = part0 + ext_scan(parts > 1 ? tiles * parts : 0, s_scan, &all_p);
+    const int first_s = split0 + ext_scan(parts > 1 ? tiles : 0, s_scan, &all_s);
     item0 += all_i;
     part0 += all_p;
-    __syncthreads();
+    split0 += all_s;
+    for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 0); todo; todo &= todo - 1) {
+      const int l = __ffs(todo) - 1;
+      ExtSeq x;
+      x.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+      x.n = __shfl_sync(0xffffffffu, s.n, l);
+      x.len = __shfl_sync(0xffffffffu, s.len, l);
+      const int xb = __shfl_sync(0xffffffffu, b, l);
+      const int np = __shfl_sync(0xffffffffu, parts, l), nt = __shfl_sync(0xffffffffu, tiles, l);
+      const int wi = __shfl_sync(0xffffffffu, first_i, l);
+      const int wp = __shfl_sync(0xffffffffu, first_p, l);
+      const int wt = __shfl_sync(0xffffffffu, first_s, l);
+      for (int k = lane; k < nt * np; k += 32) {
+        const int tile = nt - 1 - k / np, part = k % np;   // the longest tiles first
+        const ExtTile e = ext_tile(p, x, tile);
+        const int i0 = tile * p.tokens, i1 = min(i0 + p.tokens, x.n) - 1, off = x.len - x.n;
+        const int per = (e.blocks + np - 1) / np, skip = min(e.blocks, part * per);
+        ExtItem it;
+        it.num = min(per, e.blocks - skip);
+        it.blk0 = e.lo / kBlockN + skip;
+        it.seq = xb;
+        it.row0 = x.q0 + i0;
+        it.lo = e.lo;
+        it.hi = e.hi;
+        // blocks before mlo hold keys behind some token's window, blocks from mhi
+        // on keys after some token
+        const int lost = i1 + off - p.window;              // last key some token has lost
+        it.mlo = p.window > 0 && lost >= 0 ? lost / kBlockN + 1 - it.blk0 : 0;
+        it.mhi = max(0, min(x.len, i0 + off + 1)) / kBlockN - it.blk0;
+        it.rows = (i1 - i0 + 1) * p.group;
+        it.at0 = i0 + off;
+        it.split = part << 16 | np;
+        it.first = wp + (k / np) * np;
+        // both bounds hold for every cu_seqlens that ascends; one that does not
+        // may list more, which is dropped (and was recorded)
+        if (np > 1 && it.first + np > p.max_parts) it.num = -1;
+        if (np > 1 && part == 0 && wt + k / np < p.max_tiles)
+          p.tiles[wt + k / np] =
+              ExtTileRef{it.first, it.num < 0 ? 0 : np, it.num < 0 ? 0 : it.rows, it.row0};
+        if (wi + k >= p.n_items) continue;
+        const uint4* src = reinterpret_cast<const uint4*>(&it);
+        uint4* dst = reinterpret_cast<uint4*>(p.items + wi + k);
+        dst[0] = src[0];
+        dst[1] = src[1];
+        dst[2] = src[2];
+      }
+    }
   }
-  for (int k = item0 + tid; k < p.n_items; k += kExtSchedThreads) p.items[k].seq = kExtNone;
+  for (int k = item0 + tid; k < p.n_items; k += kExtSchedThreads) p.items[k].num = -1;
+  if (tid == 0) *p.n_tiles = min(split0, p.max_tiles);
+}
+
+// The bits below bit n of a word.
+__device__ __forceinline__ uint32_t ext_below(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
 template <bool kTma>
@@ -215,55 +303,48 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
   __shared__ volatile int abort_flag;
   __shared__ float s_mx[2][2][kBlockM];
   __shared__ float s_red_l[2][kBlockM];
-  __shared__ int s_last;
+  __shared__ int s_at[kBlockM];            // key position of a row's token
+  __shared__ int s_lo, s_hi, s_bad;        // keys of the tile; some page is missing
 
   const int item = (int)(blockIdx.x / (unsigned)p.heads_kv);
   const int g = (int)(blockIdx.x - (unsigned)item * (unsigned)p.heads_kv);
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p.items) + item);
-  if (raw.x == kExtNone) return;                          // uniform per CTA
-  const int seq = (int)raw.x, tile = (int)raw.y;
-  const int part = (int)(raw.z >> 16), parts = (int)(raw.z & 0xFFFFu);
-  bool dummy = false;
-  const ExtSeq sp = ext_seq(p, seq, &dummy);
-  const int i0 = tile * p.tokens;
-  const int i1 = min(i0 + p.tokens, sp.n) - 1;            // last token of the tile
-  const int rows = (i1 - i0 + 1) * p.group;               // rows that hold a token
-  const int off = sp.len - sp.n;
+  const uint4* desc = reinterpret_cast<const uint4*>(p.items + item);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const uint4 d0 = __ldcg(desc), d1 = __ldcg(desc + 1), d2 = __ldcg(desc + 2);
+  const int num = (int)d0.x, blk0 = (int)d0.y, row0 = (int)d0.w;
+  if (num < 0) return;                                    // uniform per CTA
+  const int lo = (int)d1.x, hi = (int)d1.y, mlo0 = (int)d1.z, mhi0 = (int)d1.w;
+  const int rows = (int)d2.x;                             // rows that hold a token
+  const int part = (int)(d2.z >> 16), parts = (int)(d2.z & 0xFFFFu), first = (int)d2.w;
+  const int row_warps = (rows + 31) / 32;                 // the other rows' warps only wait
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  // keys [lo, hi) of the tile, and of them the blocks [blk0, blk0 + num) of
-  // this part
-  int lo, hi;
-  ext_keys(sp, i0, i1, p.window, &lo, &hi);
-  int blk0 = lo / kBlockN, num = ext_blocks(lo, hi);
-  if (parts > 1) {
-    const int per = (num + parts - 1) / parts;
-    const int skip = min(num, part * per);
-    blk0 += skip;
-    num = min(per, num - skip);
-  }
-  const size_t pidx = (size_t)(raw.w + part) * p.heads_kv + g;   // this CTA's partial result
-  const int* table = p.block_table + (size_t)seq * p.max_pages;
+  const size_t pidx = (size_t)(first + part) * p.heads_kv + g;   // this CTA's partial result
+  const int* table = p.block_table + (size_t)d0.z * p.max_pages;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + kTileBytes;
   uint8_t* sV = sK + kFwdKStages * kTileBytes;
-  bool failed = false;
 
   if (num > 0) {
-    // Does every page of these keys lie in the cache?  (Rarely not: then the
-    // softmax looks its keys' entries up one by one.)
-    bool bad_page = false;
-    {
-      const int k0 = max(lo, blk0 * kBlockN), k1 = min(hi, (blk0 + num) * kBlockN);
-      const int pg1 = (k1 - 1) / p.page_size;
-      for (int pg = k0 / p.page_size + tid; pg <= pg1; pg += kExtThreads) {
-        const int e = __ldg(table + pg);
-        bad_page |= e < 0 || e >= p.num_pages;
+    // The copy warp's first table entries, on their way while the CTA sets up.
+    // Lanes 0-15 copy the K boxes of a block, lanes 16-31 know the V boxes; each
+    // holds the table entry of its next box, loaded one block ahead.
+    const int half = lane >> 4, ci = lane & 15;
+    int ent = -1, in_page = 0;
+    auto fetch = [&](int n) {
+      const int j = (blk0 + n) * kBlockN + ci * p.box;
+      ent = -1;
+      if (ci * p.box < kBlockN && n < num && j < hi && j + p.box > lo) {
+        const int pg = j / p.page_size;
+        in_page = j - pg * p.page_size;
+        ent = __ldg(table + pg);
       }
-    }
+    };
+    if (kTma && warp == kFwdTmaWarp) fetch(0);
     if (tid == 0) {
       abort_flag = 0;
       mbar_init(&q_full, 1);
@@ -277,20 +358,22 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
         mbar_init(&v_empty[s], 1);
       }
       mbar_init(&s_full, 1);
-      mbar_init(&s_free, 2 * kBlockM);
-      mbar_init(&p_full, 2 * kBlockM);
+      mbar_init(&s_free, 64 * row_warps);
+      mbar_init(&p_full, 64 * row_warps);
       mbar_init(&pv_done, 1);
       fence_mbarrier_init();
+      s_lo = lo;
+      s_hi = hi;
     }
+    if (tid < kBlockM) s_at[tid] = (int)d2.y + tid / p.group;
     if (warp == kFwdMmaWarp) {
       tmem_alloc(&tmem_base_sh, kFwdTmemCols);
       tmem_relinquish();
     }
     tc_fence_before();
-    bad_page = __syncthreads_or(bad_page);
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-    if (bad_page && tid == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
 
     if (warp == kFwdTmaWarp) {
       // -------------------------------------------------------------- copies
@@ -298,24 +381,17 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
       if (lane == 0) {
         tma_prefetch_desc(&p.tm_q);
         mbar_arrive_expect_tx(&q_full, q_bytes);
-        tma_load_3d(&p.tm_q, &q_full, sQ, 0, g * p.group, sp.q0 + i0);
+        tma_load_3d(&p.tm_q, &q_full, sQ, 0, g * p.group, row0);
       }
       __syncwarp();
       if (kTma) {
-        // Lanes 0-15 copy the K boxes of a block, lanes 16-31 the V boxes; each
-        // holds the page of its next box, read one block ahead.
-        const int half = lane >> 4, ci = lane & 15;
-        const int boxes = kBlockN / p.box;
-        const bool mine = ci < boxes;
-        const int oob = p.num_pages * p.page_size;          // first row past the cache
-        auto row_of = [&](int n) -> int {                   // cache row of this lane's box
-          const int j = (blk0 + n) * kBlockN + ci * p.box;
-          if (!mine || n >= num || j >= hi || j + p.box <= lo) return oob;
-          const int pg = j / p.page_size;
-          const int e = __ldg(table + pg);
-          return e >= 0 && e < p.num_pages ? e * p.page_size + (j - pg * p.page_size) : oob;
+        const bool mine = ci < kBlockN / p.box;
+        // cache row of the fetched box; past the tensor (zero fill) without a page
+        auto row = [&]() {
+          return (unsigned)ent < (unsigned)p.num_pages ? ent * p.page_size + in_page
+                                                       : p.num_pages * p.page_size;
         };
-        int row = row_of(0);
+        const uint64_t keep = l2_policy_evict_last();
         int nk = 0, nv = 0;
         unsigned long long t_last = global_timer_ns();
         bool ok = true;
@@ -339,9 +415,9 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
             if (half == 0) {
               const int st = nk % kFwdKStages;
               if (mine)
-                tma_load_3d(&p.tm_k, &k_full[st], sK + st * kTileBytes + ci * p.box * 128, 0, g,
-                            row);
-              row = row_of(nk + 1);
+                tma_load_3d_hint(&p.tm_k, &k_full[st], sK + st * kTileBytes + ci * p.box * 128, 0,
+                                 g, row(), keep);
+              fetch(nk + 1);
             }
             ++nk;
           }
@@ -349,9 +425,9 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
             if (half == 1) {
               const int st = nv % kFwdVStages;
               if (mine)
-                tma_load_3d(&p.tm_v, &v_full[st], sV + st * kTileBytes + ci * p.box * 128, 0, g,
-                            row);
-              row = row_of(nv + 1);
+                tma_load_3d_hint(&p.tm_v, &v_full[st], sV + st * kTileBytes + ci * p.box * 128, 0,
+                                 g, row(), keep);
+              fetch(nv + 1);
             }
             ++nv;
           }
@@ -494,154 +570,163 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
       }
     } else {
       // -------------------------------------------------------------- softmax warps
-      // Key half c = warp / 4; thread = row = TMEM lane.
+      // Key half c = warp / 4; thread = row = TMEM lane.  Warps whose rows hold no
+      // token go straight to the end.
       const int c = warp >> 2;
       const int r = tid & 127;
-      const int tok = r / p.group;
-      const int hq = g * p.group + (r - tok * p.group);
-      const int i = i0 + tok;
-      const bool valid = r < rows;
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t tS = tmem + kFwdColS + 64 * c + lane_base;
       const uint32_t tP = tmem + kFwdColP + 32 * c + lane_base;
       const uint32_t tO = tmem + kFwdColO + 32 * c + lane_base;
-      // a warp without a row that holds a token only keeps the barriers going
-      const bool idle = 32 * (warp & 3) >= rows;
+      const bool working = (warp & 3) < row_warps;
+      // Does every page of these keys lie in the cache?  (Rarely not: then every
+      // block is masked, and the entries of its keys are looked up one by one.)
+      bool bad_page = false;
+      {
+        const int k0 = max(lo, blk0 * kBlockN), k1 = min(hi, (blk0 + num) * kBlockN);
+        const int pg1 = (k1 - 1) / p.page_size;
+        for (int pg = k0 / p.page_size + tid; pg <= pg1; pg += 2 * kBlockM) {
+          const int e = __ldg(table + pg);
+          bad_page |= e < 0 || e >= p.num_pages;
+        }
+      }
+      bad_page = !named_barrier_and(1, 2 * kBlockM, !bad_page);
+      s_bad = bad_page;                                     // by every thread, for itself
+      if (bad_page && tid == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
       float m = -INFINITY, l = 0.0f;
       const float sl2 = p.scale_log2;
       const uint64_t sl2x2 = f2(sl2, sl2);
-      const int jmax = min(sp.len - 1, i + off);            // inclusive
-      const int jmin = p.window > 0 ? i + off - p.window + 1 : 0;
+      // Blocks before mlo hold keys behind some token's window, blocks from mhi on
+      // keys after some token; with a missing page every block is masked.
+      int mlo = 0, mhi = 0;
+      if (!bad_page) {
+        mlo = mlo0;
+        mhi = mhi0;
+      }
       bool ok = true;
-      for (int it = 0; it < num; ++it) {
+      for (int it = 0; working && it < num; ++it) {
         uint32_t a[64];
-        const int jb = (blk0 + it) * kBlockN;
         bool got = mbar_wait_warp(&s_full, it & 1, &abort_flag);
         float mx_half = -INFINITY;
         if (got) {
           tc_fence_after();
-          if (!idle) {
-            tmem_ld_x32(tS, a);
-            tmem_ld_x32(tS + 32, a + 32);
-            tmem_ld_wait();
-          }
+          tmem_ld_x32(tS, a);
+          tmem_ld_x32(tS + 32, a + 32);
+          tmem_ld_wait();
           tc_fence_before();
           mbar_arrive(&s_free);
-          if (!idle) {
-            const int j0 = jb + 64 * c;                     // first key of this half
-            const bool need_mask = j0 + 64 > sp.len || j0 + 63 > i0 + off ||
-                                   (p.window > 0 && j0 <= i1 + off - p.window);
-            if (need_mask) {
-              #pragma unroll
-              for (int e = 0; e < 64; ++e) {
-                const int j = j0 + e;
-                if (j > jmax || j < jmin) a[e] = __float_as_uint(-INFINITY);
-              }
-            }
-            if (bad_page) {
-              uint32_t off_lo = 0, off_hi = 0;              // keys without a page
+          if (it < mlo || it >= mhi) {
+            const int j0 = (blk0 + it) * kBlockN + 64 * c;  // first key of this half
+            const int at = s_at[r];
+            const int jmax = min(s_hi - 1, at) - j0;        // inclusive, within the half
+            const int jmin = (p.window > 0 ? at - p.window + 1 : 0) - j0;
+            // bit e: key e of the half is not seen (two words tested bit by bit cost
+            // half of what two comparisons an element do)
+            uint32_t w0 = ~(ext_below(jmax + 1) & ~ext_below(jmin));
+            uint32_t w1 = ~(ext_below(jmax - 31) & ~ext_below(jmin - 32));
+            if (s_bad) {                                    // keys without a page
               #pragma unroll 1
               for (int e = 0; e < 64; ++e) {
                 const int j = j0 + e;
-                if (j < lo || j >= hi) continue;
+                if (j < s_lo || j >= s_hi) continue;
                 const int pe = __ldg(table + j / p.page_size);
                 if (pe >= 0 && pe < p.num_pages) continue;
-                if (e < 32) off_lo |= 1u << e;
-                else off_hi |= 1u << (e - 32);
+                if (e < 32) w0 |= 1u << e;
+                else w1 |= 1u << (e - 32);
               }
-              #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (((e < 32 ? off_lo : off_hi) >> (e & 31)) & 1u)
-                  a[e] = __float_as_uint(-INFINITY);
             }
-            float q0 = __uint_as_float(a[0]), q1 = __uint_as_float(a[1]);
-            float q2 = __uint_as_float(a[2]), q3 = __uint_as_float(a[3]);
             #pragma unroll
-            for (int e = 4; e < 64; e += 8) {
-              q0 = fmax3(q0, __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-              q1 = fmax3(q1, __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
-              q2 = fmax3(q2, __uint_as_float(a[e + 4]), __uint_as_float(a[e + 5]));
-              q3 = fmax3(q3, __uint_as_float(a[e + 6]), __uint_as_float(a[e + 7]));
+            for (int e = 0; e < 32; ++e) {
+              if (w0 & (1u << e)) a[e] = __float_as_uint(-INFINITY);
+              if (w1 & (1u << e)) a[32 + e] = __float_as_uint(-INFINITY);
             }
-            mx_half = valid ? fmaxf(fmax3(q0, q1, q2), q3) : -INFINITY;
-            s_mx[it & 1][c][r] = mx_half;
           }
+          // row max over the 64 columns: four independent 3-input max chains
+          float q0 = __uint_as_float(a[0]), q1 = __uint_as_float(a[1]);
+          float q2 = __uint_as_float(a[2]), q3 = __uint_as_float(a[3]);
+          #pragma unroll
+          for (int e = 4; e < 64; e += 8) {
+            q0 = fmax3(q0, __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
+            q1 = fmax3(q1, __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]));
+            q2 = fmax3(q2, __uint_as_float(a[e + 4]), __uint_as_float(a[e + 5]));
+            q3 = fmax3(q3, __uint_as_float(a[e + 6]), __uint_as_float(a[e + 7]));
+          }
+          mx_half = fmaxf(fmax3(q0, q1, q2), q3);
+          s_mx[it & 1][c][r] = mx_half;
         }
         if (!named_barrier_and(2 + (warp & 3), 64, got && ok)) {
           ok = false;
           abort_flag = 1;
           break;
         }
-        // A block at the edge of the keys: value rows that no token sees may hold
-        // anything, and 0 * inf is not 0.
-        if (jb < lo || jb + kBlockN > hi) {
-          const int sv = it % kFwdVStages;
-          if (mbar_wait_warp(&v_full[sv], (it / kFwdVStages) & 1, &abort_flag)) {
-            const uint32_t base = smem_u32(sV + sv * kTileBytes);
-            #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int chunk = u * 256 + tid;
-              const int j = jb + (chunk >> 3);
-              if (j < lo || j >= hi) st_shared_v4(base + (uint32_t)chunk * 16u, 0, 0, 0, 0);
+        // The first and the last block may hold value rows that no token sees, and
+        // those may hold anything: 0 * inf is not 0.
+        if (it == 0 || it == num - 1) {
+          const int jb = (blk0 + it) * kBlockN;
+          if (jb < s_lo || jb + kBlockN > s_hi) {
+            const int sv = it % kFwdVStages;
+            if (mbar_wait_warp(&v_full[sv], (it / kFwdVStages) & 1, &abort_flag)) {
+              const uint32_t base = smem_u32(sV + sv * kTileBytes);
+              // 16-byte chunks over the 64 * row_warps threads
+              for (int ch = 32 * (2 * (warp & 3) + c) + lane; ch < kBlockN * 8;
+                   ch += 64 * row_warps) {
+                const int j = jb + (ch >> 3);
+                if (j < s_lo || j >= s_hi) st_shared_v4(base + (uint32_t)ch * 16u, 0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+            } else {
+              ok = false;
             }
-            fence_proxy_async_smem();
-          } else {
-            ok = false;
           }
         }
+        const float mx = fmaxf(mx_half, s_mx[it & 1][c ^ 1][r]) * sl2;
+        // lazy rescale: the max only moves when it grows by more than the threshold
         float alpha = 1.0f;
-        if (!idle) {
-          const float mx = fmaxf(mx_half, s_mx[it & 1][c ^ 1][r]) * sl2;
-          if (mx > m + kRescaleThreshold || (m == -INFINITY && mx > -INFINITY)) {
-            alpha = ex2_approx(m - mx);
-            m = mx;
-          }
+        if (mx > m + kRescaleThreshold || (m == -INFINITY && mx > -INFINITY)) {
+          alpha = ex2_approx(m - mx);
+          m = mx;
         }
         const float m_use = (m == -INFINITY) ? 0.0f : m;
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t rs = f2(0.0f, 0.0f);
         uint32_t pk[16];
-        if (!idle) {
-          #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t x =
-                ffma2(f2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), sl2x2, negm2);
-            const float e0 = ex2_approx(f2_lo(x));
-            const float e1 = ex2_approx(f2_hi(x));
-            rs = fadd2(rs, f2(e0, e1));
-            pk[e >> 1] = pack_bf16x2(e0, e1);
-          }
+        #pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t x =
+              ffma2(f2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), sl2x2, negm2);
+          const float e0 = ex2_approx(f2_lo(x));
+          const float e1 = ex2_approx(f2_hi(x));
+          rs = fadd2(rs, f2(e0, e1));
+          pk[e >> 1] = pack_bf16x2(e0, e1);
         }
         // PV(it - 1) has read the P columns and updated O
         if (it > 0 && !mbar_wait_warp(&pv_done, (it - 1) & 1, &abort_flag)) ok = false;
         if (ok) {
           tc_fence_after();
-          if (!idle) {
-            tmem_st_x16(tP, pk);
-            #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t x =
-                  ffma2(f2(__uint_as_float(a[32 + e]), __uint_as_float(a[33 + e])), sl2x2, negm2);
-              const float e0 = ex2_approx(f2_lo(x));
-              const float e1 = ex2_approx(f2_hi(x));
-              rs = fadd2(rs, f2(e0, e1));
-              pk[e >> 1] = pack_bf16x2(e0, e1);
-            }
-            tmem_st_x16(tP + 16, pk);
-            l = l * alpha + (f2_lo(rs) + f2_hi(rs));
-            if (it > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-              #pragma unroll
-              for (int q = 0; q < 32; q += 16) {
-                uint32_t o[16];
-                tmem_ld_x16(tO + q, o);
-                tmem_ld_wait();
-                #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st_x16(tO + q, o);
-              }
-            }
-            tmem_st_wait();
+          tmem_st_x16(tP, pk);
+          #pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t x =
+                ffma2(f2(__uint_as_float(a[32 + e]), __uint_as_float(a[33 + e])), sl2x2, negm2);
+            const float e0 = ex2_approx(f2_lo(x));
+            const float e1 = ex2_approx(f2_hi(x));
+            rs = fadd2(rs, f2(e0, e1));
+            pk[e >> 1] = pack_bf16x2(e0, e1);
           }
+          tmem_st_x16(tP + 16, pk);
+          l = l * alpha + (f2_lo(rs) + f2_hi(rs));
+          if (it > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            #pragma unroll
+            for (int q = 0; q < 32; q += 16) {
+              uint32_t o[16];
+              tmem_ld_x16(tO + q, o);
+              tmem_ld_wait();
+              #pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_x16(tO + q, o);
+            }
+          }
+          tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full);
         } else {
@@ -656,6 +741,9 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
         atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 8);
       } else {
         tc_fence_after();
+        const int tok = r / p.group;
+        const int hq = g * p.group + (r - tok * p.group);
+        const bool valid = r < rows;
         const float lt = s_red_l[0][r] + s_red_l[1][r];
         uint32_t o[32];
         tmem_ld_x32(tO, o);
@@ -679,8 +767,8 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
           const float wk = ex2_approx(m - mb);
           const float z = fmaf(lt, wk, ex2_approx(s2 - mb));
           const float scale = z > 0.0f ? wk / z : 0.0f;
-          const bool whole = i0 + p.tokens <= sp.n;         // same for every row
-          const size_t row = (size_t)sp.q0 + i;
+          const bool whole = rows == p.tokens * p.group;    // same for every row
+          const size_t row = (size_t)row0 + tok;
           if (whole || valid) {
             const size_t base = (row * p.heads_q + hq) * kHeadDim + 32 * c;
             #pragma unroll
@@ -705,8 +793,7 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
             fence_proxy_async_smem();
             named_barrier_sync(1, 2 * kBlockM);
             if (warp == 0 && lane == 0) {
-              tma_store_3d_hint(&p.tm_out, sK, 0, g * p.group, sp.q0 + i0,
-                                l2_policy_evict_first());
+              tma_store_3d_hint(&p.tm_out, sK, 0, g * p.group, row0, l2_policy_evict_first());
               bulk_commit_group();
               bulk_wait_group_read0();
             }
@@ -716,12 +803,10 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
     }
     tc_fence_before();
     __syncthreads();
-    failed = abort_flag != 0;
     if (warp == kFwdMmaWarp) {
       tc_fence_after();
       tmem_dealloc(tmem, kFwdTmemCols);
     }
-    if (failed) return;                                     // uniform: recorded, nothing joined
   } else if (parts > 1) {
     for (int r = tid; r < rows; r += kExtThreads)
       p.ml_part[pidx * kBlockM + r] = make_float2(-INFINITY, 0.0f);
@@ -730,54 +815,80 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
     for (int x = tid; x < rows * 8; x += kExtThreads) {
       const int r = x >> 3, tok = r / p.group;
       const int hq = g * p.group + (r - tok * p.group);
-      const size_t row = (size_t)sp.q0 + i0 + tok;
+      const size_t row = (size_t)row0 + tok;
       reinterpret_cast<uint4*>(p.out + (row * p.heads_q + hq) * kHeadDim)[x & 7] =
           make_uint4(0, 0, 0, 0);
       if ((x & 7) == 0) p.lse[(size_t)hq * p.total_q + row] = __ldg(p.sink + hq);
     }
   }
-  if (parts == 1) return;
+}
 
-  // ---- the last CTA of the tile joins the parts, in the order of their keys,
-  // with the sink: M = max(m_c, sink), Z = sum l_c 2^(m_c - M) + 2^(sink - M).
-  __threadfence();
-  __syncthreads();
-  if (tid == 0)
-    s_last = atomicAdd(p.done + (size_t)raw.w * p.heads_kv + g, 1) == parts - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  for (int x = tid; x < rows * 16; x += kExtThreads) {      // thread: a row, 4 dimensions
-    const int r = x >> 4, d = 4 * (x & 15);
+// Joins the parts of the split tiles, in the order of their keys, with the sink:
+// M = max(m_c, sink), Z = sum l_c 2^(m_c - M) + 2^(sink - M).  Sixteen lanes take
+// a row (tile, kv head, row), 4 dimensions each.  A kernel of its own: joined by
+// the CTA that stored the last part, 38 parts of 128 rows (1.2 MB through one
+// SM) took 60 us.
+__global__ void __launch_bounds__(kExtJoinThreads)
+attn_sink_extend_join_kernel(const __grid_constant__ ExtParams p) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 15, d = 4 * lane;
+  const int n = *p.n_tiles * p.heads_kv * kBlockM;
+  const int groups = gridDim.x * (kExtJoinThreads / 16);
+  // whole warps go round together (the shuffles stay within 16 lanes)
+  for (int x0 = (blockIdx.x * kExtJoinThreads + threadIdx.x) / 32 * 2; x0 < n; x0 += groups) {
+    const int x = x0 + (threadIdx.x >> 4 & 1);              // n is even
+    const int r = x % kBlockM, tg = x / kBlockM, t = tg / p.heads_kv, g = tg - t * p.heads_kv;
+    const ExtTileRef ref = p.tiles[t];
+    const int parts = r < ref.rows ? ref.parts : 0;
+    if (!__any_sync(0xffffffffu, parts > 0)) continue;
     const int tok = r / p.group;
-    const int hq = g * p.group + (r - tok * p.group);
-    const size_t row = (size_t)sp.q0 + i0 + tok;
-    const size_t first = ((size_t)raw.w * p.heads_kv + g) * kBlockM + r;
+    const int hq = min(g * p.group + (r - tok * p.group), p.heads_q - 1);
+    const size_t pr = ((size_t)ref.first * p.heads_kv + g) * kBlockM + r;
     const size_t step = (size_t)p.heads_kv * kBlockM;
+    static_assert(kExtMaxSplits <= 64, "four parts a lane");
     const float s2 = __ldg(p.sink + hq) * kLog2e;
+    float2 ml[4];                                           // of parts lane + 16 u
     float mf = s2;
-    #pragma unroll 8
-    for (int c = 0; c < parts; ++c) mf = fmaxf(mf, __ldcg(p.ml_part + first + c * step).x);
-    const float mb = (mf == -INFINITY) ? 0.0f : mf;
-    float z = ex2_approx(s2 - mb);
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    #pragma unroll 8
-    for (int c = 0; c < parts; ++c) {
-      const float2 ml = __ldcg(p.ml_part + first + c * step);
-      const float4 o = __ldcg(
-          reinterpret_cast<const float4*>(p.o_part + (first + c * step) * kHeadDim + d));
-      if (ml.x == -INFINITY) continue;                      // no key: its sums were not written
-      const float wt = ex2_approx(ml.x - mb);
-      z = fmaf(ml.y, wt, z);
-      acc.x = fmaf(o.x, wt, acc.x);
-      acc.y = fmaf(o.y, wt, acc.y);
-      acc.z = fmaf(o.z, wt, acc.z);
-      acc.w = fmaf(o.w, wt, acc.w);
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      ml[u] = lane + 16 * u < parts ? p.ml_part[pr + (lane + 16 * u) * step]
+                                    : make_float2(-INFINITY, 0.0f);
+      mf = fmaxf(mf, ml[u].x);
     }
+    #pragma unroll
+    for (int k = 8; k > 0; k >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, k));
+    const float mb = (mf == -INFINITY) ? 0.0f : mf;
+    float w[4], z = 0.0f;
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      w[u] = ex2_approx(ml[u].x - mb);                      // 0 for an empty part
+      z = fmaf(ml[u].y, w[u], z);
+    }
+    #pragma unroll
+    for (int k = 8; k > 0; k >>= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
+    z += ex2_approx(s2 - mb);
+    const int most = __reduce_max_sync(0xffffffffu, parts);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      #pragma unroll 8
+      for (int c = 0; c < min(16, most - 16 * u); ++c) {
+        const float wt = __shfl_sync(0xffffffffu, w[u], c, 16);
+        if (wt == 0.0f) continue;                           // an empty part stored no sums
+        const float4 o = __ldcs(reinterpret_cast<const float4*>(
+            p.o_part + (pr + (16 * u + c) * step) * kHeadDim + d));
+        acc.x = fmaf(o.x, wt, acc.x);
+        acc.y = fmaf(o.y, wt, acc.y);
+        acc.z = fmaf(o.z, wt, acc.z);
+        acc.w = fmaf(o.w, wt, acc.w);
+      }
+    }
+    if (parts == 0) continue;
     const float inv = z > 0.0f ? 1.0f / z : 0.0f;
-    *reinterpret_cast<uint2*>(p.out + (row * p.heads_q + hq) * kHeadDim + d) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (d == 0)
+    const size_t row = (size_t)ref.row0 + tok;
+    *reinterpret_cast<uint2*>(p.out + (row * p.heads_q + hq) * kHeadDim + d) = make_uint2(
+        pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0)
       p.lse[(size_t)hq * p.total_q + row] = z > 0.0f ? (mb + __log2f(z)) * kLn2 : -INFINITY;
   }
 }

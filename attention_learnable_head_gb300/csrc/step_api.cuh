@@ -6,6 +6,32 @@
 
 namespace {
 
+// A launch that may begin while the kernel before it in the stream runs (the
+// kernel waits for it itself: grid_dependency_wait).
+template <typename P>
+bool launch_dependent(void (*kernel)(P), unsigned grid, unsigned threads, size_t smem,
+                      cudaStream_t s, const P& params) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    g_last_cuda_error.store((int)e, std::memory_order_relaxed);
+    return false;
+  }
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return true;
+}
+
 // ----------------------------------------------------------------------------- plan
 // Tokens a CTA of the plan writes; more CTAs per group only repeat the sums.
 constexpr int kPlanTokensPerCta = 4 * kPlanThreads;
@@ -81,15 +107,11 @@ void rope_bwd_launch(const RopeParams& rp, int ctas, bool fp32, cudaStream_t s) 
 // ----------------------------------------------------------------------------- extend
 struct ExtendLayout {
   int tokens;        // per tile
-  int n_items, max_parts, target;
-  size_t off_done, off_ml, off_o, total;
+  int n_items, max_parts, max_tiles, slots;
+  size_t off_tiles, off_ml, off_o, total;
 };
 
-// CTAs an SM holds at once (shared memory, TMEM and registers allow two), and
-// key blocks a part has at least (each part stores and joins a 128-row fp32
-// result).
-constexpr int kExtCtasPerSm = 2;
-constexpr int kExtMinBlocks = 4;
+constexpr int kExtCtasPerSm = 2;   // shared memory, TMEM and registers allow two
 
 int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   if (p == nullptr) return ATTN_SINK_ERR_INVALID_ARG;
@@ -102,17 +124,18 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   const int group = p->heads_q / p->heads_kv;
   if (group > kExtMaxGroup) return ATTN_SINK_ERR_UNSUPPORTED;
   L->tokens = kBlockM / group;
-  L->target = kExtCtasPerSm * sms;
-  const long long shares = (L->target + p->heads_kv - 1) / p->heads_kv;
+  L->slots = kExtCtasPerSm * sms;
+  const long long shares = (2 * L->slots + p->heads_kv - 1) / p->heads_kv;
   // the bounds of attn_sink_extend_plan_kernel
   const long long items = p->total_q / L->tokens + (long long)p->batch + shares;
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
   L->n_items = (int)items;
   L->max_parts = (int)std::min<long long>(items, 2 * shares);
+  L->max_tiles = L->max_parts / 2;         // two parts at least
   const size_t parts = (size_t)L->max_parts * p->heads_kv;
   size_t off = align256((size_t)L->n_items * sizeof(ExtItem));
-  L->off_done = off;
-  off += align256(parts * sizeof(int));
+  L->off_tiles = off;                      // their number, then the tiles
+  off += 256 + align256((size_t)L->max_tiles * sizeof(ExtTileRef));
   L->off_ml = off;
   off += align256(parts * kBlockM * sizeof(float2));
   L->off_o = off;
@@ -385,7 +408,8 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
   ep.out = static_cast<__nv_bfloat16*>(out);
   ep.lse = lse;
   ep.items = reinterpret_cast<ExtItem*>(ws);
-  ep.done = reinterpret_cast<int*>(ws + L.off_done);
+  ep.n_tiles = reinterpret_cast<int*>(ws + L.off_tiles);
+  ep.tiles = reinterpret_cast<ExtTileRef*>(ws + L.off_tiles + 256);
   ep.ml_part = reinterpret_cast<float2*>(ws + L.off_ml);
   ep.o_part = reinterpret_cast<float*>(ws + L.off_o);
   ep.err = err;
@@ -401,8 +425,8 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
   ep.window = params->window > 0 ? params->window : 0;
   ep.n_items = L.n_items;
   ep.max_parts = L.max_parts;
-  ep.target = L.target;
-  ep.min_blocks = kExtMinBlocks;
+  ep.max_tiles = L.max_tiles;
+  ep.slots = L.slots;
   ep.scale_log2 = params->softmax_scale * kLog2e;
 #ifdef ATTN_SINK_TEST_HOOKS
   ep.skip_k_tile = g_test_skip_k_tile.load();
@@ -427,11 +451,11 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
   attn_sink_extend_plan_kernel<<<1, kExtSchedThreads, 0, s>>>(ep);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   const unsigned grid = (unsigned)L.n_items * (unsigned)params->heads_kv;
-  if (tma)
-    attn_sink_extend_kernel<true><<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
-  else
-    attn_sink_extend_kernel<false><<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
-  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+  if (!launch_dependent(tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>, grid,
+                        kExtThreads, kFwdSmemBytes, s, ep) ||
+      !launch_dependent(attn_sink_extend_join_kernel, 6 * sms, kExtJoinThreads, 0, s, ep))
+    return ATTN_SINK_ERR_CUDA;
+  return ATTN_SINK_OK;
 }
 
 }  // extern "C"
