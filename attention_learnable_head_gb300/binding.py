@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import re
@@ -607,6 +608,10 @@ def attn_sink_extend(params: AttnSinkExtendParams, q, k_cache, v_cache, block_ta
 
 
 _NOTHING = contextlib.nullcontext()
+# The current stream of a device as an integer; Stream objects cost a few
+# microseconds, which is what the smallest of these calls take.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on(device, stream):
@@ -626,16 +631,25 @@ def _on(device, stream):
     return torch.cuda.stream(stream)
 
 
-def _want(name, t, dtype, device, shape, contiguous: bool = True):
-    """Check one tensor argument; `shape` holds None where any size will do."""
+def _want(name, t, dtype, device, shape):
+    """Check one tensor argument: its type, device and shape, and that it is
+    contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} has to be {dtype}, not {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} has to be contiguous")
+    raise ValueError(f"{name} has to be contiguous")
+
+
+def _dims(name, t, n):
+    """The shape of a tensor that has to have n dimensions."""
+    if t.dim() != n:
+        raise ValueError(f"{name} has to have {n} dimensions, not shape {tuple(t.shape)}")
+    return t.shape
 
 
 class PagePlan(NamedTuple):
@@ -653,24 +667,26 @@ def page_plan(cached_lens, new_lens, free_pages, block_table, *, page_size: int,
     cached_lens[b] keys and gets new_lens[b] new tokens; new pages are taken from
     free_pages in order and written into block_table [B, max_pages] in place.
     Nothing is read back: max_tokens bounds the tokens of the step."""
-    dev = block_table.device
-    b, i32 = cached_lens.shape[0], torch.int32
+    dev, i32 = block_table.device, torch.int32
+    b, = _dims("cached_lens", cached_lens, 1)
+    cols, free = _dims("block_table", block_table, 2)[1], _dims("free_pages", free_pages, 1)[0]
     _want("cached_lens", cached_lens, i32, dev, (b,))
     _want("new_lens", new_lens, i32, dev, (b,))
-    _want("free_pages", free_pages, i32, dev, (None,))
-    _want("block_table", block_table, i32, dev, (b, None))
+    _want("free_pages", free_pages, i32, dev, (free,))
+    _want("block_table", block_table, i32, dev, (b, cols))
     if max_tokens < 0:
         raise ValueError(f"max_tokens is {max_tokens}")
     with _on(dev, stream):
         slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
         positions = torch.empty(max_tokens, dtype=i32, device=dev)
         small = torch.empty(2 * b + 2, dtype=i32, device=dev)
-        cu, lens, needed = small[:b + 1], small[b + 1:2 * b + 1], small[2 * b + 1:]
-        p = AttnSinkPlanParams(b, page_size, num_pages, block_table.shape[1],
-                               free_pages.shape[0], max_tokens)
-        _check(attn_sink_page_plan(p, cached_lens, new_lens, free_pages, block_table, slots,
-                                   positions, cu, lens, needed), "attn_sink_page_plan")
-    return PagePlan(slots, positions, cu, lens, needed)
+        at = small.data_ptr()
+        p = AttnSinkPlanParams(b, page_size, num_pages, cols, free, max_tokens)
+        _check(lib().attn_sink_page_plan(
+            ctypes.byref(p), cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+            block_table.data_ptr(), slots.data_ptr(), positions.data_ptr(), at, at + 4 * (b + 1),
+            at + 4 * (2 * b + 1), _raw_stream(dev.index)), "attn_sink_page_plan")
+        return PagePlan(slots, positions, *small.split_with_sizes((b + 1, b, 1)))
 
 
 def axis_sections(*sections: int) -> list[int]:
@@ -698,37 +714,65 @@ def make_rope_params(tokens: int, heads_q: int, heads_kv: int, *, rotary_dim: in
     return p
 
 
-def _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
-                 **kw) -> AttnSinkRopeParams:
-    """Checks of qkv_rope and its backward, and their params."""
-    dev, t, rows = qkv.device, qkv.shape[0], heads_q + 2 * heads_kv
-    _want("qkv", qkv, torch.bfloat16, dev, (None, rows, 64), contiguous=False)
-    stride = qkv.stride(0) if t > 1 else rows * 64
-    if t and (qkv.stride(2) != 1 or qkv.stride(1) != 64 or stride < rows * 64 or stride % 8):
-        raise ValueError("qkv: the heads of a token have to be contiguous and the tokens a "
-                         f"multiple of 8 elements apart (strides {tuple(qkv.stride())})")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _want("positions", positions, torch.int32, dev, (t,) if positions.dim() == 1 else (axes, t))
-    _want("inv_freq", inv_freq, torch.float32, dev, (None,))
-    pairs = inv_freq.shape[0]
+@functools.lru_cache(maxsize=256)
+def _rope_params_of(t, heads_q, heads_kv, pairs, stride, axes, pair_axis, norm, weight_bf16, eps,
+                    interleaved, amplitude, page_size, num_pages, grad_dtype):
+    """The params of a shape, kept for its next call (they are only read)."""
     if pairs > 32:
         raise ValueError(f"inv_freq has {pairs} entries: a head has 32 pairs")
     if pair_axis is None:
         if axes > 1:
             raise ValueError("positions with several axes need pair_axis")
-    elif len(pair_axis) != pairs or not all(0 <= a < axes for a in pair_axis):
+    elif len(pair_axis) != pairs or max(pair_axis, default=0) >= axes:
         raise ValueError(f"pair_axis needs {pairs} entries in [0, {axes}), one per pair")
+    return make_rope_params(t, heads_q, heads_kv, rotary_dim=2 * pairs, row_stride=stride,
+                            num_axes=axes, pair_axis=pair_axis, interleaved=interleaved, norm=norm,
+                            weight_bf16=weight_bf16, eps=eps, amplitude=amplitude,
+                            page_size=page_size, num_pages=num_pages, grad_dtype=grad_dtype)
+
+
+def _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
+                 eps=1e-6, interleaved=False, amplitude=1.0, page_size=0, num_pages=0,
+                 grad_dtype=0) -> AttnSinkRopeParams:
+    """Checks of qkv_rope and its backward, and their params."""
+    dev, rows = qkv.device, heads_q + 2 * heads_kv
+    t = _dims("qkv", qkv, 3)[0]
+    if qkv.dtype is not torch.bfloat16 or qkv.shape != (t, rows, 64):
+        raise ValueError(f"qkv has to be bfloat16 [T, {rows}, 64], not {qkv.dtype} "
+                         f"{tuple(qkv.shape)}")
+    stride, head, one = qkv.stride()
+    if t and (one != 1 or head != 64 or stride < rows * 64 or stride % 8):
+        if t > 1 or one != 1 or head != 64:
+            raise ValueError("qkv: the heads of a token have to be contiguous and the tokens a "
+                             f"multiple of 8 elements apart (strides {tuple(qkv.stride())})")
+        stride = rows * 64                  # a single token: its stride means nothing
+    elif t == 0:
+        stride = rows * 64
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _want("positions", positions, torch.int32, dev, (axes, t) if positions.dim() == 2 else (t,))
+    pairs, = _dims("inv_freq", inv_freq, 1)
+    _want("inv_freq", inv_freq, torch.float32, dev, (pairs,))
     norm = q_weight is not None
     if norm != (k_weight is not None):
         raise ValueError("q_weight and k_weight go together")
     if norm:
-        if q_weight.dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError(f"q_weight has to be float32 or bfloat16, not {q_weight.dtype}")
-        _want("q_weight", q_weight, q_weight.dtype, dev, (64,))
-        _want("k_weight", k_weight, q_weight.dtype, dev, (64,))
-    return make_rope_params(t, heads_q, heads_kv, rotary_dim=2 * pairs, row_stride=stride,
-                            num_axes=axes, pair_axis=pair_axis, norm=norm,
-                            weight_bf16=norm and q_weight.dtype == torch.bfloat16, **kw)
+        kind = q_weight.dtype
+        if kind is not torch.float32 and kind is not torch.bfloat16:
+            raise ValueError(f"q_weight has to be float32 or bfloat16, not {kind}")
+        _want("q_weight", q_weight, kind, dev, (64,))
+        _want("k_weight", k_weight, kind, dev, (64,))
+    if pair_axis is not None:
+        try:
+            pair_axis = bytes(pair_axis)
+        except ValueError:
+            raise ValueError(f"pair_axis: entries in [0, {axes})") from None
+    return _rope_params_of(t, heads_q, heads_kv, pairs, stride, axes, pair_axis, norm,
+                           norm and kind is torch.bfloat16, eps, interleaved, amplitude, page_size,
+                           num_pages, grad_dtype)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def qkv_rope(qkv, positions, inv_freq, *, heads_q: int, heads_kv: int, q_weight=None,
@@ -745,29 +789,31 @@ def qkv_rope(qkv, positions, inv_freq, *, heads_q: int, heads_kv: int, q_weight=
     v_cache [pages, page_size, heads_kv, 64], and k and v are None unless
     keep_kv."""
     paged = slots is not None
-    p = _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
-                     eps=eps, interleaved=interleaved, amplitude=amplitude,
-                     page_size=k_cache.shape[1] if paged and k_cache is not None else 0,
-                     num_pages=k_cache.shape[0] if paged and k_cache is not None else 0)
-    dev, t, bf16 = qkv.device, qkv.shape[0], torch.bfloat16
+    pages = page = 0
     if paged:
         if k_cache is None or v_cache is None:
             raise ValueError("slots need k_cache and v_cache")
-        _want("slots", slots, torch.int64, dev, (t,))
-        _want("k_cache", k_cache, bf16, dev, (None, None, heads_kv, 64))
-        _want("v_cache", v_cache, bf16, dev, tuple(k_cache.shape))
+        pages, page = _dims("k_cache", k_cache, 4)[:2]
     elif k_cache is not None or v_cache is not None:
         raise ValueError("k_cache and v_cache need slots")
+    p = _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
+                     eps, interleaved, amplitude, page, pages)
+    dev, t, bf16 = qkv.device, qkv.shape[0], torch.bfloat16
+    if paged:
+        _want("slots", slots, torch.int64, dev, (t,))
+        _want("k_cache", k_cache, bf16, dev, (pages, page, heads_kv, 64))
+        _want("v_cache", v_cache, bf16, dev, (pages, page, heads_kv, 64))
     keep = not paged if keep_kv is None else keep_kv
     with _on(dev, stream):
         q = torch.empty((t, heads_q, 64), dtype=bf16, device=dev)
         k = torch.empty((t, heads_kv, 64), dtype=bf16, device=dev) if keep else None
         v = torch.empty((t, heads_kv, 64), dtype=bf16, device=dev) if keep else None
         base = qkv.data_ptr()
-        _check(attn_sink_qkv_rope(p, base, base + 128 * heads_q,
-                                  base + 128 * (heads_q + heads_kv), positions, inv_freq,
-                                  q_weight, k_weight, slots, q, k, v, k_cache, v_cache),
-               "attn_sink_qkv_rope")
+        _check(lib().attn_sink_qkv_rope(
+            ctypes.byref(p), base, base + 128 * heads_q, base + 128 * (heads_q + heads_kv),
+            positions.data_ptr(), inv_freq.data_ptr(), _at(q_weight), _at(k_weight), _at(slots),
+            q.data_ptr(), _at(k), _at(v), _at(k_cache), _at(v_cache), _raw_stream(dev.index)),
+            "attn_sink_qkv_rope")
     return q, k, v
 
 
@@ -779,30 +825,29 @@ def qkv_rope_backward(qkv, positions, inv_freq, dq, dk, dv, *, heads_q: int, hea
     backward gives them); dqkv [T, heads_q + 2 heads_kv, 64] bf16, the weights'
     gradients [64] fp32 (None without norm), bitwise reproducible."""
     kind = dq.dtype
-    if kind not in (torch.float32, torch.bfloat16):
+    if kind is not torch.float32 and kind is not torch.bfloat16:
         raise ValueError(f"dq has to be float32 or bfloat16, not {kind}")
     p = _rope_params(qkv, positions, inv_freq, heads_q, heads_kv, q_weight, k_weight, pair_axis,
-                     eps=eps, interleaved=interleaved, amplitude=amplitude,
-                     grad_dtype=int(kind == torch.float32))
+                     eps, interleaved, amplitude, 0, 0, int(kind is torch.float32))
     dev, t, rows = qkv.device, qkv.shape[0], heads_q + 2 * heads_kv
     _want("dq", dq, kind, dev, (t, heads_q, 64))
     _want("dk", dk, kind, dev, (t, heads_kv, 64))
     _want("dv", dv, kind, dev, (t, heads_kv, 64))
     with _on(dev, stream):
         dqkv = torch.empty((t, rows, 64), dtype=torch.bfloat16, device=dev)
-        dw = ws = None
+        dwq = dwk = ws = None
+        nbytes = 0
         if p.norm:
-            dw = torch.empty((2, 64), dtype=torch.float32, device=dev)
-            ws = torch.empty(attn_sink_qkv_rope_bwd_workspace_size(p), dtype=torch.uint8,
-                             device=dev)
+            dwq, dwk = torch.empty((2, 64), dtype=torch.float32, device=dev).unbind()
+            nbytes = attn_sink_qkv_rope_bwd_workspace_size(p)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         src, dst, kq, kk = qkv.data_ptr(), dqkv.data_ptr(), 128 * heads_q, 128 * heads_kv
-        _check(attn_sink_qkv_rope_bwd(p, src, src + kq, positions, inv_freq, q_weight, k_weight,
-                                      dq, dk, dv, dst, dst + kq, dst + kq + kk, rows * 64,
-                                      rows * 64, rows * 64, None if dw is None else dw[0],
-                                      None if dw is None else dw[1], ws,
-                                      0 if ws is None else ws.numel()),
-               "attn_sink_qkv_rope_bwd")
-    return (dqkv, None, None) if dw is None else (dqkv, dw[0], dw[1])
+        _check(lib().attn_sink_qkv_rope_bwd(
+            ctypes.byref(p), src, src + kq, positions.data_ptr(), inv_freq.data_ptr(),
+            _at(q_weight), _at(k_weight), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dst,
+            dst + kq, dst + kq + kk, rows * 64, rows * 64, rows * 64, _at(dwq), _at(dwk), _at(ws),
+            nbytes, _raw_stream(dev.index)), "attn_sink_qkv_rope_bwd")
+    return dqkv, dwq, dwk
 
 
 class QkvRopeFunction(torch.autograd.Function):
@@ -848,12 +893,14 @@ def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, wi
     [H_q] fp32.  Rows of out and lse behind cu_seqlens_q[B] are not written:
     give out and lse to keep what they hold there."""
     dev, bf16, i32 = q.device, torch.bfloat16, torch.int32
-    b = seq_lens.shape[0]
-    _want("q", q, bf16, dev, (None, None, 64))
-    t, hq = q.shape[0], q.shape[1]
-    _want("k_cache", k_cache, bf16, dev, (None, None, None, 64))
-    _want("v_cache", v_cache, bf16, dev, tuple(k_cache.shape))
-    _want("block_table", block_table, i32, dev, (b, None))
+    b, = _dims("seq_lens", seq_lens, 1)
+    t, hq, _ = _dims("q", q, 3)
+    pages, page, hkv, _ = _dims("k_cache", k_cache, 4)
+    cols = _dims("block_table", block_table, 2)[1]
+    _want("q", q, bf16, dev, (t, hq, 64))
+    _want("k_cache", k_cache, bf16, dev, (pages, page, hkv, 64))
+    _want("v_cache", v_cache, bf16, dev, (pages, page, hkv, 64))
+    _want("block_table", block_table, i32, dev, (b, cols))
     _want("seq_lens", seq_lens, i32, dev, (b,))
     _want("cu_seqlens_q", cu_seqlens_q, i32, dev, (b + 1,))
     _want("sink", sink, torch.float32, dev, (hq,))
@@ -861,16 +908,18 @@ def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, wi
         _want("out", out, bf16, dev, (t, hq, 64))
     if lse is not None:
         _want("lse", lse, torch.float32, dev, (hq, t))
-    p = AttnSinkExtendParams(b, t, hq, k_cache.shape[2], 64, k_cache.shape[1], k_cache.shape[0],
-                             block_table.shape[1], window,
+    p = AttnSinkExtendParams(b, t, hq, hkv, 64, page, pages, cols, window,
                              0.125 if softmax_scale is None else softmax_scale)
     with _on(dev, stream):
         if out is None:
             out = torch.empty((t, hq, 64), dtype=bf16, device=dev)
         if lse is None:
             lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
-        nbytes = attn_sink_extend_workspace_size(p)
+        nbytes = lib().attn_sink_extend_workspace_size(ctypes.byref(p))
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(attn_sink_extend(p, q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink,
-                                out, lse, ws, nbytes), "attn_sink_extend")
+        _check(lib().attn_sink_extend(
+            ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), sink.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev.index)),
+            "attn_sink_extend")
     return out, lse

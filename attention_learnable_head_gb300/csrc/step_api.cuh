@@ -59,25 +59,19 @@ bool rope_stride_ok(long long stride, int heads) {
   return stride % 8 == 0 && stride >= (long long)heads * kHeadDim && stride < (1ll << 40);
 }
 
-// Warps that share a token's heads, and the grid.  One warp per token where
-// that fills the GPU (the token's angles are computed once); with fewer tokens
-// the heads are spread over more warps, four heads at the least each.
-struct RopeGrid {
-  int parts, ctas;
-};
-RopeGrid rope_grid(const attn_sink_rope_params* p, int sms, int ctas_per_sm) {
-  RopeGrid g;
-  const long long warps = (long long)sms * ctas_per_sm * kRopeWarps;
-  const int most = (p->heads_q + 3) / 4;
-  long long parts = p->tokens > 0 ? warps / p->tokens : 1;
-  g.parts = (int)std::max<long long>(1, std::min<long long>(parts, most));
-  const long long items = (long long)p->tokens * g.parts;
-  g.ctas = (int)std::max<long long>(
-      1, std::min<long long>((items + kRopeWarps - 1) / kRopeWarps, (long long)sms * ctas_per_sm));
-  return g;
+// The grid: x CTAs, over whose warps the tokens go round, by the parts that a
+// token's heads are cut into.  One part where the tokens fill the GPU (a token's
+// angles are computed once); with fewer tokens the heads are spread over more
+// warps, four heads at the least each.
+dim3 rope_grid(const attn_sink_rope_params* p, int sms, int ctas_per_sm) {
+  const long long ctas = (long long)sms * ctas_per_sm;
+  const long long most = std::min((p->heads_q + 3) / 4, 65535);
+  const long long parts =
+      std::max<long long>(1, std::min(ctas * kRopeWarps / std::max(1, p->tokens), most));
+  const long long x = std::min<long long>(((long long)p->tokens + kRopeWarps - 1) / kRopeWarps,
+                                          std::max<long long>(1, ctas / parts));
+  return dim3((unsigned)std::max<long long>(1, x), (unsigned)parts);
 }
-constexpr int kRopeCtas = 6;       // resident CTAs per SM the grids are sized for
-constexpr int kRopeBwdCtas = 4;
 
 RopeParams rope_params(const attn_sink_rope_params* p) {
   RopeParams rp;
@@ -97,11 +91,11 @@ RopeParams rope_params(const attn_sink_rope_params* p) {
 }
 
 template <bool kNorm, bool kInter>
-void rope_bwd_launch(const RopeParams& rp, int ctas, bool fp32, cudaStream_t s) {
+void rope_bwd_launch(const RopeParams& rp, dim3 grid, bool fp32, cudaStream_t s) {
   if (fp32)
-    attn_sink_rope_bwd_kernel<kNorm, kInter, true><<<ctas, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_bwd_kernel<kNorm, kInter, true><<<grid, kRopeThreads, 0, s>>>(rp);
   else
-    attn_sink_rope_bwd_kernel<kNorm, kInter, false><<<ctas, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_bwd_kernel<kNorm, kInter, false><<<grid, kRopeThreads, 0, s>>>(rp);
 }
 
 // ----------------------------------------------------------------------------- extend
@@ -262,24 +256,23 @@ int attn_sink_qkv_rope(const attn_sink_rope_params* params, const void* q, const
   rp.v_cache = static_cast<__nv_bfloat16*>(v_cache);
   rp.cache_rows = slots != nullptr ? (long long)params->num_pages * params->page_size : 0;
   rp.err = err;
-  const RopeGrid g = rope_grid(params, sms, kRopeCtas);
-  rp.parts = g.parts;
+  const dim3 g = rope_grid(params, sms, kRopeCtas);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (params->norm && params->interleaved)
-    attn_sink_rope_kernel<true, true><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_kernel<true, true><<<g, kRopeThreads, 0, s>>>(rp);
   else if (params->norm)
-    attn_sink_rope_kernel<true, false><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_kernel<true, false><<<g, kRopeThreads, 0, s>>>(rp);
   else if (params->interleaved)
-    attn_sink_rope_kernel<false, true><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_kernel<false, true><<<g, kRopeThreads, 0, s>>>(rp);
   else
-    attn_sink_rope_kernel<false, false><<<g.ctas, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_kernel<false, false><<<g, kRopeThreads, 0, s>>>(rp);
   return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 
 size_t attn_sink_qkv_rope_bwd_workspace_size(const attn_sink_rope_params* params) {
   if (rope_validate(params) != ATTN_SINK_OK || !params->norm || params->tokens == 0) return 0;
-  const RopeGrid g = rope_grid(params, sm_count_or_default(), kRopeBwdCtas);
-  return align256((size_t)g.ctas * 2 * kHeadDim * sizeof(float));
+  const dim3 g = rope_grid(params, sm_count_or_default(), kRopeBwdCtas);
+  return align256((size_t)g.x * g.y * 2 * kHeadDim * sizeof(float));
 }
 
 int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, const void* k,
@@ -322,10 +315,10 @@ int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, c
   int sms = 0;
   int* err = nullptr;
   if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
-  const RopeGrid g = rope_grid(params, sms, kRopeBwdCtas);
+  const dim3 g = rope_grid(params, sms, kRopeBwdCtas);
   if (params->norm &&
       (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-       workspace_bytes < align256((size_t)g.ctas * 2 * kHeadDim * sizeof(float))))
+       workspace_bytes < align256((size_t)g.x * g.y * 2 * kHeadDim * sizeof(float))))
     return ATTN_SINK_ERR_WORKSPACE;
   RopeParams rp = rope_params(params);
   rp.q = static_cast<const __nv_bfloat16*>(q);
@@ -345,21 +338,20 @@ int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, c
   rp.dv_in_stride = dv_in_stride;
   rp.dw_part = static_cast<float*>(workspace);
   rp.err = err;
-  rp.parts = g.parts;
   const bool fp32 = params->grad_dtype == 1;
   if (params->norm && params->interleaved)
-    rope_bwd_launch<true, true>(rp, g.ctas, fp32, s);
+    rope_bwd_launch<true, true>(rp, g, fp32, s);
   else if (params->norm)
-    rope_bwd_launch<true, false>(rp, g.ctas, fp32, s);
+    rope_bwd_launch<true, false>(rp, g, fp32, s);
   else if (params->interleaved)
-    rope_bwd_launch<false, true>(rp, g.ctas, fp32, s);
+    rope_bwd_launch<false, true>(rp, g, fp32, s);
   else
-    rope_bwd_launch<false, false>(rp, g.ctas, fp32, s);
+    rope_bwd_launch<false, false>(rp, g, fp32, s);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   if (params->norm) {
-    attn_sink_rope_dw_kernel<<<1, kRopeSumThreads, 0, s>>>(rp.dw_part, g.ctas, dq_weight,
-                                                           dk_weight);
-    if (!launched()) return ATTN_SINK_ERR_CUDA;
+    const RopeSum sum{rp.dw_part, dq_weight, dk_weight, (int)(g.x * g.y)};
+    if (!launch_dependent(attn_sink_rope_dw_kernel, 1, kRopeSumThreads, 0, s, sum))
+      return ATTN_SINK_ERR_CUDA;
   }
   return ATTN_SINK_OK;
 }
