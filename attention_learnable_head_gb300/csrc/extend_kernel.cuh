@@ -39,6 +39,7 @@ constexpr int kExtThreads = 320;           // 8 softmax warps, copy warp, MMA wa
 constexpr int kExtMaxGroup = 128;
 constexpr int kExtMaxSplits = 64;          // parts of a tile
 constexpr int kExtMinBlocks = 4;           // key blocks of a part
+constexpr int kExtTries = 24;              // candidates for the cut, up to 3 rounds of CTAs
 constexpr int kExtOver = 5;                // what a CTA costs beside its blocks, in blocks
 constexpr int kExtSchedThreads = 1024;
 constexpr int kExtJoinThreads = 256;
@@ -146,19 +147,22 @@ __device__ __forceinline__ int ext_scan(int x, int* s_warp, int* all) {
 }
 
 // Lists the work items.  With W the key blocks of all tiles (each taken as long
-// as its sequence's last) times the kv heads, a part has at least c blocks and a
-// tile ceil(blocks / c) parts.  Tried are c = all blocks (nothing is split), W /
-// slots and W / (2 slots), slots being the CTAs the GPU holds at once; taken is
-// the one with the least ceil(CTAs / slots) * (c + kExtOver): rounds of CTAs, and
-// what a CTA costs beside its blocks.  That makes tiles + 2 slots / H_kv items at
-// most.
-// A thread takes a sequence (neighbours go to different warps), its warp writes
-// the sequence's items.
+// as its sequence's last) times the kv heads, a tile is cut into ceil(blocks / c)
+// parts.  Candidates for c spread W over 1/8, 2/8, .. 3 times the CTAs the GPU
+// holds at once (slots); the first leaves whole what a slot's share would not
+// cut.  Taken is the one with the least ceil(CTAs / slots) * (blocks of the
+// longest part + kExtOver): rounds of CTAs, and what a CTA costs beside its
+// blocks.  (With c = W / slots, W / (2 slots) or no cut alone, 32 sequences of
+// 4096 to 8192 keys and 5 new tokens fill 2.2 rounds and take 104 us.)  That
+// makes tiles + 3 slots / H_kv items at most.  A thread takes a sequence
+// (neighbours go to different warps), its warp writes the sequence's items.
 __global__ void __launch_bounds__(kExtSchedThreads, 1)
 attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
   __shared__ int s_scan[kExtSchedThreads / 32];
-  __shared__ unsigned long long s_work, s_items[3];
-  __shared__ int s_most;
+  __shared__ unsigned long long s_work;
+  __shared__ int s_tiles[kExtSchedThreads], s_blocks[kExtSchedThreads];
+  __shared__ long long s_cost[kExtSchedThreads / 32];
+  __shared__ int s_chunk[kExtSchedThreads / 32];
   grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool bad = false;
@@ -172,55 +176,64 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
     tiles = (s.n + p.tokens - 1) / p.tokens;
     if (tiles > 0) blocks = ext_tile(p, s, tiles - 1).blocks;
   };
-  if (tid == 0) {
-    s_work = s_items[0] = s_items[1] = s_items[2] = 0;
-    s_most = 0;
-  }
+  if (tid == 0) s_work = 0;
   __syncthreads();
   unsigned long long w = 0;
-  int most = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
     load(b0 + 32 * lane + warp);
     w += (unsigned long long)tiles * (unsigned)blocks;
-    most = max(most, blocks);
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
   #pragma unroll
   for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0 && w > 0) {                                // whole numbers: any order
-    atomicAdd(&s_work, w);
-    atomicMax(&s_most, most);
-  }
+  if (lane == 0 && w > 0) atomicAdd(&s_work, w);           // whole numbers: any order
   __syncthreads();
-  int chunk = 0;
+  int chunk;
   {
-    int c[3];
-    #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const long long share =
-          i == 0 ? s_most : ((long long)s_work * p.heads_kv + i * p.slots - 1) / (i * p.slots);
-      c[i] = (int)min(max((long long)kExtMinBlocks, share), 1ll << 24);   // > any tile's
-      long long n = 0;
-      for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
-        if (p.batch > kExtSchedThreads) load(b0 + 32 * lane + warp);     // else still at hand
-        if (tiles > 0) n += (long long)tiles * ext_parts(blocks, c[i]);
+    // warp i tries candidate i; the sequences' tiles and blocks go by rounds
+    // through shared memory
+    const long long per = (long long)s_work * p.heads_kv;
+    const int c = (int)min(max((8 * per + (long long)(warp + 1) * p.slots - 1) /
+                                   ((long long)(warp + 1) * p.slots), (long long)kExtMinBlocks),
+                           1ll << 24);     // > any tile's blocks
+    long long ctas = 0;
+    int longest = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
+      if (p.batch > kExtSchedThreads) load(b0 + 32 * lane + warp);       // else still at hand
+      __syncthreads();                     // the last round's have been read
+      s_tiles[32 * lane + warp] = tiles;   // in the order of the sequences
+      s_blocks[32 * lane + warp] = blocks;
+      __syncthreads();
+      for (int i = lane; i < min(kExtSchedThreads, p.batch - b0); i += 32) {
+        const int n = s_blocks[i];
+        if (s_tiles[i] == 0) continue;
+        const int k = ext_parts(n, c);
+        ctas += (long long)s_tiles[i] * k;
+        longest = max(longest, (n + k - 1) / k);
       }
-      #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-      if (lane == 0 && n > 0) atomicAdd(&s_items[i], (unsigned long long)n);
+    }
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, d);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      s_cost[warp] = warp < kExtTries ? (ctas * p.heads_kv + p.slots - 1) / p.slots *
+                                            (longest + kExtOver)
+                                      : LLONG_MAX;
+      s_chunk[warp] = c;
     }
     __syncthreads();
-    long long least = LLONG_MAX;
+    long long cost = s_cost[lane];
+    int best = lane;
     #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const long long ctas = (long long)s_items[i] * p.heads_kv;
-      const long long cost = (ctas + p.slots - 1) / p.slots * (min(c[i], s_most) + kExtOver);
-      if (cost < least) {
-        least = cost;
-        chunk = c[i];
+    for (int d = 16; d > 0; d >>= 1) {
+      const long long other = __shfl_xor_sync(0xffffffffu, cost, d);
+      const int who = __shfl_xor_sync(0xffffffffu, best, d);
+      if (other < cost || (other == cost && who < best)) {
+        cost = other;
+        best = who;
       }
     }
+    chunk = s_chunk[best];
   }
 
   int item0 = 0, part0 = 0, split0 = 0;    // of the sequences before this round

@@ -119,7 +119,7 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   if (group > kExtMaxGroup) return ATTN_SINK_ERR_UNSUPPORTED;
   L->tokens = kBlockM / group;
   L->slots = kExtCtasPerSm * sms;
-  const long long shares = (2 * L->slots + p->heads_kv - 1) / p->heads_kv;
+  const long long shares = (3 * L->slots + p->heads_kv - 1) / p->heads_kv;
   // the bounds of attn_sink_extend_plan_kernel
   const long long items = p->total_q / L->tokens + (long long)p->batch + shares;
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
