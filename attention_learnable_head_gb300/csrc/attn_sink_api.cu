@@ -18,6 +18,7 @@
 #include "bwd_kernel.cuh"
 #include "decode_kernel.cuh"
 #include "extend_kernel.cuh"
+#include "extend_window.cuh"
 #include "fwd_band_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "merge_kernel.cuh"
@@ -152,7 +153,7 @@ int device_state(int* sm_count, int** err) {
   if (!g_attr_set[dev]) {
     if (cudaFuncSetAttribute(attn_sink_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kFwdSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_sink_fwd_band_kernel,
+        cudaFuncSetAttribute(attn_sink_fwd_band_kernel<false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kBandSmemMax) != cudaSuccess ||
         cudaFuncSetAttribute(attn_sink_bwd_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -458,7 +459,7 @@ int fwd_band(const attn_sink_params* params, const Geometry& g, const void* q, c
   const int smem = std::max(80 * 1024, band_smem_bytes(n_cols));
   const int grid = (int)std::min<long long>(n_items, (long long)kBandCtasPerSm * sms);
   const TimedLaunch t = timing_begin(ATTN_SINK_KERNEL_FWD, static_cast<cudaStream_t>(stream));
-  attn_sink_fwd_band_kernel<<<grid, kBandThreads, smem, static_cast<cudaStream_t>(stream)>>>(bp);
+  attn_sink_fwd_band_kernel<false><<<grid, kBandThreads, smem, static_cast<cudaStream_t>(stream)>>>(bp);
   const bool ok = launched();
   timing_end(t, static_cast<cudaStream_t>(stream), ok);
   return ok ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;

@@ -74,6 +74,7 @@ struct FwdBandParams {
   CUtensorMap tm_out_lo;  // residual, box as tm_q (stores; unused without it)
   const int* cu_q;    // null for a dense batch
   const int* cu_k;
+  const int4* spans;  // or, per sequence, its rows [x, y) of q and [z, w) of k
   const float* sink;  // [H_q] fp32, or
   const __nv_bfloat16* sink_bf16;   // [H_q] bf16 when non-null
   __nv_bfloat16* out;     // [T_q][H_q][64]
@@ -125,7 +126,13 @@ __device__ __forceinline__ SeqBounds band_bounds(const FwdBandParams& p, int ite
   if (item >= p.n_items) return b;
   const int seq = fast_div(fast_div(item, p.div_hkv_mul, p.div_hkv_shift), p.div_tb_mul,
                            p.div_tb_shift);
-  if (p.cu_q != nullptr) {
+  if (p.spans != nullptr) {
+    const int4 x = __ldg(p.spans + seq);
+    b.q0 = x.x;
+    b.q1 = x.y;
+    b.k0 = x.z;
+    b.k1 = x.w;
+  } else if (p.cu_q != nullptr) {
     b.q0 = __ldg(p.cu_q + seq);
     b.q1 = __ldg(p.cu_q + seq + 1);
     b.k0 = __ldg(p.cu_k + seq);
@@ -248,10 +255,11 @@ __device__ __forceinline__ float band_chunk_max(uint32_t taddr, int lo, int hi, 
 
 // P = exp2(S * scale log2 e - m) of one chunk (masked columns hold -inf and
 // give 0), written as fp16 pairs to TMEM at tp (NC / 2 columns).  The row sum
-// of P is not formed here: the O product sums the fp16 P it multiplies.
-template <int NC>
+// of P is not formed here: the O product sums the fp16 P it multiplies (kSum: the
+// fp32 P are added to *sum, for lse).
+template <int NC, bool kSum>
 __device__ __forceinline__ void band_chunk_exp(uint32_t ts, uint32_t tp, uint64_t sl2x2,
-                                               uint64_t negm2) {
+                                               uint64_t negm2, uint64_t* sum) {
   uint32_t a[NC];
   band_ld<NC>(ts, a);
   tmem_ld_wait();
@@ -260,14 +268,19 @@ __device__ __forceinline__ void band_chunk_exp(uint32_t ts, uint32_t tp, uint64_
   for (int e = 0; e < NC; e += 2) {
     const uint64_t x =
         ffma2(f2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), sl2x2, negm2);
-    pk[e >> 1] = pack_f16x2(ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)));
+    const float e0 = ex2_approx(f2_lo(x)), e1 = ex2_approx(f2_hi(x));
+    if constexpr (kSum) *sum = fadd2(*sum, f2(e0, e1));
+    pk[e >> 1] = pack_f16x2(e0, e1);
   }
   if constexpr (NC == 32) tmem_st_x16(tp, pk);
   else tmem_st_x8(tp, pk);
 }
 
 // Registers are split per SM sub-partition; two CTAs of 10 warps allow 102
-// per thread: 96 is used.
+// per thread: 96 is used.  kSum: lse comes from the fp32 P (for callers that
+// promise an fp32 lse) instead of the row sum of the fp16 P, which moves it by up
+// to 2^-11; out is divided by the sum of the fp16 P in both.
+template <bool kSum>
 __global__ void __maxnreg__(96)
 attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -280,6 +293,9 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
   // next item, before whose pass 1 a half rewrites its entry, needs P of this
   // item from every thread, i.e. after its partner read it.
   __shared__ float s_mx[2][kBlockM];
+  // kSum: the halves' sums.  Rewritten behind the next item's pair barrier, which
+  // a partner passes after it has read them.
+  __shared__ float s_sum[2][kSum ? kBlockM : 1];
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -504,12 +520,13 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
     int pg = 0, ptok = 0, prem = 0;
     float pm = -INFINITY;
     float psink = 0.0f;   // the previous item's sink term of the row sum, 2^(sink - m)
+    float psum = 0.0f;    // kSum: this half's sum of its P
     BandWalk w;
     w.start(p);
     while (true) {
       const bool have = w.more(p);
       int ng = 0, ntok = 0, nrem = 0;
-      float m = -INFINITY, nsink = 0.0f;
+      float m = -INFINITY, nsink = 0.0f, nsum = 0.0f;
       if (have) {
         const BandItem& it = w.it;
         const int h = it.g * p.group + hh;
@@ -547,10 +564,12 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
           // P of keys [cc, cc + 32) goes to columns [cc / 2, cc / 2 + 16) of the
           // half: S columns this thread has already read.
           int cc = 0;
+          uint64_t sum = f2(0.0f, 0.0f);
           #pragma unroll 1
           for (; cc + 32 <= nc; cc += 32)
-            band_chunk_exp<32>(tS + cc, tS + (cc >> 1), sl2x2, negm2);
-          if (cc < nc) band_chunk_exp<16>(tS + cc, tS + (cc >> 1), sl2x2, negm2);
+            band_chunk_exp<32, kSum>(tS + cc, tS + (cc >> 1), sl2x2, negm2, &sum);
+          if (cc < nc) band_chunk_exp<16, kSum>(tS + cc, tS + (cc >> 1), sl2x2, negm2, &sum);
+          if constexpr (kSum) nsum = f2_lo(sum) + f2_hi(sum);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full);
@@ -564,6 +583,7 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         // The staging tiles are free once the stores of item li - 2 have read them.
         if (leader) bulk_wait_group_read0();
         const bool fin = ok && mbar_wait_warp(&pv_done, (li - 1) & 1, &abort_flag);
+        if constexpr (kSum) s_sum[c][r] = psum;
         if (!named_barrier_and(1, 2 * kBlockM, fin)) {
           abort_flag = 1;
           atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 6);
@@ -608,8 +628,10 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
                   make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
           }
         }
+        float lz = lt;
+        if constexpr (kSum) lz = s_sum[0][r] + s_sum[1][r] + psink;
         if (c == 0 && t < prem)
-          p.lse[(size_t)h * p.total_q + row] = (lt > 0.0f) ? (pm + __log2f(lt)) * kLn2 : -INFINITY;
+          p.lse[(size_t)h * p.total_q + row] = (lz > 0.0f) ? (pm + __log2f(lz)) * kLn2 : -INFINITY;
         if (whole) {
           fence_proxy_async_smem();
           named_barrier_sync(6, 2 * kBlockM);
@@ -626,6 +648,7 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
       prem = nrem;
       pm = m;
       psink = nsink;
+      psum = nsum;
       ++li;
       w.advance(p);
     }

@@ -9,11 +9,11 @@ namespace {
 // A launch that may begin while the kernel before it in the stream runs (the
 // kernel waits for it itself: grid_dependency_wait).
 template <typename P>
-bool launch_dependent(void (*kernel)(P), unsigned grid, unsigned threads, size_t smem,
+bool launch_dependent(void (*kernel)(P), dim3 grid, unsigned threads, size_t smem,
                       cudaStream_t s, const P& params) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -103,7 +103,19 @@ struct ExtendLayout {
   int tokens;        // per tile
   int n_items, max_parts, max_tiles, slots;
   size_t off_tiles, off_ml, off_o, total;
+  // the band kernel's path (extend_window.cuh)
+  int band_cols;     // 0: not taken
+  long long band_rows;
+  size_t off_regions, off_k, off_v;
 };
+
+// Windows go to the band kernel where one product covers a tile's keys (as in the
+// forward) and there are kExtBandTokens new tokens a sequence on average; below,
+// the workspace (176 + W rows of K and V for every sequence) is out of proportion.
+// Device time of the band kernel's and of the general way, 64 + 8 heads, W = 128:
+// 8 x 257..513 tokens 28 and 61 us, 32 x 64..128 32 and 67, 128 x 12..24 46 and 74,
+// 128 x 4..8 38 and 50, 8 x 4..8 12 and 17.
+constexpr int kExtBandTokens = 8;
 
 constexpr int kExtCtasPerSm = 2;   // shared memory, TMEM and registers allow two
 
@@ -135,6 +147,25 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   L->off_o = off;
   off += align256(parts * kBlockM * kHeadDim * sizeof(float));
   L->total = off;
+  L->band_cols = 0;
+  if (p->window > 0 && kBlockM % group == 0 &&
+      (long long)L->tokens + p->window - 1 <= kBandMaxCols &&
+      p->total_q >= (long long)kExtBandTokens * p->batch) {
+    L->band_rows = p->total_q + (long long)p->batch * (p->window - 1 + kGatherPad) + kGatherPad;
+    const long long span_tiles = p->total_q / L->tokens + (long long)p->batch;
+    if (L->band_rows < (1ll << 30) && span_tiles * p->heads_kv < (1ll << 30)) {
+      L->band_cols = (L->tokens + p->window - 1 + 15) / 16 * 16;
+      L->n_items = (int)span_tiles;        // tiles that are listed
+      const size_t kv = align256((size_t)L->band_rows * p->heads_kv * kHeadDim * 2);
+      off = align256((size_t)span_tiles * sizeof(int4));
+      L->off_regions = off;
+      off += align256((size_t)p->batch * sizeof(GatherRegion));
+      L->off_k = off;
+      off += kv;
+      L->off_v = off;
+      L->total = off + kv;
+    }
+  }
   return ATTN_SINK_OK;
 }
 
@@ -152,11 +183,72 @@ int extend_attributes() {
                              kFwdSmemBytes) != cudaSuccess ||
         cudaFuncSetAttribute(attn_sink_extend_kernel<false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kFwdSmemBytes) != cudaSuccess)
+                             kFwdSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_sink_fwd_band_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kBandSmemMax) != cudaSuccess)
       return ATTN_SINK_ERR_CUDA;
     g_ext_attr_set[dev] = true;
   }
   return ATTN_SINK_OK;
+}
+
+// The windowed path: gather, then the band kernel with every tile a sequence.
+int extend_window(const attn_sink_extend_params* p, const ExtendLayout& L, const ExtParams& ep,
+                  const void* q, void* out, uint8_t* ws, int sms, cudaStream_t s) {
+  GatherParams gp;
+  gp.e = ep;
+  gp.spans = reinterpret_cast<int4*>(ws);
+  gp.regions = reinterpret_cast<GatherRegion*>(ws + L.off_regions);
+  gp.k = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
+  gp.v = reinterpret_cast<uint16_t*>(ws + L.off_v);
+  gp.max_tiles = L.n_items;
+  gp.rows = L.band_rows;
+  FwdBandParams bp;
+  std::memset(&bp, 0, sizeof(bp));
+  int st;
+  if ((st = encode_rows(&bp.tm_q, q, p->total_q, p->heads_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        L.tokens, ep.group)) != ATTN_SINK_OK ||
+      (st = encode_rows(&bp.tm_k, gp.k, L.band_rows, p->heads_kv,
+                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.band_cols)) != ATTN_SINK_OK ||
+      (st = encode_rows(&bp.tm_v, gp.v, L.band_rows, p->heads_kv,
+                        CU_TENSOR_MAP_DATA_TYPE_FLOAT16, L.band_cols)) != ATTN_SINK_OK ||
+      (st = encode_rows(&bp.tm_out, out, p->total_q, p->heads_q,
+                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.tokens, ep.group)) != ATTN_SINK_OK)
+    return st;
+  bp.tm_out_lo = bp.tm_out;                // unused without a residual
+  bp.spans = gp.spans;
+  bp.sink = ep.sink;
+  bp.out = ep.out;
+  bp.lse = ep.lse;
+  bp.err = ep.err;
+  bp.total_q = p->total_q;
+  bp.heads_q = p->heads_q;
+  bp.heads_kv = p->heads_kv;
+  bp.group = ep.group;
+  while ((1 << bp.log2_group) < ep.group) ++bp.log2_group;
+  bp.tokens = L.tokens;
+  bp.n_cols = L.band_cols;
+  bp.half0_cols = 16 * ((L.band_cols / 16 + 1) / 2);
+  bp.window = p->window;
+  bp.scale_log2 = ep.scale_log2;
+  bp.n_tb = 1;
+  bp.n_items = L.n_items * p->heads_kv;
+  fast_div_init(p->heads_kv, &bp.div_hkv_mul, &bp.div_hkv_shift);
+  fast_div_init(bp.n_tb, &bp.div_tb_mul, &bp.div_tb_shift);
+#ifdef ATTN_SINK_TEST_HOOKS
+  bp.skip_k_tile = g_test_skip_k_tile.load();
+#endif
+  attn_sink_gather_plan_kernel<<<1, kExtSchedThreads, 0, s>>>(gp);
+  if (!launched()) return ATTN_SINK_ERR_CUDA;
+  // about eight CTAs an SM, over the sequences and the rows of each
+  const int y = std::min(p->batch, 8 * sms), x = std::max(1, 8 * sms / y);
+  if (!launch_dependent(attn_sink_gather_kernel, dim3(x, y), kGatherThreads, 0, s, gp))
+    return ATTN_SINK_ERR_CUDA;
+  const int smem = std::max(80 * 1024, band_smem_bytes(L.band_cols));   // two CTAs an SM
+  const int grid = (int)std::min<long long>(bp.n_items, (long long)kBandCtasPerSm * sms);
+  attn_sink_fwd_band_kernel<true><<<grid, kBandThreads, smem, s>>>(bp);
+  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 
 }  // namespace
@@ -423,6 +515,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
 #ifdef ATTN_SINK_TEST_HOOKS
   ep.skip_k_tile = g_test_skip_k_tile.load();
 #endif
+  if (L.band_cols > 0) return extend_window(params, L, ep, q, out, ws, sms, s);
   // Page sizes that are a multiple of 8 keys (whole swizzle atoms) are copied by
   // TMA, in boxes of the largest power of two that divides the page, at most a
   // block; the rows have to fit a copy's 32-bit coordinates.

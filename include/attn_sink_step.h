@@ -165,8 +165,9 @@ typedef struct attn_sink_extend_params {
 } attn_sink_extend_params;
 
 /* Bytes of device workspace attn_sink_extend needs (0 if the params are
- * invalid or there is nothing to do): the list of work items and the partial
- * results of key ranges that are split over several CTAs. */
+ * invalid or there is nothing to do): the list of work items and either the
+ * partial results of key ranges that are split over several CTAs or, for windows
+ * on the band kernel, the keys and values gathered from their pages. */
 size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
 
 /*
@@ -182,13 +183,17 @@ size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
  * token's window are not used, whatever they hold (block-table entries of such
  * pages are not read); a value of +-inf or NaN in a key or value row that some
  * token of a tile sees reaches that tile's outputs.
- * S = q k^T multiplies the bf16 inputs exactly; the probabilities are rounded
- * to bf16 for their product with the bf16 values (fp32 accumulation, sums in
- * fp32 before the rounding).  A length outside [0, max_pages * page_size] is
- * clamped, the keys of a block-table entry outside [0, num_pages) are skipped
- * and cu_seqlens_q is clamped to [0, T]; each is recorded as 0x800.  The
- * workspace is 256-byte aligned.  The result does not depend on timing: the
- * same inputs give the same bits.
+ * S = q k^T multiplies the bf16 inputs exactly with fp32 sums, and lse comes
+ * from fp32 probabilities.  For O = P v they are rounded to bf16 next to the bf16
+ * values; with a window that the band kernel of attn_sink_fwd covers (128 / G +
+ * W - 1 <= 176 keys, G a power of two) and 8 new tokens a sequence on average, to
+ * fp16 next to fp16 copies of the values, which have to lie within the fp16 range
+ * there (|v| <= 65504, else 0x400 is recorded, as by attn_sink_fwd).
+ * A length outside [0, max_pages * page_size] is clamped, the keys of a
+ * block-table entry outside [0, num_pages) are skipped (on the band kernel they
+ * read as zero keys and values), and cu_seqlens_q is clamped to [0, T]; each is
+ * recorded as 0x800.  The workspace is 256-byte aligned.  The result does not
+ * depend on timing: the same inputs give the same bits.
  */
 int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const void* k_cache,
                      const void* v_cache, const int* block_table, const int* seq_lens,
