@@ -268,6 +268,18 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       }
       __syncthreads();
     }
+    // TMA copies whole pages: value rows outside [lo, k1) may hold anything (cache
+    // rows that no token was written to), and 0 * inf is not 0.
+    const int base = k0 + blk * kDecKeys;
+    if (kTma && (base < lo || base + kDecKeys > k1)) {         // same for the whole CTA
+      for (int c = tid; c < kDecKeys * 8; c += kDecThreads) {
+        const int j = base + (c >> 3);
+        if (j < lo || j >= k1)
+          *reinterpret_cast<uint4*>(&s_kv[st][1][c * 16]) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();     // the stage's next copy comes through the async proxy
+      __syncthreads();
+    }
     const uint32_t kt = smem_u32(&s_kv[st][0][0]);
     const uint32_t vt = smem_u32(&s_kv[st][1][0]);
 
