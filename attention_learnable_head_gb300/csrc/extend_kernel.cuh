@@ -280,13 +280,13 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
         it.at0 = i0 + off;
         it.split = part << 16 | np;
         it.first = wp + (k / np) * np;
-        // both bounds hold for every cu_seqlens that ascends; one that does not
-        // may list more, which is dropped (and was recorded)
-        if (np > 1 && it.first + np > p.max_parts) it.num = -1;
-        if (np > 1 && part == 0 && wt + k / np < p.max_tiles)
+        // the bounds hold for every cu_seqlens that ascends; one that does not may
+        // list more (past 2^31 as well), which is dropped (and was recorded)
+        if (np > 1 && (it.first < 0 || it.first > p.max_parts - np)) it.num = -1;
+        if (np > 1 && part == 0 && (unsigned)(wt + k / np) < (unsigned)p.max_tiles)
           p.tiles[wt + k / np] =
               ExtTileRef{it.first, it.num < 0 ? 0 : np, it.num < 0 ? 0 : it.rows, it.row0};
-        if (wi + k >= p.n_items) continue;
+        if ((unsigned)(wi + k) >= (unsigned)p.n_items) continue;
         const uint4* src = reinterpret_cast<const uint4*>(&it);
         uint4* dst = reinterpret_cast<uint4*>(p.items + wi + k);
         dst[0] = src[0];
@@ -295,8 +295,8 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
       }
     }
   }
-  for (int k = item0 + tid; k < p.n_items; k += kExtSchedThreads) p.items[k].num = -1;
-  if (tid == 0) *p.n_tiles = min(split0, p.max_tiles);
+  for (int k = max(item0, 0) + tid; k < p.n_items; k += kExtSchedThreads) p.items[k].num = -1;
+  if (tid == 0) *p.n_tiles = max(0, min(split0, p.max_tiles));
 }
 
 // The bits below bit n of a word.

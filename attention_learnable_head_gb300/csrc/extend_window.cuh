@@ -74,12 +74,13 @@ attn_sink_gather_plan_kernel(const __grid_constant__ GatherParams g) {
         const int q0 = x.q0 + t * p.tokens, q1 = min(q0 + p.tokens, x.q0 + x.n);
         const int lo = min(e.lo, e.hi);    // no key: an empty span
         // more tiles than fit are only listed by a cu_seqlens that descends
-        if (at + t < g.max_tiles) g.spans[at + t] = make_int4(q0, q1, lo + shift, e.hi + shift);
+        if ((unsigned)(at + t) < (unsigned)g.max_tiles)
+          g.spans[at + t] = make_int4(q0, q1, lo + shift, e.hi + shift);
       }
     }
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-  for (int t = tile0 + tid; t < g.max_tiles; t += kExtSchedThreads)
+  for (int t = max(tile0, 0) + tid; t < g.max_tiles; t += kExtSchedThreads)
     g.spans[t] = make_int4(0, 0, 0, 0);
 }
 

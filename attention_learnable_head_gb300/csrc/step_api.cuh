@@ -264,6 +264,7 @@ int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_l
       params->max_pages < 0 || params->num_free < 0 || params->max_tokens < 0 ||
       (long long)params->max_pages * params->page_size > (1ll << 30))
     return ATTN_SINK_ERR_INVALID_ARG;
+  if (params->batch > (1 << 24)) return ATTN_SINK_ERR_UNSUPPORTED;
   if (cu_seqlens == nullptr || pages_needed == nullptr ||
       (params->batch > 0 &&
        (cached_lens == nullptr || new_lens == nullptr || seq_lens == nullptr)) ||
@@ -506,7 +507,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
   ep.page_size = params->page_size;
   ep.num_pages = params->num_pages;
   ep.max_pages = params->max_pages;
-  ep.window = params->window > 0 ? params->window : 0;
+  ep.window = params->window > 0 ? std::min(params->window, 1 << 30) : 0;   // >= any length
   ep.n_items = L.n_items;
   ep.max_parts = L.max_parts;
   ep.max_tiles = L.max_tiles;

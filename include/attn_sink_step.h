@@ -42,7 +42,7 @@ extern "C" {
 #define ATTN_SINK_DEVERR_PLAN 0x1000
 
 typedef struct attn_sink_plan_params {
-  int batch;      /* B >= 0 sequences */
+  int batch;      /* 0 <= B <= 2^24 sequences */
   int page_size;  /* keys per page, >= 1 */
   int num_pages;  /* pages of the cache: valid page indices are [0, num_pages) */
   int max_pages;  /* columns of block_table; max_pages * page_size <= 2^30 */
@@ -129,7 +129,8 @@ int attn_sink_qkv_rope(const attn_sink_rope_params* params, const void* q, const
                        void* stream);
 
 /* Bytes of device workspace attn_sink_qkv_rope_bwd needs: the weight
- * gradients' partial sums (0 with norm = 0, tokens = 0 or invalid params). */
+ * gradients' partial sums (0 with norm = 0, tokens = 0 or invalid params).
+ * Query it on the device the call will run on. */
 size_t attn_sink_qkv_rope_bwd_workspace_size(const attn_sink_rope_params* params);
 
 /*
@@ -152,8 +153,8 @@ int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, c
                            void* stream);
 
 typedef struct attn_sink_extend_params {
-  int batch;          /* B >= 0 sequences */
-  int total_q;        /* T: rows of q and out; cu_seqlens_q[B] <= T */
+  int batch;          /* 0 <= B <= 2^24 sequences */
+  int total_q;        /* T <= 2^30: rows of q and out; cu_seqlens_q[B] <= T */
   int heads_q;        /* G * heads_kv with 1 <= G <= 128 */
   int heads_kv;       /* >= 1 */
   int head_dim;       /* must be 64 */
@@ -164,8 +165,8 @@ typedef struct attn_sink_extend_params {
   float softmax_scale;/* multiplies q.k only; finite and > 0 */
 } attn_sink_extend_params;
 
-/* Bytes of device workspace attn_sink_extend needs (0 if the params are
- * invalid or there is nothing to do): the list of work items and either the
+/* Bytes of device workspace attn_sink_extend needs, on the current device (0 if
+ * the params are invalid or there is nothing to do): the list of work items and either the
  * partial results of key ranges that are split over several CTAs or, for windows
  * on the band kernel, the keys and values gathered from their pages. */
 size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
