@@ -24,6 +24,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 import re
@@ -31,7 +32,7 @@ from typing import NamedTuple
 
 import torch
 
-from .build import LIB_PATH, INCLUDE
+from .build import FAST_PATH, INCLUDE, LIB_PATH
 
 c_int, c_float, c_void_p, c_size_t = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 c_longlong = ctypes.c_longlong
@@ -607,6 +608,31 @@ def attn_sink_extend(params: AttnSinkExtendParams, q, k_cache, v_cache, block_ta
                                   int(workspace_bytes), _stream(stream))
 
 
+_FAST = None
+
+
+def _fast():
+    """The native module attn_sink_fast (csrc/fast_calls.cpp) on libattn_sink.so:
+    the conveniences' checks, allocations and calls in the plain case.  Its
+    functions return None where a call is anything else; the Python code behind
+    each use then checks the arguments one by one."""
+    global _FAST
+    if _FAST is None:
+        if not os.path.exists(FAST_PATH):
+            raise RuntimeError(
+                f"{FAST_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        L = lib()
+        spec = importlib.util.spec_from_file_location("attn_sink_fast", FAST_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init(*(ctypes.cast(f, c_void_p).value for f in (
+            L.attn_sink_page_plan, L.attn_sink_qkv_rope, L.attn_sink_qkv_rope_bwd_workspace_size,
+            L.attn_sink_qkv_rope_bwd, L.attn_sink_extend_workspace_size, L.attn_sink_extend)))
+        _FAST = module
+    return _FAST
+
+
 _NOTHING = contextlib.nullcontext()
 # The current stream of a device as an integer; Stream objects cost a few
 # microseconds, which is what the smallest of these calls take.
@@ -667,6 +693,13 @@ def page_plan(cached_lens, new_lens, free_pages, block_table, *, page_size: int,
     cached_lens[b] keys and gets new_lens[b] new tokens; new pages are taken from
     free_pages in order and written into block_table [B, max_pages] in place.
     Nothing is read back: max_tokens bounds the tokens of the step."""
+    if stream is None:
+        r = (_FAST or _fast()).page_plan(cached_lens, new_lens, free_pages, block_table,
+                                         page_size, num_pages, max_tokens)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_page_plan")
+            return PagePlan(*r)
     dev, i32 = block_table.device, torch.int32
     b, = _dims("cached_lens", cached_lens, 1)
     cols, free = _dims("block_table", block_table, 2)[1], _dims("free_pages", free_pages, 1)[0]
@@ -788,6 +821,14 @@ def qkv_rope(qkv, positions, inv_freq, *, heads_q: int, heads_kv: int, q_weight=
     With slots [T] int64, k and v are written to those rows of k_cache and
     v_cache [pages, page_size, heads_kv, 64], and k and v are None unless
     keep_kv."""
+    if stream is None:
+        r = (_FAST or _fast()).qkv_rope(qkv, positions, inv_freq, heads_q, heads_kv, q_weight,
+                                        k_weight, eps, pair_axis, interleaved, amplitude, slots,
+                                        k_cache, v_cache, keep_kv)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_qkv_rope")
+            return r
     paged = slots is not None
     pages = page = 0
     if paged:
@@ -824,6 +865,14 @@ def qkv_rope_backward(qkv, positions, inv_freq, dq, dk, dv, *, heads_q: int, hea
     [T, heads_q, 64], dk and dv [T, heads_kv, 64], all bf16 or all fp32 (as
     backward gives them); dqkv [T, heads_q + 2 heads_kv, 64] bf16, the weights'
     gradients [64] fp32 (None without norm), bitwise reproducible."""
+    if stream is None:
+        r = (_FAST or _fast()).qkv_rope_backward(qkv, positions, inv_freq, heads_q, heads_kv,
+                                                 q_weight, k_weight, eps, pair_axis, interleaved,
+                                                 amplitude, dq, dk, dv)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_qkv_rope_bwd")
+            return r
     kind = dq.dtype
     if kind is not torch.float32 and kind is not torch.bfloat16:
         raise ValueError(f"dq has to be float32 or bfloat16, not {kind}")
@@ -892,6 +941,15 @@ def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, wi
     block_table [B, max_pages] int32, seq_lens [B] int32 (cached + new), sink
     [H_q] fp32.  Rows of out and lse behind cu_seqlens_q[B] are not written:
     give out and lse to keep what they hold there."""
+    if softmax_scale is None:
+        softmax_scale = 0.125
+    if stream is None:
+        r = (_FAST or _fast()).extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
+                                      sink, window, softmax_scale, out, lse)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_extend")
+            return r
     dev, bf16, i32 = q.device, torch.bfloat16, torch.int32
     b, = _dims("seq_lens", seq_lens, 1)
     t, hq, _ = _dims("q", q, 3)
@@ -908,8 +966,7 @@ def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, wi
         _want("out", out, bf16, dev, (t, hq, 64))
     if lse is not None:
         _want("lse", lse, torch.float32, dev, (hq, t))
-    p = AttnSinkExtendParams(b, t, hq, hkv, 64, page, pages, cols, window,
-                             0.125 if softmax_scale is None else softmax_scale)
+    p = AttnSinkExtendParams(b, t, hq, hkv, 64, page, pages, cols, window, softmax_scale)
     with _on(dev, stream):
         if out is None:
             out = torch.empty((t, hq, 64), dtype=bf16, device=dev)
