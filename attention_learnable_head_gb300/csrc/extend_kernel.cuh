@@ -74,7 +74,7 @@ struct ExtParams {
   float* o_part;           // [partial][kv head][128 rows][64]
   float2* ml_part;         // [partial][kv head][128 rows]: maximum (log2 units), sum
   ExtTileRef* tiles;       // tiles that are split, for the join
-  int* n_tiles;            // and how many
+  int2* n_tiles;           // how many, and the rows of the largest
   int* err;
   int batch, total_q, heads_q, heads_kv, group, tokens;
   int page_size, num_pages, max_pages, window;
@@ -146,6 +146,41 @@ __device__ __forceinline__ int ext_scan(int x, int* s_warp, int* all) {
   return (warp > 0 ? before : 0) + inc - x;
 }
 
+// Exclusive scans of three values a thread, in one pass; all[i] receives the sums.
+__device__ __forceinline__ void ext_scan3(int (&x)[3], int (*s_warp)[32], int (&all)[3]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int inc[3], sum[3];
+  #pragma unroll
+  for (int i = 0; i < 3; ++i) inc[i] = x[i];
+  #pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+    #pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int y = __shfl_up_sync(0xffffffffu, inc[i], d);
+      if (lane >= d) inc[i] += y;
+    }
+  __syncthreads();                         // the last round's sums have been read
+  if (lane == 31)
+    #pragma unroll
+    for (int i = 0; i < 3; ++i) s_warp[i][warp] = inc[i];
+  __syncthreads();
+  #pragma unroll
+  for (int i = 0; i < 3; ++i) sum[i] = s_warp[i][lane];
+  #pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+    #pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int y = __shfl_up_sync(0xffffffffu, sum[i], d);
+      if (lane >= d) sum[i] += y;
+    }
+  #pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    all[i] = __shfl_sync(0xffffffffu, sum[i], 31);
+    const int before = __shfl_sync(0xffffffffu, sum[i], max(warp - 1, 0));
+    x[i] = (warp > 0 ? before : 0) + inc[i] - x[i];
+  }
+}
+
 // Lists the work items.  With W the key blocks of all tiles (each taken as long
 // as its sequence's last) times the kv heads, a tile is cut into ceil(blocks / c)
 // parts.  Candidates for c spread W over 1/8, 2/8, .. 3 times the CTAs the GPU
@@ -154,15 +189,19 @@ __device__ __forceinline__ int ext_scan(int x, int* s_warp, int* all) {
 // longest part + kExtOver): rounds of CTAs, and what a CTA costs beside its
 // blocks.  (With c = W / slots, W / (2 slots) or no cut alone, 32 sequences of
 // 4096 to 8192 keys and 5 new tokens fill 2.2 rounds and take 104 us.)  That
-// makes tiles + 3 slots / H_kv items at most.  A thread takes a sequence
-// (neighbours go to different warps), its warp writes the sequence's items.
+// makes tiles + 3 slots / H_kv items at most.  A thread takes a sequence, later
+// an item, whose sequence it finds by bisection of the scanned counts: 5 us in
+// front of the tiles (7 with a warp per sequence and a scan for each count).
 __global__ void __launch_bounds__(kExtSchedThreads, 1)
 attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
-  __shared__ int s_scan[kExtSchedThreads / 32];
+  __shared__ int s_scan[3][32];
   __shared__ unsigned long long s_work;
   __shared__ int s_tiles[kExtSchedThreads], s_blocks[kExtSchedThreads];
-  __shared__ long long s_cost[kExtSchedThreads / 32];
-  __shared__ int s_chunk[kExtSchedThreads / 32];
+  __shared__ int s_item[kExtSchedThreads], s_part[kExtSchedThreads], s_split[kExtSchedThreads];
+  __shared__ ExtSeq s_seq[kExtSchedThreads];
+  __shared__ unsigned long long s_cost[kExtTries];
+  __shared__ int s_chunk[kExtTries], s_rows;
+  static_assert(kExtTries <= 32 && kExtSchedThreads == 1024, "a warp per candidate");
   grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool bad = false;
@@ -176,57 +215,71 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
     tiles = (s.n + p.tokens - 1) / p.tokens;
     if (tiles > 0) blocks = ext_tile(p, s, tiles - 1).blocks;
   };
-  if (tid == 0) s_work = 0;
+  if (tid == 0) {
+    s_work = 0;
+    s_rows = 0;
+  }
   __syncthreads();
   unsigned long long w = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
-    load(b0 + 32 * lane + warp);
+    load(b0 + tid);
     w += (unsigned long long)tiles * (unsigned)blocks;
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-  #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  if (lane == 0 && w > 0) atomicAdd(&s_work, w);           // whole numbers: any order
+  if (__any_sync(0xffffffffu, w > 0)) {
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+    if (lane == 0) atomicAdd(&s_work, w);                  // whole numbers: any order
+  }
+  s_tiles[tid] = tiles;                    // of the last (mostly the only) round
+  s_blocks[tid] = blocks;
   __syncthreads();
   int chunk;
   {
-    // warp i tries candidate i; the sequences' tiles and blocks go by rounds
-    // through shared memory
-    const long long per = (long long)s_work * p.heads_kv;
-    const int c = (int)min(max((8 * per + (long long)(warp + 1) * p.slots - 1) /
-                                   ((long long)(warp + 1) * p.slots), (long long)kExtMinBlocks),
-                           1ll << 24);     // > any tile's blocks
-    long long ctas = 0;
+    // warp i tries candidate i; with several rounds of sequences they go through
+    // shared memory again
+    const unsigned long long per = s_work * (unsigned)p.heads_kv;
+    const unsigned share = (unsigned)(warp + 1) * (unsigned)p.slots;
+    const int c = 8 * per < (1ull << 31)   // the division of 64 bits takes 0.3 us
+                      ? max((int)(((unsigned)(8 * per) + share - 1) / share), kExtMinBlocks)
+                      : (int)min((8 * per + share - 1) / share, 1ull << 24);   // > any tile's
+    unsigned long long ctas = 0;
     int longest = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
-      if (p.batch > kExtSchedThreads) load(b0 + 32 * lane + warp);       // else still at hand
-      __syncthreads();                     // the last round's have been read
-      s_tiles[32 * lane + warp] = tiles;   // in the order of the sequences
-      s_blocks[32 * lane + warp] = blocks;
-      __syncthreads();
+      if (p.batch > kExtSchedThreads) {
+        load(b0 + tid);
+        __syncthreads();                   // the last round's have been read
+        s_tiles[tid] = tiles;
+        s_blocks[tid] = blocks;
+        __syncthreads();
+      }
+      if (warp >= kExtTries) continue;
       for (int i = lane; i < min(kExtSchedThreads, p.batch - b0); i += 32) {
         const int n = s_blocks[i];
         if (s_tiles[i] == 0) continue;
         const int k = ext_parts(n, c);
-        ctas += (long long)s_tiles[i] * k;
+        ctas += (unsigned long long)s_tiles[i] * (unsigned)k;
         longest = max(longest, (n + k - 1) / k);
       }
     }
-    #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, d);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) {
-      s_cost[warp] = warp < kExtTries ? (ctas * p.heads_kv + p.slots - 1) / p.slots *
-                                            (longest + kExtOver)
-                                      : LLONG_MAX;
-      s_chunk[warp] = c;
+    if (warp < kExtTries) {
+      #pragma unroll
+      for (int d = 16; d > 0; d >>= 1) ctas += __shfl_xor_sync(0xffffffffu, ctas, d);
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      if (lane == 0) {
+        // the grid is below 2^31 CTAs, more of them are a cu_seqlens that does not ascend
+        const unsigned all = (unsigned)min(ctas * (unsigned)p.heads_kv, 1ull << 31);
+        s_cost[warp] = (unsigned long long)((all + (unsigned)p.slots - 1) / (unsigned)p.slots) *
+                       (unsigned)(longest + kExtOver);
+        s_chunk[warp] = c;
+      }
     }
     __syncthreads();
-    long long cost = s_cost[lane];
+    unsigned long long cost = lane < kExtTries ? s_cost[lane] : ~0ull;
     int best = lane;
     #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-      const long long other = __shfl_xor_sync(0xffffffffu, cost, d);
+      const unsigned long long other = __shfl_xor_sync(0xffffffffu, cost, d);
       const int who = __shfl_xor_sync(0xffffffffu, best, d);
       if (other < cost || (other == cost && who < best)) {
         cost = other;
@@ -236,38 +289,43 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
     chunk = s_chunk[best];
   }
 
-  int item0 = 0, part0 = 0, split0 = 0;    // of the sequences before this round
+  int done = 0, part0 = 0, split0 = 0;     // items listed; partial results, split tiles so far
+  bool over = false;                       // more than the workspace holds: no valid cu_seqlens
   for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
-    const int b = b0 + 32 * lane + warp;
-    if (p.batch > kExtSchedThreads) load(b);               // else still at hand
+    if (p.batch > kExtSchedThreads) load(b0 + tid);        // else still at hand
     const int parts = tiles > 0 ? ext_parts(blocks, chunk) : 0;
-    int all_i, all_p, all_s;
-    const int first_i = item0 + ext_scan(tiles * parts, s_scan, &all_i);
-    const int first_p = part0 + ext_scan(parts > 1 ? tiles * parts : 0, s_scan, &all_p);
-    const int first_s = split0 + ext_scan(parts > 1 ? tiles : 0, s_scan, &all_s);
-    item0 += all_i;
-    part0 += all_p;
-    split0 += all_s;
-    for (unsigned todo = __ballot_sync(0xffffffffu, tiles > 0); todo; todo &= todo - 1) {
-      const int l = __ffs(todo) - 1;
-      ExtSeq x;
-      x.q0 = __shfl_sync(0xffffffffu, s.q0, l);
-      x.n = __shfl_sync(0xffffffffu, s.n, l);
-      x.len = __shfl_sync(0xffffffffu, s.len, l);
-      const int xb = __shfl_sync(0xffffffffu, b, l);
-      const int np = __shfl_sync(0xffffffffu, parts, l), nt = __shfl_sync(0xffffffffu, tiles, l);
-      const int wi = __shfl_sync(0xffffffffu, first_i, l);
-      const int wp = __shfl_sync(0xffffffffu, first_p, l);
-      const int wt = __shfl_sync(0xffffffffu, first_s, l);
-      for (int k = lane; k < nt * np; k += 32) {
-        const int tile = nt - 1 - k / np, part = k % np;   // the longest tiles first
+    int at[3] = {tiles * parts, parts > 1 ? tiles * parts : 0, parts > 1 ? tiles : 0}, all[3];
+    const int rows = parts > 1 ? min(s.n, p.tokens) * p.group : 0;
+    const int most = __reduce_max_sync(0xffffffffu, rows);
+    if (lane == 0 && most > 0) atomicMax(&s_rows, most);
+    ext_scan3(at, s_scan, all);            // and its barriers: the last round has been written
+    s_item[tid] = at[0];
+    s_part[tid] = part0 + at[1];
+    s_split[tid] = split0 + at[2];
+    s_tiles[tid] = tiles;
+    s_blocks[tid] = parts;
+    s_seq[tid] = s;
+    __syncthreads();
+    over = all[0] < 0 || all[0] > p.n_items - done || all[1] < 0 ||
+           all[1] > p.max_parts - part0 || all[2] < 0 || all[2] > p.max_tiles - split0;
+    if (over) break;
+    for (int k = tid; k < all[0]; k += kExtSchedThreads) {
+      int i = 0;                           // the last sequence that starts at or before k
+      #pragma unroll
+      for (int d = kExtSchedThreads / 2; d > 0; d >>= 1)
+        if (s_item[i + d] <= k) i += d;
+      const ExtSeq x = s_seq[i];
+      const int np = max(s_blocks[i], 1), nt = s_tiles[i], j = k - s_item[i];
+      const int up = j / np, tile = nt - 1 - up, part = j - up * np;   // the longest tiles first
+      ExtItem it;
+      it.num = -1;
+      if ((unsigned)tile < (unsigned)nt) {                 // sums that wrapped round
         const ExtTile e = ext_tile(p, x, tile);
         const int i0 = tile * p.tokens, i1 = min(i0 + p.tokens, x.n) - 1, off = x.len - x.n;
         const int per = (e.blocks + np - 1) / np, skip = min(e.blocks, part * per);
-        ExtItem it;
         it.num = min(per, e.blocks - skip);
         it.blk0 = e.lo / kBlockN + skip;
-        it.seq = xb;
+        it.seq = b0 + i;
         it.row0 = x.q0 + i0;
         it.lo = e.lo;
         it.hi = e.hi;
@@ -279,24 +337,27 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
         it.rows = (i1 - i0 + 1) * p.group;
         it.at0 = i0 + off;
         it.split = part << 16 | np;
-        it.first = wp + (k / np) * np;
-        // the bounds hold for every cu_seqlens that ascends; one that does not may
-        // list more (past 2^31 as well), which is dropped (and was recorded)
-        if (np > 1 && (it.first < 0 || it.first > p.max_parts - np)) it.num = -1;
-        if (np > 1 && part == 0 && (unsigned)(wt + k / np) < (unsigned)p.max_tiles)
-          p.tiles[wt + k / np] =
+        it.first = s_part[i] + up * np;
+        // for every cu_seqlens that ascends the bounds hold; one that does not has
+        // been recorded
+        if (np > 1 && (unsigned)it.first > (unsigned)(p.max_parts - np)) it.num = -1;
+        if (np > 1 && part == 0 && (unsigned)(s_split[i] + up) < (unsigned)p.max_tiles)
+          p.tiles[s_split[i] + up] =
               ExtTileRef{it.first, it.num < 0 ? 0 : np, it.num < 0 ? 0 : it.rows, it.row0};
-        if ((unsigned)(wi + k) >= (unsigned)p.n_items) continue;
-        const uint4* src = reinterpret_cast<const uint4*>(&it);
-        uint4* dst = reinterpret_cast<uint4*>(p.items + wi + k);
-        dst[0] = src[0];
-        dst[1] = src[1];
-        dst[2] = src[2];
       }
+      const uint4* src = reinterpret_cast<const uint4*>(&it);
+      uint4* dst = reinterpret_cast<uint4*>(p.items + done + k);
+      dst[0] = src[0];
+      dst[1] = src[1];
+      dst[2] = src[2];
     }
+    done += all[0];
+    part0 += all[1];
+    split0 += all[2];
   }
-  for (int k = max(item0, 0) + tid; k < p.n_items; k += kExtSchedThreads) p.items[k].num = -1;
-  if (tid == 0) *p.n_tiles = max(0, min(split0, p.max_tiles));
+  // over: uniform, as the sums are
+  for (int k = (over ? 0 : done) + tid; k < p.n_items; k += kExtSchedThreads) p.items[k].num = -1;
+  if (tid == 0) *p.n_tiles = over ? make_int2(0, 0) : make_int2(split0, s_rows);
 }
 
 // The bits below bit n of a word.
@@ -837,70 +898,92 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
 }
 
 // Joins the parts of the split tiles, in the order of their keys, with the sink:
-// M = max(m_c, sink), Z = sum l_c 2^(m_c - M) + 2^(sink - M).  Sixteen lanes take
-// a row (tile, kv head, row), 4 dimensions each.  A kernel of its own: joined by
-// the CTA that stored the last part, 38 parts of 128 rows (1.2 MB through one
-// SM) took 60 us.
-__global__ void __launch_bounds__(kExtJoinThreads)
+// M = max(m_c, sink), Z = sum l_c 2^(m_c - M) + 2^(sink - M).  A warp takes a row
+// (tile, kv head, row): 16 lanes of 4 dimensions for the even parts, 16 for the
+// odd ones.  What it costs is the chain of its loads (count, tile, statistics and
+// sums), so those of 16 parts go out together, before their weights are known.
+// It adds 5 us to a call (two rows a warp, loads behind the weights: 6.5).  A
+// kernel of its own: joined by the CTA that stored the last part, 38 parts of 128
+// rows (1.2 MB through one SM) took 60 us.
+__global__ void __launch_bounds__(kExtJoinThreads, 4)
 attn_sink_extend_join_kernel(const __grid_constant__ ExtParams p) {
   grid_dependency_wait();
-  const int lane = threadIdx.x & 15, d = 4 * lane;
-  const int n = *p.n_tiles * p.heads_kv * kBlockM;
-  const int groups = gridDim.x * (kExtJoinThreads / 16);
-  // whole warps go round together (the shuffles stay within 16 lanes)
-  for (int x0 = (blockIdx.x * kExtJoinThreads + threadIdx.x) / 32 * 2; x0 < n; x0 += groups) {
-    const int x = x0 + (threadIdx.x >> 4 & 1);              // n is even
-    const int r = x % kBlockM, tg = x / kBlockM, t = tg / p.heads_kv, g = tg - t * p.heads_kv;
-    const ExtTileRef ref = p.tiles[t];
-    const int parts = r < ref.rows ? ref.parts : 0;
-    if (!__any_sync(0xffffffffu, parts > 0)) continue;
+  const int lane = threadIdx.x & 31, odd = lane >> 4, d = 4 * (lane & 15);
+  const int2 n = __ldcg(p.n_tiles);
+  const unsigned pairs = (unsigned)n.x * (unsigned)p.heads_kv;            // < 2^30
+  if (pairs == 0) return;
+  const unsigned warps = gridDim.x * (kExtJoinThreads / 32);
+  const unsigned up = warps / pairs, on = warps - up * pairs;
+  unsigned x = blockIdx.x * (kExtJoinThreads / 32) + (threadIdx.x >> 5);
+  unsigned row_at = x / pairs;
+  x -= row_at * pairs;
+  const size_t step = (size_t)p.heads_kv * kBlockM;         // from part to part
+  // rows in the outer order: the warps of a last round are those of rows that
+  // few tiles have
+  for (; (int)row_at < n.y; row_at += up, x += on) {
+    if (x >= pairs) {
+      x -= pairs;
+      if ((int)++row_at >= n.y) break;
+    }
+    const int r = (int)row_at;
+    const unsigned t = x / (unsigned)p.heads_kv;
+    const int g = (int)(x - t * (unsigned)p.heads_kv);
+    const int4 ref = __ldcg(reinterpret_cast<const int4*>(p.tiles + t));   // an ExtTileRef
+    const int parts = ref.y;
+    if (r >= ref.z) continue;
     const int tok = r / p.group;
-    const int hq = min(g * p.group + (r - tok * p.group), p.heads_q - 1);
-    const size_t pr = ((size_t)ref.first * p.heads_kv + g) * kBlockM + r;
-    const size_t step = (size_t)p.heads_kv * kBlockM;
-    static_assert(kExtMaxSplits <= 64, "four parts a lane");
+    const int hq = g * p.group + (r - tok * p.group);
+    const size_t pr = ((size_t)ref.x * p.heads_kv + g) * kBlockM + r;
+    const float* o = p.o_part + (pr + odd * step) * kHeadDim + d;
+    auto load = [&](int c) {                                // parts c + odd, c + odd + 2, ..
+      return c + odd < parts ? __ldcs(reinterpret_cast<const float4*>(o + c * step * kHeadDim))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    static_assert(kExtMaxSplits <= 64, "two parts a lane");
     const float s2 = __ldg(p.sink + hq) * kLog2e;
-    float2 ml[4];                                           // of parts lane + 16 u
-    float mf = s2;
+    float2 ml[2];                                           // of parts lane and lane + 32
     #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      ml[u] = lane + 16 * u < parts ? p.ml_part[pr + (lane + 16 * u) * step]
+    for (int u = 0; u < 2; ++u)
+      ml[u] = lane + 32 * u < parts ? __ldcg(p.ml_part + pr + (lane + 32 * u) * step)
                                     : make_float2(-INFINITY, 0.0f);
-      mf = fmaxf(mf, ml[u].x);
-    }
+    float4 v[8];
     #pragma unroll
-    for (int k = 8; k > 0; k >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, k));
+    for (int u = 0; u < 8; ++u) v[u] = load(2 * u);
+    float mf = fmaxf(s2, fmaxf(ml[0].x, ml[1].x));
+    #pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, k));
     const float mb = (mf == -INFINITY) ? 0.0f : mf;
-    float w[4], z = 0.0f;
+    const float w0 = ex2_approx(ml[0].x - mb), w1 = ex2_approx(ml[1].x - mb);   // 0: empty part
+    float z = fmaf(ml[1].y, w1, ml[0].y * w0);
     #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      w[u] = ex2_approx(ml[u].x - mb);                      // 0 for an empty part
-      z = fmaf(ml[u].y, w[u], z);
-    }
-    #pragma unroll
-    for (int k = 8; k > 0; k >>= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
+    for (int k = 16; k > 0; k >>= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
     z += ex2_approx(s2 - mb);
-    const int most = __reduce_max_sync(0xffffffffu, parts);
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      #pragma unroll 8
-      for (int c = 0; c < min(16, most - 16 * u); ++c) {
-        const float wt = __shfl_sync(0xffffffffu, w[u], c, 16);
-        if (wt == 0.0f) continue;                           // an empty part stored no sums
-        const float4 o = __ldcs(reinterpret_cast<const float4*>(
-            p.o_part + (pr + (16 * u + c) * step) * kHeadDim + d));
-        acc.x = fmaf(o.x, wt, acc.x);
-        acc.y = fmaf(o.y, wt, acc.y);
-        acc.z = fmaf(o.z, wt, acc.z);
-        acc.w = fmaf(o.w, wt, acc.w);
+    for (int c = 0; c < parts; c += 16) {
+      #pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k = c + 2 * u + odd;
+        const float wk = __shfl_sync(0xffffffffu, c < 32 ? w0 : w1, k & 31);
+        if (wk != 0.0f) {                                   // an empty part stored no sums
+          acc.x = fmaf(v[u].x, wk, acc.x);
+          acc.y = fmaf(v[u].y, wk, acc.y);
+          acc.z = fmaf(v[u].z, wk, acc.z);
+          acc.w = fmaf(v[u].w, wk, acc.w);
+        }
       }
+      if (c + 16 < parts)
+        #pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = load(c + 16 + 2 * u);
     }
-    if (parts == 0) continue;
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
     const float inv = z > 0.0f ? 1.0f / z : 0.0f;
-    const size_t row = (size_t)ref.row0 + tok;
-    *reinterpret_cast<uint2*>(p.out + (row * p.heads_q + hq) * kHeadDim + d) = make_uint2(
-        pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    const size_t row = (size_t)ref.w + tok;
+    if (odd == 0)
+      *reinterpret_cast<uint2*>(p.out + (row * p.heads_q + hq) * kHeadDim + d) = make_uint2(
+          pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0)
       p.lse[(size_t)hq * p.total_q + row] = z > 0.0f ? (mb + __log2f(z)) * kLn2 : -INFINITY;
   }

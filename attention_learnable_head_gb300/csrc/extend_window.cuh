@@ -88,6 +88,7 @@ attn_sink_gather_plan_kernel(const __grid_constant__ GatherParams g) {
 __global__ void __launch_bounds__(kGatherThreads)
 attn_sink_gather_kernel(const __grid_constant__ GatherParams g) {
   grid_dependency_wait();
+  grid_launch_dependents();
   const ExtParams& p = g.e;
   const int per = p.heads_kv * 8;          // chunks of a row
   bool over = false, lost = false;

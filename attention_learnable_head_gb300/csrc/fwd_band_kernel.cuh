@@ -346,6 +346,7 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  if constexpr (kSum) grid_dependency_wait();          // the kernel that gathers its keys
 
   if (warp == kBandTmaWarp) {
     // ---------------------------------------------------------------- TMA producer

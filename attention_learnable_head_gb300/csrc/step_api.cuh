@@ -247,8 +247,9 @@ int extend_window(const attn_sink_extend_params* p, const ExtendLayout& L, const
     return ATTN_SINK_ERR_CUDA;
   const int smem = std::max(80 * 1024, band_smem_bytes(L.band_cols));   // two CTAs an SM
   const int grid = (int)std::min<long long>(bp.n_items, (long long)kBandCtasPerSm * sms);
-  attn_sink_fwd_band_kernel<true><<<grid, kBandThreads, smem, s>>>(bp);
-  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+  return launch_dependent(attn_sink_fwd_band_kernel<true>, grid, kBandThreads, smem, s, bp)
+             ? ATTN_SINK_OK
+             : ATTN_SINK_ERR_CUDA;
 }
 
 }  // namespace
@@ -493,7 +494,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
   ep.out = static_cast<__nv_bfloat16*>(out);
   ep.lse = lse;
   ep.items = reinterpret_cast<ExtItem*>(ws);
-  ep.n_tiles = reinterpret_cast<int*>(ws + L.off_tiles);
+  ep.n_tiles = reinterpret_cast<int2*>(ws + L.off_tiles);
   ep.tiles = reinterpret_cast<ExtTileRef*>(ws + L.off_tiles + 256);
   ep.ml_part = reinterpret_cast<float2*>(ws + L.off_ml);
   ep.o_part = reinterpret_cast<float*>(ws + L.off_o);
