@@ -45,7 +45,7 @@ constexpr int kExtSchedThreads = 1024;
 constexpr int kExtJoinThreads = 256;
 
 // One CTA's work for each kv head: a tile, or a range of its key blocks.
-struct ExtItem {
+struct alignas(16) ExtItem {
   int num, blk0, seq, row0;                // blocks (-1: unused entry); first block; sequence;
   int lo, hi, mlo, mhi;                    // first row of q; keys the tile sees; blocks [mlo, mhi)
   int rows, at0, split, first;             // that need no mask; rows with a token; key position of
@@ -70,7 +70,7 @@ struct ExtParams {
   const float* sink;       // [H_q]
   __nv_bfloat16* out;      // [T][H_q][64]
   float* lse;              // [H_q][T]
-  ExtItem* items;
+  ExtItem* items;          // null: see ext_find
   float* o_part;           // [partial][kv head][128 rows][64]
   float2* ml_part;         // [partial][kv head][128 rows]: maximum (log2 units), sum
   ExtTileRef* tiles;       // tiles that are split, for the join
@@ -115,6 +115,60 @@ __device__ __forceinline__ ExtTile ext_tile(const ExtParams& p, const ExtSeq& s,
   x.lo = p.window > 0 ? max(0, i0 + off - p.window + 1) : 0;
   x.blocks = x.hi > x.lo ? (x.hi + kBlockN - 1) / kBlockN - x.lo / kBlockN : 0;
   return x;
+}
+
+// Part `part` of `np` of a tile; `first`: the tile's first partial result.
+__device__ __forceinline__ ExtItem ext_item(const ExtParams& p, const ExtSeq& s, int seq, int tile,
+                                            int part, int np, int first) {
+  const ExtTile e = ext_tile(p, s, tile);
+  const int i0 = tile * p.tokens, i1 = min(i0 + p.tokens, s.n) - 1, off = s.len - s.n;
+  const int per = (e.blocks + np - 1) / np, skip = min(e.blocks, part * per);
+  ExtItem it;
+  it.num = min(per, e.blocks - skip);
+  it.blk0 = e.lo / kBlockN + skip;
+  it.seq = seq;
+  it.row0 = s.q0 + i0;
+  it.lo = e.lo;
+  it.hi = e.hi;
+  // blocks before mlo hold keys behind some token's window, blocks from mhi on
+  // keys after some token
+  const int lost = i1 + off - p.window;    // last key some token has lost
+  it.mlo = p.window > 0 && lost >= 0 ? lost / kBlockN + 1 - it.blk0 : 0;
+  it.mhi = max(0, min(s.len, i0 + off + 1)) / kBlockN - it.blk0;
+  it.rows = (i1 - i0 + 1) * p.group;
+  it.at0 = i0 + off;
+  it.split = part << 16 | np;
+  it.first = first;
+  return it;
+}
+
+// Without a list (items null: up to 32 sequences, tiles that are not cut): item i
+// is the i-th tile of the batch, found by every warp for itself.
+__device__ __forceinline__ ExtItem ext_find(const ExtParams& p, int i, bool record) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  ExtSeq s{0, 0, 0};
+  if (lane < p.batch) s = ext_seq(p, lane, &bad);
+  if (bad && record) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  // < 2^27 tiles a sequence; more than the grid has are not asked for
+  const int tiles = (s.n + p.tokens - 1) / p.tokens;
+  int upto = tiles;
+  #pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto = (int)min((unsigned)upto + (unsigned)y, 1u << 30);
+  }
+  const unsigned after = __ballot_sync(0xffffffffu, upto > i);
+  ExtItem it;
+  it.num = -1;
+  if (after == 0) return it;
+  const int b = __ffs(after) - 1;
+  ExtSeq x;
+  x.q0 = __shfl_sync(0xffffffffu, s.q0, b);
+  x.n = __shfl_sync(0xffffffffu, s.n, b);
+  x.len = __shfl_sync(0xffffffffu, s.len, b);
+  const int tile = i - __shfl_sync(0xffffffffu, upto - tiles, b);
+  return ext_item(p, x, b, tile, 0, 1, 0);
 }
 
 // Parts of a tile of `blocks` blocks, of at least c blocks each (rounded up).
@@ -319,25 +373,8 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
       const int up = j / np, tile = nt - 1 - up, part = j - up * np;   // the longest tiles first
       ExtItem it;
       it.num = -1;
-      if ((unsigned)tile < (unsigned)nt) {                 // sums that wrapped round
-        const ExtTile e = ext_tile(p, x, tile);
-        const int i0 = tile * p.tokens, i1 = min(i0 + p.tokens, x.n) - 1, off = x.len - x.n;
-        const int per = (e.blocks + np - 1) / np, skip = min(e.blocks, part * per);
-        it.num = min(per, e.blocks - skip);
-        it.blk0 = e.lo / kBlockN + skip;
-        it.seq = b0 + i;
-        it.row0 = x.q0 + i0;
-        it.lo = e.lo;
-        it.hi = e.hi;
-        // blocks before mlo hold keys behind some token's window, blocks from mhi
-        // on keys after some token
-        const int lost = i1 + off - p.window;              // last key some token has lost
-        it.mlo = p.window > 0 && lost >= 0 ? lost / kBlockN + 1 - it.blk0 : 0;
-        it.mhi = max(0, min(x.len, i0 + off + 1)) / kBlockN - it.blk0;
-        it.rows = (i1 - i0 + 1) * p.group;
-        it.at0 = i0 + off;
-        it.split = part << 16 | np;
-        it.first = s_part[i] + up * np;
+      if ((unsigned)tile < (unsigned)nt) {                 // else sums that wrapped round
+        it = ext_item(p, x, b0 + i, tile, part, np, s_part[i] + up * np);
         // for every cu_seqlens that ascends the bounds hold; one that does not has
         // been recorded
         if (np > 1 && (unsigned)it.first > (unsigned)(p.max_parts - np)) it.num = -1;
@@ -382,10 +419,21 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
 
   const int item = (int)(blockIdx.x / (unsigned)p.heads_kv);
   const int g = (int)(blockIdx.x - (unsigned)item * (unsigned)p.heads_kv);
-  const uint4* desc = reinterpret_cast<const uint4*>(p.items + item);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const uint4 d0 = __ldcg(desc), d1 = __ldcg(desc + 1), d2 = __ldcg(desc + 2);
+  uint4 d0, d1, d2;                                       // an ExtItem
+  if (p.items != nullptr) {
+    const uint4* desc = reinterpret_cast<const uint4*>(p.items + item);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    d0 = __ldcg(desc);
+    d1 = __ldcg(desc + 1);
+    d2 = __ldcg(desc + 2);
+  } else {
+    const ExtItem it = ext_find(p, item, blockIdx.x == 0 && threadIdx.x < 32);
+    const uint4* desc = reinterpret_cast<const uint4*>(&it);
+    d0 = desc[0];
+    d1 = desc[1];
+    d2 = desc[2];
+  }
   const int num = (int)d0.x, blk0 = (int)d0.y, row0 = (int)d0.w;
   if (num < 0) return;                                    // uniform per CTA
   const int lo = (int)d1.x, hi = (int)d1.y, mlo0 = (int)d1.z, mhi0 = (int)d1.w;
@@ -536,6 +584,25 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
           const int n = x >> 1;
           mbar_arrive((x & 1) ? &v_full[n % kFwdVStages] : &k_full[n % kFwdKStages]);
         };
+        // Lane l holds the cache rows (128-byte units) of keys l, l + 32, .. of a
+        // block, and all lanes which keys have one; the table entries of the next
+        // block are on their way meanwhile.
+        uint32_t at[4], has[4];
+        bool all = true;
+        int pg_e[4], pg_at[4];
+        auto entries = [&](int n) {
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = (blk0 + n) * kBlockN + 32 * i + lane;
+            pg_e[i] = -1;
+            if (n < num && j >= lo && j < hi) {
+              const int pg = j / p.page_size;
+              pg_at[i] = j - pg * p.page_size;
+              pg_e[i] = __ldg(table + pg);
+            }
+          }
+        };
+        entries(0);
         bool ok = true;
         int x = 0;
         for (; x < 2 * num; ++x) {
@@ -544,6 +611,19 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
           if (!is_v && !TEST_HOOK_FWD_ISSUE_K(n)) {
             ok = false;
             break;
+          }
+          if (!is_v) {
+            all = true;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool in = (unsigned)pg_e[i] < (unsigned)p.num_pages;
+              at[i] = in ? ((uint32_t)pg_e[i] * (uint32_t)p.page_size + (uint32_t)pg_at[i]) *
+                                   (uint32_t)p.heads_kv + (uint32_t)g
+                         : 0;
+              has[i] = __ballot_sync(0xffffffffu, in);
+              all = all && has[i] == 0xffffffffu;
+            }
+            entries(n + 1);
           }
           if (is_v ? n >= kFwdVStages : n >= kFwdKStages) {
             uint64_t* e = is_v ? &v_empty[n % kFwdVStages] : &k_empty[n % kFwdKStages];
@@ -555,25 +635,31 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
           }
           const uint32_t dst = smem_u32(is_v ? sV + (n % kFwdVStages) * kTileBytes
                                              : sK + (n % kFwdKStages) * kTileBytes);
-          const __nv_bfloat16* cache = is_v ? p.v_cache : p.k_cache;
-          const int jb = (blk0 + n) * kBlockN;
           const int c = lane & 7;
-          #pragma unroll 4
-          for (int u = 0; u < kBlockN / 4; ++u) {
-            const int r = 4 * u + (lane >> 3);
-            const int j = jb + r;
-            const void* src = p.out;                        // any address: 0 bytes are read
-            uint32_t bytes = 0;
-            if (j >= lo && j < hi) {
-              const int pg = j / p.page_size;
-              const int e = __ldg(table + pg);
-              if (e >= 0 && e < p.num_pages) {
-                src = cache + ((size_t)e * p.page_size + (j - pg * p.page_size)) *
-                                  ((size_t)p.heads_kv * 64) + g * 64 + 8 * c;
-                bytes = 16;
+          const __nv_bfloat16* cache = (is_v ? p.v_cache : p.k_cache) + 8 * c;
+          if (all) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+              #pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const int r = 4 * u + (lane >> 3);
+                const uint32_t row = __shfl_sync(0xffffffffu, at[i], r);
+                cp_async_16_zfill(dst + sw128_offset((uint32_t)(32 * i + r), (uint32_t)c),
+                                  cache + (size_t)row * 64, 16);
               }
-            }
-            cp_async_16_zfill(dst + sw128_offset((uint32_t)r, (uint32_t)c), src, bytes);
+          } else {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+              #pragma unroll 2
+              for (int u = 0; u < 8; ++u) {
+                const int r = 4 * u + (lane >> 3);
+                const uint32_t row = __shfl_sync(0xffffffffu, at[i], r);
+                const bool in = has[i] >> r & 1u;           // else nothing is read, 0 written
+                cp_async_16_zfill(dst + sw128_offset((uint32_t)(32 * i + r), (uint32_t)c),
+                                  in ? (const void*)(cache + (size_t)row * 64)
+                                     : (const void*)p.out,
+                                  in ? 16u : 0u);
+              }
           }
           cp_async_commit();
           if (x >= 2) {

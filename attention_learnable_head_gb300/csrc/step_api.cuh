@@ -102,6 +102,7 @@ void rope_bwd_launch(const RopeParams& rp, dim3 grid, bool fp32, cudaStream_t s)
 struct ExtendLayout {
   int tokens;        // per tile
   int n_items, max_parts, max_tiles, slots;
+  bool split;                              // tiles may be cut: a join
   size_t off_tiles, off_ml, off_o, total;
   // the band kernel's path (extend_window.cuh)
   int band_cols;     // 0: not taken
@@ -127,16 +128,21 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
       p->max_pages < 0 || !(p->softmax_scale > 0.0f) || !std::isfinite(p->softmax_scale))
     return ATTN_SINK_ERR_INVALID_ARG;
   if ((long long)p->max_pages * p->page_size > (1ll << 30)) return ATTN_SINK_ERR_INVALID_ARG;
+  // rows of the cache of one head, 128 bytes each: 512 GB
+  if ((long long)p->num_pages * p->page_size > ((1ll << 32) - 1) / p->heads_kv)
+    return ATTN_SINK_ERR_UNSUPPORTED;
   const int group = p->heads_q / p->heads_kv;
   if (group > kExtMaxGroup) return ATTN_SINK_ERR_UNSUPPORTED;
   L->tokens = kBlockM / group;
   L->slots = kExtCtasPerSm * sms;
   const long long shares = (3 * L->slots + p->heads_kv - 1) / p->heads_kv;
+  // no tile of so few keys is cut
+  L->split = (long long)p->max_pages * p->page_size > kExtMinBlocks * kBlockN;
   // the bounds of attn_sink_extend_plan_kernel
-  const long long items = p->total_q / L->tokens + (long long)p->batch + shares;
+  const long long items = p->total_q / L->tokens + (long long)p->batch + (L->split ? shares : 0);
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
   L->n_items = (int)items;
-  L->max_parts = (int)std::min<long long>(items, 2 * shares);
+  L->max_parts = L->split ? (int)std::min<long long>(items, 2 * shares) : 0;
   L->max_tiles = L->max_parts / 2;         // two parts at least
   const size_t parts = (size_t)L->max_parts * p->heads_kv;
   size_t off = align256((size_t)L->n_items * sizeof(ExtItem));
@@ -535,12 +541,17 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
        (st = encode_rows(&ep.tm_v, v_cache, rows, params->heads_kv,
                          CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ep.box)) != ATTN_SINK_OK))
     return st;
-  attn_sink_extend_plan_kernel<<<1, kExtSchedThreads, 0, s>>>(ep);
-  if (!launched()) return ATTN_SINK_ERR_CUDA;
+  const auto kernel = tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>;
   const unsigned grid = (unsigned)L.n_items * (unsigned)params->heads_kv;
-  if (!launch_dependent(tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>, grid,
-                        kExtThreads, kFwdSmemBytes, s, ep) ||
-      !launch_dependent(attn_sink_extend_join_kernel, 6 * sms, kExtJoinThreads, 0, s, ep))
+  if (!L.split && params->batch <= 32) {   // one launch: each CTA finds its tile
+    ep.items = nullptr;
+    kernel<<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
+    return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+  }
+  attn_sink_extend_plan_kernel<<<1, kExtSchedThreads, 0, s>>>(ep);
+  if (!launched() || !launch_dependent(kernel, grid, kExtThreads, kFwdSmemBytes, s, ep) ||
+      (L.split &&
+       !launch_dependent(attn_sink_extend_join_kernel, 6 * sms, kExtJoinThreads, 0, s, ep)))
     return ATTN_SINK_ERR_CUDA;
   return ATTN_SINK_OK;
 }
