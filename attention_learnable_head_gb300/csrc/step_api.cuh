@@ -543,7 +543,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
     return st;
   const auto kernel = tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>;
   const unsigned grid = (unsigned)L.n_items * (unsigned)params->heads_kv;
-  if (!L.split && params->batch <= 32) {   // one launch: each CTA finds its tile
+  if (!L.split && params->batch <= 32) {   // a lane a sequence: see ext_find
     ep.items = nullptr;
     kernel<<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
     return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
@@ -551,7 +551,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
   attn_sink_extend_plan_kernel<<<1, kExtSchedThreads, 0, s>>>(ep);
   if (!launched() || !launch_dependent(kernel, grid, kExtThreads, kFwdSmemBytes, s, ep) ||
       (L.split &&
-       !launch_dependent(attn_sink_extend_join_kernel, 6 * sms, kExtJoinThreads, 0, s, ep)))
+       !launch_dependent(attn_sink_extend_join_kernel, kExtJoinCtas * sms, kExtJoinThreads, 0, s, ep)))
     return ATTN_SINK_ERR_CUDA;
   return ATTN_SINK_OK;
 }

@@ -159,16 +159,16 @@ typedef struct attn_sink_extend_params {
   int heads_kv;       /* >= 1 */
   int head_dim;       /* must be 64 */
   int page_size;      /* keys per page, >= 1 */
-  int num_pages;      /* pages of the cache */
+  int num_pages;      /* pages of the cache; num_pages * page_size * heads_kv < 2^32 */
   int max_pages;      /* columns of block_table; max_pages * page_size <= 2^30 */
   int window;         /* <= 0: none; W > 0: the W most recent keys */
   float softmax_scale;/* multiplies q.k only; finite and > 0 */
 } attn_sink_extend_params;
 
 /* Bytes of device workspace attn_sink_extend needs, on the current device (0 if
- * the params are invalid or there is nothing to do): the list of work items and either the
- * partial results of key ranges that are split over several CTAs or, for windows
- * on the band kernel, the keys and values gathered from their pages. */
+ * the params are invalid or there is nothing to do): the list of work items and
+ * either the partial results of key ranges that are split over several CTAs or,
+ * for windows on the band kernel, the keys and values gathered from their pages. */
 size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
 
 /*

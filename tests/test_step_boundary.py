@@ -189,6 +189,16 @@ def test_extend_rejects_bad_pointers_and_workspaces():
         assert binding.attn_sink_extend_workspace_size(_ext_params(**kw)) == 0
 
 
+@pytest.mark.parametrize("pages,page,heads,status", [
+    (1 << 27, 16, 2, UNSUPPORTED), ((1 << 31) - 1, 1, 3, UNSUPPORTED),
+    ((1 << 27) - 1, 16, 2, OK), ((1 << 31) - 1, 1, 2, OK), (1 << 31 - 4, 7, 4, OK)])
+def test_extend_counts_the_cache_rows_of_all_heads_in_32_bits(pages, page, heads, status):
+    p = _ext_params(num_pages=pages, page_size=page, heads_kv=heads, heads_q=heads)
+    assert (binding.attn_sink_extend_workspace_size(p) > 0) == (status == OK)
+    # without room in the workspace nothing is launched
+    assert _extend(p, ws=None, ws_bytes=0) == (WORKSPACE if status == OK else status)
+
+
 # ----------------------------------------------------------------------------- conveniences
 def test_conveniences_reject_bad_tensors():
     i32, bf16 = torch.int32, torch.bfloat16
