@@ -23,9 +23,9 @@
 // the launch's work are split, so that a long cache with few new tokens fills
 // the GPU; the parts leave fp32 sums in the workspace and a third kernel joins
 // them and adds the sink.  The three are chained by programmatic dependent
-// launch.  Where the table holds too few keys for a tile to be cut there is no
-// join, and up to 32 sequences need no schedule either: each CTA finds its tile
-// (5 new tokens on 10 keys: 7.5 us, 14.4 with all three).
+// launch.  Where the table or the window leaves too few keys for a tile to be cut
+// there is no join, and up to 32 sequences need no schedule either: each CTA finds
+// its tile (5 new tokens on 10 keys: 7.5 us, 14.4 with all three).
 //
 // The rest is the forward kernel's pipeline: S = Q K^T into TMEM, online
 // softmax by two warpgroups (one per key half), P to TMEM, O += P V with P

@@ -111,12 +111,17 @@ struct ExtendLayout {
 };
 
 // Windows go to the band kernel where one product covers a tile's keys (as in the
-// forward) and there are kExtBandTokens new tokens a sequence on average; below,
-// the workspace (176 + W rows of K and V for every sequence) is out of proportion.
-// Device time of the band kernel's and of the general way, 64 + 8 heads, W = 128:
-// 8 x 257..513 tokens 28 and 61 us, 32 x 64..128 32 and 67, 128 x 12..24 46 and 74,
-// 128 x 4..8 38 and 50, 8 x 4..8 12 and 17.
+// forward), the tiles are more than the GPU holds at once or have no single launch
+// (ext_find), and the sequences have enough new tokens: kExtBandTokens on average,
+// below which the workspace (176 + W rows of K and V for each) is out of
+// proportion; two full tiles with two heads a group, where gathering costs as much
+// as it saves (with one it always did).  Device time of the band kernel's and of
+// the general way, W = 128, 64 + 8 heads: 8 x 513 tokens 28 and 61 us, 32 x 64 23
+// and 33, 128 x 8 38 and 42, 8 x 64 13.4 and 13.8, 32 x 16 15.2 and 14.8, 1 x 256
+// 10.7 and 9.2; 8 + 1 heads, 64 x 8 11.7 and 14.4; W = 100, 16 + 8 heads: 128 x 64
+// 52 and 46, 128 x 200 95 and 108; W = 40, 8 + 8 heads: 128 x 200 72 and 68.
 constexpr int kExtBandTokens = 8;
+constexpr int kExtFindMax = 32;    // sequences of a single launch: a lane each
 
 constexpr int kExtCtasPerSm = 2;   // shared memory, TMEM and registers allow two
 
@@ -136,8 +141,11 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   L->tokens = kBlockM / group;
   L->slots = kExtCtasPerSm * sms;
   const long long shares = (3 * L->slots + p->heads_kv - 1) / p->heads_kv;
-  // no tile of so few keys is cut
-  L->split = (long long)p->max_pages * p->page_size > kExtMinBlocks * kBlockN;
+  // tiles that see so few keys are not cut: kExtMinBlocks blocks of them at most,
+  // as the table is no wider or as the window touches no more
+  const long long seen = p->window > 0 ? (long long)p->window + L->tokens - 1 : LLONG_MAX / 2;
+  L->split = (long long)p->max_pages * p->page_size > kExtMinBlocks * kBlockN &&
+             (seen + kBlockN - 2) / kBlockN + 1 > kExtMinBlocks;
   // the bounds of attn_sink_extend_plan_kernel
   const long long items = p->total_q / L->tokens + (long long)p->batch + (L->split ? shares : 0);
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
@@ -154,11 +162,13 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   off += align256(parts * kBlockM * kHeadDim * sizeof(float));
   L->total = off;
   L->band_cols = 0;
-  if (p->window > 0 && kBlockM % group == 0 &&
+  const long long span_tiles = p->total_q / L->tokens + (long long)p->batch;
+  const long long enough = group == 2 ? 2 * L->tokens : kExtBandTokens;
+  if (p->window > 0 && group > 1 && kBlockM % group == 0 &&
       (long long)L->tokens + p->window - 1 <= kBandMaxCols &&
-      p->total_q >= (long long)kExtBandTokens * p->batch) {
+      (p->batch > kExtFindMax || span_tiles * p->heads_kv > L->slots) &&
+      p->total_q >= enough * p->batch) {
     L->band_rows = p->total_q + (long long)p->batch * (p->window - 1 + kGatherPad) + kGatherPad;
-    const long long span_tiles = p->total_q / L->tokens + (long long)p->batch;
     if (L->band_rows < (1ll << 30) && span_tiles * p->heads_kv < (1ll << 30)) {
       L->band_cols = (L->tokens + p->window - 1 + 15) / 16 * 16;
       L->n_items = (int)span_tiles;        // tiles that are listed
@@ -543,7 +553,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
     return st;
   const auto kernel = tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>;
   const unsigned grid = (unsigned)L.n_items * (unsigned)params->heads_kv;
-  if (!L.split && params->batch <= 32) {   // a lane a sequence: see ext_find
+  if (!L.split && params->batch <= kExtFindMax) {
     ep.items = nullptr;
     kernel<<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
     return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;

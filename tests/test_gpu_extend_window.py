@@ -1,5 +1,5 @@
-"""GPU parity of windowed attn_sink_extend calls with many new tokens a sequence,
-whose keys are gathered for the band kernel.  Tolerances: P and the values are
+"""GPU parity of windowed attn_sink_extend calls, of few tiles (the general kernel)
+and of many, whose keys are gathered for the band kernel.  Tolerances: P and the values are
 fp16 there (2^-11 each) and the output bf16 (2^-8), so those of the general
 kernel hold with room; the values' fp16 conversion is exact for bf16 numbers in
 the fp16 normal range, and below it off by 2^-25 at most."""
@@ -26,8 +26,12 @@ CASES = [  # name, new, lens, page, hq, hkv, window
 ]
 
 
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("name,new,lens,page,hq,hkv,window", CASES, ids=[c[0] for c in CASES])
-def test_windowed_chunks(name, new, lens, page, hq, hkv, window):
+def test_windowed_chunks(name, new, lens, page, hq, hkv, window, many):
+    if many:                               # more than 32 sequences
+        n = 12 if hq // hkv > 2 else 260
+        new, lens = new + [n] * 32, lens + [n + i * i for i in range(32)]
     c = _extend_case(len(name) + page, new, lens, page, hq, hkv)
     got = _run_extend(c, window)
     _clean()
@@ -55,19 +59,23 @@ def test_both_ways_agree():
 
 
 @pytest.mark.parametrize("page", [16, 12])
-def test_evicted_pages_and_rows_behind(page):
-    c = _extend_case(6, [70, 130], [900, 400], page, 8, 2, rows=256, evict=130 + 64)
-    out = torch.full((256, 8, 64), 7.0, dtype=BF, device=DEV)
-    lse = torch.full((8, 256), 7.0, device=DEV)
+@pytest.mark.parametrize("more", [0, 32])
+def test_evicted_pages_and_rows_behind(page, more):
+    c = _extend_case(6, [70, 130] + [9] * more, [900, 400] + [400] * more, page, 8, 2, rows=512,
+                     evict=130 + 64)
+    out = torch.full((512, 8, 64), 7.0, dtype=BF, device=DEV)
+    lse = torch.full((8, 512), 7.0, device=DEV)
     got = _run_extend(c, 64, out=out, lse=lse)
     _clean()
+    n = 200 + 9 * more
     _check_extend(got, oracle_extend(*c[:4], c[4].tolist(), c[5].tolist(), c[6], scale=0.125,
-                                     window=64), 200)
-    assert (out[200:] == 7).all() and (lse[:, 200:] == 7).all()
+                                     window=64), n)
+    assert (out[n:] == 7).all() and (lse[:, n:] == 7).all()
 
 
-def test_a_sequence_of_nan_keeps_to_itself():
-    c = _extend_case(9, [70, 70, 70], [300, 300, 300], 16, 8, 2)
+@pytest.mark.parametrize("more", [0, 32])
+def test_a_sequence_of_nan_keeps_to_itself(more):
+    c = _extend_case(9, [70, 70, 70] + [9] * more, [300, 300, 300] + [9] * more, 16, 8, 2)
     held = c[3][1][c[3][1] >= 0].long()
     c[1][held], c[2][held] = math.nan, math.nan
     got = _run_extend(c, 100)
@@ -81,7 +89,8 @@ def test_a_sequence_of_nan_keeps_to_itself():
 
 
 def test_inputs_out_of_range_are_reported():
-    c = list(_extend_case(8, [70, 100], [200, 190], 16, 8, 2, fill=0.0))
+    c = list(_extend_case(8, [70, 100] + [12] * 32, [200, 190] + [12] * 32, 16, 8, 2, fill=0.0))
+    cu = c[5]
     good = c[3].clone()
     c[3] = good.clone()
     c[3][0, 12] = c[1].shape[0] + 5
@@ -91,24 +100,27 @@ def test_inputs_out_of_range_are_reported():
     c[2][int(good[1, 11])] = 1e6
     _run_extend(c, 100)
     assert _code() == 0x400
-    for cu in ([0, 70, 4000], [0, 170, 100], [-4, 70, 170]):
-        c[5] = torch.tensor(cu, dtype=torch.int32)
+    for at, bad in ((2, 4000), (1, 300), (0, -4)):
+        c[5] = cu.clone()
+        c[5][at] = bad
         _run_extend(c, 100)
         assert _code() in (0x400, 0x800)
     c[2][int(good[1, 11])] = 0.0
-    c[5] = torch.tensor([0, 70, 170], dtype=torch.int32)
+    c[5] = cu
     _run_extend(c, 100)
     _clean()
 
 
-def test_captured_and_replayed():
-    cases = [_extend_case(20 + i, n, m, 16, 8, 2, rows=256, fill=0.0) for i, (n, m) in enumerate(
+@pytest.mark.parametrize("more", [0, 32])
+def test_captured_and_replayed(more):
+    cases = [_extend_case(20 + i, n + [9] * more, m + [9] * more, 16, 8, 2, rows=256 + 9 * more,
+                          fill=0.0) for i, (n, m) in enumerate(
         [([100, 30], [300, 40]), ([128, 128], [2000, 128]), ([0, 200], [0, 1999])])]
     pages, cols = max(c[1].shape[0] for c in cases), max(c[3].shape[1] for c in cases)
 
     def padded(c):
         kc = torch.zeros(pages, 16, 2, 64, dtype=BF)
-        vc, table = torch.zeros_like(kc), torch.full((2, cols), -1, dtype=torch.int32)
+        vc, table = torch.zeros_like(kc), torch.full((2 + more, cols), -1, dtype=torch.int32)
         kc[:c[1].shape[0]], vc[:c[2].shape[0]], table[:, :c[3].shape[1]] = c[1], c[2], c[3]
         return (c[0], kc, vc, table, *c[4:])
 
