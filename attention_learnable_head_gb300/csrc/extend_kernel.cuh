@@ -23,9 +23,9 @@
 // the launch's work are split, so that a long cache with few new tokens fills
 // the GPU; the parts leave fp32 sums in the workspace and a third kernel joins
 // them and adds the sink.  The three are chained by programmatic dependent
-// launch.  Where the table or the window leaves too few keys for a tile to be cut
-// there is no join, and up to 32 sequences need no schedule either: each CTA finds
-// its tile (5 new tokens on 10 keys: 7.5 us, 14.4 with all three).
+// launch.  Where the table or the window leaves a tile too few keys for a cut to
+// pay there is no join, and up to 128 sequences need no schedule either: each CTA
+// finds its tile (5 new tokens on 10 keys: 7.5 us, 14.4 with all three).
 //
 // The rest is the forward kernel's pipeline: S = Q K^T into TMEM, online
 // softmax by two warpgroups (one per key half), P to TMEM, O += P V with P
@@ -43,6 +43,7 @@ constexpr int kExtThreads = 320;           // 8 softmax warps, copy warp, MMA wa
 constexpr int kExtMaxGroup = 128;
 constexpr int kExtMaxSplits = 64;          // parts of a tile
 constexpr int kExtMinBlocks = 4;           // key blocks of a part
+constexpr int kExtFindMax = 128;           // sequences of a single launch
 constexpr int kExtTries = 24;              // candidates for the cut, up to 3 rounds of CTAs
 constexpr int kExtOver = 5;                // what a CTA costs beside its blocks, in blocks
 constexpr int kExtSchedThreads = 1024;
@@ -147,16 +148,30 @@ __device__ __forceinline__ ExtItem ext_item(const ExtParams& p, const ExtSeq& s,
   return it;
 }
 
-// Without a list (items null: up to 32 sequences, tiles that are not cut): item i
-// is the i-th tile of the batch, found by every warp for itself.
+// Without a list (items null: up to kExtFindMax sequences, tiles that are not cut):
+// item i is the i-th tile of the batch, found by every warp for itself.  A lane
+// holds up to four neighbouring sequences.
 __device__ __forceinline__ ExtItem ext_find(const ExtParams& p, int i, bool record) {
   const int lane = threadIdx.x & 31;
+  const int each = (p.batch + 31) >> 5;
+  static_assert(kExtFindMax == 4 * 32, "four sequences a lane");
   bool bad = false;
-  ExtSeq s{0, 0, 0};
-  if (lane < p.batch) s = ext_seq(p, lane, &bad);
+  ExtSeq s[4];
+  // < 2^30 tiles each; sums stay there too: for a cu_seqlens that ascends they do by
+  // themselves, others have been recorded
+  int tiles = 0, before[4];
+  #pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int b = lane * each + u;
+    s[u] = ExtSeq{0, 0, 0};
+    if (u < each && b < p.batch) s[u] = ext_seq(p, b, &bad);
+  }
+  #pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    before[u] = tiles;
+    tiles = min(tiles + (s[u].n + p.tokens - 1) / p.tokens, 1 << 30);
+  }
   if (bad && record) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-  // < 2^27 tiles a sequence; more than the grid has are not asked for
-  const int tiles = (s.n + p.tokens - 1) / p.tokens;
   int upto = tiles;
   #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -167,13 +182,29 @@ __device__ __forceinline__ ExtItem ext_find(const ExtParams& p, int i, bool reco
   ExtItem it;
   it.num = -1;
   if (after == 0) return it;
-  const int b = __ffs(after) - 1;
-  ExtSeq x;
-  x.q0 = __shfl_sync(0xffffffffu, s.q0, b);
-  x.n = __shfl_sync(0xffffffffu, s.n, b);
-  x.len = __shfl_sync(0xffffffffu, s.len, b);
-  const int tile = i - __shfl_sync(0xffffffffu, upto - tiles, b);
-  return ext_item(p, x, b, tile, 0, 1, 0);
+  const int who = __ffs(after) - 1;
+  const int j = i - __shfl_sync(0xffffffffu, upto - tiles, who);   // tile of that lane's
+  int u = 0;
+  #pragma unroll
+  for (int v = 1; v < 4; ++v)
+    if (__shfl_sync(0xffffffffu, before[v], who) <= j &&
+        __shfl_sync(0xffffffffu, s[v].n, who) > 0)
+      u = v;
+  ExtSeq x{0, 0, 0};
+  int tile = 0;
+  #pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int q0 = __shfl_sync(0xffffffffu, s[v].q0, who);
+    const int n = __shfl_sync(0xffffffffu, s[v].n, who);
+    const int len = __shfl_sync(0xffffffffu, s[v].len, who);
+    const int at = __shfl_sync(0xffffffffu, before[v], who);
+    if (v == u) {
+      x = ExtSeq{q0, n, len};
+      tile = j - at;
+    }
+  }
+  if ((long long)tile * p.tokens >= x.n) return it;        // sums that were cut off
+  return ext_item(p, x, who * each + u, tile, 0, 1, 0);
 }
 
 // Parts of a tile of `blocks` blocks, of at least c blocks each (rounded up).
@@ -293,8 +324,8 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
   s_tiles[tid] = tiles;                    // of the last (mostly the only) round
   s_blocks[tid] = blocks;
   __syncthreads();
-  int chunk;
-  {
+  int chunk = 1 << 24;                     // > any tile's blocks
+  if (p.max_parts > 0) {
     // warp i tries candidate i; with several rounds of sequences they go through
     // shared memory again
     const unsigned long long per = s_work * (unsigned)p.heads_kv;

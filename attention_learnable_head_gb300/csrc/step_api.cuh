@@ -121,7 +121,17 @@ struct ExtendLayout {
 // 10.7 and 9.2; 8 + 1 heads, 64 x 8 11.7 and 14.4; W = 100, 16 + 8 heads: 128 x 64
 // 52 and 46, 128 x 200 95 and 108; W = 40, 8 + 8 heads: 128 x 200 72 and 68.
 constexpr int kExtBandTokens = 8;
-constexpr int kExtFindMax = 32;    // sequences of a single launch: a lane each
+
+// Tiles that see few blocks of keys are left whole: cutting them costs a schedule, a
+// join and the parts' sums on their way through memory, 8 us at the least.  Few or
+// many blocks, whether there are kExtWholeCtas tiles x kv heads.  Device time whole
+// and cut: 1 x 1 token (8 CTAs) on 900 keys 15 and 18 us, on 1200 16.5 and 16.8, on
+// 2400 26 and 17.5; 8 x 1 (64 CTAs) on 1800 22.4 and 22.1, on 2400 26 and 22.5; 1 x
+// 256 (128 CTAs) on 2400 27 and 39; 32 x 1 (256 CTAs) on 2400 31 and 41; 32 x 256
+// (4096 CTAs) on 2400 258 and 264.
+constexpr int kExtWholeCtas = 100;
+constexpr int kExtWholeFew = 10;
+constexpr int kExtWholeMany = 20;
 
 constexpr int kExtCtasPerSm = 2;   // shared memory, TMEM and registers allow two
 
@@ -141,13 +151,16 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   L->tokens = kBlockM / group;
   L->slots = kExtCtasPerSm * sms;
   const long long shares = (3 * L->slots + p->heads_kv - 1) / p->heads_kv;
-  // tiles that see so few keys are not cut: kExtMinBlocks blocks of them at most,
-  // as the table is no wider or as the window touches no more
-  const long long seen = p->window > 0 ? (long long)p->window + L->tokens - 1 : LLONG_MAX / 2;
-  L->split = (long long)p->max_pages * p->page_size > kExtMinBlocks * kBlockN &&
-             (seen + kBlockN - 2) / kBlockN + 1 > kExtMinBlocks;
+  // Blocks of keys that a tile sees at most, as the table is no wider or the window
+  // touches no more; whether the tiles are cut.
+  const long long span_tiles = p->total_q / L->tokens + (long long)p->batch;
+  const long long most =
+      std::min(((long long)p->max_pages * p->page_size + kBlockN - 1) / kBlockN,
+               p->window > 0 ? ((long long)p->window + L->tokens + kBlockN - 3) / kBlockN + 1
+                             : LLONG_MAX);
+  L->split = most > (span_tiles * p->heads_kv < kExtWholeCtas ? kExtWholeFew : kExtWholeMany);
   // the bounds of attn_sink_extend_plan_kernel
-  const long long items = p->total_q / L->tokens + (long long)p->batch + (L->split ? shares : 0);
+  const long long items = span_tiles + (L->split ? shares : 0);
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
   L->n_items = (int)items;
   L->max_parts = L->split ? (int)std::min<long long>(items, 2 * shares) : 0;
@@ -162,7 +175,6 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
   off += align256(parts * kBlockM * kHeadDim * sizeof(float));
   L->total = off;
   L->band_cols = 0;
-  const long long span_tiles = p->total_q / L->tokens + (long long)p->batch;
   const long long enough = group == 2 ? 2 * L->tokens : kExtBandTokens;
   if (p->window > 0 && group > 1 && kBlockM % group == 0 &&
       (long long)L->tokens + p->window - 1 <= kBandMaxCols &&

@@ -188,8 +188,8 @@ size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
  * from fp32 probabilities.  For O = P v they are rounded to bf16 next to the bf16
  * values.  With a window that the band kernel of attn_sink_fwd covers (128 / G +
  * W - 1 <= 176 keys, G > 1 a power of two), 8 new tokens a sequence on average
- * (256 / G where G = 2) and more than 32 sequences or more tiles than the GPU holds
- * at once, they are rounded to fp16 next to fp16 copies of the values, which have
+ * (128 where G = 2) and more than 128 sequences or more tiles than the GPU holds at
+ * once, they are rounded to fp16 next to fp16 copies of the values, which have
  * to lie within the fp16 range there (|v| <= 65504, else 0x400 is recorded, as by
  * attn_sink_fwd).
  * A length outside [0, max_pages * page_size] is clamped, the keys of a

@@ -1,7 +1,7 @@
-"""extend where the table holds 512 keys at most: no tile is cut, so up to 32
-sequences are one launch whose CTAs find their tiles, and more have a schedule but
-no join.  A wider table with the same pages takes the general way: the same tiles,
-the same bits."""
+"""extend where the table holds few keys (1280, or 2560 with many tiles): no tile is
+cut, so up to 128 sequences are one launch whose CTAs find their tiles, and more
+have a schedule but no join.  A wider table with the same pages takes the general
+way: tiles of four blocks of keys are not cut there either and give the same bits."""
 import math
 
 import pytest
@@ -15,8 +15,8 @@ pytestmark = pytest.mark.gpu
 
 
 def _wide(c, page):
-    """The same call with a table of more than 512 keys."""
-    more = torch.full((len(c[4]), 512 // page + 1), -1, dtype=torch.int32)
+    """The same call with a table of more than 2560 keys."""
+    more = torch.full((len(c[4]), 2560 // page + 1), -1, dtype=torch.int32)
     return (*c[:3], torch.cat([c[3], more], 1), *c[4:])
 
 
@@ -35,17 +35,25 @@ CASES = [  # new, lens, page, hq, hkv, window
     ([17] * 33, [min(512, 16 * i + 15) for i in range(33)], 16, 16, 2, 0),
     ([0] * 31 + [9], [0] * 31 + [9], 8, 8, 1, 0),
     ([2, 1] * 40, [400, 90] * 40, 32, 64, 8, 0),
+    ([3, 0, 20] * 42 + [1, 17], [400, 5, 90] * 42 + [1, 512], 32, 16, 2, 0),
+    ([3, 0, 20] * 43, [400, 5, 90] * 43, 32, 16, 2, 0),
+    ([0] * 70 + [40] + [0] * 30, [3] * 70 + [500] + [0] * 30, 16, 8, 1, 0),
+    ([5, 17, 1], [1280, 1153, 1025], 16, 8, 2, 0),
+    ([1, 33], [1200, 1270], 8, 8, 1, 1000),
+    ([256] * 8, [2400 + 20 * i for i in range(8)], 64, 8, 2, 0),
+    ([10] * 50, [100 + 49 * i for i in range(50)], 16, 32, 4, 0),
+    ([10] * 130, [100 + 18 * i for i in range(130)], 16, 4, 4, 0),
 ]
 
 
 @pytest.mark.parametrize("new,lens,page,hq,hkv,window", CASES)
 def test_small_tables(new, lens, page, hq, hkv, window):
     c = _extend_case(page + len(new), new, lens, page, hq, hkv)
-    assert c[3].shape[1] * page <= 512
     got, n = _launches(lambda: _run_extend(c, window))
     general, m = _launches(lambda: _run_extend(_wide(c, page), window))
-    if window == 0:
-        assert (n, m) == (1 if len(new) <= 32 else 2, 3)
+    # the windows here are narrow enough for whole tiles
+    assert (n, m) == (1 if len(new) <= 128 else 2, 1 if window else 3)
+    if max(lens) <= 512:
         assert torch.equal(got[0], general[0]) and torch.equal(got[1], general[1])
     _check_extend(got, oracle_extend(*c[:4], c[4].tolist(), c[5].tolist(), c[6], scale=0.125,
                                      window=window), sum(new))

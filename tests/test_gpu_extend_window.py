@@ -29,9 +29,9 @@ CASES = [  # name, new, lens, page, hq, hkv, window
 @pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("name,new,lens,page,hq,hkv,window", CASES, ids=[c[0] for c in CASES])
 def test_windowed_chunks(name, new, lens, page, hq, hkv, window, many):
-    if many:                               # more than 32 sequences
-        n = 12 if hq // hkv > 2 else 260
-        new, lens = new + [n] * 32, lens + [n + i * i for i in range(32)]
+    if many:                               # more than 128 sequences
+        n = 12 if hq // hkv > 2 else 130
+        new, lens = new + [n] * 130, lens + [n + i * i % 1000 for i in range(130)]
     c = _extend_case(len(name) + page, new, lens, page, hq, hkv)
     got = _run_extend(c, window)
     _clean()
@@ -59,12 +59,12 @@ def test_both_ways_agree():
 
 
 @pytest.mark.parametrize("page", [16, 12])
-@pytest.mark.parametrize("more", [0, 32])
+@pytest.mark.parametrize("more", [0, 130])
 def test_evicted_pages_and_rows_behind(page, more):
-    c = _extend_case(6, [70, 130] + [9] * more, [900, 400] + [400] * more, page, 8, 2, rows=512,
+    c = _extend_case(6, [70, 130] + [9] * more, [900, 400] + [400] * more, page, 8, 2, rows=1536,
                      evict=130 + 64)
-    out = torch.full((512, 8, 64), 7.0, dtype=BF, device=DEV)
-    lse = torch.full((8, 512), 7.0, device=DEV)
+    out = torch.full((1536, 8, 64), 7.0, dtype=BF, device=DEV)
+    lse = torch.full((8, 1536), 7.0, device=DEV)
     got = _run_extend(c, 64, out=out, lse=lse)
     _clean()
     n = 200 + 9 * more
@@ -73,7 +73,7 @@ def test_evicted_pages_and_rows_behind(page, more):
     assert (out[n:] == 7).all() and (lse[:, n:] == 7).all()
 
 
-@pytest.mark.parametrize("more", [0, 32])
+@pytest.mark.parametrize("more", [0, 130])
 def test_a_sequence_of_nan_keeps_to_itself(more):
     c = _extend_case(9, [70, 70, 70] + [9] * more, [300, 300, 300] + [9] * more, 16, 8, 2)
     held = c[3][1][c[3][1] >= 0].long()
@@ -89,7 +89,7 @@ def test_a_sequence_of_nan_keeps_to_itself(more):
 
 
 def test_inputs_out_of_range_are_reported():
-    c = list(_extend_case(8, [70, 100] + [12] * 32, [200, 190] + [12] * 32, 16, 8, 2, fill=0.0))
+    c = list(_extend_case(8, [70, 100] + [12] * 130, [200, 190] + [12] * 130, 16, 8, 2, fill=0.0))
     cu = c[5]
     good = c[3].clone()
     c[3] = good.clone()
@@ -111,7 +111,7 @@ def test_inputs_out_of_range_are_reported():
     _clean()
 
 
-@pytest.mark.parametrize("more", [0, 32])
+@pytest.mark.parametrize("more", [0, 130])
 def test_captured_and_replayed(more):
     cases = [_extend_case(20 + i, n + [9] * more, m + [9] * more, 16, 8, 2, rows=256 + 9 * more,
                           fill=0.0) for i, (n, m) in enumerate(
