@@ -79,6 +79,20 @@ at::Tensor make(const at::Tensor& like, at::ScalarType type, at::IntArrayRef siz
   return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
 }
 
+// Tensors that live in one buffer, each at a multiple of 256 bytes: a call's small
+// outputs from one allocation (an allocation takes the host 0.7 us, a tensor on it
+// 0.1 us).
+int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+at::Tensor part(const at::Tensor& buffer, int64_t at, at::ScalarType type,
+                at::IntArrayRef sizes) {
+  const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+  auto impl = c10::make_intrusive<c10::TensorImpl>(
+      c10::TensorImpl::VIEW, c10::Storage(buffer.storage()), buffer.key_set(), meta);
+  impl->set_storage_offset(at / (int64_t)meta.itemsize());
+  impl->set_sizes_contiguous(sizes);
+  return at::Tensor(std::move(impl));
+}
+
 // An int argument in [INT_MIN, INT_MAX].
 bool integer(PyObject* o, int* out) {
   if (!PyLong_Check(o)) return false;
@@ -148,11 +162,14 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int st;
   {
     const Unlocked unlocked;
-    slots = make(*cached, at::kLong, {p.max_tokens});
-    positions = make(*cached, at::kInt, {p.max_tokens});
-    cu = make(*cached, at::kInt, {b + 1});
-    lens = make(*cached, at::kInt, {b});
-    needed = make(*cached, at::kInt, {1});
+    const int64_t at1 = padded(8ll * p.max_tokens), at2 = at1 + padded(4ll * p.max_tokens);
+    const int64_t at3 = at2 + padded(4 * (b + 1)), at4 = at3 + padded(4 * b);
+    const at::Tensor all = make(*cached, at::kByte, {at4 + 4});
+    slots = part(all, 0, at::kLong, {p.max_tokens});
+    positions = part(all, at1, at::kInt, {p.max_tokens});
+    cu = part(all, at2, at::kInt, {b + 1});
+    lens = part(all, at3, at::kInt, {b});
+    needed = part(all, at4, at::kInt, {1});
     st = f_plan(&p, data_as<int>(cached), data_as<int>(fresh), data_as<int>(free),
                 data_as<int>(table), data_as<long long>(&slots), data_as<int>(&positions),
                 data_as<int>(&cu), data_as<int>(&lens), data_as<int>(&needed),
@@ -296,8 +313,9 @@ PyObject* qkv_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     size_t bytes = 0;
     dqkv = make(*r.qkv, at::kBFloat16, {r.t, r.rows, 64});
     if (p.norm) {
-      dwq = make(*r.qkv, at::kFloat, {64});
-      dwk = make(*r.qkv, at::kFloat, {64});
+      const at::Tensor dw = make(*r.qkv, at::kFloat, {128});
+      dwq = part(dw, 0, at::kFloat, {64});
+      dwk = part(dw, 256, at::kFloat, {64});
       bytes = f_rope_ws(&p);
       ws = make(*r.qkv, at::kByte, {(int64_t)bytes});
     }

@@ -302,6 +302,9 @@ int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_l
       (params->max_tokens > 0 && (slots == nullptr || positions == nullptr)))
     return ATTN_SINK_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return ATTN_SINK_ERR_INVALID_ARG;
+  // CTAs read the lengths while others write seq_lens
+  if (params->batch > 0 && (seq_lens == cached_lens || seq_lens == new_lens))
+    return ATTN_SINK_ERR_INVALID_ARG;
   int sms = 0;
   int* err = nullptr;
   int st;

@@ -70,7 +70,9 @@ typedef struct attn_sink_plan_params {
  * A second call with the same inputs gives the same plan.  Lengths are clamped
  * to [0, max_pages * page_size] and cu_seqlens to max_tokens; when free_pages
  * runs out the entries are -1.  Each of these records ATTN_SINK_DEVERR_PLAN.
- * No workspace; one launch.
+ * Sequences may share pages that are full (a common prefix), not one that is
+ * partly filled and gets new tokens.  Outputs must not overlap inputs: seq_lens
+ * in the place of cached_lens or new_lens is refused.  No workspace; one launch.
  */
 int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_lens,
                         const int* new_lens, const int* free_pages, int* block_table,
@@ -142,7 +144,8 @@ size_t attn_sink_qkv_rope_bwd_workspace_size(const attn_sink_rope_params* params
  * dk_in_stride, dv_in_stride: views of one packed gradient, or tensors of
  * their own) and, with norm = 1, the weights' gradients dq_weight and
  * dk_weight [64] fp32, summed in a fixed order (bitwise reproducible).  dv and
- * dv_in may both be NULL.  positions and inv_freq as in the forward.
+ * dv_in may both be NULL.  positions and inv_freq as in the forward.  Outputs
+ * must not overlap inputs.
  */
 int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, const void* k,
                            const int* positions, const float* inv_freq, const void* q_weight,
@@ -195,7 +198,8 @@ size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
  * A length outside [0, max_pages * page_size] is clamped, the keys of a
  * block-table entry outside [0, num_pages) are skipped (on the band kernel they
  * read as zero keys and values), and cu_seqlens_q is clamped to [0, T]; each is
- * recorded as 0x800.  The workspace is 256-byte aligned.  The result does not
+ * recorded as 0x800.  The workspace is 256-byte aligned.  out and lse must not
+ * overlap the inputs.  The result does not
  * depend on timing: the same inputs give the same bits.
  */
 int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const void* k_cache,

@@ -46,7 +46,7 @@ def _plan(p=(), **kw):
     f = dict(batch=4, page_size=16, num_pages=64, max_pages=8, num_free=10, max_tokens=32)
     f.update(p)
     a = dict(cached=FAKE, new=FAKE, free=FAKE, table=FAKE, slots=FAKE, pos=FAKE, cu=FAKE,
-             lens=FAKE, needed=FAKE)
+             lens=FAKE + 4096, needed=FAKE)
     a.update(kw)
     return binding.attn_sink_page_plan(binding.AttnSinkPlanParams(*f.values()), *a.values(),
                                        stream=0)
@@ -68,6 +68,11 @@ def test_plan_rejects_null_pointers(name):
 def test_plan_rejects_misaligned_slots_and_null_params():
     assert _plan(slots=FAKE + 4) == INVALID
     assert binding.attn_sink_page_plan(None, *[FAKE] * 9, stream=0) == INVALID
+
+
+@pytest.mark.parametrize("name", ["cached", "new"])
+def test_plan_rejects_lengths_in_place(name):
+    assert _plan(**{name: FAKE + 4096}) == INVALID
 
 
 # ----------------------------------------------------------------------------- rope
