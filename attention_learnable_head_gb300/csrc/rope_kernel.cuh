@@ -19,11 +19,14 @@
 // a time.  What keeps the memory busy is a ring of chunks of heads per warp in
 // shared memory, filled by bulk copies several chunks ahead and across tokens:
 // loads into registers (four steps ahead, then a wait) left 57 % of the time
-// waiting, and 16-byte cp.async cost 20 instructions a step.  A warp computes the 32 angles of a token once, one per lane, and keeps C and S
-// in shared memory for all heads of the token.  The angle is positions *
-// inv_freq / 2 pi in fp64, reduced to one turn there, so that the fp32 sine and
-// cosine of a position of a million are as exact as those of position one (an
-// fp32 product would be off by 0.06 radians).
+// waiting, and 16-byte cp.async cost 20 instructions a step.  A warp computes the
+// 32 angles of a token once, one per lane, and keeps C and S in shared memory for
+// all heads of the token.  The angle is positions * inv_freq / 2 pi; with the
+// factor's fraction of a turn as a 64-bit integer the product's upper bits are the
+// fraction that is left (whole turns drop out of the multiplication), so the fp32
+// sine and cosine of a position of a million are as exact as those of position one
+// (an fp32 product would be off by 0.06 radians).  The fp64 multiplication and
+// rounding this replaces took 2 to 3 % more with few heads a token.
 #pragma once
 #include <cuda_bf16.h>
 #include "sm103_ptx.cuh"
@@ -137,7 +140,8 @@ __device__ __forceinline__ float rope_weight(const void* w, int bf16, int d) {
 struct RopeLane {
   int sub, d0, d1;      // head of the step; dimensions of numbers 0-3 and 4-7
   int at0;              // place of numbers 0-3 in a table of 64 (4-7: at0 ^ 4)
-  double freq;
+  long long freq;       // pair `lane`'s turns a position, times 2^64 (without whole turns)
+  float bad;            // 0, NaN where inv_freq is not finite
 };
 template <bool kInter>
 __device__ __forceinline__ RopeLane rope_lane(const RopeParams& p, int lane) {
@@ -150,23 +154,24 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeParams& p, int lane) {
   r.d0 = odd ? hi : lo;
   r.d1 = odd ? lo : hi;
   r.at0 = 8 * j + (odd ? 4 : 0);
-  r.freq = lane < (p.rotary >> 1)
-               ? (double)__ldg(p.inv_freq + lane) * 0.15915494309189533577   // 1 / (2 pi)
-               : 0.0;
+  const float f = lane < (p.rotary >> 1) ? __ldg(p.inv_freq + lane) : 0.0f;
+  const double turns = (double)f * 0.15915494309189533577;                  // 1 / (2 pi)
+  r.freq = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);  // 2^64
+  r.bad = f - f;
   return r;
 }
 
 // C and S of a token in tables of 64: the numbers of lane j of an even head at 8 j
 // (rope_table_dim).  Lane i computes pair i.
 template <bool kInter>
-__device__ __forceinline__ void rope_angles(const RopeParams& p, int pos, int lane, double freq,
-                                            float* sC, float* sS) {
+__device__ __forceinline__ void rope_angles(const RopeParams& p, int pos, int lane,
+                                            const RopeLane& me, float* sC, float* sS) {
   __syncwarp();                            // the last token's heads have read C and S
   if (lane < (p.rotary >> 1)) {
-    double turns = (double)pos * freq;     // freq = inv_freq / 2 pi
-    turns -= rint(turns);
+    // positions are whole numbers: whole turns leave the 64 bits at the top
+    const int turns = (int)(((long long)pos * me.freq) >> 32);
     float s, c;
-    sincospif(2.0f * (float)turns, &s, &c);
+    sincospif((float)turns * 4.656612873077392578e-10f + me.bad, &s, &c);   // 2^-31
     s *= p.amplitude;
     c *= p.amplitude;
     const int a = kInter ? 2 * lane : (lane >> 2) * 8 + (lane & 3);
@@ -320,7 +325,7 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
   long long slot = p.slots ? __ldg(p.slots + t) : -1;
   const size_t kv_row = (size_t)p.heads_kv * 64;
   while (ok) {
-    rope_angles<kInter>(p, pos, lane, me.freq, sC, sS);
+    rope_angles<kInter>(p, pos, lane, me, sC, sS);
     if (slot < -1 || slot >= p.cache_rows) {
       if (lane == 0 && p.slots) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
       slot = -1;
@@ -508,7 +513,7 @@ attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
     pos = position(t);
   }
   while (ok) {
-    rope_angles<kInter>(p, pos, lane, me.freq, sC, sS);
+    rope_angles<kInter>(p, pos, lane, me, sC, sS);
     const unsigned ty = t + x.stride;
     if (ty < tokens) pos = position(ty);
     #pragma unroll 1

@@ -154,3 +154,33 @@ def test_two_gradients_at_once():
         for a, b in zip(got, alone):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     _clean()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_of_extreme_positions(interleaved):
+    """x = (1, 0) in every pair gives (cos, sin).  The angle is off by 2^-32 turns,
+    and by inv_freq / 2 pi in fp64 (2^-52, as the product of two roundings) times a
+    position of up to 2^31: 2^-21 turns, 2^-18 radians with the reference's own; the
+    sine and cosine by 2^-22, the result by half a bf16 step: eps / 2 = 2^-8 of it."""
+    pos = torch.tensor([0, 1, -1, 4097, 1_000_003, -99_999_999, 2 ** 31 - 1, -2 ** 31])
+    freq = torch.tensor([1.0, -1.0, 0.75, 2.0 ** -30, 1e-9, -0.3, 0.0, 3.0] + [0.5 ** i for i in
+                                                                                range(24)])
+    bad = {5: math.nan, 9: math.inf}
+    x = torch.zeros(len(pos), 3, 64)
+    a = torch.arange(32) * 2 if interleaved else torch.arange(32)
+    b = a + 1 if interleaved else a + 32
+    x[:, :, a] = 1.0
+    got = freq.clone()
+    for i, f in bad.items():
+        got[i] = f
+    q, k, v = binding.qkv_rope(x.to(BF).to(DEV), pos.int().to(DEV), got.to(DEV), heads_q=1,
+                               heads_kv=1, interleaved=interleaved)
+    angle = pos.double()[:, None] * freq.double()
+    keep = torch.tensor([i not in bad for i in range(32)])
+    for y in (q[:, 0].cpu().double(), k[:, 0].cpu().double()):
+        for d, ref in ((a, angle.cos()), (b, angle.sin())):
+            err = (y[:, d] - ref).abs()[:, keep]
+            assert (err <= 2.0 ** -8 * ref.abs()[:, keep] + 2.0 ** -17).all(), err.max()
+            assert y[:, d][:, ~keep].isnan().all()
+    assert torch.equal(v[:, 0].cpu(), x[:, 2].to(BF))
+    _clean()
