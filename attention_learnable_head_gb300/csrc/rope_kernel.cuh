@@ -40,14 +40,25 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 // measured copy rate 198) with 5 x 8 x 2 or 3 x 16 x 3, and 214 to 254 with more
 // or larger copies in flight, which set the reads against the writes; the
 // gradient 296 us (floor 287) with 4 x 8 x 3 and 317 to 380 with smaller chunks
-// or more CTAs.  Of 16 + 2 + 2 heads, where a token's angles and its half-filled
-// steps of k weigh more, the forward takes 83 us (floor 49).
+// or more CTAs.
 constexpr int kRopeCtas = 5;       // resident CTAs per SM, forward
 constexpr int kRopeChunk = 8;      // heads of a bulk copy
 constexpr int kRopeDepth = 2;      // chunks in a warp's ring
 constexpr int kRopeBwdCtas = 4;    // and of the gradient
 constexpr int kRopeBwdChunk = 8;
 constexpr int kRopeBwdDepth = 3;
+// Where a warp's share of a token is this many heads of q, k and v together or less,
+// a stage of the ring takes them all, with one wait for the three tensors (kWhole): a
+// token of few heads is bound by instructions (750 for 5 + 1 + 1 heads with a wait for
+// each tensor) and few tokens by the chain of waits.  Whole and by chunks: 65536
+// tokens of 8 + 1 + 1 heads 61 and 69 us, of 10 + 2 + 2 58 and 79, of 16 + 2 + 2 60
+// and 82, of 20 + 4 + 4 85 and 94, of 16 + 8 + 8 (not taken) 98 and 92; 64 tokens 4.3
+// and 5.1.  The gradient, 10 + 2 + 2 heads 83 and 113, 8 + 1 + 1 73 and 95; its stages
+// hold dy too and have to fit 48 KB with four warps.
+constexpr int kRopeWhole = 28;
+constexpr int kRopeBwdWhole = 14;      // of the gradient, dy in bf16
+constexpr int kRopeBwdWholeFp32 = 8;
+constexpr int kRopeWholeDepth = 2;
 
 struct RopeParams {
   const __nv_bfloat16* q;      // [T] rows of q_stride elements
@@ -240,18 +251,21 @@ __device__ __forceinline__ RopePart rope_part(const RopeParams& p, int warp) {
 // A copy did not land within the wait limit: record it, and give those in flight
 // (chunks used - 1 .. issued - 1) time to land before the CTA leaves its memory.
 __device__ __forceinline__ void rope_give_up(const RopeParams& p, uint64_t* full, int used,
-                                             int issued, int depth = kRopeDepth) {
+                                             int issued, int depth) {
   atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 9);
   for (int i = used - 1; i < issued; ++i) mbar_wait(&full[i % depth], (i / depth) & 1, nullptr);
 }
 
-template <bool kNorm, bool kInter>
+template <bool kNorm, bool kInter, bool kWhole>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kDepth = kWhole ? kRopeWholeDepth : kRopeDepth;
+  // a step of four heads may read three behind the last
+  constexpr int kStage = (kWhole ? kRopeWhole + 4 : kRopeChunk) * 128;
   __shared__ __align__(16) float s_w[2][2][64];            // q, k: weight, the other number's
   __shared__ __align__(16) float s_cs[kRopeWarps][2][64];
-  __shared__ __align__(128) uint8_t s_ring[kRopeWarps][kRopeDepth][kRopeChunk * 128];
-  __shared__ __align__(8) uint64_t s_full[kRopeWarps][kRopeDepth];
+  __shared__ __align__(128) uint8_t s_ring[kRopeWarps][kDepth][kStage];
+  __shared__ __align__(8) uint64_t s_full[kRopeWarps][kDepth];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RopeLane me = rope_lane<kInter>(p, lane);
   const int j8 = 8 * (lane & 7);
@@ -269,7 +283,7 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
     sS[d] = 0.0f;
   }
   if (lane == 0) {
-    for (int i = 0; i < kRopeDepth; ++i) mbar_init(&s_full[warp][i], 1);
+    for (int i = 0; i < kDepth; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbarrier_init();
   }
   __syncthreads();
@@ -285,7 +299,24 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
   unsigned ft = t;
   int fk = -1, left = 0, issued = 0;
   const __nv_bfloat16* src = nullptr;
+  const int in_q = x.q1 - x.q0, in_k = with_kv ? x.k1 - x.k0 : 0;
+  const int in_v = with_v ? x.k1 - x.k0 : 0;
   auto fetch = [&]() {
+    if constexpr (kWhole) {
+      if (ft >= tokens) return;
+      const int st = issued % kDepth;
+      uint8_t* to = s_ring[warp][st];
+      uint64_t* bar = &s_full[warp][st];
+      mbar_arrive_expect_tx(bar, (in_q + in_k + in_v) * 128);
+      if (in_q > 0) bulk_load(to, p.q + (size_t)ft * p.q_stride + x.q0 * 64, in_q * 128, bar);
+      to += in_q * 128;
+      if (in_k > 0) bulk_load(to, p.k + (size_t)ft * p.k_stride + x.k0 * 64, in_k * 128, bar);
+      to += in_k * 128;
+      if (in_v > 0) bulk_load(to, p.v + (size_t)ft * p.v_stride + x.k0 * 64, in_v * 128, bar);
+      ft += x.stride;
+      ++issued;
+      return;
+    }
     while (left == 0) {
       if (++fk == 3) {
         fk = 0;
@@ -297,7 +328,7 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
             : fk == 1 ? p.k + (size_t)ft * p.k_stride + x.k0 * 64
                       : p.v + (size_t)ft * p.v_stride + x.k0 * 64;
     }
-    const int n = min(left, kRopeChunk), st = issued % kRopeDepth;
+    const int n = min(left, kRopeChunk), st = issued % kDepth;
     mbar_arrive_expect_tx(&s_full[warp][st], n * 128);
     bulk_load(s_ring[warp][st], src, n * 128, &s_full[warp][st]);
     src += n * 64;
@@ -305,15 +336,15 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
     ++issued;
   };
   if (lane == 0)
-    for (int i = 0; i < kRopeDepth - 1; ++i) fetch();
+    for (int i = 0; i < kDepth - 1; ++i) fetch();
   // The next chunk has landed; the stage before it may be filled again.
   int used = 0;
   bool ok = true;
   auto next = [&]() -> const uint8_t* {
     __syncwarp();                                          // the last chunk has been read
     if (lane == 0) fetch();
-    const int st = used % kRopeDepth;
-    ok = mbar_wait_warp(&s_full[warp][st], (used / kRopeDepth) & 1, nullptr);
+    const int st = used % kDepth;
+    ok = mbar_wait_warp(&s_full[warp][st], (used / kDepth) & 1, nullptr);
     ++used;
     return s_ring[warp][st];
   };
@@ -336,6 +367,11 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
     if (ty < tokens) {
       pos = position(ty);
       if (p.slots) slot = __ldg(p.slots + ty);
+    }
+    const uint8_t* token = nullptr;                        // kWhole: the token's heads
+    if constexpr (kWhole) {
+      token = next();
+      if (!ok) break;
     }
     #pragma unroll
     for (int which = 0; which < 2; ++which) {              // q, then k
@@ -360,9 +396,9 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
         if (here >= 0) dst2 = p.k_cache + (size_t)here * kv_row + (h0 + me.sub) * 64;
       }
       while (heads > 0 && ok) {
-        const uint8_t* at = next() + me.sub * 128;
+        const uint8_t* at = (kWhole ? token + (which ? in_q * 128 : 0) : next()) + me.sub * 128;
         if (!ok) break;
-        const int n = min(heads, kRopeChunk);
+        const int n = kWhole ? heads : min(heads, kRopeChunk);
         heads -= n;
         #pragma unroll 2
         for (int h = 0; h < n; h += 4, at += 512) {
@@ -397,9 +433,9 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
       }
     }
     for (int heads = with_v ? x.k1 - x.k0 : 0, h0 = x.k0; heads > 0 && ok;) {
-      const uint8_t* at = next();
+      const uint8_t* at = kWhole ? token + (in_q + in_k) * 128 : next();
       if (!ok) break;
-      const int n = min(heads, kRopeChunk);
+      const int n = kWhole ? heads : min(heads, kRopeChunk);
       for (int h = me.sub; h < n; h += 4) {
         const uint4 r = *reinterpret_cast<const uint4*>(at + h * 128 + 2 * j8);
         const size_t off = (size_t)(h0 + h) * 64 + j8;
@@ -412,20 +448,22 @@ attn_sink_rope_kernel(const __grid_constant__ RopeParams p) {
     t = ty;
     if (t >= tokens) break;
   }
-  if (!ok && lane == 0) rope_give_up(p, s_full[warp], used, issued);
+  if (!ok && lane == 0) rope_give_up(p, s_full[warp], used, issued, kDepth);
 }
 
-template <bool kNorm, bool kInter, bool kFp32>
+template <bool kNorm, bool kInter, bool kFp32, bool kWhole>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
 attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kDyHead = kFp32 ? 256 : 128;               // bytes of a head of dy
-  constexpr int kDy = kRopeBwdChunk * kDyHead;             // of a chunk; then x
-  constexpr int kDepth = kRopeBwdDepth;
+  // heads of a stage (a step of four may read three behind the last), dy and then x
+  constexpr int kHeads = kWhole ? (kFp32 ? kRopeBwdWholeFp32 : kRopeBwdWhole) + 3 : kRopeBwdChunk;
+  constexpr int kDy = kHeads * kDyHead;
+  constexpr int kDepth = kWhole ? kRopeWholeDepth : kRopeBwdDepth;
   __shared__ __align__(16) float s_w[2][64];
   __shared__ __align__(16) float s_cs[kRopeWarps][2][64];
   __shared__ __align__(16) float s_dw[2][kRopeWarps][32][8];   // each lane's sums, q and k
   __shared__ __align__(128) uint8_t
-      s_ring[kRopeWarps][kDepth][kDy + (kNorm ? kRopeBwdChunk * 128 : 0)];
+      s_ring[kRopeWarps][kDepth][kDy + (kNorm ? kHeads * 128 : 0)];
   __shared__ __align__(8) uint64_t s_full[kRopeWarps][kDepth];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RopeLane me = rope_lane<kInter>(p, lane);
@@ -457,7 +495,34 @@ attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   int fk = -1, left = 0, issued = 0, used = 0;
   const char* dy = nullptr;
   const __nv_bfloat16* src = nullptr;
+  const int in_q = x.q1 - x.q0, in_k = x.k1 - x.k0, in_v = with_v ? in_k : 0;
   auto fetch = [&]() {
+    if constexpr (kWhole) {
+      if (ft >= tokens) return;
+      const int st = issued % kDepth;
+      uint8_t* to = s_ring[warp][st];
+      uint64_t* bar = &s_full[warp][st];
+      auto load = [&](int at, const void* base, int heads, int h0, int n) {
+        if (n > 0)
+          bulk_load(to + at * kDyHead,
+                    static_cast<const char*>(base) + ((size_t)ft * heads + h0) * kDyHead,
+                    n * kDyHead, bar);
+      };
+      mbar_arrive_expect_tx(bar, (in_q + in_k + in_v) * kDyHead +
+                                     (kNorm ? (in_q + in_k) * 128 : 0));
+      load(0, p.dq, p.heads_q, x.q0, in_q);
+      load(in_q, p.dk, p.heads_kv, x.k0, in_k);
+      load(in_q + in_k, p.dv, p.heads_kv, x.k0, in_v);
+      if (kNorm) {
+        to += kDy;
+        if (in_q > 0) bulk_load(to, p.q + (size_t)ft * p.q_stride + x.q0 * 64, in_q * 128, bar);
+        to += in_q * 128;
+        if (in_k > 0) bulk_load(to, p.k + (size_t)ft * p.k_stride + x.k0 * 64, in_k * 128, bar);
+      }
+      ft += x.stride;
+      ++issued;
+      return;
+    }
     while (left == 0) {
       if (++fk == 3) {
         fk = 0;
@@ -516,6 +581,11 @@ attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
     rope_angles<kInter>(p, pos, lane, me, sC, sS);
     const unsigned ty = t + x.stride;
     if (ty < tokens) pos = position(ty);
+    const uint8_t* token = nullptr;        // kWhole: the token's heads
+    if constexpr (kWhole) {
+      token = next();
+      if (!ok) break;
+    }
     #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const Oct c = oct_load(sC, me.at0), s = oct_load(sS, me.at0);
@@ -529,12 +599,13 @@ attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
       __nv_bfloat16* dst = (which ? p.dk_in + (size_t)t * p.dk_in_stride
                                   : p.dq_in + (size_t)t * p.dq_in_stride) + (h0 + me.sub) * 64;
       while (heads > 0 && ok) {
-        const uint8_t* at = next();
+        const uint8_t* at = kWhole ? token : next();
         if (!ok) break;
-        const int n = min(heads, kRopeBwdChunk);
+        const int n = kWhole ? heads : min(heads, kRopeBwdChunk);
         heads -= n;
-        const uint8_t* ax = at + kDy + me.sub * 128;
-        at += me.sub * kDyHead;
+        const int first = (kWhole && which ? in_q : 0) + me.sub;
+        const uint8_t* ax = at + kDy + first * 128;
+        at += first * kDyHead;
         #pragma unroll 1
         for (int h = me.sub; h - me.sub < n; h += 4, at += 4 * kDyHead, ax += 512, dst += 256) {
           const bool on = h < n;           // heads behind the last: stale bytes
@@ -580,9 +651,9 @@ attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
       }
     }
     for (int heads = with_v ? x.k1 - x.k0 : 0, h0 = x.k0; heads > 0 && ok;) {
-      const uint8_t* at = next();
+      const uint8_t* at = kWhole ? token + (in_q + in_k) * kDyHead : next();
       if (!ok) break;
-      const int n = min(heads, kRopeBwdChunk);
+      const int n = kWhole ? heads : min(heads, kRopeBwdChunk);
       for (int h = me.sub; h < n; h += 4) {
         uint64_t e[4];
         four(at + h * kDyHead, j8, &e[0], &e[1]);

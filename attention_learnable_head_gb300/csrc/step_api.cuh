@@ -90,12 +90,31 @@ RopeParams rope_params(const attn_sink_rope_params* p) {
   return rp;
 }
 
+// Heads of q, k and v that a warp takes of a token at most (rope_share).
+long long rope_most(const attn_sink_rope_params* p, int parts) {
+  if (parts == 1) return p->heads_q + 2ll * p->heads_kv;
+  auto share = [&](int heads) { return 4ll * (((heads + 3) / 4 + parts - 1) / parts); };
+  return share(p->heads_q) + 2 * share(p->heads_kv);
+}
+
 template <bool kNorm, bool kInter>
-void rope_bwd_launch(const RopeParams& rp, dim3 grid, bool fp32, cudaStream_t s) {
-  if (fp32)
-    attn_sink_rope_bwd_kernel<kNorm, kInter, true><<<grid, kRopeThreads, 0, s>>>(rp);
+void rope_launch(const RopeParams& rp, dim3 grid, bool whole, cudaStream_t s) {
+  if (whole)
+    attn_sink_rope_kernel<kNorm, kInter, true><<<grid, kRopeThreads, 0, s>>>(rp);
   else
-    attn_sink_rope_bwd_kernel<kNorm, kInter, false><<<grid, kRopeThreads, 0, s>>>(rp);
+    attn_sink_rope_kernel<kNorm, kInter, false><<<grid, kRopeThreads, 0, s>>>(rp);
+}
+
+template <bool kNorm, bool kInter>
+void rope_bwd_launch(const RopeParams& rp, dim3 grid, bool fp32, bool whole, cudaStream_t s) {
+  if (fp32 && whole)
+    attn_sink_rope_bwd_kernel<kNorm, kInter, true, true><<<grid, kRopeThreads, 0, s>>>(rp);
+  else if (fp32)
+    attn_sink_rope_bwd_kernel<kNorm, kInter, true, false><<<grid, kRopeThreads, 0, s>>>(rp);
+  else if (whole)
+    attn_sink_rope_bwd_kernel<kNorm, kInter, false, true><<<grid, kRopeThreads, 0, s>>>(rp);
+  else
+    attn_sink_rope_bwd_kernel<kNorm, kInter, false, false><<<grid, kRopeThreads, 0, s>>>(rp);
 }
 
 // ----------------------------------------------------------------------------- extend
@@ -383,14 +402,15 @@ int attn_sink_qkv_rope(const attn_sink_rope_params* params, const void* q, const
   rp.err = err;
   const dim3 g = rope_grid(params, sms, kRopeCtas);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool whole = rope_most(params, (int)g.y) <= kRopeWhole;
   if (params->norm && params->interleaved)
-    attn_sink_rope_kernel<true, true><<<g, kRopeThreads, 0, s>>>(rp);
+    rope_launch<true, true>(rp, g, whole, s);
   else if (params->norm)
-    attn_sink_rope_kernel<true, false><<<g, kRopeThreads, 0, s>>>(rp);
+    rope_launch<true, false>(rp, g, whole, s);
   else if (params->interleaved)
-    attn_sink_rope_kernel<false, true><<<g, kRopeThreads, 0, s>>>(rp);
+    rope_launch<false, true>(rp, g, whole, s);
   else
-    attn_sink_rope_kernel<false, false><<<g, kRopeThreads, 0, s>>>(rp);
+    rope_launch<false, false>(rp, g, whole, s);
   return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 
@@ -464,14 +484,15 @@ int attn_sink_qkv_rope_bwd(const attn_sink_rope_params* params, const void* q, c
   rp.dw_part = static_cast<float*>(workspace);
   rp.err = err;
   const bool fp32 = params->grad_dtype == 1;
+  const bool whole = rope_most(params, (int)g.y) <= (fp32 ? kRopeBwdWholeFp32 : kRopeBwdWhole);
   if (params->norm && params->interleaved)
-    rope_bwd_launch<true, true>(rp, g, fp32, s);
+    rope_bwd_launch<true, true>(rp, g, fp32, whole, s);
   else if (params->norm)
-    rope_bwd_launch<true, false>(rp, g, fp32, s);
+    rope_bwd_launch<true, false>(rp, g, fp32, whole, s);
   else if (params->interleaved)
-    rope_bwd_launch<false, true>(rp, g, fp32, s);
+    rope_bwd_launch<false, true>(rp, g, fp32, whole, s);
   else
-    rope_bwd_launch<false, false>(rp, g, fp32, s);
+    rope_bwd_launch<false, false>(rp, g, fp32, whole, s);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   if (params->norm) {
     const RopeSum sum{rp.dw_part, dq_weight, dk_weight, (int)(g.x * g.y)};
