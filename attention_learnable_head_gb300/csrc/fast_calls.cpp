@@ -4,7 +4,7 @@
 // kernels take 3 to 10 us; with these steps in Python (ctypes, torch.empty) the
 // host took longer than they did.  A call, host and device, Python -> native:
 // page_plan of 128 sequences 28 -> 6.2 us, qkv_rope of 128 tokens into the pages
-// 22 -> 8.2 us, qkv_rope_backward with norm 43 -> 11.9 us; the larger calls, bound
+// 22 -> 6.3 us, qkv_rope_backward with norm 43 -> 11.9 us; the larger calls, bound
 // by their kernels, are as before.
 //
 // Only the plain case is handled here: CUDA tensors of the current device, on its
