@@ -33,6 +33,13 @@
 // holds bf16 values, and an fp16 product would need every value tile converted
 // by each CTA; one more rounding of 2^-8 next to that of the bf16 output.  The
 // row sums add the fp32 probabilities.
+//
+// With full tiles a CTA's chain bounds it, 2400 clocks per 128 keys (S from TMEM 300,
+// maximum and its exchange 550, 64 exponentials a thread and P 1300, waits 250), two
+// CTAs an SM: 4 sequences of 8192 to 16384 keys with up to 1024 new tokens, 64 + 8
+// heads, take 760 us, 835 TFLOP/s.  With few tokens the cache does: 32 sequences of
+// 4096 to 8192 keys with up to 5 new tokens 91 us (393 MB, 58 us at the copy rate), 5
+// of them each for the schedule and the join.
 #pragma once
 #include <climits>
 #include "fwd_kernel.cuh"

@@ -84,7 +84,8 @@ attn_sink_gather_plan_kernel(const __grid_constant__ GatherParams g) {
     g.spans[t] = make_int4(0, 0, 0, 0);
 }
 
-// A thread copies 16 bytes of K and of V of a row.
+// A thread copies 16 bytes of K and of V of a row.  Bound by the latency of the table
+// entries and rows behind them: 8 sequences of 513 + 127 keys, 8 heads, 6.5 us.
 __global__ void __launch_bounds__(kGatherThreads)
 attn_sink_gather_kernel(const __grid_constant__ GatherParams g) {
   grid_dependency_wait();
