@@ -24,8 +24,8 @@
 // the GPU; the parts leave fp32 sums in the workspace and a third kernel joins
 // them and adds the sink.  The three are chained by programmatic dependent
 // launch.  Where the table or the window leaves a tile too few keys for a cut to
-// pay there is no join, and up to 128 sequences need no schedule either: each CTA
-// finds its tile (5 new tokens on 10 keys: 7.5 us, 14.4 with all three).
+// pay there is no join, and few CTAs of up to 128 sequences need no schedule either:
+// each finds its tile (5 new tokens on 10 keys: 7.5 us, 14.4 with all three).
 //
 // The rest is the forward kernel's pipeline: S = Q K^T into TMEM, online
 // softmax by two warpgroups (one per key half), P to TMEM, O += P V with P

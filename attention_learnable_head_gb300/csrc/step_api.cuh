@@ -122,6 +122,7 @@ struct ExtendLayout {
   int tokens;        // per tile
   int n_items, max_parts, max_tiles, slots;
   bool split;                              // tiles may be cut: a join
+  bool find;                               // no schedule: see ext_find
   size_t off_tiles, off_ml, off_o, total;
   // the band kernel's path (extend_window.cuh)
   int band_cols;     // 0: not taken
@@ -148,6 +149,12 @@ constexpr int kExtBandTokens = 8;
 // 2400 26 and 17.5; 8 x 1 (64 CTAs) on 1800 22.4 and 22.1, on 2400 26 and 22.5; 1 x
 // 256 (128 CTAs) on 2400 27 and 39; 32 x 1 (256 CTAs) on 2400 31 and 41; 32 x 256
 // (4096 CTAs) on 2400 258 and 264.
+//
+// Then a CTA finds its tile by itself, in a single launch, unless it is one of many:
+// the search costs each 1 us, the schedule kernel a call 4.  Found and listed, 8
+// sequences of 120 new tokens (40 + 8 heads, 264 CTAs) 10.5 and 13 us, 32 x 64 (648)
+// 22 and 23.4, 8 x 500 on 512 keys (1048) 41.8 and 40, 32 x 500 (3976) 139 and 127.
+constexpr int kExtFindRounds = 3;  // CTAs, in what the GPU holds at once
 constexpr int kExtWholeCtas = 100;
 constexpr int kExtWholeFew = 10;
 constexpr int kExtWholeMany = 20;
@@ -178,6 +185,8 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
                p->window > 0 ? ((long long)p->window + L->tokens + kBlockN - 3) / kBlockN + 1
                              : LLONG_MAX);
   L->split = most > (span_tiles * p->heads_kv < kExtWholeCtas ? kExtWholeFew : kExtWholeMany);
+  L->find = !L->split && p->batch <= kExtFindMax &&
+            span_tiles * p->heads_kv <= kExtFindRounds * (long long)L->slots;
   // the bounds of attn_sink_extend_plan_kernel
   const long long items = span_tiles + (L->split ? shares : 0);
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
@@ -589,7 +598,7 @@ int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const
     return st;
   const auto kernel = tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>;
   const unsigned grid = (unsigned)L.n_items * (unsigned)params->heads_kv;
-  if (!L.split && params->batch <= kExtFindMax) {
+  if (L.find) {
     ep.items = nullptr;
     kernel<<<grid, kExtThreads, kFwdSmemBytes, s>>>(ep);
     return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;

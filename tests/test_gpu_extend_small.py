@@ -1,6 +1,6 @@
 """extend where the table holds few keys (1280, or 2560 with many tiles): no tile is
-cut, so up to 128 sequences are one launch whose CTAs find their tiles, and more
-have a schedule but no join.  A wider table with the same pages takes the general
+cut, so up to 128 sequences (of tiles for a few rounds of CTAs) are one launch whose
+CTAs find their tiles, and more have a schedule but no join.  A wider table with the same pages takes the general
 way: tiles of four blocks of keys are not cut there either and give the same bits."""
 import math
 
@@ -43,6 +43,7 @@ CASES = [  # new, lens, page, hq, hkv, window
     ([256] * 8, [2400 + 20 * i for i in range(8)], 64, 8, 2, 0),
     ([10] * 50, [100 + 49 * i for i in range(50)], 16, 32, 4, 0),
     ([10] * 130, [100 + 18 * i for i in range(130)], 16, 4, 4, 0),
+    ([300] * 8, [320 + 20 * i for i in range(8)], 32, 64, 8, 0),
 ]
 
 
@@ -52,7 +53,8 @@ def test_small_tables(new, lens, page, hq, hkv, window):
     got, n = _launches(lambda: _run_extend(c, window))
     general, m = _launches(lambda: _run_extend(_wide(c, page), window))
     # the windows here are narrow enough for whole tiles
-    assert (n, m) == (1 if len(new) <= 128 else 2, 1 if window else 3)
+    listed = len(new) > 128 or sum(new) >= 2400
+    assert (n, m) == (2 if listed else 1, 1 if window else 3)
     if max(lens) <= 512:
         assert torch.equal(got[0], general[0]) and torch.equal(got[1], general[1])
     _check_extend(got, oracle_extend(*c[:4], c[4].tolist(), c[5].tolist(), c[6], scale=0.125,
