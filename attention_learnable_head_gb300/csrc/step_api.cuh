@@ -148,7 +148,8 @@ constexpr int kExtBandTokens = 8;
 // and cut: 1 x 1 token (8 CTAs) on 900 keys 15 and 18 us, on 1200 16.5 and 16.8, on
 // 2400 26 and 17.5; 8 x 1 (64 CTAs) on 1800 22.4 and 22.1, on 2400 26 and 22.5; 1 x
 // 256 (128 CTAs) on 2400 27 and 39; 32 x 1 (256 CTAs) on 2400 31 and 41; 32 x 256
-// (4096 CTAs) on 2400 258 and 264.
+// (4096 CTAs) on 2400 258 and 264.  Keys copied one by one take twice as long, so
+// half as many blocks: 1 x 2 tokens on 1100 keys in pages of one 26.5 whole, 19.9 cut.
 //
 // Then a CTA finds its tile by itself, in a single launch, unless it is one of many:
 // the search costs each 1 us, the schedule kernel a call 4.  Found and listed, 8
@@ -184,7 +185,8 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
       std::min(((long long)p->max_pages * p->page_size + kBlockN - 1) / kBlockN,
                p->window > 0 ? ((long long)p->window + L->tokens + kBlockN - 3) / kBlockN + 1
                              : LLONG_MAX);
-  L->split = most > (span_tiles * p->heads_kv < kExtWholeCtas ? kExtWholeFew : kExtWholeMany);
+  const int few = p->page_size % 8 == 0 ? kExtWholeFew : kExtWholeFew / 2;   // key by key
+  L->split = most > (span_tiles * p->heads_kv < kExtWholeCtas ? few : kExtWholeMany);
   L->find = !L->split && p->batch <= kExtFindMax &&
             span_tiles * p->heads_kv <= kExtFindRounds * (long long)L->slots;
   // the bounds of attn_sink_extend_plan_kernel

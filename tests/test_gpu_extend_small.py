@@ -44,6 +44,8 @@ CASES = [  # new, lens, page, hq, hkv, window
     ([10] * 50, [100 + 49 * i for i in range(50)], 16, 32, 4, 0),
     ([10] * 130, [100 + 18 * i for i in range(130)], 16, 4, 4, 0),
     ([300] * 8, [320 + 20 * i for i in range(8)], 32, 64, 8, 0),
+    ([5, 3], [640, 600], 1, 8, 2, 0),
+    ([5, 3], [640, 513], 20, 8, 2, 0),
 ]
 
 
