@@ -145,3 +145,44 @@ def test_another_stream_is_used():
     side.synchronize()
     assert (q == 1).all()
     _clean()
+
+
+def test_out_of_memory_is_an_exception():
+    """An allocation that fails in the native module raises torch's own error, and
+    the next call works."""
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    kw = dict(page_size=16, num_pages=4)
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.01)
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            binding.page_plan(one, one, one, one.view(1, 1), max_tokens=1 << 30, **kw)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert binding.page_plan(one, one, one, one.view(1, 1), max_tokens=1, **kw).slots.tolist() == [17]
+    _clean()
+
+
+def test_threads_share_the_module():
+    """Calls from several threads, each on a stream of its own."""
+    import threading
+
+    s = {k: _dev(v) for k, v in _rope_case(5, 400, 8, 2, 64, 1, True).items()}
+    want = binding.qkv_rope(**s, heads_q=8, heads_kv=2)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = binding.qkv_rope(**s, heads_q=8, heads_kv=2)
+            torch.cuda.current_stream().synchronize()
+            bad.extend(not torch.equal(a, b) for a, b in zip(got, want))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(bad) == 12 and not any(bad)
+    _clean()
