@@ -15,7 +15,9 @@ the workspace with torch and raise on a non-zero status.  The entry points of
 ``include/attn_sink_step.h`` (``attn_sink_page_plan``, ``attn_sink_qkv_rope``,
 ``attn_sink_qkv_rope_bwd``, ``attn_sink_extend`` and their workspace sizes) and
 their conveniences ``page_plan``, ``qkv_rope``, ``qkv_rope_backward``,
-``qkv_rope_autograd`` and ``extend`` come after them.  Every step of the
+``qkv_rope_autograd`` and ``extend`` come after them; a plain call of these goes
+through the native module ``attn_sink_fast`` (``csrc/fast_calls.cpp``) to the same
+entry points.  Every step of the
 computation runs in the library's CUDA kernels; there is no other code path,
 and loading fails loudly when the library has not been built.
 """
