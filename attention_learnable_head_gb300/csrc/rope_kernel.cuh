@@ -53,11 +53,11 @@ constexpr int kRopeBwdDepth = 3;
 // each tensor) and few tokens by the chain of waits.  Whole and by chunks: 65536
 // tokens of 8 + 1 + 1 heads 61 and 69 us, of 10 + 2 + 2 58 and 79, of 16 + 2 + 2 60
 // and 82, of 20 + 4 + 4 85 and 94, of 16 + 8 + 8 (not taken) 98 and 92; 64 tokens 4.3
-// and 5.1.  The gradient, 10 + 2 + 2 heads 83 and 113, 8 + 1 + 1 73 and 95; its stages
-// hold dy too and have to fit 48 KB with four warps.
+// and 5.1.  The gradient, 12 + 2 + 2 heads 83 and 113, 8 + 1 + 1 73 and 95, with fp32
+// gradients 75 and 97; its stages hold dy too and have to fit 48 KB with four warps.
 constexpr int kRopeWhole = 28;
-constexpr int kRopeBwdWhole = 14;      // of the gradient, dy in bf16
-constexpr int kRopeBwdWholeFp32 = 8;
+constexpr int kRopeBwdWhole = 17;      // of the gradient, dy in bf16
+constexpr int kRopeBwdWholeFp32 = 11;
 constexpr int kRopeWholeDepth = 2;
 
 struct RopeParams {
@@ -455,15 +455,18 @@ template <bool kNorm, bool kInter, bool kFp32, bool kWhole>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
 attn_sink_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kDyHead = kFp32 ? 256 : 128;               // bytes of a head of dy
-  // heads of a stage (a step of four may read three behind the last), dy and then x
-  constexpr int kHeads = kWhole ? (kFp32 ? kRopeBwdWholeFp32 : kRopeBwdWhole) + 3 : kRopeBwdChunk;
-  constexpr int kDy = kHeads * kDyHead;
+  // heads of a stage, dy and then x; a step of four may read three behind the last
+  // (of dy: from the x behind it)
+  constexpr int kHeads = kWhole ? (kFp32 ? kRopeBwdWholeFp32 : kRopeBwdWhole) : kRopeBwdChunk;
+  constexpr int kSlack = kWhole ? 3 : 0;
+  constexpr int kDy = (kHeads + (kNorm ? 0 : kSlack)) * kDyHead;
+  static_assert(!kNorm || !kWhole || kSlack * kDyHead <= kHeads * 128, "the x behind dy");
   constexpr int kDepth = kWhole ? kRopeWholeDepth : kRopeBwdDepth;
   __shared__ __align__(16) float s_w[2][64];
   __shared__ __align__(16) float s_cs[kRopeWarps][2][64];
   __shared__ __align__(16) float s_dw[2][kRopeWarps][32][8];   // each lane's sums, q and k
   __shared__ __align__(128) uint8_t
-      s_ring[kRopeWarps][kDepth][kDy + (kNorm ? kHeads * 128 : 0)];
+      s_ring[kRopeWarps][kDepth][kDy + (kNorm ? (kHeads + kSlack) * 128 : 0)];
   __shared__ __align__(8) uint64_t s_full[kRopeWarps][kDepth];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RopeLane me = rope_lane<kInter>(p, lane);
