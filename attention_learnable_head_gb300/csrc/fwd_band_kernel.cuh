@@ -293,8 +293,9 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
   // next item, before whose pass 1 a half rewrites its entry, needs P of this
   // item from every thread, i.e. after its partner read it.
   __shared__ float s_mx[2][kBlockM];
-  // kSum: the halves' sums.  Rewritten behind the next item's pair barrier, which
-  // a partner passes after it has read them.
+  // kSum: the halves' sums.  Both threads of a row read them before they arrive on
+  // o_free; the next item's overwrite them behind pv_done, and its product waits for
+  // all arrivals on o_free (no other barrier stands between in a CTA's last pass).
   __shared__ float s_sum[2][kSum ? kBlockM : 1];
 
   const int tid = threadIdx.x;
@@ -598,6 +599,8 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         const uint32_t lsum = tmem_ld_x1(tO - 32u * c + 64u);
         tmem_ld_wait();
         const float lt = __uint_as_float(lsum) + psink;
+        float lz = lt;
+        if constexpr (kSum) lz = s_sum[0][r] + s_sum[1][r] + psink;
         tc_fence_before();
         mbar_arrive(&o_free);
         const float inv_l = (lt > 0.0f) ? 1.0f / lt : 0.0f;
@@ -629,8 +632,6 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
                   make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
           }
         }
-        float lz = lt;
-        if constexpr (kSum) lz = s_sum[0][r] + s_sum[1][r] + psink;
         if (c == 0 && t < prem)
           p.lse[(size_t)h * p.total_q + row] = (lz > 0.0f) ? (pm + __log2f(lz)) * kLn2 : -INFINITY;
         if (whole) {

@@ -1,0 +1,40 @@
+"""Windowed attn_sink_extend calls on the band kernel (three launches: regions and
+tiles, gather, band kernel), each padded with sequences so that it is taken.
+Tolerances as in test_gpu_extend_window.py."""
+import math
+
+import pytest
+import torch
+
+from attention_learnable_head_gb300 import binding
+from oracle.step import oracle_extend
+from test_gpu_step import BF, DEV, _check_extend, _clean, _code, _extend_case, _run_extend
+
+pytestmark = pytest.mark.gpu
+
+
+def _band(run):
+    """What `run` returns; it has to be a call on the band kernel."""
+    n = binding.attn_sink_launch_count()
+    r = run()
+    assert binding.attn_sink_launch_count() - n == 3
+    return r
+
+
+def _oracle(c, window):
+    return oracle_extend(*c[:4], c[4].tolist(), c[5].tolist(), c[6], scale=0.125, window=window)
+
+
+def test_lse_of_partial_tiles_is_the_same_every_time():
+    """Every tile is partial and every CTA has several: the sums of a row's halves
+    must not be overwritten by the next tile's before both have been read, also in a
+    CTA's last pass."""
+    new = [8 + i % 7 for i in range(420)]
+    c = _extend_case(1, new, [n + i * 37 % 300 for i, n in enumerate(new)], 16, 16, 2)
+    d = [x.to(DEV) for x in c]
+    first = _band(lambda: binding.extend(*d, window=128))
+    _check_extend(first, _oracle(c, 128), sum(new))
+    for _ in range(300):
+        out, lse = binding.extend(*d, window=128)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    _clean()
