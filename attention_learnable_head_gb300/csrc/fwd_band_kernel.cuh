@@ -277,9 +277,13 @@ __device__ __forceinline__ void band_chunk_exp(uint32_t ts, uint32_t tp, uint64_
 }
 
 // Registers are split per SM sub-partition; two CTAs of 10 warps allow 102
-// per thread: 96 is used.  kSum: lse comes from the fp32 P (for callers that
-// promise an fp32 lse) instead of the row sum of the fp16 P, which moves it by up
-// to 2^-11; out is divided by the sum of the fp16 P in both.
+// per thread: 96 is used.  kSum (for callers that promise an fp32 lse, and a
+// precision that does not depend on the sink): lse comes from the fp32 P instead of
+// the row sum of the fp16 P, which moves it by up to 2^-11 (out is divided by the
+// sum of the fp16 P in both), and the maximum is that of the scores alone, so that P
+// keeps its bits below a large sink, which is joined in the epilogue: with
+// M = max(m, sink), Z = l 2^(m - M) + 2^(sink - M), out = O 2^(m - M) / Z,
+// lse = ln 2 (M + log2 Z).
 template <bool kSum>
 __global__ void __maxnreg__(96)
 attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
@@ -521,7 +525,8 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
     // left in its sequence from there, this row's max (log2 units)
     int pg = 0, ptok = 0, prem = 0;
     float pm = -INFINITY;
-    float psink = 0.0f;   // the previous item's sink term of the row sum, 2^(sink - m)
+    // the previous item's sink term of the row sum, 2^(sink - m); kSum: the sink (log2)
+    float psink = 0.0f;
     float psum = 0.0f;    // kSum: this half's sum of its P
     BandWalk w;
     w.start(p);
@@ -559,7 +564,8 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         ok = named_barrier_and(2 + (warp & 3), 64, got);
         if (ok) {
           const float sink_l2 = sink_h * kLog2e;          // -inf without a sink
-          m = fmaxf(fmaxf(mx, s_mx[c ^ 1][r]) * sl2, sink_l2);
+          m = fmaxf(mx, s_mx[c ^ 1][r]) * sl2;
+          if constexpr (!kSum) m = fmaxf(m, sink_l2);
           const float m_use = (m == -INFINITY) ? 0.0f : m;
           const uint64_t negm2 = f2(-m_use, -m_use);
 
@@ -575,7 +581,8 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full);
-          if (sink_h > -INFINITY) nsink = ex2_approx(sink_l2 - m_use);
+          if constexpr (kSum) nsink = sink_l2;
+          else if (sink_h > -INFINITY) nsink = ex2_approx(sink_l2 - m_use);
         } else {
           abort_flag = 1;
         }
@@ -598,12 +605,24 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         tmem_ld_x32(tO, o);
         const uint32_t lsum = tmem_ld_x1(tO - 32u * c + 64u);
         tmem_ld_wait();
-        const float lt = __uint_as_float(lsum) + psink;
-        float lz = lt;
-        if constexpr (kSum) lz = s_sum[0][r] + s_sum[1][r] + psink;
+        float lz = 0.0f;                        // kSum: the fp32 sum of P
+        if constexpr (kSum) lz = s_sum[0][r] + s_sum[1][r];
         tc_fence_before();
         mbar_arrive(&o_free);
-        const float inv_l = (lt > 0.0f) ? 1.0f / lt : 0.0f;
+        float lt = __uint_as_float(lsum), inv_l;
+        if constexpr (kSum) {
+          const float mf = fmaxf(pm, psink);
+          const float mb = (mf == -INFINITY) ? 0.0f : mf;
+          const float wk = ex2_approx(pm - mb), ws = ex2_approx(psink - mb);
+          lt = fmaf(lt, wk, ws);
+          lz = fmaf(lz, wk, ws);
+          inv_l = (lt > 0.0f) ? wk / lt : 0.0f;
+          pm = mb;
+        } else {
+          lt += psink;
+          lz = lt;
+          inv_l = (lt > 0.0f) ? 1.0f / lt : 0.0f;
+        }
         const bool whole = prem >= p.tokens;      // same for every row of the item
         const int h = pg * p.group + hh;
         const size_t row = (size_t)(ptok + t);

@@ -38,3 +38,15 @@ def test_lse_of_partial_tiles_is_the_same_every_time():
         out, lse = binding.extend(*d, window=128)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     _clean()
+
+
+def test_extreme_sinks():
+    """A sink far above the scores leaves the probabilities their bits: out is small, not
+    zero."""
+    c = list(_extend_case(2, [40] + [12] * 130, [300] + [12 + i for i in range(130)], 16, 8, 2))
+    c[6] = torch.tensor([-math.inf, 80.0, 30.0, 17.0, 12.0, 8.0, -30.0, 0.0])
+    got = _band(lambda: _run_extend(c, 100))
+    ref = _oracle(c, 100)
+    _check_extend(got, ref, 40 + 12 * 130)
+    assert got[0][:, 2].any() and got[0][:, 3].any() and (ref[0][:, 1].abs().max() > 0)
+    _clean()
