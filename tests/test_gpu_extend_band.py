@@ -50,3 +50,21 @@ def test_extreme_sinks():
     _check_extend(got, ref, 40 + 12 * 130)
     assert got[0][:, 2].any() and got[0][:, 3].any() and (ref[0][:, 1].abs().max() > 0)
     _clean()
+
+
+@pytest.mark.parametrize("window", [100, 128])
+@pytest.mark.parametrize("value", [math.nan, math.inf, 1e6])
+def test_values_behind_a_tile_do_not_reach_it(window, value):
+    """The box of a tile's keys is rounded up to 16: the rows behind its last key hold
+    values of later tokens, which no token of the tile sees."""
+    new, lens = [40] + [12] * 130, [300] + [12] * 130
+    c = _extend_case(3, new, lens, 16, 16, 2, fill=0.0)
+    j = 300 - 40 + 16                      # the first token of the second tile of 16
+    ref = _oracle(c, window)               # (in sums of the oracle 0 * inf is not 0 either)
+    page = int(c[3][0, j // 16])
+    c[1][page, j % 16], c[2][page, j % 16] = value, value
+    got = _band(lambda: _run_extend(c, window))
+    assert _code() == (0 if math.isnan(value) else 0x400)
+    for a, b in ((0, 16), (40, sum(new))):
+        _check_extend((got[0][a:b], got[1][:, a:b]),
+                      (ref[0][a:b], ref[1][:, a:b], ref[2][a:b]), b - a)
