@@ -969,7 +969,7 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
           const float mb = (mf == -INFINITY) ? 0.0f : mf;
           const float wk = ex2_approx(m - mb);
           const float z = fmaf(lt, wk, ex2_approx(s2 - mb));
-          const float scale = z > 0.0f ? wk / z : 0.0f;
+          const float scale = z != 0.0f ? wk / z : 0.0f;
           const bool whole = rows == p.tokens * p.group;    // same for every row
           const size_t row = (size_t)row0 + tok;
           if (whole || valid) {
@@ -989,8 +989,8 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
                     make_uint4(hi2[0], hi2[1], hi2[2], hi2[3]);
             }
             if (c == 0 && valid)
-              p.lse[(size_t)hq * p.total_q + row] =
-                  z > 0.0f ? (mb + __log2f(z)) * kLn2 : -INFINITY;
+              p.lse[(size_t)hq * p.total_q + row] =         // NaN for a NaN score
+                  z != 0.0f ? (mb + __log2f(z)) * kLn2 : -INFINITY;
           }
           if (whole) {
             fence_proxy_async_smem();
@@ -1108,13 +1108,13 @@ attn_sink_extend_join_kernel(const __grid_constant__ ExtParams p) {
     acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
-    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+    const float inv = z != 0.0f ? 1.0f / z : 0.0f;          // NaN for a NaN score
     const size_t row = (size_t)ref.w + tok;
     if (odd == 0)
       *reinterpret_cast<uint2*>(p.out + (row * p.heads_q + hq) * kHeadDim + d) = make_uint2(
           pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0)
-      p.lse[(size_t)hq * p.total_q + row] = z > 0.0f ? (mb + __log2f(z)) * kLn2 : -INFINITY;
+      p.lse[(size_t)hq * p.total_q + row] = z != 0.0f ? (mb + __log2f(z)) * kLn2 : -INFINITY;
   }
 }
 

@@ -667,8 +667,10 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
                   make_uint4(lo2[0], lo2[1], lo2[2], lo2[3]);
           }
         }
+        // kSum: a NaN score gives a NaN, not the mark of a row without keys
         if (c == 0 && t < prem)
-          p.lse[(size_t)h * p.total_q + row] = (lz > 0.0f) ? (pm + __log2f(lz)) * kLn2 : -INFINITY;
+          p.lse[(size_t)h * p.total_q + row] =
+              (kSum ? lz != 0.0f : lz > 0.0f) ? (pm + __log2f(lz)) * kLn2 : -INFINITY;
         if (whole) {
           fence_proxy_async_smem();
           named_barrier_sync(6, 2 * kBlockM);

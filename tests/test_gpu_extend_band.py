@@ -68,3 +68,17 @@ def test_values_behind_a_tile_do_not_reach_it(window, value):
     for a, b in ((0, 16), (40, sum(new))):
         _check_extend((got[0][a:b], got[1][:, a:b]),
                       (ref[0][a:b], ref[1][:, a:b], ref[2][a:b]), b - a)
+
+
+def test_a_nan_score_gives_a_nan_lse():
+    """-inf is the mark of a row without keys."""
+    c = _extend_case(6, [40] + [12] * 130, [300] + [12] * 130, 16, 8, 2, fill=0.0)
+    j = 300 - 20
+    c[1][int(c[3][0, j // 16]), j % 16, 1] = math.nan
+    out, lse = _band(lambda: _run_extend(c, 100))
+    seen = torch.zeros(8, 40 + 12 * 130, dtype=torch.bool)
+    seen[4:, 20:40] = True                 # tokens from that key on, heads of kv head 1
+    assert torch.equal(lse.isnan().cpu(), seen)
+    assert torch.equal(out.isnan().all(-1).cpu(), seen.T)
+    assert torch.equal(out.isnan().any(-1).cpu(), seen.T)
+    _clean()
