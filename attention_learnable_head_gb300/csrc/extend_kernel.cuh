@@ -440,6 +440,11 @@ attn_sink_extend_plan_kernel(const __grid_constant__ ExtParams p) {
   if (tid == 0) *p.n_tiles = over ? make_int2(0, 0) : make_int2(split0, s_rows);
 }
 
+// The sink's term 2^(s - m) of a row sum, s <= m; 1 where both are inf.
+__device__ __forceinline__ float ext_sink(float s, float m) {
+  return s == m ? 1.0f : ex2_approx(s - m);
+}
+
 // The bits below bit n of a word.
 __device__ __forceinline__ uint32_t ext_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -968,7 +973,7 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
           const float mf = fmaxf(m, s2);
           const float mb = (mf == -INFINITY) ? 0.0f : mf;
           const float wk = ex2_approx(m - mb);
-          const float z = fmaf(lt, wk, ex2_approx(s2 - mb));
+          const float z = fmaf(lt, wk, ext_sink(s2, mb));
           const float scale = z != 0.0f ? wk / z : 0.0f;
           const bool whole = rows == p.tokens * p.group;    // same for every row
           const size_t row = (size_t)row0 + tok;
@@ -1086,7 +1091,7 @@ attn_sink_extend_join_kernel(const __grid_constant__ ExtParams p) {
     float z = fmaf(ml[1].y, w1, ml[0].y * w0);
     #pragma unroll
     for (int k = 16; k > 0; k >>= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
-    z += ex2_approx(s2 - mb);
+    z += ext_sink(s2, mb);
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int c = 0; c < parts; c += 16) {
       #pragma unroll

@@ -629,7 +629,8 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         if constexpr (kSum) {
           const float mf = fmaxf(pm, psink);
           const float mb = (mf == -INFINITY) ? 0.0f : mf;
-          const float wk = ex2_approx(pm - mb), ws = ex2_approx(psink - mb);
+          const float wk = ex2_approx(pm - mb);
+          const float ws = psink == mb ? 1.0f : ex2_approx(psink - mb);   // also where inf
           lt = fmaf(lt, wk, ws);
           lz = fmaf(lz, wk, ws);
           inv_l = (lt > 0.0f) ? wk / lt : 0.0f;

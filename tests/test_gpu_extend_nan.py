@@ -1,10 +1,12 @@
-"""attn_sink_extend with scores that are not numbers, in whole and in cut tiles."""
+"""attn_sink_extend with scores that are not numbers, in whole and in cut tiles, and with
+sinks of +inf, on the band kernel too."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_step import _clean, _extend_case, _run_extend
+from oracle.step import oracle_extend
+from test_gpu_step import _check_extend, _clean, _extend_case, _run_extend
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +39,17 @@ def test_a_nan_query_gives_nan(length):
     assert torch.equal(out.isnan().all(-1).cpu(), seen.T)
     assert torch.equal(out.isnan().any(-1).cpu(), seen.T)
     _clean()
+
+
+@pytest.mark.parametrize("length,window,more", [(60, 0, 0), (9000, 0, 0), (300, 100, 130)])
+def test_a_sink_of_infinity_takes_all(length, window, more):
+    """out = 0 and lse = inf; the other heads as ever."""
+    c = list(_extend_case(length, [20, 3] + [12] * more, [length, 0] + [12] * more, 16, 8, 2))
+    c[6] = torch.tensor([0.5, math.inf, 1.0, 0.0, math.inf, -1.0, -math.inf, 2.0])
+    n = 23 + 12 * more
+    out, lse = _run_extend(c, window)
+    _clean()
+    assert not out[:, [1, 4]].any() and (lse[[1, 4]] == math.inf).all()
+    rest = [0, 2, 3, 5, 6, 7]
+    ref = oracle_extend(*c[:4], c[4].tolist(), c[5].tolist(), c[6], scale=0.125, window=window)
+    _check_extend((out[:, rest], lse[rest]), (ref[0][:, rest], ref[1][rest], ref[2][:, rest]), n)
