@@ -10,7 +10,8 @@
 // sequence's keys, find zeros there and nothing of another sequence.  A schedule
 // kernel of one CTA lays out the regions and lists every tile as a sequence of
 // its own for the band kernel: queries [q0, q1) and the keys [k0, k1) that they
-// see, bottom-right aligned.
+// see, bottom-right aligned.  Keys whose block-table entry is outside the cache are
+// marked, and the band kernel skips them.
 #pragma once
 #include "extend_kernel.cuh"
 #include "fwd_band_kernel.cuh"
@@ -30,6 +31,8 @@ struct GatherParams {
   GatherRegion* regions;                   // [B]
   __nv_bfloat16* k;                        // [rows][H_kv][64]
   uint16_t* v;                             // the same, fp16
+  unsigned char* lost;                     // [rows]: 1 for a key without a page
+  int* any_lost;                           // is there any?
   int max_tiles;
   long long rows;                          // of k and v
 };
@@ -41,6 +44,7 @@ attn_sink_gather_plan_kernel(const __grid_constant__ GatherParams g) {
   const ExtParams& p = g.e;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool bad = false;
+  if (tid == 0) *g.any_lost = 0;
   int row0 = kGatherPad, tile0 = 0;        // of the sequences before this round
   for (int b0 = 0; b0 < p.batch; b0 += kExtSchedThreads) {
     const int b = b0 + 32 * lane + warp;   // neighbours go to different warps
@@ -114,10 +118,14 @@ attn_sink_gather_kernel(const __grid_constant__ GatherParams g) {
          u += (long long)gridDim.x * kGatherThreads) {
       const int i = (int)(u / per), c = (int)(u - (long long)i * per);
       uint4 k = zero, v = zero;
+      const long long row = (long long)r.x + i;
       if (i < r.z) {
         const int j = r.y + i, pg = j / p.page_size;
         const int e = __ldg(table + pg);
-        if (e >= 0 && e < p.num_pages) {
+        const bool held = e >= 0 && e < p.num_pages;
+        if (c == 0 && (unsigned long long)row < (unsigned long long)g.rows)
+          g.lost[row] = held ? 0 : 1;
+        if (held) {
           const size_t src = (((size_t)e * p.page_size + (j - pg * p.page_size)) * per + c) * 8;
           k = *reinterpret_cast<const uint4*>(p.k_cache + src);
           v = *reinterpret_cast<const uint4*>(p.v_cache + src);
@@ -129,10 +137,13 @@ attn_sink_gather_kernel(const __grid_constant__ GatherParams g) {
           lost = true;
         }
       }
-      put((long long)r.x + i, c, k, v);
+      put(row, c, k, v);
     }
   }
-  if (lost) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  if (lost) {
+    *g.any_lost = 1;
+    atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  }
   if (over) atomicCAS(p.err, 0, DEVERR_FP16_RANGE);
 }
 

@@ -75,6 +75,10 @@ struct FwdBandParams {
   const int* cu_q;    // null for a dense batch
   const int* cu_k;
   const int4* spans;  // or, per sequence, its rows [x, y) of q and [z, w) of k
+  // kSum: rows of k that no query sees (one byte each), where *any_lost is not 0
+  const unsigned char* lost;
+  const int* any_lost;
+  int lost_rows;
   const float* sink;  // [H_q] fp32, or
   const __nv_bfloat16* sink_bf16;   // [H_q] bf16 when non-null
   __nv_bfloat16* out;     // [T_q][H_q][64]
@@ -528,6 +532,8 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
     // the previous item's sink term of the row sum, 2^(sink - m); kSum: the sink (log2)
     float psink = 0.0f;
     float psum = 0.0f;    // kSum: this half's sum of its P
+    bool holes = false;
+    if constexpr (kSum) holes = __ldcg(p.any_lost) != 0;
     BandWalk w;
     w.start(p);
     while (true) {
@@ -554,6 +560,24 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
           tc_fence_after();
           bool wrote = false;
           int cc = 0;
+          if (kSum && holes) {           // rare: keys whose page is missing
+            const int row0 = it.sp.k0 + it.kb + c0;
+            #pragma unroll 1
+            for (; cc < nc; cc += 16) {
+              uint32_t a[16];
+              tmem_ld_x16(tS + cc, a);
+              tmem_ld_wait();
+              #pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (cc + e >= lo && cc + e <= hi &&
+                    (unsigned)(row0 + cc + e) < (unsigned)p.lost_rows &&
+                    __ldcg(p.lost + (row0 + cc + e)) != 0)
+                  a[e] = __float_as_uint(-INFINITY);
+              tmem_st_x16(tS + cc, a);
+            }
+            tmem_st_wait();
+            cc = 0;
+          }
           #pragma unroll 1
           for (; cc + 32 <= nc; cc += 32)
             mx = fmaxf(mx, band_chunk_max<32>(tS + cc, lo - cc, hi - cc, wrote));

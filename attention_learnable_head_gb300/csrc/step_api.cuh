@@ -127,7 +127,7 @@ struct ExtendLayout {
   // the band kernel's path (extend_window.cuh)
   int band_cols;     // 0: not taken
   long long band_rows;
-  size_t off_regions, off_k, off_v;
+  size_t off_regions, off_k, off_v, off_lost;
 };
 
 // Windows go to the band kernel where one product covers a tile's keys (as in the
@@ -221,7 +221,9 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
       L->off_k = off;
       off += kv;
       L->off_v = off;
-      L->total = off + kv;
+      off += kv;
+      L->off_lost = off;                   // whether any is lost, then a byte a row
+      L->total = off + 256 + align256((size_t)L->band_rows);
     }
   }
   return ATTN_SINK_OK;
@@ -260,6 +262,8 @@ int extend_window(const attn_sink_extend_params* p, const ExtendLayout& L, const
   gp.regions = reinterpret_cast<GatherRegion*>(ws + L.off_regions);
   gp.k = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
   gp.v = reinterpret_cast<uint16_t*>(ws + L.off_v);
+  gp.any_lost = reinterpret_cast<int*>(ws + L.off_lost);
+  gp.lost = ws + L.off_lost + 256;
   gp.max_tiles = L.n_items;
   gp.rows = L.band_rows;
   FwdBandParams bp;
@@ -276,6 +280,9 @@ int extend_window(const attn_sink_extend_params* p, const ExtendLayout& L, const
     return st;
   bp.tm_out_lo = bp.tm_out;                // unused without a residual
   bp.spans = gp.spans;
+  bp.lost = gp.lost;
+  bp.any_lost = gp.any_lost;
+  bp.lost_rows = (int)L.band_rows;
   bp.sink = ep.sink;
   bp.out = ep.out;
   bp.lse = ep.lse;

@@ -196,11 +196,10 @@ size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
  * to lie within the fp16 range there (|v| <= 65504, else 0x400 is recorded, as by
  * attn_sink_fwd).
  * A length outside [0, max_pages * page_size] is clamped, the keys of a
- * block-table entry outside [0, num_pages) are skipped (on the band kernel they
- * read as zero keys and values), and cu_seqlens_q is clamped to [0, T]; each is
- * recorded as 0x800.  The workspace is 256-byte aligned.  out and lse must not
- * overlap the inputs.  The result does not
- * depend on timing: the same inputs give the same bits.
+ * block-table entry outside [0, num_pages) are skipped, and cu_seqlens_q is
+ * clamped to [0, T]; each is recorded as 0x800.  The workspace is 256-byte
+ * aligned.  out and lse must not overlap the inputs.  The result does not depend
+ * on timing: the same inputs give the same bits.
  */
 int attn_sink_extend(const attn_sink_extend_params* params, const void* q, const void* k_cache,
                      const void* v_cache, const int* block_table, const int* seq_lens,

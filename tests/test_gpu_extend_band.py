@@ -82,3 +82,25 @@ def test_a_nan_score_gives_a_nan_lse():
     assert torch.equal(out.isnan().all(-1).cpu(), seen.T)
     assert torch.equal(out.isnan().any(-1).cpu(), seen.T)
     _clean()
+
+
+@pytest.mark.parametrize("page", [16, 12])
+def test_keys_without_a_page_are_skipped(page):
+    """As on the general kernel: such a key takes no weight."""
+    new, lens = [70, 40] + [12] * 130, [200, 190] + [12 + i for i in range(130)]
+    c = list(_extend_case(4, new, lens, page, 8, 2))
+    c[3] = c[3].clone()
+    for b, j in ((0, 199), (0, 120), (1, 150), (1, 151 + page), (9, 3), (50, 40)):
+        c[3][b, j // page] = -1
+    c[3][0, 140 // page] = c[1].shape[0]
+    got = _band(lambda: _run_extend(c, 100))
+    assert _code() == 0x800
+    _check_extend(got, _oracle(c, 100), sum(new))
+    # none of the keys of a token is left
+    c[3][:] = -1
+    got = _band(lambda: _run_extend(c, 100))
+    assert _code() == 0x800 and not got[0].any()
+    _check_extend(got, _oracle(c, 100), sum(new))
+    c = _extend_case(5, new, lens, page, 8, 2)
+    _check_extend(_band(lambda: _run_extend(c, 100)), _oracle(c, 100), sum(new))
+    _clean()
