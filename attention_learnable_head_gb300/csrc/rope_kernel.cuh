@@ -179,10 +179,13 @@ __device__ __forceinline__ void rope_angles(const RopeParams& p, int pos, int la
                                             const RopeLane& me, float* sC, float* sS) {
   __syncwarp();                            // the last token's heads have read C and S
   if (lane < (p.rotary >> 1)) {
-    // positions are whole numbers: whole turns leave the 64 bits at the top
-    const int turns = (int)(((long long)pos * me.freq) >> 32);
+    // positions are whole numbers: whole turns leave the 64 bits at the top.  All 64 go
+    // into the conversion, so that an angle far below a turn keeps 24 bits (with the
+    // upper 32 alone one of 1e-7 had six).
+    const long long turns =
+        (long long)((unsigned long long)(long long)pos * (unsigned long long)me.freq);
     float s, c;
-    sincospif((float)turns * 4.656612873077392578e-10f + me.bad, &s, &c);   // 2^-31
+    sincospif(__ll2float_rn(turns) * 1.0842021724855044e-19f + me.bad, &s, &c);   // 2^-63
     s *= p.amplitude;
     c *= p.amplitude;
     const int a = kInter ? 2 * lane : (lane >> 2) * 8 + (lane & 3);

@@ -119,8 +119,9 @@ typedef struct attn_sink_rope_params {
  * page_size, heads_kv, 64]; a slot of -1 writes no row, any other slot outside
  * the cache is skipped and recorded as 0x800.  Slots of one call have to be
  * distinct (as attn_sink_page_plan makes them).  Outputs must not overlap
- * inputs.  The angle and its reduction to one turn are computed in 64 bits, so
- * far positions lose nothing; the rest is fp32, rounded once.  q_weight and
+ * inputs.  The angle is reduced to one turn in 64 bits (inv_freq / 2 pi to 2^-64
+ * turns, times the position) and rounded to fp32 then, so far positions lose nothing
+ * and small angles keep 24 bits; the rest is fp32, rounded once.  q_weight and
  * k_weight may be NULL with norm = 0, inv_freq and positions with rotary_dim = 0.
  * No workspace; one launch.
  */
