@@ -220,6 +220,7 @@ bool rope_args(PyObject* const* a, Rope* r) {
   p.q_stride = p.k_stride = p.v_stride = stride;
   const c10::Device dev = x.device();
   const bool flat = r->positions->dim() == 1;
+  if (!flat && r->positions->dim() != 2) return false;
   p.num_axes = flat ? 1 : (int)std::min<int64_t>(r->positions->size(0), INT_MAX);
   if (!(flat ? fits(r->positions, at::kInt, dev, {r->t})
              : fits(r->positions, at::kInt, dev, {-1, r->t})) ||

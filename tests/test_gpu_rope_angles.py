@@ -1,4 +1,4 @@
-"""attn_sink_qkv_rope at angles far below a turn."""
+"""attn_sink_qkv_rope at angles far below a turn, and its check of positions."""
 import pytest
 import torch
 
@@ -29,4 +29,15 @@ def test_small_angles_keep_their_bits(interleaved):
         for d, ref in ((a, angle.cos()), (b, angle.sin())):
             err = (y[:, d] - ref).abs()
             assert (err <= (2.0 ** -8 + 2.0 ** -20) * ref.abs() + far).all(), (err / ref.abs()).max()
+    _clean()
+
+
+def test_positions_without_a_dimension_are_refused():
+    x = torch.zeros(1, 3, 64, dtype=BF, device=DEV)
+    one = torch.zeros((), dtype=torch.int32, device=DEV)
+    for run in (lambda: binding.qkv_rope(x, one, torch.ones(32, device=DEV), heads_q=1, heads_kv=1),
+                lambda: binding.qkv_rope_backward(x, one, torch.ones(32, device=DEV), x[:, :1],
+                                                  x[:, 1:2], x[:, 2:], heads_q=1, heads_kv=1)):
+        with pytest.raises(ValueError, match="positions"):
+            run()
     _clean()
