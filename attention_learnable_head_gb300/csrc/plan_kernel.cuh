@@ -10,8 +10,9 @@
 // writes, and the whole plan is one launch.
 //
 // CTA (x, y) handles the 256 sequences of group x: it sums the lengths of the
-// groups before it (reads that stay in L2), scans its own group in shared
-// memory, and writes every gridDim.y-th block of the group's tokens and new
+// groups before it (reads that stay in L2; of many sequences, where that would grow
+// with their square, a kernel of one CTA before it does), scans its own group in
+// shared memory, and writes every gridDim.y-th block of the group's tokens and new
 // pages, found by bisection of the scanned offsets, so ragged lengths spread
 // evenly.  What bounds it is latency: a plan moves 12 bytes a token and 8 a
 // new page.  A decode step of 128 sequences takes 3.1 us, 1024 prompts of 64 to 128
@@ -38,6 +39,7 @@ struct PlanParams {
   int* needed;            // [1]
   int* err;
   int batch, page_size, num_pages, max_pages, num_free, max_tokens;
+  int summed;             // the sums before each group are in cu and lens
 };
 
 struct PlanSeq {
@@ -68,6 +70,58 @@ __device__ __forceinline__ int plan_find(const long long* first, long long t) {
   return lo;
 }
 
+// Tokens and pages of the sequences before each group, left in the group's first
+// entries of cu and lens, which the plan overwrites (its one CTA per group reads them
+// first).  As unsigned 32-bit numbers: no max_tokens or num_free reaches the largest.
+// A warp sums a group, 32 of them at a time.
+constexpr int kPlanSumThreads = 1024;
+__global__ void __launch_bounds__(kPlanSumThreads, 1)
+attn_sink_plan_sum_kernel(const PlanParams p) {
+  __shared__ long long s_tok[32], s_page[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool dummy = false;
+  long long tok0 = 0, pag0 = 0;            // before this round; kept by the first warp
+  for (int b0 = 0; b0 < p.batch; b0 += 32 * kPlanSeqs) {
+    long long tok = 0, pag = 0;
+    #pragma unroll
+    for (int i = 0; i < kPlanSeqs; i += 32) {
+      const PlanSeq s = plan_seq(p, b0 + warp * kPlanSeqs + i + lane, &dummy);
+      tok += s.fresh;
+      pag += s.need;
+    }
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      tok += __shfl_xor_sync(0xffffffffu, tok, d);
+      pag += __shfl_xor_sync(0xffffffffu, pag, d);
+    }
+    if (lane == 0) {
+      s_tok[warp] = tok;
+      s_page[warp] = pag;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      long long t = s_tok[lane], g = s_page[lane];
+      const long long my_t = t, my_g = g;
+      #pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, t, d), c = __shfl_up_sync(0xffffffffu, g, d);
+        if (lane >= d) {
+          t += a;
+          g += c;
+        }
+      }
+      const int b = b0 + lane * kPlanSeqs;
+      if (b < p.batch) {
+        p.cu[b] = (int)(unsigned)min(tok0 + t - my_t, (long long)UINT_MAX);
+        p.lens[b] = (int)(unsigned)min(pag0 + g - my_g, (long long)UINT_MAX);
+      }
+      tok0 += __shfl_sync(0xffffffffu, t, 31);
+      pag0 += __shfl_sync(0xffffffffu, g, 31);
+    }
+    __syncthreads();
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
 attn_sink_plan_kernel(const PlanParams p) {
   constexpr int kWarps = kPlanThreads / 32;
@@ -81,12 +135,16 @@ attn_sink_plan_kernel(const PlanParams p) {
   // tokens and pages of the sequences before this group (64-bit: lengths are
   // data; their sums are clamped only where they are stored)
   long long tok = 0, pag = 0;
-  for (int b = tid; b < b0; b += kPlanThreads) {
-    const PlanSeq s = plan_seq(p, b, &dummy);
-    tok += s.fresh;
-    pag += s.need;
-  }
-  if (b0 > 0) {
+  if (p.summed) {
+    tok = (unsigned)p.cu[b0];
+    pag = (unsigned)p.lens[b0];
+    __syncthreads();                       // before they are overwritten
+  } else if (b0 > 0) {
+    for (int b = tid; b < b0; b += kPlanThreads) {
+      const PlanSeq s = plan_seq(p, b, &dummy);
+      tok += s.fresh;
+      pag += s.need;
+    }
     #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       tok += __shfl_xor_sync(0xffffffffu, tok, d);

@@ -35,6 +35,11 @@ bool launch_dependent(void (*kernel)(P), dim3 grid, unsigned threads, size_t sme
 // ----------------------------------------------------------------------------- plan
 // Tokens a CTA of the plan writes; more CTAs per group only repeat the sums.
 constexpr int kPlanTokensPerCta = 4 * kPlanThreads;
+// From this many sequences on a kernel of its own sums the lengths before each group
+// (and a group has one CTA, as it has by then anyway).  Device time with the CTAs' own
+// sums and with that kernel: 32768 sequences of up to 1 token 44 and 27 us, of up to 40
+// 120 and 185; 65536 86 and 50, 350 and 353; 131072 184 and 91, 838 and 658.
+constexpr int kPlanSummed = 1 << 16;
 
 // ----------------------------------------------------------------------------- rope
 int rope_validate(const attn_sink_rope_params* p) {
@@ -367,10 +372,15 @@ int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_l
   const int groups = std::max(1, (params->batch + kPlanSeqs - 1) / kPlanSeqs);
   const long long per_group = (params->max_tokens + groups - 1) / groups;
   const long long blocks = (per_group + kPlanTokensPerCta - 1) / kPlanTokensPerCta;
-  const int y = (int)std::max<long long>(
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  pp.summed = params->batch >= kPlanSummed;
+  const int y = pp.summed ? 1 : (int)std::max<long long>(
       1, std::min<long long>(blocks, std::max(1, 2 * sms / groups)));
-  attn_sink_plan_kernel<<<dim3(groups, y), kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      pp);
+  if (pp.summed) {
+    attn_sink_plan_sum_kernel<<<1, kPlanSumThreads, 0, s>>>(pp);
+    if (!launched()) return ATTN_SINK_ERR_CUDA;
+  }
+  attn_sink_plan_kernel<<<dim3(groups, y), kPlanThreads, 0, s>>>(pp);
   return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 

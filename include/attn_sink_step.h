@@ -72,7 +72,8 @@ typedef struct attn_sink_plan_params {
  * runs out the entries are -1.  Each of these records ATTN_SINK_DEVERR_PLAN.
  * Sequences may share pages that are full (a common prefix), not one that is
  * partly filled and gets new tokens.  Outputs must not overlap inputs: seq_lens
- * in the place of cached_lens or new_lens is refused.  No workspace; one launch.
+ * in the place of cached_lens or new_lens is refused.  No workspace; one launch, two
+ * from 65536 sequences on.
  */
 int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_lens,
                         const int* new_lens, const int* free_pages, int* block_table,
