@@ -34,7 +34,7 @@ from typing import NamedTuple
 
 import torch
 
-from .build import FAST_PATH, INCLUDE, LIB_PATH
+from .build import FAST_PATH, INCLUDE, LIB_PATH, fast_built_for, fast_target
 
 c_int, c_float, c_void_p, c_size_t = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 c_longlong = ctypes.c_longlong
@@ -620,9 +620,9 @@ def _fast():
     each use then checks the arguments one by one."""
     global _FAST
     if _FAST is None:
-        if not os.path.exists(FAST_PATH):
+        if not os.path.exists(FAST_PATH) or fast_built_for() != fast_target():
             raise RuntimeError(
-                f"{FAST_PATH} is missing: build it with "
+                f"{FAST_PATH} is missing or not built for {fast_target()}: build it with "
                 "`python -c 'import __graft_entry__ as g; g.build()'`")
         L = lib()
         spec = importlib.util.spec_from_file_location("attn_sink_fast", FAST_PATH)

@@ -4,8 +4,10 @@ g++ against the installed torch's headers."""
 from __future__ import annotations
 
 import os
+import platform
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ TEST_LIB_PATH = os.path.join(LIB_DIR, "libattn_sink_test.so")
 TEST_FLAGS = ["-DATTN_SINK_TEST_HOOKS", "-DATTN_SINK_WAIT_LIMIT_NS=2000000ull"]
 FAST_PATH = os.path.join(LIB_DIR, "attn_sink_fast.so")
 FAST_SOURCE = os.path.join(CSRC, "fast_calls.cpp")
+FAST_STAMP = FAST_PATH + ".built-for"    # which torch and Python the module is for
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,6 +43,21 @@ def _sources() -> list[str]:
 def _up_to_date(path: str, sources: list[str]) -> bool:
     return (os.path.exists(path)
             and os.path.getmtime(path) >= max(os.path.getmtime(s) for s in sources))
+
+
+def fast_target() -> str:
+    """What the native module depends on beside its sources."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}, {platform.machine()}"
+
+
+def fast_built_for() -> str | None:
+    """The fast_target() the native module was built for, None without one."""
+    try:
+        with open(FAST_STAMP) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _start(cmd: list[str], verbose: bool) -> subprocess.Popen:
@@ -88,12 +106,16 @@ def build(force: bool = False, verbose: bool = False, test: bool = False) -> str
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         jobs.append((_start(cmd, verbose), tmp, path))
-    if not test and (force or not _up_to_date(
-            FAST_PATH, [FAST_SOURCE, os.path.join(INCLUDE, "attn_sink_step.h")])):
+    fast = not test and (force or fast_built_for() != fast_target() or not _up_to_date(
+        FAST_PATH, [FAST_SOURCE, os.path.join(INCLUDE, "attn_sink_step.h")]))
+    if fast:
         tmp = FAST_PATH + ".tmp"
         jobs.append((_start(_fast_command(tmp), verbose), tmp, FAST_PATH))
     for job in jobs:                       # they compile side by side
         _finish(*job, verbose)
+    if fast:
+        with open(FAST_STAMP, "w") as f:
+            f.write(fast_target())
     return path
 
 
