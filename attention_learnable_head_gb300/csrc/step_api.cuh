@@ -174,6 +174,7 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
       p->heads_q % p->heads_kv != 0 || p->page_size < 1 || p->num_pages < 0 ||
       p->max_pages < 0 || !(p->softmax_scale > 0.0f) || !std::isfinite(p->softmax_scale))
     return ATTN_SINK_ERR_INVALID_ARG;
+  if (p->batch > (1 << 24) || p->total_q > (1 << 30)) return ATTN_SINK_ERR_UNSUPPORTED;
   if ((long long)p->max_pages * p->page_size > (1ll << 30)) return ATTN_SINK_ERR_INVALID_ARG;
   // rows of the cache of one head, 128 bytes each: 512 GB
   if ((long long)p->num_pages * p->page_size > ((1ll << 32) - 1) / p->heads_kv)
