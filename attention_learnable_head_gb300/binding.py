@@ -680,6 +680,13 @@ def _dims(name, t, n):
     return t.shape
 
 
+def _in_32_bits(**sizes):
+    """ctypes would cut an integer to 32 bits without a word."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name} is {n}: it has to fit 32 bits")
+
+
 class PagePlan(NamedTuple):
     """What a serving step needs to know of its tokens (see page_plan)."""
     slots: torch.Tensor          # [max_tokens] int64: cache row of each new token, -1: none
@@ -711,6 +718,8 @@ def page_plan(cached_lens, new_lens, free_pages, block_table, *, page_size: int,
     _want("block_table", block_table, i32, dev, (b, cols))
     if max_tokens < 0:
         raise ValueError(f"max_tokens is {max_tokens}")
+    _in_32_bits(page_size=page_size, num_pages=num_pages, max_tokens=max_tokens, cached_lens=b,
+                block_table=cols, free_pages=free)
     with _on(dev, stream):
         slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
         positions = torch.empty(max_tokens, dtype=i32, device=dev)
@@ -739,6 +748,8 @@ def make_rope_params(tokens: int, heads_q: int, heads_kv: int, *, rotary_dim: in
     """Params of attn_sink_qkv_rope / _bwd for a packed projection whose tokens
     are row_stride elements apart."""
     p = AttnSinkRopeParams()
+    _in_32_bits(tokens=tokens, heads_q=heads_q, heads_kv=heads_kv, num_axes=num_axes,
+                page_size=page_size, num_pages=num_pages)
     p.q_stride = p.k_stride = p.v_stride = row_stride
     p.tokens, p.heads_q, p.heads_kv, p.head_dim = tokens, heads_q, heads_kv, head_dim
     p.rotary_dim, p.interleaved, p.num_axes = rotary_dim, int(interleaved), num_axes
@@ -968,6 +979,8 @@ def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, wi
         _want("out", out, bf16, dev, (t, hq, 64))
     if lse is not None:
         _want("lse", lse, torch.float32, dev, (hq, t))
+    _in_32_bits(seq_lens=b, q=max(t, hq), k_cache=max(pages, page, hkv), block_table=cols)
+    window = min(max(window, 0), 2 ** 31 - 1)             # any length is below 2^30
     p = AttnSinkExtendParams(b, t, hq, hkv, 64, page, pages, cols, window, softmax_scale)
     with _on(dev, stream):
         if out is None:
