@@ -196,7 +196,7 @@ size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
  * (128 where G = 2) and more than 128 sequences or more tiles than the GPU holds at
  * once, they are rounded to fp16 next to fp16 copies of the values, which have
  * to lie within the fp16 range there (|v| <= 65504, else 0x400 is recorded, as by
- * attn_sink_fwd).
+ * attn_sink_fwd; below 2^-14 they are rounded to multiples of 2^-24).
  * A length outside [0, max_pages * page_size] is clamped, the keys of a
  * block-table entry outside [0, num_pages) are skipped, and cu_seqlens_q is
  * clamped to [0, T]; each is recorded as 0x800.  The workspace is 256-byte

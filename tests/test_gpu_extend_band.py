@@ -104,3 +104,83 @@ def test_keys_without_a_page_are_skipped(page):
     c = _extend_case(5, new, lens, page, 8, 2)
     _check_extend(_band(lambda: _run_extend(c, 100)), _oracle(c, 100), sum(new))
     _clean()
+
+
+def test_both_ways_agree_on_the_same_tokens():
+    """The same sequences in one call on the band kernel and alone on the general one."""
+    new, lens = [96, 41, 130] + [12] * 130, [1000, 41, 777] + [12 + 5 * i for i in range(130)]
+    c = _extend_case(7, new, lens, 16, 8, 2)
+    d = [x.to(DEV) for x in c]
+    out, lse = _band(lambda: binding.extend(*d, window=100))
+    ref = _oracle(c, 100)
+    for b in (0, 1, 2, 80):
+        a, e = int(c[5][b]), int(c[5][b + 1])
+        before = binding.attn_sink_launch_count()
+        one = binding.extend(d[0][a:e], d[1], d[2], d[3][b:b + 1].contiguous(), d[4][b:b + 1],
+                             torch.tensor([0, e - a], dtype=torch.int32, device=DEV), d[6], window=100)
+        assert binding.attn_sink_launch_count() - before == 1
+        # P in fp16 and in bf16, the output in bf16 twice
+        spread = ref[2][a:e]
+        err = (out[a:e].double() - one[0].double()).abs().cpu()
+        assert (err <= 2.0 ** -7 * ref[0][a:e].abs() + (2.0 ** -8 + 2.0 ** -10) * spread).all()
+        assert (lse[:, a:e] - one[1]).abs().max() <= 2.0 ** -12
+    _clean()
+
+
+def test_far_rows_are_gathered():
+    """Pages whose offsets pass 32 bits, shared by all sequences."""
+    hkv, page, n = 8, 16, 40
+    pages = (1 << 32) // (page * hkv * 64) + 2048
+    kc = torch.empty(pages, page, hkv, 64, dtype=BF, device=DEV)
+    vc = torch.empty_like(kc)
+    near = [torch.randn(3, page, hkv, 64, device=DEV).to(BF) for _ in range(2)]
+    kc[-3:], vc[-3:] = near[0], near[1]
+    i32 = dict(dtype=torch.int32, device=DEV)
+    lens, cu = torch.full((131,), n, **i32), torch.arange(132, **i32) * n
+    q = torch.randn(131 * n, 64, 64, device=DEV).to(BF)
+    sink = torch.randn(64, device=DEV)
+    far = torch.arange(pages - 3, pages, **i32).expand(131, 3).contiguous()
+    a = _band(lambda: binding.extend(q, kc, vc, far, lens, cu, sink, window=100))
+    b = _band(lambda: binding.extend(q, *near, torch.arange(3, **i32).expand(131, 3).contiguous(),
+                                     lens, cu, sink, window=100))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c = (q, *near, torch.arange(3, **i32)[None].expand(131, 3), lens, cu, sink)
+    c = [x.cpu() for x in c]
+    part = oracle_extend(c[0][:n], c[1], c[2], c[3][:1], [n], [0, n], c[6], scale=0.125, window=100)
+    _check_extend((a[0][:n], a[1][:, :n]), part, n)
+    _clean()
+
+
+@pytest.mark.parametrize("cu", [{2: 4000}, {1: 300}, {0: -4}, {3: 0, 60: 10 ** 6}, {131: 1 << 30}])
+def test_bad_lists_of_sequences(cu):
+    """Offsets that descend or lie outside q are recorded as such, nothing outside the
+    outputs is touched, and the next call is right."""
+    new, lens = [70, 100] + [12] * 130, [200, 190] + [12] * 130
+    n = sum(new)
+    c = list(_extend_case(8, new, lens, 16, 8, 2))
+    good = c[5]
+    c[5] = good.clone()
+    for at, x in cu.items():
+        c[5][at] = x
+    room = torch.full((3, n, 8, 64), 7.0, dtype=BF, device=DEV)
+    rest = torch.full((3, 8, n), 7.0, device=DEV)
+    _band(lambda: _run_extend(c, 100, out=room[1], lse=rest[1]))
+    assert _code() == 0x800
+    for x in (room, rest):
+        assert (x[0] == 7).all() and (x[2] == 7).all()
+    c[5] = good
+    _check_extend(_band(lambda: _run_extend(c, 100)), _oracle(c, 100), n)
+    _clean()
+
+
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -20, 2.0 ** -30])
+def test_small_values(size):
+    """Values below 2^-14 are rounded to multiples of 2^-24 here: off by 2^-25."""
+    new, lens = [40] + [12] * 130, [300] + [12 + i for i in range(130)]
+    c = list(_extend_case(9, new, lens, 16, 8, 2, fill=0.0))
+    c[2] = (c[2].float() * size).to(BF)
+    got = _band(lambda: _run_extend(c, 100))
+    ref = _oracle(c, 100)
+    err = (got[0].cpu().double() - ref[0]).abs()
+    assert (err <= 2.0 ** -8 * ref[0].abs() + (2.0 ** -8 + 2.0 ** -11) * ref[2] + 2.0 ** -25).all()
+    _clean()
