@@ -371,7 +371,7 @@ int attn_sink_page_plan(const attn_sink_plan_params* params, const int* cached_l
   pp.max_tokens = params->max_tokens;
   // groups of sequences x blocks of a group's tokens, two CTAs per SM at most
   const int groups = std::max(1, (params->batch + kPlanSeqs - 1) / kPlanSeqs);
-  const long long per_group = (params->max_tokens + groups - 1) / groups;
+  const long long per_group = ((long long)params->max_tokens + groups - 1) / groups;
   const long long blocks = (per_group + kPlanTokensPerCta - 1) / kPlanTokensPerCta;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   pp.summed = params->batch >= kPlanSummed;

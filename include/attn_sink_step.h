@@ -67,6 +67,8 @@ typedef struct attn_sink_plan_params {
  *   seq_lens [B] int32: cached + new
  *   pages_needed [1] int32: entries of free_pages this plan takes (more than
  *     num_free when they ran out)
+ * The next step's free list is this one without its first pages_needed entries; to
+ * shift it on the device, fill its end with -1 (no page: outside the cache).
  * A second call with the same inputs gives the same plan.  Lengths are clamped
  * to [0, max_pages * page_size] and cu_seqlens to max_tokens; when free_pages
  * runs out the entries are -1.  Each of these records ATTN_SINK_DEVERR_PLAN.
