@@ -471,6 +471,18 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         // whether another item follows, found while the softmax works on this one
         w.advance(p);
         have = w.more(p);
+        if constexpr (kSum) {
+          // The rows of the box behind the tile's last key (15 at most) belong to later
+          // tokens, and their values may be anything: 0 * inf is not 0.  Zeroed here,
+          // while the softmax works.
+          if (!mbar_wait(&v_full, li & 1, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          for (int ch = 8 * (p.tokens + p.window - 1); ch < 8 * N; ++ch)
+            st_shared_v4(smem_u32(sV) + 16u * (uint32_t)ch, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
         if (!mbar_wait(&p_full, li & 1, &abort_flag) || !mbar_wait(&v_full, li & 1, &abort_flag) ||
             (li > 0 && !mbar_wait(&o_free, (li - 1) & 1, &abort_flag))) {
           ok = false;
@@ -602,25 +614,9 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
             band_chunk_exp<32, kSum>(tS + cc, tS + (cc >> 1), sl2x2, negm2, &sum);
           if (cc < nc) band_chunk_exp<16, kSum>(tS + cc, tS + (cc >> 1), sl2x2, negm2, &sum);
           if constexpr (kSum) nsum = f2_lo(sum) + f2_hi(sum);
-          if constexpr (kSum) {
-            // The rows of the box behind the tile's last key belong to later tokens, and
-            // their values may be anything: 0 * inf is not 0.  A warp zeroes four.
-            const int used = p.tokens + p.window - 1;
-            if (used + 4 * warp < N) {
-              if (mbar_wait_warp(&v_full, li & 1, &abort_flag)) {
-                const int row = used + (tid >> 3);
-                if (row < N)
-                  st_shared_v4(smem_u32(sV) + (uint32_t)(row * 128 + (tid & 7) * 16), 0, 0, 0, 0);
-                fence_proxy_async_smem();
-              } else {
-                ok = false;
-                abort_flag = 1;
-              }
-            }
-          }
           tmem_st_wait();
           tc_fence_before();
-          if (!kSum || ok) mbar_arrive(&p_full);
+          mbar_arrive(&p_full);
           if constexpr (kSum) nsink = sink_l2;
           else if (sink_h > -INFINITY) nsink = ex2_approx(sink_l2 - m_use);
         } else {
