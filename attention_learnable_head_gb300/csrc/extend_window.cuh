@@ -9,9 +9,9 @@
 // between the sequences, so that the band kernel's boxes, which reach beyond a
 // sequence's keys, find zeros there and nothing of another sequence.  A schedule
 // kernel of one CTA lays out the regions and lists every tile as a sequence of
-// its own for the band kernel: queries [q0, q1) and the keys [k0, k1) that they
-// see, bottom-right aligned.  Keys whose block-table entry is outside the cache are
-// marked, and the band kernel skips them.
+// its own for the band kernel: its queries and the keys that they see, bottom-right
+// aligned.  Where a block-table entry is outside the cache the
+// gather says so, and the band kernel masks the keys of such entries.
 #pragma once
 #include "extend_kernel.cuh"
 #include "fwd_band_kernel.cuh"
@@ -27,12 +27,11 @@ struct GatherRegion {
 
 struct GatherParams {
   ExtParams e;                             // lengths, tables, cache, window
-  int4* spans;                             // [max_tiles] q0, q1, k0, k1
+  int4* spans;                             // [max_tiles], see FwdBandParams
   GatherRegion* regions;                   // [B]
   __nv_bfloat16* k;                        // [rows][H_kv][64]
   uint16_t* v;                             // the same, fp16
-  unsigned char* lost;                     // [rows]: 1 for a key without a page
-  int* any_lost;                           // is there any?
+  int* any_lost;                           // is there a key without a page?
   int max_tiles;
   long long rows;                          // of k and v
 };
@@ -73,13 +72,15 @@ attn_sink_gather_plan_kernel(const __grid_constant__ GatherParams g) {
       x.len = __shfl_sync(0xffffffffu, s.len, l);
       const int nt = __shfl_sync(0xffffffffu, tiles, l), at = __shfl_sync(0xffffffffu, tile, l);
       const int shift = __shfl_sync(0xffffffffu, base - first, l);
+      const int seq = b0 + 32 * l + warp;
       for (int t = lane; t < nt; t += 32) {
         const ExtTile e = ext_tile(p, x, t);
-        const int q0 = x.q0 + t * p.tokens, q1 = min(q0 + p.tokens, x.q0 + x.n);
-        const int lo = min(e.lo, e.hi);    // no key: an empty span
+        const int n = min(p.tokens, x.n - t * p.tokens);       // < 128
+        const int lo = min(e.lo, e.hi);    // no key: an empty span; kBandMaxCols keys at most
         // more tiles than fit are only listed by a cu_seqlens that descends
         if ((unsigned)(at + t) < (unsigned)g.max_tiles)
-          g.spans[at + t] = make_int4(q0, q1, lo + shift, e.hi + shift);
+          g.spans[at + t] =
+              make_int4(x.q0 + t * p.tokens, lo + shift, (e.hi - lo) << 8 | n, seq);
       }
     }
   }
@@ -118,14 +119,10 @@ attn_sink_gather_kernel(const __grid_constant__ GatherParams g) {
          u += (long long)gridDim.x * kGatherThreads) {
       const int i = (int)(u / per), c = (int)(u - (long long)i * per);
       uint4 k = zero, v = zero;
-      const long long row = (long long)r.x + i;
       if (i < r.z) {
         const int j = r.y + i, pg = j / p.page_size;
         const int e = __ldg(table + pg);
-        const bool held = e >= 0 && e < p.num_pages;
-        if (c == 0 && (unsigned long long)row < (unsigned long long)g.rows)
-          g.lost[row] = held ? 0 : 1;
-        if (held) {
+        if (e >= 0 && e < p.num_pages) {
           const size_t src = (((size_t)e * p.page_size + (j - pg * p.page_size)) * per + c) * 8;
           k = *reinterpret_cast<const uint4*>(p.k_cache + src);
           v = *reinterpret_cast<const uint4*>(p.v_cache + src);
@@ -137,7 +134,7 @@ attn_sink_gather_kernel(const __grid_constant__ GatherParams g) {
           lost = true;
         }
       }
-      put(row, c, k, v);
+      put((long long)r.x + i, c, k, v);
     }
   }
   if (lost) {

@@ -69,16 +69,20 @@ constexpr int kBandSmemMax = band_smem_bytes(kBandMaxCols);
 struct FwdBandParams {
   CUtensorMap tm_q;   // [T_q][H_q][64] bf16, box 64 x G x T, 128B swizzle
   CUtensorMap tm_k;   // [T_k][H_kv][64] bf16, box 64 x 1 x N
-  CUtensorMap tm_v;   // [T_k][H_kv][64] fp16 copy of v, box 64 x 1 x N
+  CUtensorMap tm_v;   // [T_k][H_kv][64] fp16 copy of v, box 64 x 1 x N (kSum: T + W - 1)
   CUtensorMap tm_out;     // out, box as tm_q (stores)
   CUtensorMap tm_out_lo;  // residual, box as tm_q (stores; unused without it)
   const int* cu_q;    // null for a dense batch
   const int* cu_k;
-  const int4* spans;  // or, per sequence, its rows [x, y) of q and [z, w) of k
-  // kSum: rows of k that no query sees (one byte each), where *any_lost is not 0
-  const unsigned char* lost;
+  // or, per tile, its rows from x of q and from y of k, how many (z: of q, and of k << 8),
+  // and the sequence w it is of
+  const int4* spans;
+  // kSum: where *any_lost is not 0, keys whose block-table entry is outside the cache are
+  // masked; a sequence's gathered rows start at row x with key y (extend_window.cuh)
   const int* any_lost;
-  int lost_rows;
+  const int4* regions;    // per sequence
+  const int* block_table; // [sequences][max_pages]
+  int page_size, num_pages, max_pages;
   const float* sink;  // [H_q] fp32, or
   const __nv_bfloat16* sink_bf16;   // [H_q] bf16 when non-null
   __nv_bfloat16* out;     // [T_q][H_q][64]
@@ -133,9 +137,9 @@ __device__ __forceinline__ SeqBounds band_bounds(const FwdBandParams& p, int ite
   if (p.spans != nullptr) {
     const int4 x = __ldg(p.spans + seq);
     b.q0 = x.x;
-    b.q1 = x.y;
-    b.k0 = x.z;
-    b.k1 = x.w;
+    b.q1 = x.x + (x.z & 255);
+    b.k0 = x.y;
+    b.k1 = x.y + (x.z >> 8);
   } else if (p.cu_q != nullptr) {
     b.q0 = __ldg(p.cu_q + seq);
     b.q1 = __ldg(p.cu_q + seq + 1);
@@ -257,6 +261,31 @@ __device__ __forceinline__ float band_chunk_max(uint32_t taddr, int lo, int hi, 
   return fmaxf(q0, q1);
 }
 
+// Masks the columns [lo, hi] of a half's S whose key has no page; row0: the gathered row
+// of the half's first column.  Rare, and out of the way of the loop that calls it.
+__device__ __noinline__ void band_mask_lost(const FwdBandParams& p, int item, int row0,
+                                            uint32_t ts, int nc, int lo, int hi) {
+  const int seq = __ldg(p.spans + fast_div(item, p.div_hkv_mul, p.div_hkv_shift)).w;
+  const int4 reg = __ldcg(p.regions + seq);
+  const int* table = p.block_table + (size_t)seq * p.max_pages;
+  const int key0 = row0 - reg.x + reg.y;
+  #pragma unroll 1
+  for (int cc = 0; cc < nc; cc += 16) {
+    uint32_t a[16];
+    tmem_ld_x16(ts + cc, a);
+    tmem_ld_wait();
+    #pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (cc + e >= lo && cc + e <= hi) {
+        const unsigned pg = (unsigned)(key0 + cc + e) / (unsigned)p.page_size;
+        if (pg >= (unsigned)p.max_pages || (unsigned)__ldg(table + pg) >= (unsigned)p.num_pages)
+          a[e] = __float_as_uint(-INFINITY);
+      }
+    tmem_st_x16(ts + cc, a);
+  }
+  tmem_st_wait();
+}
+
 // P = exp2(S * scale log2 e - m) of one chunk (masked columns hold -inf and
 // give 0), written as fp16 pairs to TMEM at tp (NC / 2 columns).  The row sum
 // of P is not formed here: the O product sums the fp16 P it multiplies (kSum: the
@@ -329,7 +358,15 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
     const int first = ((0 ^ (row & 7)) << 2);          // word 0 of chunk 0, swizzled
     reinterpret_cast<uint32_t*>(sOnes)[i] = (word == first) ? 0x3C00u : 0u;   // fp16 1.0
   }
-  fence_proxy_async_smem();                            // the MMA (async proxy) reads it
+  // kSum: the rows behind a tile's last key, up to the 16 of a step, would hold values of
+  // later tokens, which may be anything, and 0 * inf is not 0.  V's box ends with the
+  // last key, and the rows behind it stay zero.
+  const uint32_t v_rows = kSum ? (uint32_t)(p.tokens + p.window - 1) : (uint32_t)N;
+  if constexpr (kSum) {
+    for (uint32_t i = 8 * v_rows + tid; i < 8 * (uint32_t)N; i += kBandThreads)
+      reinterpret_cast<uint4*>(sV)[i] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();                            // the MMA (async proxy) reads them
   if (tid == 0) {
     abort_flag = 0;
     for (int s = 0; s < 2; ++s) {
@@ -412,7 +449,7 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&v_full, kv_bytes);
+        mbar_arrive_expect_tx(&v_full, v_rows * 128u);
         tma_load_3d_hint(&p.tm_v, &v_full, sV, 0, it.g, it.sp.k0 + it.kb, keep);
         last_v = li;
         ++li;
@@ -471,18 +508,6 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
         // whether another item follows, found while the softmax works on this one
         w.advance(p);
         have = w.more(p);
-        if constexpr (kSum) {
-          // The rows of the box behind the tile's last key (15 at most) belong to later
-          // tokens, and their values may be anything: 0 * inf is not 0.  Zeroed here,
-          // while the softmax works.
-          if (!mbar_wait(&v_full, li & 1, &abort_flag)) {
-            ok = false;
-            break;
-          }
-          for (int ch = 8 * (p.tokens + p.window - 1); ch < 8 * N; ++ch)
-            st_shared_v4(smem_u32(sV) + 16u * (uint32_t)ch, 0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
         if (!mbar_wait(&p_full, li & 1, &abort_flag) || !mbar_wait(&v_full, li & 1, &abort_flag) ||
             (li > 0 && !mbar_wait(&o_free, (li - 1) & 1, &abort_flag))) {
           ok = false;
@@ -572,24 +597,7 @@ attn_sink_fwd_band_kernel(const __grid_constant__ FwdBandParams p) {
           tc_fence_after();
           bool wrote = false;
           int cc = 0;
-          if (kSum && holes) {           // rare: keys whose page is missing
-            const int row0 = it.sp.k0 + it.kb + c0;
-            #pragma unroll 1
-            for (; cc < nc; cc += 16) {
-              uint32_t a[16];
-              tmem_ld_x16(tS + cc, a);
-              tmem_ld_wait();
-              #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (cc + e >= lo && cc + e <= hi &&
-                    (unsigned)(row0 + cc + e) < (unsigned)p.lost_rows &&
-                    __ldcg(p.lost + (row0 + cc + e)) != 0)
-                  a[e] = __float_as_uint(-INFINITY);
-              tmem_st_x16(tS + cc, a);
-            }
-            tmem_st_wait();
-            cc = 0;
-          }
+          if (kSum && holes) band_mask_lost(p, w.item, it.sp.k0 + it.kb + c0, tS, nc, lo, hi);
           #pragma unroll 1
           for (; cc + 32 <= nc; cc += 32)
             mx = fmaxf(mx, band_chunk_max<32>(tS + cc, lo - cc, hi - cc, wrote));

@@ -228,8 +228,8 @@ int extend_layout(const attn_sink_extend_params* p, int sms, ExtendLayout* L) {
       off += kv;
       L->off_v = off;
       off += kv;
-      L->off_lost = off;                   // whether any is lost, then a byte a row
-      L->total = off + 256 + align256((size_t)L->band_rows);
+      L->off_lost = off;
+      L->total = off + 256;
     }
   }
   return ATTN_SINK_OK;
@@ -269,7 +269,6 @@ int extend_window(const attn_sink_extend_params* p, const ExtendLayout& L, const
   gp.k = reinterpret_cast<__nv_bfloat16*>(ws + L.off_k);
   gp.v = reinterpret_cast<uint16_t*>(ws + L.off_v);
   gp.any_lost = reinterpret_cast<int*>(ws + L.off_lost);
-  gp.lost = ws + L.off_lost + 256;
   gp.max_tiles = L.n_items;
   gp.rows = L.band_rows;
   FwdBandParams bp;
@@ -280,15 +279,19 @@ int extend_window(const attn_sink_extend_params* p, const ExtendLayout& L, const
       (st = encode_rows(&bp.tm_k, gp.k, L.band_rows, p->heads_kv,
                         CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.band_cols)) != ATTN_SINK_OK ||
       (st = encode_rows(&bp.tm_v, gp.v, L.band_rows, p->heads_kv,
-                        CU_TENSOR_MAP_DATA_TYPE_FLOAT16, L.band_cols)) != ATTN_SINK_OK ||
+                        CU_TENSOR_MAP_DATA_TYPE_FLOAT16, L.tokens + p->window - 1)) !=
+          ATTN_SINK_OK ||
       (st = encode_rows(&bp.tm_out, out, p->total_q, p->heads_q,
                         CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.tokens, ep.group)) != ATTN_SINK_OK)
     return st;
   bp.tm_out_lo = bp.tm_out;                // unused without a residual
   bp.spans = gp.spans;
-  bp.lost = gp.lost;
   bp.any_lost = gp.any_lost;
-  bp.lost_rows = (int)L.band_rows;
+  bp.regions = reinterpret_cast<const int4*>(gp.regions);
+  bp.block_table = ep.block_table;
+  bp.page_size = p->page_size;
+  bp.num_pages = p->num_pages;
+  bp.max_pages = p->max_pages;
   bp.sink = ep.sink;
   bp.out = ep.out;
   bp.lse = ep.lse;
