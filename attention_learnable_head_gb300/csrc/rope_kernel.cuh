@@ -51,9 +51,9 @@ constexpr int kRopeBwdDepth = 3;
 // a stage of the ring takes them all, with one wait for the three tensors (kWhole): a
 // token of few heads is bound by instructions (750 for 5 + 1 + 1 heads with a wait for
 // each tensor) and few tokens by the chain of waits.  Whole and by chunks: 65536
-// tokens of 8 + 1 + 1 heads 61 and 69 us, of 10 + 2 + 2 58 and 79, of 16 + 2 + 2 60
-// and 82, of 20 + 4 + 4 85 and 94, of 16 + 8 + 8 (not taken) 98 and 92; 64 tokens 4.3
-// and 5.1.  The gradient, 12 + 2 + 2 heads 83 and 113, 8 + 1 + 1 73 and 95, with fp32
+// tokens of 8 + 1 + 1 heads 58 and 69 us, of 10 + 2 + 2 59 and 79, of 16 + 2 + 2 61
+// and 82, of 20 + 4 + 4 86 and 94, of 16 + 8 + 8 (not taken) 97 and 92; 64 tokens 4.4
+// and 5.2.  The gradient, 12 + 2 + 2 heads 82 and 112, 8 + 1 + 1 73 and 95, with fp32
 // gradients 75 and 97; its stages hold dy too and have to fit 48 KB with four warps.
 constexpr int kRopeWhole = 28;
 constexpr int kRopeBwdWhole = 17;      // of the gradient, dy in bf16

@@ -132,7 +132,7 @@ struct ExtendLayout {
   // the band kernel's path (extend_window.cuh)
   int band_cols;     // 0: not taken
   long long band_rows;
-  size_t off_regions, off_k, off_v, off_lost;
+  size_t off_regions, off_k, off_v, off_lost;   // off_lost: GatherParams::any_lost
 };
 
 // Windows go to the band kernel where one product covers a tile's keys (as in the
@@ -140,11 +140,11 @@ struct ExtendLayout {
 // (ext_find), and the sequences have enough new tokens: kExtBandTokens on average,
 // below which the workspace (176 + W rows of K and V for each) is out of
 // proportion; two full tiles with two heads a group, where gathering costs as much
-// as it saves (with one it always did).  Device time of the band kernel's and of
-// the general way, W = 128, 64 + 8 heads: 8 x 513 tokens 28 and 61 us, 32 x 64 23
-// and 33, 128 x 8 38 and 42, 8 x 64 13.4 and 13.8, 32 x 16 15.2 and 14.8, 1 x 256
-// 10.7 and 9.2; 8 + 1 heads, 64 x 8 11.7 and 14.4; W = 100, 16 + 8 heads: 128 x 64
-// 52 and 46, 128 x 200 95 and 108; W = 40, 8 + 8 heads: 128 x 200 72 and 68.
+// as it saves (with one it always did).  Device time of the band kernel's and of the general way behind 1024
+// cached keys, W = 128, 64 + 8 heads: 8 x 513 tokens 34 and 69 us, 140 x 200 197 and
+// 443, 32 x 64 26 and 39, 128 x 8 39.5 and 39.3, 8 x 64 13.4 and 12.6, 32 x 16 15.3
+// and 13.1, 1 x 256 (not taken) 10.8 and 9.7; 8 + 1 heads, 64 x 8 (not taken) 11.8 and
+// 9.9; W = 100, 16 + 8 heads: 128 x 64 (not taken) 55 and 44, 128 x 200 120 and 135.
 constexpr int kExtBandTokens = 8;
 
 // Tiles that see few blocks of keys are left whole: cutting them costs a schedule, a
