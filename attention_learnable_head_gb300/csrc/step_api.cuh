@@ -140,11 +140,12 @@ struct ExtendLayout {
 // (ext_find), and the sequences have enough new tokens: kExtBandTokens on average,
 // below which the workspace (176 + W rows of K and V for each) is out of
 // proportion; two full tiles with two heads a group, where gathering costs as much
-// as it saves (with one it always did).  Device time of the band kernel's and of the general way behind 1024
-// cached keys, W = 128, 64 + 8 heads: 8 x 513 tokens 34 and 69 us, 140 x 200 197 and
-// 443, 32 x 64 26 and 39, 128 x 8 39.5 and 39.3, 8 x 64 13.4 and 12.6, 32 x 16 15.3
-// and 13.1, 1 x 256 (not taken) 10.8 and 9.7; 8 + 1 heads, 64 x 8 (not taken) 11.8 and
-// 9.9; W = 100, 16 + 8 heads: 128 x 64 (not taken) 55 and 44, 128 x 200 120 and 135.
+// as it saves (with one it always did).  Device time of the band kernel's and of
+// the general way behind 1024 cached keys, W = 128, 64 + 8 heads: 8 x 513 tokens 34
+// and 69 us, 140 x 200 197 and 443, 32 x 64 26 and 39, 128 x 8 39.5 and 39.3, 8 x 64
+// 13.4 and 12.6, 32 x 16 15.3 and 13.1, 1 x 256 (not taken) 10.8 and 9.7; 8 + 1 heads,
+// 64 x 8 (not taken) 11.8 and 9.9; W = 100, 16 + 8 heads: 128 x 64 (not taken) 55 and
+// 44, 128 x 200 120 and 135.
 constexpr int kExtBandTokens = 8;
 
 // Tiles that see few blocks of keys are left whole: cutting them costs a schedule, a

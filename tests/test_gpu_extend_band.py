@@ -184,3 +184,45 @@ def test_small_values(size):
     err = (got[0].cpu().double() - ref[0]).abs()
     assert (err <= 2.0 ** -8 * ref[0].abs() + (2.0 ** -8 + 2.0 ** -11) * ref[2] + 2.0 ** -25).all()
     _clean()
+
+
+def test_a_wait_that_runs_out():
+    """The test build withholds a tile's keys: the call comes back with a timeout code,
+    and later calls are clean."""
+    import ctypes
+    import time
+
+    from attention_learnable_head_gb300.build import build
+    L = binding.load_library(build(test=True))
+    new, lens = [40] * 140, [60 + i for i in range(140)]
+    c = [x.to(DEV) for x in _extend_case(31, new, lens, 16, 16, 2)]
+    n = sum(new)
+    p = binding.AttnSinkExtendParams(140, n, 16, 2, 64, 16, c[1].shape[0], c[3].shape[1], 100, 0.125)
+    out, lse = torch.zeros(n, 16, 64, dtype=BF, device=DEV), torch.zeros(16, n, device=DEV)
+    ws = torch.empty(L.attn_sink_extend_workspace_size(ctypes.byref(p)), dtype=torch.uint8,
+                     device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def run():
+        before = L.attn_sink_launch_count()
+        st = L.attn_sink_extend(ctypes.byref(p), *(x.data_ptr() for x in c), out.data_ptr(),
+                                lse.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        assert L.attn_sink_launch_count() - before == 3
+        return st
+
+    def error():
+        code = ctypes.c_int(0)
+        return L.attn_sink_device_error(stream, ctypes.byref(code)), code.value
+
+    assert run() == 0 and error() == (0, 0)
+    ref = out.clone()
+    L.attn_sink_test_withhold(1, -1)
+    try:
+        t0 = time.monotonic()
+        assert run() == 0
+        st, code = error()
+        assert time.monotonic() - t0 < 2.0 and st == 5 and code & 0xF00 == 0x100
+    finally:
+        L.attn_sink_test_withhold(-1, -1)
+    out.zero_()
+    assert run() == 0 and error() == (0, 0) and torch.equal(out, ref)
