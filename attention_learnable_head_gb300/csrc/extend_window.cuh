@@ -10,8 +10,8 @@
 // sequence's keys, find zeros there and nothing of another sequence.  A schedule
 // kernel of one CTA lays out the regions and lists every tile as a sequence of
 // its own for the band kernel: its queries and the keys that they see, bottom-right
-// aligned.  Where a block-table entry is outside the cache the
-// gather says so, and the band kernel masks the keys of such entries.
+// aligned.  Where a block-table entry is outside the cache the gather says so, and the
+// band kernel masks the keys of such entries.
 #pragma once
 #include "extend_kernel.cuh"
 #include "fwd_band_kernel.cuh"

@@ -185,7 +185,8 @@ size_t attn_sink_extend_workspace_size(const attn_sink_extend_params* params);
  * the call): token i of sequence b sits at key position L_b - n_b + i and sees
  * the keys up to it, or the last W of them.  n_b = 0 and L_b = 0 are allowed,
  * and n_b > L_b too: a token before the first key sees none and gets out = 0,
- * lse = sink.  Layouts as attn_sink_decode, with q, out [T, heads_q, 64] bf16
+ * lse = sink.  A sink of -inf is none, one of +inf gives out = 0, lse = inf.
+ * Layouts as attn_sink_decode, with q, out [T, heads_q, 64] bf16
  * and lse [heads_q, T] fp32; rows of out and lse behind cu_seqlens_q[B] are
  * left as they were.  Cache rows past a sequence's keys and pages behind every
  * token's window are not used, whatever they hold (block-table entries of such
