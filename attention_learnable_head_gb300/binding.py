@@ -17,7 +17,8 @@ the workspace with torch and raise on a non-zero status.  The entry points of
 their conveniences ``page_plan``, ``qkv_rope``, ``qkv_rope_backward``,
 ``qkv_rope_autograd`` and ``extend`` come after them; a plain call of these goes
 through the native module ``attn_sink_fast`` (``csrc/fast_calls.cpp``) to the same
-entry points.  Every step of the
+entry points; so do those of ``include/attn_sink_cache.h`` (``decode_shared``,
+``page_bounds``, ``select_pages``, ``decode_pages``, ``key_mass``, ``evict``).  Every step of the
 computation runs in the library's CUDA kernels; there is no other code path,
 and loading fails loudly when the library has not been built.
 """
@@ -91,6 +92,59 @@ class AttnSinkExtendParams(ctypes.Structure):
         ("batch", c_int), ("total_q", c_int), ("heads_q", c_int), ("heads_kv", c_int),
         ("head_dim", c_int), ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int),
         ("window", c_int), ("softmax_scale", c_float),
+    ]
+
+
+class AttnSinkSharedParams(ctypes.Structure):
+    """Mirror of ``attn_sink_shared_params`` in include/attn_sink_cache.h."""
+    _fields_ = [
+        ("batch", c_int), ("num_groups", c_int), ("heads_q", c_int), ("heads_kv", c_int),
+        ("head_dim", c_int), ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int),
+        ("softmax_scale", c_float),
+    ]
+
+
+class AttnSinkBoundsParams(ctypes.Structure):
+    """Mirror of ``attn_sink_bounds_params`` in include/attn_sink_cache.h."""
+    _fields_ = [
+        ("batch", c_int), ("heads_kv", c_int), ("head_dim", c_int), ("page_size", c_int),
+        ("num_pages", c_int), ("max_pages", c_int),
+    ]
+
+
+class AttnSinkSelectParams(ctypes.Structure):
+    """Mirror of ``attn_sink_select_params`` in include/attn_sink_cache.h."""
+    _fields_ = [
+        ("batch", c_int), ("heads_q", c_int), ("heads_kv", c_int), ("head_dim", c_int),
+        ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int), ("count", c_int),
+        ("keep_first", c_int), ("keep_last", c_int),
+    ]
+
+
+class AttnSinkPagesParams(ctypes.Structure):
+    """Mirror of ``attn_sink_pages_params`` in include/attn_sink_cache.h."""
+    _fields_ = [
+        ("batch", c_int), ("heads_q", c_int), ("heads_kv", c_int), ("head_dim", c_int),
+        ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int), ("count", c_int),
+        ("softmax_scale", c_float),
+    ]
+
+
+class AttnSinkMassParams(ctypes.Structure):
+    """Mirror of ``attn_sink_mass_params`` in include/attn_sink_cache.h."""
+    _fields_ = [
+        ("batch", c_int), ("total_q", c_int), ("heads_q", c_int), ("heads_kv", c_int),
+        ("head_dim", c_int), ("page_size", c_int), ("num_pages", c_int), ("max_pages", c_int),
+        ("max_keys", c_int), ("accumulate", c_int), ("softmax_scale", c_float),
+    ]
+
+
+class AttnSinkEvictParams(ctypes.Structure):
+    """Mirror of ``attn_sink_evict_params`` in include/attn_sink_cache.h."""
+    _fields_ = [
+        ("batch", c_int), ("heads_kv", c_int), ("head_dim", c_int), ("page_size", c_int),
+        ("num_pages", c_int), ("max_pages", c_int), ("max_keys", c_int), ("budget", c_int),
+        ("keep_first", c_int), ("keep_last", c_int), ("max_freed", c_int),
     ]
 
 
@@ -195,6 +249,21 @@ def load_library(path: str):
     L.attn_sink_extend_workspace_size.restype = c_size_t
     L.attn_sink_extend.argtypes = [PE] + [c_void_p] * 10 + [c_size_t, c_void_p]
     L.attn_sink_extend.restype = c_int
+    for name, params, pointers, work in (
+            ("decode_shared", AttnSinkSharedParams, 10, True),
+            ("page_bounds", AttnSinkBoundsParams, 5, False),
+            ("select_pages", AttnSinkSelectParams, 5, True),
+            ("decode_pages", AttnSinkPagesParams, 9, True),
+            ("key_mass", AttnSinkMassParams, 7, False),
+            ("evict", AttnSinkEvictParams, 9, True)):
+        f = getattr(L, "attn_sink_" + name)
+        f.argtypes = ([ctypes.POINTER(params)] + [c_void_p] * pointers +
+                      ([c_void_p, c_size_t] if work else []) + [c_void_p])
+        f.restype = c_int
+        if work:
+            f = getattr(L, f"attn_sink_{name}_workspace_size")
+            f.argtypes = [ctypes.POINTER(params)]
+            f.restype = c_size_t
     if hasattr(L, "attn_sink_test_withhold"):
         L.attn_sink_test_withhold.argtypes = [c_int, c_int]
         L.attn_sink_test_withhold.restype = c_int
@@ -630,7 +699,12 @@ def _fast():
         spec.loader.exec_module(module)
         module.init(*(ctypes.cast(f, c_void_p).value for f in (
             L.attn_sink_page_plan, L.attn_sink_qkv_rope, L.attn_sink_qkv_rope_bwd_workspace_size,
-            L.attn_sink_qkv_rope_bwd, L.attn_sink_extend_workspace_size, L.attn_sink_extend)))
+            L.attn_sink_qkv_rope_bwd, L.attn_sink_extend_workspace_size, L.attn_sink_extend,
+            L.attn_sink_decode_shared_workspace_size, L.attn_sink_decode_shared,
+            L.attn_sink_page_bounds, L.attn_sink_select_pages_workspace_size,
+            L.attn_sink_select_pages, L.attn_sink_decode_pages_workspace_size,
+            L.attn_sink_decode_pages, L.attn_sink_key_mass, L.attn_sink_evict_workspace_size,
+            L.attn_sink_evict)))
         _FAST = module
     return _FAST
 
@@ -995,3 +1069,304 @@ def extend(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, sink, *, wi
             out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev.index)),
             "attn_sink_extend")
     return out, lse
+
+
+# ----------------------------------------------------------------------------- include/attn_sink_cache.h
+def attn_sink_decode_shared_workspace_size(params: AttnSinkSharedParams) -> int:
+    return int(lib().attn_sink_decode_shared_workspace_size(_pref(params)))
+
+
+def attn_sink_decode_shared(params: AttnSinkSharedParams, q, k_cache, v_cache, block_table,
+                            seq_lens, cu_groups, prefix_lens, sink, out, lse, workspace,
+                            workspace_bytes: int, stream=None) -> int:
+    return lib().attn_sink_decode_shared(_pref(params), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                         _ptr(block_table), _ptr(seq_lens), _ptr(cu_groups),
+                                         _ptr(prefix_lens), _ptr(sink), _ptr(out), _ptr(lse),
+                                         _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def attn_sink_page_bounds(params: AttnSinkBoundsParams, k_cache, block_table, cached_lens,
+                          seq_lens, bounds, stream=None) -> int:
+    return lib().attn_sink_page_bounds(_pref(params), _ptr(k_cache), _ptr(block_table),
+                                       _ptr(cached_lens), _ptr(seq_lens), _ptr(bounds),
+                                       _stream(stream))
+
+
+def attn_sink_select_pages_workspace_size(params: AttnSinkSelectParams) -> int:
+    return int(lib().attn_sink_select_pages_workspace_size(_pref(params)))
+
+
+def attn_sink_select_pages(params: AttnSinkSelectParams, q, bounds, block_table, seq_lens,
+                           selected, workspace, workspace_bytes: int, stream=None) -> int:
+    return lib().attn_sink_select_pages(_pref(params), _ptr(q), _ptr(bounds), _ptr(block_table),
+                                        _ptr(seq_lens), _ptr(selected), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream))
+
+
+def attn_sink_decode_pages_workspace_size(params: AttnSinkPagesParams) -> int:
+    return int(lib().attn_sink_decode_pages_workspace_size(_pref(params)))
+
+
+def attn_sink_decode_pages(params: AttnSinkPagesParams, q, k_cache, v_cache, block_table,
+                           seq_lens, selected, sink, out, lse, workspace, workspace_bytes: int,
+                           stream=None) -> int:
+    return lib().attn_sink_decode_pages(_pref(params), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                        _ptr(block_table), _ptr(seq_lens), _ptr(selected),
+                                        _ptr(sink), _ptr(out), _ptr(lse), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream))
+
+
+def attn_sink_key_mass(params: AttnSinkMassParams, q, k_cache, block_table, seq_lens,
+                       cu_seqlens_q, lse, mass, stream=None) -> int:
+    return lib().attn_sink_key_mass(_pref(params), _ptr(q), _ptr(k_cache), _ptr(block_table),
+                                    _ptr(seq_lens), _ptr(cu_seqlens_q), _ptr(lse), _ptr(mass),
+                                    _stream(stream))
+
+
+def attn_sink_evict_workspace_size(params: AttnSinkEvictParams) -> int:
+    return int(lib().attn_sink_evict_workspace_size(_pref(params)))
+
+
+def attn_sink_evict(params: AttnSinkEvictParams, k_cache, v_cache, block_table, seq_lens, mass,
+                    mass_out, new_lens, freed_pages, num_freed, workspace, workspace_bytes: int,
+                    stream=None) -> int:
+    return lib().attn_sink_evict(_pref(params), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                 _ptr(seq_lens), _ptr(mass), _ptr(mass_out), _ptr(new_lens),
+                                 _ptr(freed_pages), _ptr(num_freed), _ptr(workspace),
+                                 int(workspace_bytes), _stream(stream))
+
+
+def _paged(k_cache, v_cache, block_table, seq_lens, dev):
+    """Checks of a paged cache and its tables; (batch, pages, page size, kv heads,
+    columns).  v_cache may be None."""
+    b, = _dims("seq_lens", seq_lens, 1)
+    pages, page, hkv, _ = _dims("k_cache", k_cache, 4)
+    cols = _dims("block_table", block_table, 2)[1]
+    _want("k_cache", k_cache, torch.bfloat16, dev, (pages, page, hkv, 64))
+    if v_cache is not None:
+        _want("v_cache", v_cache, torch.bfloat16, dev, (pages, page, hkv, 64))
+    _want("block_table", block_table, torch.int32, dev, (b, cols))
+    _want("seq_lens", seq_lens, torch.int32, dev, (b,))
+    _in_32_bits(seq_lens=b, k_cache=max(pages, page, hkv), block_table=cols)
+    return b, pages, page, hkv, cols
+
+
+def decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, sink, *,
+                  softmax_scale: float | None = None, out=None, lse=None, stream=None):
+    """(out, lse) of one decode step over a paged cache in which groups of sequences
+    share their first keys (attn_sink_decode_shared): decode with, beside its
+    arguments, cu_groups [P + 1] int32, the groups' first sequences from 0 to B, and
+    prefix_lens [P] int32, how many keys each group shares.  Those are read through
+    the block-table row of the group's first sequence, once for all of it."""
+    if softmax_scale is None:
+        softmax_scale = 0.125
+    if stream is None:
+        r = (_FAST or _fast()).decode_shared(q, k_cache, v_cache, block_table, seq_lens, cu_groups,
+                                             prefix_lens, sink, softmax_scale, out, lse)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_decode_shared")
+            return r
+    dev, i32 = q.device, torch.int32
+    b, pages, page, hkv, cols = _paged(k_cache, v_cache, block_table, seq_lens, dev)
+    hq = _dims("q", q, 3)[1]
+    groups, = _dims("prefix_lens", prefix_lens, 1)
+    _want("q", q, torch.bfloat16, dev, (b, hq, 64))
+    _want("cu_groups", cu_groups, i32, dev, (groups + 1,))
+    _want("prefix_lens", prefix_lens, i32, dev, (groups,))
+    _want("sink", sink, torch.float32, dev, (hq,))
+    _in_32_bits(q=hq, prefix_lens=groups)
+    out, lse = _results(out, lse, q, dev, stream)
+    p = AttnSinkSharedParams(b, groups, hq, hkv, 64, page, pages, cols, softmax_scale)
+    with _on(dev, stream):
+        nbytes = attn_sink_decode_shared_workspace_size(p)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(attn_sink_decode_shared(p, q, k_cache, v_cache, block_table, seq_lens, cu_groups,
+                                       prefix_lens, sink, out, lse, ws, nbytes,
+                                       _raw_stream(dev.index)), "attn_sink_decode_shared")
+    return out, lse
+
+
+def _results(out, lse, q, dev, stream):
+    """out [T, H_q, 64] and lse [H_q, T] of a call with these queries: the caller's own,
+    checked, or new ones."""
+    t, hq, _ = q.shape
+    if out is not None:
+        _want("out", out, torch.bfloat16, dev, (t, hq, 64))
+    if lse is not None:
+        _want("lse", lse, torch.float32, dev, (hq, t))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((t, hq, 64), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
+    return out, lse
+
+
+def page_bounds(k_cache, block_table, cached_lens, seq_lens, bounds, *, stream=None) -> None:
+    """Bring the bounds [pages, heads_kv, 2, 64] bf16 of a paged cache's keys (the
+    elementwise minimum and maximum over each page) up to date after keys
+    [cached_lens[b], seq_lens[b]) of every sequence were written
+    (attn_sink_page_bounds); in place."""
+    if stream is None:
+        r = (_FAST or _fast()).page_bounds(k_cache, block_table, cached_lens, seq_lens, bounds)
+        if r is not None:
+            _check(r, "attn_sink_page_bounds")
+            return
+    dev = k_cache.device
+    b, pages, page, hkv, cols = _paged(k_cache, None, block_table, seq_lens, dev)
+    _want("cached_lens", cached_lens, torch.int32, dev, (b,))
+    _want("bounds", bounds, torch.bfloat16, dev, (pages, hkv, 2, 64))
+    p = AttnSinkBoundsParams(b, hkv, 64, page, pages, cols)
+    with _on(dev, stream):
+        _check(attn_sink_page_bounds(p, k_cache, block_table, cached_lens, seq_lens, bounds,
+                                     _raw_stream(dev.index)), "attn_sink_page_bounds")
+
+
+def select_pages(q, bounds, block_table, seq_lens, *, count: int, page_size: int,
+                 keep_first: int = 1, keep_last: int = 1, stream=None):
+    """The pages of each sequence and kv head whose bounds promise the largest scores
+    for the new token's queries q [B, H_q, 64] (attn_sink_select_pages): selected
+    [B, heads_kv, count] int32, columns of the block table in ascending order, -1
+    behind the last.  The first keep_first and the last keep_last pages are always
+    there."""
+    if stream is None:
+        r = (_FAST or _fast()).select_pages(q, bounds, block_table, seq_lens, count, page_size,
+                                            keep_first, keep_last)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_select_pages")
+            return r
+    dev, i32 = q.device, torch.int32
+    b, = _dims("seq_lens", seq_lens, 1)
+    hq = _dims("q", q, 3)[1]
+    pages, hkv = _dims("bounds", bounds, 4)[:2]
+    cols = _dims("block_table", block_table, 2)[1]
+    _want("q", q, torch.bfloat16, dev, (b, hq, 64))
+    _want("bounds", bounds, torch.bfloat16, dev, (pages, hkv, 2, 64))
+    _want("block_table", block_table, i32, dev, (b, cols))
+    _want("seq_lens", seq_lens, i32, dev, (b,))
+    if count < 1:
+        raise ValueError(f"count is {count}")
+    _in_32_bits(seq_lens=b, q=hq, bounds=max(pages, hkv), block_table=cols, count=count,
+                page_size=page_size, keep_first=keep_first, keep_last=keep_last)
+    p = AttnSinkSelectParams(b, hq, hkv, 64, page_size, pages, cols, count, keep_first, keep_last)
+    with _on(dev, stream):
+        selected = torch.empty((b, hkv, count), dtype=i32, device=dev)
+        nbytes = attn_sink_select_pages_workspace_size(p)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(attn_sink_select_pages(p, q, bounds, block_table, seq_lens, selected, ws, nbytes,
+                                      _raw_stream(dev.index)), "attn_sink_select_pages")
+    return selected
+
+
+def decode_pages(q, k_cache, v_cache, block_table, seq_lens, selected, sink, *,
+                 softmax_scale: float | None = None, out=None, lse=None, stream=None):
+    """(out, lse) of one decode step over the selected pages alone
+    (attn_sink_decode_pages): decode with, beside its arguments, selected [B,
+    heads_kv, count] int32, the columns of the block table each kv head reads (as
+    select_pages gives them; a negative entry is none)."""
+    if softmax_scale is None:
+        softmax_scale = 0.125
+    if stream is None:
+        r = (_FAST or _fast()).decode_pages(q, k_cache, v_cache, block_table, seq_lens, selected,
+                                            sink, softmax_scale, out, lse)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_decode_pages")
+            return r
+    dev = q.device
+    b, pages, page, hkv, cols = _paged(k_cache, v_cache, block_table, seq_lens, dev)
+    hq = _dims("q", q, 3)[1]
+    count = _dims("selected", selected, 3)[2]
+    _want("q", q, torch.bfloat16, dev, (b, hq, 64))
+    _want("selected", selected, torch.int32, dev, (b, hkv, count))
+    _want("sink", sink, torch.float32, dev, (hq,))
+    _in_32_bits(q=hq, selected=count)
+    out, lse = _results(out, lse, q, dev, stream)
+    p = AttnSinkPagesParams(b, hq, hkv, 64, page, pages, cols, count, softmax_scale)
+    with _on(dev, stream):
+        nbytes = attn_sink_decode_pages_workspace_size(p)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(attn_sink_decode_pages(p, q, k_cache, v_cache, block_table, seq_lens, selected,
+                                      sink, out, lse, ws, nbytes, _raw_stream(dev.index)),
+               "attn_sink_decode_pages")
+    return out, lse
+
+
+def key_mass(q, k_cache, block_table, seq_lens, cu_seqlens_q, lse, mass, *,
+             accumulate: bool = True, softmax_scale: float | None = None, stream=None):
+    """The attention weight each cached key gets from the new tokens, summed over them
+    and over the query heads of its kv head (attn_sink_key_mass): added to mass [B,
+    heads_kv, C] fp32 in place (accumulate False: written, the rest of a row zero).
+    q [T, H_q, 64] packed by cu_seqlens_q [B + 1] int32 and lse [H_q, T] as extend,
+    decode and the calls above took and gave them.  Returns mass."""
+    if softmax_scale is None:
+        softmax_scale = 0.125
+    if stream is None:
+        r = (_FAST or _fast()).key_mass(q, k_cache, block_table, seq_lens, cu_seqlens_q, lse, mass,
+                                        accumulate, softmax_scale)
+        if r is not None:
+            _check(r, "attn_sink_key_mass")
+            return mass
+    dev = q.device
+    b, pages, page, hkv, cols = _paged(k_cache, None, block_table, seq_lens, dev)
+    t, hq, _ = _dims("q", q, 3)
+    keys = _dims("mass", mass, 3)[2]
+    _want("q", q, torch.bfloat16, dev, (t, hq, 64))
+    _want("cu_seqlens_q", cu_seqlens_q, torch.int32, dev, (b + 1,))
+    _want("lse", lse, torch.float32, dev, (hq, t))
+    _want("mass", mass, torch.float32, dev, (b, hkv, keys))
+    _in_32_bits(q=max(t, hq), mass=keys)
+    p = AttnSinkMassParams(b, t, hq, hkv, 64, page, pages, cols, keys, int(bool(accumulate)),
+                           softmax_scale)
+    with _on(dev, stream):
+        _check(attn_sink_key_mass(p, q, k_cache, block_table, seq_lens, cu_seqlens_q, lse, mass,
+                                  _raw_stream(dev.index)), "attn_sink_key_mass")
+    return mass
+
+
+class Evicted(NamedTuple):
+    """What evict leaves beside the caches (see there)."""
+    seq_lens: torch.Tensor       # [B] int32: min(length, budget)
+    mass: torch.Tensor           # [B, heads_kv, C] fp32: the kept keys' at their new places
+    freed_pages: torch.Tensor    # [B * max_pages] int32, -1 behind the last
+    num_freed: torch.Tensor      # [1] int32
+
+
+def evict(k_cache, v_cache, block_table, seq_lens, mass, *, budget: int, keep_first: int = 0,
+          keep_last: int = 0, stream=None) -> Evicted:
+    """Cut every sequence down to budget keys (attn_sink_evict): each kv head keeps its
+    first keep_first, its last keep_last and otherwise those with the largest mass
+    [B, heads_kv, C] fp32; the kept ones at positions >= budget move into the holes
+    below, in k_cache and v_cache in place.  freed_pages are the pages that hold no
+    key any more, a free list for page_plan.  A head's keys are then no longer in the
+    order of their tokens: no windows on such a cache, bounds to be made anew
+    (page_bounds with cached_lens = 0), and new tokens go on with positions of their
+    own."""
+    if stream is None:
+        r = (_FAST or _fast()).evict(k_cache, v_cache, block_table, seq_lens, mass, budget,
+                                     keep_first, keep_last)
+        if r is not None:
+            if type(r) is int:
+                _check(r, "attn_sink_evict")
+            return Evicted(*r)
+    dev, i32 = k_cache.device, torch.int32
+    b, pages, page, hkv, cols = _paged(k_cache, v_cache, block_table, seq_lens, dev)
+    keys = _dims("mass", mass, 3)[2]
+    _want("mass", mass, torch.float32, dev, (b, hkv, keys))
+    _in_32_bits(mass=keys, budget=budget, keep_first=keep_first, keep_last=keep_last,
+                block_table=b * cols)
+    p = AttnSinkEvictParams(b, hkv, 64, page, pages, cols, keys, budget, keep_first, keep_last,
+                            b * cols)
+    with _on(dev, stream):
+        mass_out = torch.empty_like(mass)
+        lens = torch.empty(b, dtype=i32, device=dev)
+        freed = torch.empty(b * cols, dtype=i32, device=dev)
+        count = torch.empty(1, dtype=i32, device=dev)
+        nbytes = attn_sink_evict_workspace_size(p)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(attn_sink_evict(p, k_cache, v_cache, block_table, seq_lens, mass, mass_out, lens,
+                               freed, count, ws, nbytes, _raw_stream(dev.index)),
+               "attn_sink_evict")
+    return Evicted(lens, mass_out, freed, count)

@@ -36,7 +36,8 @@ def _nvcc() -> str:
 def _sources() -> list[str]:
     files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
              if f.endswith((".cu", ".cuh", ".h"))]
-    files += [os.path.join(INCLUDE, f) for f in ("attn_sink.h", "attn_sink_step.h")]
+    files += [os.path.join(INCLUDE, f) for f in ("attn_sink.h", "attn_sink_step.h",
+                                                   "attn_sink_cache.h")]
     return files
 
 
@@ -107,7 +108,8 @@ def build(force: bool = False, verbose: bool = False, test: bool = False) -> str
             cmd.insert(1, "-Xptxas=-v")
         jobs.append((_start(cmd, verbose), tmp, path))
     fast = not test and (force or fast_built_for() != fast_target() or not _up_to_date(
-        FAST_PATH, [FAST_SOURCE, os.path.join(INCLUDE, "attn_sink_step.h")]))
+        FAST_PATH, [FAST_SOURCE, os.path.join(INCLUDE, "attn_sink_step.h"),
+                    os.path.join(INCLUDE, "attn_sink_cache.h")]))
     if fast:
         tmp = FAST_PATH + ".tmp"
         jobs.append((_start(_fast_command(tmp), verbose), tmp, FAST_PATH))

@@ -1,6 +1,6 @@
 // Host side of libattn_sink.so: argument validation, TMA tensor-map encoding,
 // launch configuration and workspace carving for the C ABI in attn_sink.h (that
-// of attn_sink_step.h is in step_api.cuh).
+// of attn_sink_step.h is in step_api.cuh, of attn_sink_cache.h in cache_api.cuh).
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <nvtx3/nvToolsExt.h>
@@ -13,18 +13,23 @@
 #include <vector>
 
 #include "attn_sink.h"
+#include "attn_sink_cache.h"
 #include "attn_sink_step.h"
+#include "bounds_kernel.cuh"
 #include "bwd_dq_kernel.cuh"
 #include "bwd_kernel.cuh"
 #include "decode_kernel.cuh"
+#include "evict_kernel.cuh"
 #include "extend_kernel.cuh"
 #include "extend_window.cuh"
 #include "fwd_band_kernel.cuh"
 #include "fwd_kernel.cuh"
+#include "mass_kernel.cuh"
 #include "merge_kernel.cuh"
 #include "plan_kernel.cuh"
 #include "rope_kernel.cuh"
 #include "schedule_kernel.cuh"
+#include "shared_kernel.cuh"
 
 // Device word a kernel sets when it gives up on a bounded wait.
 __device__ int g_attn_sink_device_error = 0;
@@ -1151,3 +1156,4 @@ int attn_sink_device_error(void* stream, int* code) {
 }  // extern "C"
 
 #include "step_api.cuh"
+#include "cache_api.cuh"

@@ -1,0 +1,431 @@
+// Bounds of the keys of a page, and the pages whose bounds promise a decode step's
+// largest scores, sm_103a.
+//
+// For any key k of a page with elementwise bounds lo <= k <= hi,
+//   q.k <= sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d,
+// a dot product of 128 numbers: (min(q, 0), max(q, 0)) with the page's 256 bytes (lo,
+// hi).  A page of 16 keys is so judged by 1/16 of what its keys and values weigh.
+//
+// Bounds: eight lanes of 16 bytes read a head's key, a warp four heads of a page, key
+// by key, all of a page's loads on their way at once up to 16.
+//
+// Scores: pages are the 16 rows, the group's heads the 8 columns of warp-level
+// products m16n8k16 (a tcgen05 product has 64 rows of one operand at least, and its
+// operands would go through shared memory: this is bound by the bounds' bytes).  As a
+// dot product does not care for the order of its terms, the k index is permuted so
+// that a lane's fragments are whole 16-byte chunks of a page's bounds: chunk 4 u + t of
+// the 16 for lane t of four, loaded straight into registers.
+//
+// Selection: one CTA for each (sequence, kv head) finds the score of the last page it
+// takes bit by bit (topk.cuh).  The scores come from fp32 sums, so every page within
+// twice their error of that one is computed again in 64 bits, where any are left out
+// (a fraction of a page a row, on average).  What is selected goes through a bitmap to
+// ascending order.
+#pragma once
+#include <climits>
+#include <cuda_bf16.h>
+#include "sm103_ptx.cuh"
+#include "topk.cuh"
+
+namespace attn_sink {
+
+// ----------------------------------------------------------------------------- bounds
+constexpr int kBoundsThreads = 256;
+
+struct BoundsParams {
+  const __nv_bfloat16* k_cache;   // [num_pages][page_size][H_kv][64]
+  const int* block_table;         // [B][max_pages]
+  const int* cached;              // [B]
+  const int* seq_lens;            // [B]
+  __nv_bfloat16* bounds;          // [num_pages][H_kv][2][64]
+  int* err;
+  int batch, heads_kv, page_size, num_pages, max_pages;
+};
+
+__global__ void __launch_bounds__(kBoundsThreads)
+attn_sink_page_bounds_kernel(const __grid_constant__ BoundsParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quads = (p.heads_kv + 3) / 4;
+  const int cap = p.max_pages * p.page_size;
+  const unsigned warps = gridDim.x * (kBoundsThreads / 32);
+  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
+    const int l0 = __ldg(p.seq_lens + b), c0 = __ldg(p.cached + b);
+    const int len = max(0, min(l0, cap)), from = max(0, min(c0, len));
+    if ((len != l0 || c0 < 0) && threadIdx.x == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+    if (from >= len) continue;
+    const int col0 = from / p.page_size, cols = (len - 1) / p.page_size + 1 - col0;
+    const unsigned long long units = (unsigned long long)cols * (unsigned)quads;
+    for (unsigned long long u = blockIdx.x * (kBoundsThreads / 32) + warp; u < units; u += warps) {
+      const int at = (int)(u / (unsigned)quads);
+      const int h = 4 * (int)(u - (unsigned long long)at * (unsigned)quads) + (lane >> 3);
+      const int col = col0 + at;
+      const int page = __ldg(p.block_table + (size_t)b * p.max_pages + col);
+      if ((unsigned)page >= (unsigned)p.num_pages) {
+        if (lane == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+        continue;
+      }
+      if (h >= p.heads_kv) continue;
+      const int keys = min(p.page_size, len - col * p.page_size);
+      const size_t step = (size_t)p.heads_kv * 8;           // 16-byte chunks from key to key
+      const uint4* src = reinterpret_cast<const uint4*>(p.k_cache) +
+                         (size_t)page * p.page_size * step + h * 8 + (lane & 7);
+      __nv_bfloat162 lo[4], hi[4];
+      const uint4 v0 = __ldg(src);
+      const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w};
+      #pragma unroll
+      for (int e = 0; e < 4; ++e) lo[e] = hi[e] = *reinterpret_cast<const __nv_bfloat162*>(&w0[e]);
+      // 16 keys at a time; one behind the last stands for it
+      for (int j = 0; j < keys; j += 16) {
+        uint4 v[16];
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __ldg(src + min(j + i, keys - 1) * step);
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+            lo[e] = __hmin2_nan(lo[e], x);
+            hi[e] = __hmax2_nan(hi[e], x);
+          }
+        }
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.bounds) + ((size_t)page * p.heads_kv + h) * 16 +
+                   (lane & 7);
+      dst[0] = *reinterpret_cast<const uint4*>(lo);
+      dst[8] = *reinterpret_cast<const uint4*>(hi);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- scores
+constexpr int kScoreThreads = 256;
+
+struct SelectParams {
+  const __nv_bfloat16* q;         // [B][H_q][64]
+  const __nv_bfloat16* bounds;    // [num_pages][H_kv][2][64]
+  const int* block_table;         // [B][max_pages]
+  const int* seq_lens;            // [B]
+  float* scores;                  // [B][H_kv][max_pages]; -inf: no page in the cache
+  unsigned* peak;                 // [B][H_kv][tiles] largest |bound| of 16 pages, bf16 bits
+  unsigned long long* exact;      // [B][H_kv][max_pages] ordered() of 64-bit scores, some
+  int* selected;                  // [B][H_kv][count]
+  int* err;
+  int batch, heads_q, heads_kv, group, page_size, num_pages, max_pages, tiles;
+  int count, keep_first, keep_last;
+};
+
+__device__ __forceinline__ int select_len(const SelectParams& p, int b, bool* bad) {
+  const int len = __ldg(p.seq_lens + b), cap = p.max_pages * p.page_size;
+  *bad = len < 0 || len > cap;
+  return max(0, min(len, cap));
+}
+
+__global__ void __launch_bounds__(kScoreThreads)
+attn_sink_page_scores_kernel(const __grid_constant__ SelectParams p) {
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const unsigned id = blockIdx.x * (kScoreThreads / 32) + warp;
+  const unsigned step = gridDim.x * (kScoreThreads / 32) / (unsigned)p.heads_kv;
+  const unsigned first = id / (unsigned)p.heads_kv;
+  const int h = (int)(id - first * (unsigned)p.heads_kv);
+  const int b = blockIdx.y;
+  bool bad;
+  const int len = select_len(p, b, &bad);
+  if (bad && id == 0 && lane == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  const int have = (len + p.page_size - 1) / p.page_size;
+  if (have <= p.count || first >= step) return;             // all are selected
+  // B: head g, the dimensions of this lane's chunks; 0 for the columns behind the group
+  uint32_t qb[16];
+  #pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (g < p.group)
+      v = __ldg(reinterpret_cast<const uint4*>(p.q) +
+                ((size_t)b * p.heads_q + h * p.group + g) * 8 + 4 * u + t);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+      const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+      const __nv_bfloat162 lo = __hmin2_nan(x, zero), hi = __hmax2_nan(x, zero);
+      qb[4 * u + e] = *reinterpret_cast<const uint32_t*>(&lo);
+      qb[8 + 4 * u + e] = *reinterpret_cast<const uint32_t*>(&hi);
+    }
+  }
+  const size_t row = (size_t)b * p.heads_kv + h;
+  const int* table = p.block_table + (size_t)b * p.max_pages;
+  const uint4* bounds = reinterpret_cast<const uint4*>(p.bounds) + (size_t)h * 16 + t;
+  const size_t pstep = (size_t)p.heads_kv * 16;
+  auto entry = [&](unsigned tile) {                         // of page 16 tile + lane % 16
+    const int c = 16 * (int)tile + (lane & 15);
+    return c < have ? __ldg(table + c) : -1;
+  };
+  const unsigned tiles = (unsigned)(have + 15) / 16;
+  int next = first < tiles ? entry(first) : -1;
+  for (unsigned tile = first; tile < tiles; tile += step) {
+    const int e0 = __shfl_sync(0xffffffffu, next, g), e1 = __shfl_sync(0xffffffffu, next, g + 8);
+    if (tile + step < tiles) next = entry(tile + step);
+    const bool in0 = (unsigned)e0 < (unsigned)p.num_pages, in1 = (unsigned)e1 < (unsigned)p.num_pages;
+    uint4 v[2][4];
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[0][u] = in0 ? __ldg(bounds + e0 * pstep + 4 * u) : make_uint4(0, 0, 0, 0);
+      v[1][u] = in1 ? __ldg(bounds + e1 * pstep + 4 * u) : make_uint4(0, 0, 0, 0);
+    }
+    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t peak = 0;
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      mma_16816_bf16(c, v[0][u].x, v[1][u].x, v[0][u].y, v[1][u].y, qb[4 * u], qb[4 * u + 1]);
+      mma_16816_bf16(c, v[0][u].z, v[1][u].z, v[0][u].w, v[1][u].w, qb[4 * u + 2], qb[4 * u + 3]);
+      #pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        peak = __vmaxu2(peak, __vmaxu2(v[r][u].x & 0x7fff7fffu, v[r][u].y & 0x7fff7fffu));
+        peak = __vmaxu2(peak, __vmaxu2(v[r][u].z & 0x7fff7fffu, v[r][u].w & 0x7fff7fffu));
+      }
+    }
+    // the largest head's score (a NaN among them counts: the row's peak says so too)
+    #pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float m = 2 * t < p.group ? c[2 * r] : -INFINITY;
+      if (2 * t + 1 < p.group) m = fmaxf(m, c[2 * r + 1]);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int at = 16 * (int)tile + g + 8 * r;
+      if (t == 0 && at < have) p.scores[row * p.max_pages + at] = (r ? in1 : in0) ? m : -INFINITY;
+    }
+    if (t == 0 && ((16 * (int)tile + g < have && !in0) || (16 * (int)tile + g + 8 < have && !in1)))
+      atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+    peak = __reduce_max_sync(0xffffffffu, max(peak & 0xffffu, peak >> 16));
+    if (lane == 0) p.peak[row * p.tiles + tile] = peak;
+  }
+}
+
+// ----------------------------------------------------------------------------- selection
+constexpr int kSelectStage = 12288;     // scores that a CTA keeps in shared memory
+constexpr int kSelectBand = 256;        // pages at the border that it ranks there
+
+// The 64-bit score of a page, by a whole warp.
+__device__ __forceinline__ unsigned long long page_score_exact(const SelectParams& p, int b, int h,
+                                                               int col) {
+  const int lane = threadIdx.x & 31;
+  const int page = __ldg(p.block_table + (size_t)b * p.max_pages + col);
+  if ((unsigned)page >= (unsigned)p.num_pages) return ordered(-(double)INFINITY);
+  const uint32_t* src =
+      reinterpret_cast<const uint32_t*>(p.bounds) + ((size_t)page * p.heads_kv + h) * 64 + lane;
+  const uint32_t lo = __ldg(src), hi = __ldg(src + 32);
+  unsigned long long best = 0;
+  for (int i = 0; i < p.group; ++i) {
+    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(p.q) +
+                             ((size_t)b * p.heads_q + h * p.group + i) * 32 + lane);
+    const float q0 = bf16_lo(q), q1 = bf16_hi(q);
+    // products of two bf16 are exact in fp64, and with usual exponents the sums are too
+    const float p0 = q0 > 0.0f || q0 != q0 ? q0 : 0.0f, n0 = q0 < 0.0f || q0 != q0 ? q0 : 0.0f;
+    const float p1 = q1 > 0.0f || q1 != q1 ? q1 : 0.0f, n1 = q1 < 0.0f || q1 != q1 ? q1 : 0.0f;
+    double s = (double)p0 * bf16_lo(hi) + (double)n0 * bf16_lo(lo);
+    s += (double)p1 * bf16_hi(hi) + (double)n1 * bf16_hi(lo);
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const unsigned long long o = ordered(s);
+    best = o > best ? o : best;
+  }
+  return best;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
+attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ uint32_t s_score[];                     // [min(max_pages, kSelectStage)]
+  __shared__ int s_sum[2][kThreads / 32];
+  __shared__ uint32_t s_sure[kThreads], s_tie[kThreads];    // bitmaps of 32 kThreads pages
+  __shared__ unsigned long long s_key[kSelectBand];
+  __shared__ int s_at[kSelectBand];
+  __shared__ int s_many;
+  __shared__ unsigned s_low, s_peak;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int b = (int)(blockIdx.x / (unsigned)p.heads_kv);
+  const int h = (int)(blockIdx.x - (unsigned)b * (unsigned)p.heads_kv);
+  const size_t row = blockIdx.x;
+  int* out = p.selected + row * p.count;
+  bool bad;
+  const int have = (select_len(p, b, &bad) + p.page_size - 1) / p.page_size;
+  if (have <= p.count) {
+    for (int i = tid; i < p.count; i += kThreads) out[i] = i < have ? i : -1;
+    grid_dependency_wait();               // not to end before the kernel in front does
+    return;
+  }
+  for (int i = tid; i < p.keep_first; i += kThreads) out[i] = i;
+  for (int i = tid; i < p.keep_last; i += kThreads)
+    out[p.count - p.keep_last + i] = have - p.keep_last + i;
+  const int n = have - p.keep_first - p.keep_last;          // pages between them
+  const int need = p.count - p.keep_first - p.keep_last;    // < n
+  if (need == 0) {
+    grid_dependency_wait();
+    return;
+  }
+  // the largest sum of |q| of a head
+  float norm = 0.0f;
+  for (int i = 0; i < p.group; ++i) {
+    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(p.q) +
+                             ((size_t)b * p.heads_q + h * p.group + i) * 32 + lane);
+    float a = fabsf(bf16_lo(q)) + fabsf(bf16_hi(q));
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+    norm = a > norm || a != a ? a : norm;
+  }
+  if (tid == 0) {
+    s_many = 0;
+    s_low = 0xFFFFFFFFu;
+    s_peak = 0;
+  }
+  grid_dependency_wait();                                   // the scores
+  const float* scores = p.scores + row * p.max_pages + p.keep_first;
+  const bool staged = n <= kSelectStage;
+  if (staged)
+    for (int i = tid; i < n; i += kThreads) s_score[i] = ordered(__ldcg(scores + i));
+  unsigned peak = 0;
+  for (int i = tid; i < (have + 15) / 16; i += kThreads)
+    peak = max(peak, __ldcg(p.peak + row * p.tiles + i));
+  peak = __reduce_max_sync(0xffffffffu, peak);
+  __syncthreads();
+  if (lane == 0) atomicMax(&s_peak, peak);
+  auto at = [&](int i) { return staged ? s_score[i] : ordered(__ldcg(scores + i)); };
+  int turn = 0;
+  bool split;
+  const uint32_t bound = block_nth_largest<kThreads, uint32_t>(
+      need, [&](auto&& take) {
+        for (int i = tid; i < n; i += kThreads) take(at(i));
+      }, s_sum, &turn, &split);
+  // the smallest score that is taken
+  uint32_t low = 0xFFFFFFFFu;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint32_t v = at(i);
+    if (v >= bound) low = min(low, v);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) atomicMin(&s_low, low);
+  __syncthreads();
+  // No score is further off than the rounding of its sums: 8 products of 16 terms, each
+  // sum cut below 2^-23 of what the terms' sizes add up to at most.
+  const float most = norm * __uint_as_float(s_peak << 16);
+  const float off = most * 0x1p-15f;                        // twice that, for both sides
+  const float last = unordered(s_low);
+  uint32_t from = s_low, upto = s_low;                      // the border, both ends inside
+  if (!(most < 1e37f)) {                                    // infinities, NaN
+    from = 0;
+    upto = 0xFFFFFFFFu;
+  } else if (off > 0.0f) {
+    from = ordered(__fsub_rd(last, off));
+    upto = ordered(__fadd_ru(last, off));
+  }
+  int sure = 0, border = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint32_t v = at(i);
+    sure += v > upto;
+    border += v >= from && v <= upto;
+  }
+  sure = block_sum<kThreads>(sure, s_sum, &turn);
+  border = block_sum<kThreads>(border, s_sum, &turn);
+  const int left = need - sure;                             // of the border, <= border
+  // which of the border: all, by their ranks in shared memory, or by a 64-bit bound
+  const bool again = left < border && (off > 0.0f || !(most < 1e37f));
+  const bool ranked = again && border <= kSelectBand;
+  const unsigned long long* exact = p.exact + row * p.max_pages;
+  unsigned long long bound64 = 0;
+  if (again) {
+    for (int i0 = tid - lane; i0 < n; i0 += kThreads) {
+      const int i = i0 + lane;
+      const uint32_t v = i < n ? at(i) : 0;
+      unsigned todo = __ballot_sync(0xffffffffu, i < n && v >= from && v <= upto);
+      while (todo != 0) {
+        const int j = i0 + __ffs(todo) - 1;
+        todo &= todo - 1;
+        const unsigned long long key = page_score_exact(p, b, h, p.keep_first + j);
+        if (lane != 0) continue;
+        if (ranked) {
+          const int x = atomicAdd(&s_many, 1);              // their order does not matter
+          s_key[x] = key;
+          s_at[x] = j;
+        } else {
+          p.exact[row * p.max_pages + j] = key;
+        }
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    if (!ranked) {
+      bool whole;
+      bound64 = block_nth_largest<kThreads, unsigned long long>(
+          left, [&](auto&& take) {
+            for (int i = tid; i < n; i += kThreads) {
+              const uint32_t v = at(i);
+              if (v >= from && v <= upto) take(exact[i]);
+            }
+          }, s_sum, &turn, &whole);
+      if (whole && bound64 > 0) --bound64;                  // all at or above it: none is a tie
+    }
+  }
+  // Taken for sure, or one of equals of which the first ones are taken?
+  auto kind = [&](int i) {
+    const uint32_t v = at(i);
+    if (v > upto) return 2;
+    if (v < from) return 0;
+    if (left == border) return 2;
+    if (!again) return 1;
+    if (ranked) {
+      int x = 0;
+      while (s_at[x] != i) ++x;
+      int before = 0;
+      for (int y = 0; y < border; ++y)
+        before += s_key[y] > s_key[x] || (s_key[y] == s_key[x] && s_at[y] < i);
+      return before < left ? 2 : 0;
+    }
+    return exact[i] > bound64 ? 2 : exact[i] == bound64 ? 1 : 0;
+  };
+  int ties = !again ? left : 0;                             // equals that are taken
+  if (again && !ranked) {
+    int above = 0;
+    for (int i = tid; i < n; i += kThreads) {
+      const uint32_t v = at(i);
+      above += v >= from && v <= upto && exact[i] > bound64;
+    }
+    ties = left - block_sum<kThreads>(above, s_sum, &turn);
+  }
+  if (left == border) ties = 0;
+  int done = p.keep_first;
+  for (int base = 0; base < n; base += 32 * kThreads) {
+    __syncthreads();                                        // the last round's words are read
+    for (int w = tid >> 5; w < kThreads; w += kThreads / 32) {
+      uint32_t s = 0, e = 0;
+      if (base + 32 * w < n) {
+        const int i = base + 32 * w + lane;
+        const int k = i < n ? kind(i) : 0;
+        s = __ballot_sync(0xffffffffu, k == 2);
+        e = __ballot_sync(0xffffffffu, k == 1);
+      }
+      if (lane == 0) {
+        s_sure[w] = s;
+        s_tie[w] = e;
+      }
+    }
+    __syncthreads();
+    uint32_t word = s_sure[tid], equal = s_tie[tid];
+    int all;
+    const int before = block_scan<kThreads>(__popc(equal), s_sum, &turn, &all);
+    for (int k = min(__popc(equal), ties - before); k > 0; --k) {
+      word |= equal & (0u - equal);
+      equal &= equal - 1;
+    }
+    ties = max(0, ties - all);
+    int place = done + block_scan<kThreads>(__popc(word), s_sum, &turn, &all);
+    done += all;
+    while (word != 0) {
+      out[place++] = p.keep_first + base + 32 * tid + __ffs(word) - 1;
+      word &= word - 1;
+    }
+  }
+}
+
+}  // namespace attn_sink

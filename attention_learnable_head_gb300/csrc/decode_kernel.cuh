@@ -28,6 +28,7 @@
 //                read with a transposing ldmatrix and converted from bf16)
 // The 4 warps' (m, l, O) states are merged through shared memory at the end.
 #pragma once
+#include <climits>
 #include <cuda_bf16.h>
 #include "sm103_ptx.cuh"
 
@@ -39,6 +40,20 @@ constexpr int kDecMaxGroup = 8;        // query heads per kv head
 constexpr int kDecKeys = 64;           // keys per stage: 16 per warp
 constexpr int kDecStages = 2;
 constexpr float kLn2Dec = 0.6931471805599453f;
+constexpr int kDecTileRows = 128;      // kDecShared: rows of a prefix tile's partial results
+constexpr int kDecNoKey = INT_MIN;     // kDecPages: no entry of the list, or behind the last key
+constexpr int kSharedMinSeqs = 2;      // kDecShared: smaller groups and shorter prefixes are read
+constexpr int kSharedMinKeys = 64;     //   by each sequence for itself
+
+// What a decode step reads: every cached key (or a window), the pages selected for
+// each kv head, or the keys behind the prefix a group of sequences shares, whose
+// results the merge then joins (shared_kernel.cuh).
+enum DecodeMode { kDecAll, kDecPages, kDecShared };
+
+// The prefix of a sequence in decode_shared: its tile's partial results.
+struct SharedRef {
+  int first, parts;               // of [partial][kv head][128 rows]; 0 parts: no prefix
+};
 
 struct DecodeParams {
   CUtensorMap tm_k;               // k_cache as [num_pages * page_size][H_kv][64], box
@@ -63,6 +78,14 @@ struct DecodeParams {
   int splits;
   int log2_page;                  // TMA path: log2(page_size)
   float scale_log2;               // softmax_scale * log2(e)
+  const int* selected;            // kDecPages: [B][H_kv][count] columns of the block table
+  int count;
+  const int* cu_groups;           // kDecShared: [num_groups + 1] first sequences
+  const int* prefix_lens;         // [num_groups]
+  const SharedRef* refs;          // [B], behind grid_dependency_wait
+  const float* prefix_o;          // [partial][H_kv][128 rows][64] sums
+  const float2* prefix_ml;        // [partial][H_kv][128 rows]: maximum (log2 units), sum
+  int num_groups;
 };
 
 // Page sizes the TMA path copies whole: a multiple of 8 keys (whole 128-byte
@@ -71,15 +94,41 @@ __host__ __device__ constexpr bool decode_tma_page(int page_size) {
   return page_size >= 8 && (page_size & (page_size - 1)) == 0;
 }
 
+// The group of sequence b: its first sequence, how many it has (0: none) and the keys
+// of the prefix that are read once for all of them: none in a group of one, and
+// no more than its shortest sequence has.  Called by a whole CTA of `threads`
+// threads; every thread gets the answer.
+struct SharedGroup {
+  int first, size, prefix;
+};
+__device__ __forceinline__ int shared_seq_len(const int* seq_lens, int b, int cap) {
+  return max(0, min(__ldg(seq_lens + b), cap));
+}
+// The last p in [0, groups] with cu[p] <= b; every lane of the warp gets it.
+__device__ __forceinline__ int shared_find(const int* cu, int groups, int b) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, span = groups + 1;             // the answer lies in [lo, lo + span)
+  while (span > 1) {
+    const int step = (span + 31) / 32;
+    const int at = lo + lane * step;
+    const bool le = lane * step < span && (lane == 0 || __ldg(cu + at) <= b);
+    const int i = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += i * step;
+    span = min(step, span - i * step);
+  }
+  return lo;
+}
+
 // G = query heads per kv head (1, 2, 4 or 8).  kTma: the blocks' pages are
 // copied by TMA (one thread issues them; page sizes of decode_tma_page),
 // otherwise by every thread with 16-byte cp.async.
-template <int G, bool kTma>
+template <int G, bool kTma, DecodeMode kMode = kDecAll>
 __global__ void __launch_bounds__(kDecThreads, 5)
 attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ __align__(1024) uint8_t s_kv[kDecStages][2][kDecKeys * 128];   // K, V blocks
   __shared__ uint8_t s_valid[kDecStages][kDecKeys];    // key inside the slice, page in range
   __shared__ uint8_t s_pageok[kDecStages][8];          // TMA path: copy i of the block is a page
+                                                       //   (kDecPages: how many of its keys are seen)
   __shared__ __align__(8) uint64_t kv_full[kDecStages];   // TMA path: the stage's copies landed
   __shared__ float s_m[kDecWarps][kDecMaxGroup];
   __shared__ float s_l[kDecWarps][kDecMaxGroup];
@@ -106,7 +155,40 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   }
   // The slices start on 64-key block boundaries (so the TMA path copies whole
   // pages into a block); keys before the window start are masked.
-  const int lo = p.window > 0 ? max(0, L - p.window) : 0;
+  int lo = p.window > 0 ? max(0, L - p.window) : 0;
+  int seq_first = 0;                 // kDecShared: the group's first sequence
+  if constexpr (kMode == kDecShared) {
+    __shared__ int s_min[kDecWarps];
+    const int gp = shared_find(p.cu_groups, p.num_groups, b);
+    int c0 = 0, c1 = 0, keys = 0;
+    if (gp < p.num_groups) {
+      c0 = max(0, __ldg(p.cu_groups + gp));
+      c1 = min(p.batch, __ldg(p.cu_groups + gp + 1));
+      keys = __ldg(p.prefix_lens + gp);
+    }
+    int least = INT_MAX;
+    for (int i = c0 + tid; i < c1; i += kDecThreads)
+      least = min(least, shared_seq_len(p.seq_lens, i, cap));
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) s_min[warp] = least;
+    __syncthreads();
+    for (int w = 0; w < kDecWarps; ++w) least = min(least, s_min[w]);
+    if (c0 <= b && b < c1 && c1 - c0 >= kSharedMinSeqs) {
+      const int shared = min(keys, least);
+      if (shared >= kSharedMinKeys) {
+        lo = shared;
+        seq_first = c0;
+      }
+    }
+  }
+  // kDecPages: the sequence's pages; L from here on counts the keys of the listed ones,
+  // in the order of the list
+  const int len = L, have = (L + p.page_size - 1) / p.page_size;
+  const int* listed = nullptr;
+  if constexpr (kMode == kDecPages) {
+    listed = p.selected + ((size_t)b * p.heads_kv + g) * p.count;
+    L = min(p.count, have) * p.page_size;
+  }
   const int lo_blk = lo & ~(kDecKeys - 1);
   const int per = ((L - lo_blk + p.splits - 1) / p.splits + kDecKeys - 1) & ~(kDecKeys - 1);
   const int k0 = lo_blk + split * per;
@@ -137,9 +219,20 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = k0 + blk * kDecKeys + (((tid >> 3) + 16 * u) & (kDecKeys - 1));
-      pg[u] = (blk < nblk && j < k1)
-                  ? __ldg(p.block_table + (size_t)b * p.max_pages + j / p.page_size)
-                  : -1;
+      if constexpr (kMode == kDecPages) {
+        pg[u] = kDecNoKey;
+        if (blk < nblk && j < k1) {
+          const int at = j / p.page_size, col = __ldg(listed + at);
+          if (col >= have)
+            pg[u] = -1;                      // reported, as a bad table entry is
+          else if (col >= 0 && col * p.page_size + (j - at * p.page_size) < len)
+            pg[u] = max(-1, __ldg(p.block_table + (size_t)b * p.max_pages + col));
+        }
+      } else {
+        pg[u] = (blk < nblk && j < k1)
+                    ? __ldg(p.block_table + (size_t)b * p.max_pages + j / p.page_size)
+                    : -1;
+      }
     }
   };
   // Block `blk` of the slice into stage `st`, with the table entries pg of its
@@ -152,7 +245,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     for (int u = 0; u < 4; ++u) {
       const int key = ((tid >> 3) + 16 * u) & (kDecKeys - 1);
       const int j = base + key;
-      const bool inside = j >= lo && j < k1;
+      const bool inside = j >= lo && j < k1 && (kMode != kDecPages || pg[u] != kDecNoKey);
       const bool valid = inside && pg[u] >= 0 && pg[u] < p.num_pages;
       if (inside && !valid && c == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
       if (c == 0) s_valid[st][key] = valid ? 1 : 0;
@@ -188,7 +281,26 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   const int log2_box = kTma ? min(p.log2_page, 6) : 0;
   const int box = 1 << log2_box;
   const int npg = kTma ? kDecKeys >> log2_box : 0;      // copies per block and tensor
-  auto tma_fetch = [&](int blk, int* pe) {
+  // (kDecPages: through the list, and seen[i] = how many of the copy's keys the
+  // sequence has.)
+  auto tma_fetch = [&](int blk, int* pe, int* seen) {
+    if constexpr (kMode == kDecPages) {
+      int col[8];
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = k0 + blk * kDecKeys + i * box;
+        col[i] = i < npg && blk < nblk && j < k1 ? __ldg(listed + (j >> p.log2_page)) : -1;
+      }
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = k0 + blk * kDecKeys + i * box;
+        const bool in = col[i] >= 0 && col[i] < have;      // one behind the sequence's: reported
+        seen[i] = in ? min(max(len - col[i] * p.page_size - (j & (p.page_size - 1)), 0), box) : 0;
+        pe[i] = in ? max(-1, __ldg(p.block_table + (size_t)b * p.max_pages + col[i]))
+                   : col[i] < 0 ? kDecNoKey : -1;
+      }
+      return;
+    }
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int j = k0 + blk * kDecKeys + i * box;       // first key of copy i
@@ -197,18 +309,19 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
                   : -1;
     }
   };
-  auto tma_issue = [&](int blk, int st, const int* pe) {
+  auto tma_issue = [&](int blk, int st, const int* pe, const int* seen) {
     const int base = k0 + blk * kDecKeys;
     const int oob = p.num_pages * p.page_size;           // first row past the cache
     int row[8];
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int j = base + i * box;
-      const bool needed = i < npg && j < k1 && j + box > lo;
+      const bool needed = i < npg && j < k1 && j + box > lo &&
+                          (kMode != kDecPages || pe[i] != kDecNoKey);
       const bool ok = pe[i] >= 0 && pe[i] < p.num_pages;
       if (needed && !ok) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
       row[i] = ok ? pe[i] * p.page_size + (j & (p.page_size - 1)) : oob;
-      if (i < npg) s_pageok[st][i] = ok ? 1 : 0;
+      if (i < npg) s_pageok[st][i] = !ok ? 0 : kMode == kDecPages ? seen[i] : 1;
     }
     mbar_arrive_expect_tx(&kv_full[st], 2 * kDecKeys * 128);
     #pragma unroll
@@ -231,16 +344,16 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   // two-stage ring: block blk + 1 is in flight while blk is used (five CTAs per
   // SM keep ten blocks in flight; measured better than three stages at four
   // CTAs per SM)
-  int pg[8], pg_next[8];
+  int pg[8], pg_next[8], seen[8], seen_next[8];
   bool ok = true;
   if (kTma) {
     if (tid == 0) {
-      tma_fetch(0, pg);
-      if (nblk > 0) tma_issue(0, 0, pg);
-      tma_fetch(1, pg);
-      if (nblk > 1) tma_issue(1, 1, pg);
+      tma_fetch(0, pg, seen);
+      if (nblk > 0) tma_issue(0, 0, pg, seen);
+      tma_fetch(1, pg, seen);
+      if (nblk > 1) tma_issue(1, 1, pg, seen);
       issued = min(nblk, 2);
-      tma_fetch(2, pg_next);
+      tma_fetch(2, pg_next, seen_next);
     }
   } else {
     fetch_pages(0, pg);
@@ -271,10 +384,18 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     // TMA copies whole pages: value rows outside [lo, k1) may hold anything (cache
     // rows that no token was written to), and 0 * inf is not 0.
     const int base = k0 + blk * kDecKeys;
-    if (kTma && (base < lo || base + kDecKeys > k1)) {         // same for the whole CTA
+    bool edge = base < lo || base + kDecKeys > k1;             // same for the whole CTA
+    if constexpr (kTma && kMode == kDecPages) {                // a page that is partly filled
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) edge |= i < npg && s_pageok[st][i] < box;
+    }
+    if (kTma && edge) {
       for (int c = tid; c < kDecKeys * 8; c += kDecThreads) {
         const int j = base + (c >> 3);
-        if (j < lo || j >= k1)
+        bool gone = j < lo || j >= k1;
+        if constexpr (kMode == kDecPages)
+          gone = gone || ((c >> 3) & (box - 1)) >= s_pageok[st][(c >> 3) >> log2_box];
+        if (gone)
           *reinterpret_cast<uint4*>(&s_kv[st][1][c * 16]) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();     // the stage's next copy comes through the async proxy
@@ -311,7 +432,10 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
         bool valid;
         if (kTma) {
           const int j = k0 + blk * kDecKeys + key;
-          valid = s_pageok[st][key >> log2_box] != 0 && j >= lo && j < k1;
+          if constexpr (kMode == kDecPages)
+            valid = (key & (box - 1)) < s_pageok[st][key >> log2_box] && j < k1;
+          else
+            valid = s_pageok[st][key >> log2_box] != 0 && j >= lo && j < k1;
         } else {
           valid = s_valid[st][key] != 0;
         }
@@ -362,9 +486,12 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     __syncthreads();   // every warp is done with stage st before it is refilled
     if (kTma && tid == 0 && blk + 2 < nblk) {
       #pragma unroll
-      for (int i = 0; i < 8; ++i) pg[i] = pg_next[i];
-      tma_fetch(blk + 3, pg_next);
-      tma_issue(blk + 2, st, pg);
+      for (int i = 0; i < 8; ++i) {
+        pg[i] = pg_next[i];
+        if constexpr (kMode == kDecPages) seen[i] = seen_next[i];
+      }
+      tma_fetch(blk + 3, pg_next, seen_next);
+      tma_issue(blk + 2, st, pg, seen);
       issued = blk + 3;
     }
   }
@@ -413,7 +540,8 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
         for (int e = 0; e < 4; ++e) acc[e] = fmaf(wt, s_o[w][h][d0 + e], acc[e]);
       }
     }
-    const float inv = (ll > 0.0f) ? 1.0f / ll : 0.0f;
+    const bool some = kMode == kDecAll ? ll > 0.0f : ll != 0.0f;   // NaN scores reach the result
+    const float inv = some ? 1.0f / ll : 0.0f;
     const int hq = g * G + h;
     const size_t oi = (((size_t)split * p.batch + b) * p.heads_q + hq) * 64 + d0;
     uint32_t hi[2], lo2[2];
@@ -427,7 +555,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     *reinterpret_cast<uint2*>(p.o_part_lo + oi) = make_uint2(lo2[0], lo2[1]);
     if (d0 == 0)
       p.lse_part[((size_t)split * p.heads_q + hq) * p.batch + b] =
-          (ll > 0.0f) ? (mm + __log2f(ll)) * kLn2Dec : -INFINITY;
+          some ? (mm + __log2f(ll)) * kLn2Dec : -INFINITY;
   }
 
   // ---- the last CTA of (b, g) merges the slices with the sink:
@@ -442,14 +570,30 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   __syncthreads();
   if (!s_last) return;
   __threadfence();
+  SharedRef ref{0, 0};
+  size_t prow = 0;                   // the prefix's first partial result of this row
+  const size_t pstep = (size_t)p.heads_kv * kDecTileRows;
+  if constexpr (kMode == kDecShared) {
+    grid_dependency_wait();
+    if (lo > 0) {
+      const int2 r = __ldcg(reinterpret_cast<const int2*>(p.refs + b));
+      ref = SharedRef{r.x, r.y};
+    }
+    prow = ((size_t)ref.first * p.heads_kv + g) * kDecTileRows +
+           (b - seq_first) % (kDecTileRows / G) * G + h;
+  }
   if (h < G) {
     const int hq = g * G + h;
     const float sk = __ldg(p.sink + hq);
     float m = sk;
+    if constexpr (kMode == kDecShared)
+      for (int c = 0; c < ref.parts; ++c)
+        m = fmaxf(m, __ldcg(p.prefix_ml + prow + c * pstep).x * kLn2Dec);
     for (int c = 0; c < p.splits; ++c)
       m = fmaxf(m, __ldcg(p.lse_part + ((size_t)c * p.heads_q + hq) * p.batch + b));
     const float m_use = (m == -INFINITY) ? 0.0f : m;
     float z = (sk == -INFINITY) ? 0.0f : __expf(sk - m_use);
+    if (kMode != kDecAll && sk == m_use) z = 1.0f;         // where both are inf, too
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int c = 0; c < p.splits; ++c) {
       const float lc = __ldcg(p.lse_part + ((size_t)c * p.heads_q + hq) * p.batch + b);
@@ -464,7 +608,21 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       acc[2] = fmaf(wc, bf16_lo(o.y) + bf16_lo(r.y), acc[2]);
       acc[3] = fmaf(wc, bf16_hi(o.y) + bf16_hi(r.y), acc[3]);
     }
-    const float inv_z = (z > 0.0f) ? 1.0f / z : 0.0f;
+    if constexpr (kMode == kDecShared)
+      for (int c = 0; c < ref.parts; ++c) {
+        const float2 ml = __ldcg(p.prefix_ml + prow + c * pstep);
+        if (ml.x == -INFINITY) continue;            // a part without a key stored no sums
+        const float wc = __expf(fmaf(ml.x, kLn2Dec, -m_use));
+        z = fmaf(wc, ml.y, z);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(
+            p.prefix_o + (prow + c * pstep) * 64 + d0));
+        acc[0] = fmaf(wc, o.x, acc[0]);
+        acc[1] = fmaf(wc, o.y, acc[1]);
+        acc[2] = fmaf(wc, o.z, acc[2]);
+        acc[3] = fmaf(wc, o.w, acc[3]);
+      }
+    const bool some = kMode == kDecAll ? z > 0.0f : z != 0.0f;
+    const float inv_z = some ? 1.0f / z : 0.0f;
     uint32_t hi[2], lo2[2];
     #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -475,7 +633,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     const size_t oi = ((size_t)b * p.heads_q + hq) * 64 + d0;
     *reinterpret_cast<uint2*>(p.out + oi) = make_uint2(hi[0], hi[1]);
     if (p.out_lo) *reinterpret_cast<uint2*>(p.out_lo + oi) = make_uint2(lo2[0], lo2[1]);
-    if (d0 == 0) p.lse[(size_t)hq * p.batch + b] = (z > 0.0f) ? m_use + __logf(z) : -INFINITY;
+    if (d0 == 0) p.lse[(size_t)hq * p.batch + b] = some ? m_use + __logf(z) : -INFINITY;
   }
 }
 

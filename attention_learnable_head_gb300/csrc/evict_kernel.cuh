@@ -1,0 +1,238 @@
+// Eviction from a paged cache by accumulated attention weight, sm_103a.
+//
+// One CTA for each (sequence, kv head) finds the weight of the last key that stays bit by
+// bit (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th
+// kept key at or behind the budget goes to the n-th hole below it.  Only as many rows
+// move as there are holes, and no row is both read and written, so that a second kernel
+// can copy them in any order, 16 lanes a move (8 for the key, 8 for the value).  One more
+// CTA of the first kernel scans the sequences for the pages that become free.
+#pragma once
+#include <climits>
+#include <cuda_bf16.h>
+#include "sm103_ptx.cuh"
+#include "topk.cuh"
+
+namespace attn_sink {
+
+constexpr int kEvictStage = 49152;      // weights that a CTA keeps in shared memory
+constexpr int kMoveThreads = 256;
+
+struct EvictParams {
+  uint4* k_cache;                 // [num_pages][page_size][H_kv][8 chunks of 16 bytes]
+  uint4* v_cache;
+  const int* block_table;         // [B][max_pages]
+  const int* seq_lens;            // [B]
+  const float* mass;              // [B][H_kv][max_keys]
+  float* mass_out;
+  int* new_lens;                  // [B]
+  int* freed;                     // [max_freed]
+  int* num_freed;                 // [1]
+  int* counts;                    // [B][H_kv] moves
+  uint2* moves;                   // [B][H_kv][max_moves] cache rows (of all heads): from, to
+  int* err;
+  int batch, heads_kv, page_size, num_pages, max_pages, max_keys;
+  int budget, keep_first, keep_last, max_freed, max_moves, stage;
+};
+
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
+__device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool* bad) {
+  const int len = __ldg(p.seq_lens + b), cap = min(p.max_pages * p.page_size, p.max_keys);
+  *bad |= len < 0 || len > cap;
+  return max(0, min(len, cap));
+}
+
+// The pages that become free, and the new lengths.
+template <int kThreads>
+__device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[kThreads / 32],
+                                            int* s_count, int* s_from, int* s_first) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int turn = 0, done = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    int count = 0, from = 0;
+    if (b < p.batch) {
+      const int len = evict_len(p, b, &bad), fewer = min(len, p.budget);
+      p.new_lens[b] = fewer;
+      from = (fewer + p.page_size - 1) / p.page_size;
+      count = (len + p.page_size - 1) / p.page_size - from;
+    }
+    int all;
+    const int before = block_scan<kThreads>(count, s_sum, &turn, &all);
+    __syncthreads();                      // the last round's have been used
+    s_count[tid] = count;
+    s_from[tid] = from;
+    s_first[tid] = done + before;
+    __syncthreads();
+    const int most = min(kThreads, p.batch - b0);
+    for (int i = warp; i < most; i += kThreads / 32)
+      for (int x = lane; x < s_count[i]; x += 32) {
+        const int to = s_first[i] + x;
+        if (to < p.max_freed)
+          p.freed[to] = __ldg(p.block_table + (size_t)(b0 + i) * p.max_pages + s_from[i] + x);
+      }
+    done += all;
+  }
+  if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  if (tid == 0) *p.num_freed = done;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
+attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t s_mass[];                      // [stage]
+  __shared__ int s_sum[2][kThreads / 32];
+  __shared__ uint32_t s_kept[kThreads], s_tie[kThreads];    // bitmaps of 32 kThreads keys
+  __shared__ int s_list[kThreads];
+  grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (blockIdx.x == gridDim.x - 1) {
+    evict_pages<kThreads>(p, s_sum, reinterpret_cast<int*>(s_kept), reinterpret_cast<int*>(s_tie),
+                          s_list);
+    return;
+  }
+  const int b = (int)(blockIdx.x / (unsigned)p.heads_kv);
+  const size_t row = blockIdx.x;
+  const float* mass = p.mass + row * p.max_keys;
+  float* mass_out = p.mass_out + row * p.max_keys;
+  bool bad = false;
+  const int len = evict_len(p, b, &bad), fewer = min(len, p.budget);
+  // what stays where it is, and nothing behind; the holes are filled at the end
+  if (len <= p.budget) {
+    for (int j = tid; j < p.max_keys; j += kThreads) mass_out[j] = j < fewer ? __ldg(mass + j) : 0.0f;
+    if (tid == 0) p.counts[row] = 0;
+    return;
+  }
+  const bool staged = len <= p.stage;
+  for (int j = tid; j < p.max_keys; j += kThreads) {
+    const float m = j < len ? __ldg(mass + j) : 0.0f;
+    if (staged && j < len) s_mass[j] = ordered(m);
+    mass_out[j] = j < fewer ? m : 0.0f;
+  }
+  __syncthreads();
+  auto at = [&](int j) { return staged ? s_mass[j] : ordered(__ldg(mass + j)); };
+  const int lo = p.keep_first, hi = len - p.keep_last;      // the keys that compete
+  const int need = p.budget - p.keep_first - p.keep_last;   // < hi - lo
+  int turn = 0, ties = 0;
+  uint32_t bound = 0xFFFFFFFFu;
+  bool exact = need == 0;
+  if (need > 0)
+    bound = block_nth_largest<kThreads, uint32_t>(
+        need, [&](auto&& take) {
+          for (int j = lo + tid; j < hi; j += kThreads) take(at(j));
+        }, s_sum, &turn, &exact);
+  if (!exact) {
+    int above = 0;
+    for (int j = lo + tid; j < hi; j += kThreads) above += at(j) > bound;
+    ties = need - block_sum<kThreads>(above, s_sum, &turn);
+  }
+  // bitmaps of 32 kThreads keys at a time, a word a thread
+  uint2* moves = p.moves + row * p.max_moves;               // positions first: x from, y to
+  int holes = 0, movers = 0;
+  for (int base = 0; base < len; base += 32 * kThreads) {
+    __syncthreads();                                        // the last round's words are read
+    for (int w = tid >> 5; w < kThreads; w += kThreads / 32) {
+      uint32_t k = 0, e = 0;
+      if (base + 32 * w < len) {
+        const int j = base + 32 * w + lane;
+        bool kept = false, tie = false;
+        if (j < len) {
+          if (j < lo || j >= hi) {
+            kept = true;
+          } else if (need > 0) {
+            const uint32_t v = at(j);
+            kept = v > bound || (exact && v == bound);
+            tie = !exact && v == bound;
+          }
+        }
+        k = __ballot_sync(0xffffffffu, kept);
+        e = __ballot_sync(0xffffffffu, tie);
+      }
+      if (lane == 0) {
+        s_kept[w] = k;
+        s_tie[w] = e;
+      }
+    }
+    __syncthreads();
+    uint32_t kept = s_kept[tid], equal = s_tie[tid];
+    int all;
+    const int before = block_scan<kThreads>(__popc(equal), s_sum, &turn, &all);
+    for (int k = min(__popc(equal), ties - before); k > 0; --k) {
+      kept |= equal & (0u - equal);
+      equal &= equal - 1;
+    }
+    ties = max(0, ties - all);
+    // bits of the word below the budget, and of keys that there are
+    const int j0 = base + 32 * tid;
+    const uint32_t below = fewer - j0 >= 32 ? 0xFFFFFFFFu : fewer <= j0 ? 0u : (1u << (fewer - j0)) - 1u;
+    uint32_t hole = ~kept & below, mover = kept & ~below;
+    int place = holes + block_scan<kThreads>(__popc(hole), s_sum, &turn, &all);
+    holes += all;
+    while (hole != 0) {
+      moves[place++].y = (uint32_t)(j0 + __ffs(hole) - 1);
+      hole &= hole - 1;
+    }
+    place = movers + block_scan<kThreads>(__popc(mover), s_sum, &turn, &all);
+    movers += all;
+    while (mover != 0) {
+      moves[place++].x = (uint32_t)(j0 + __ffs(mover) - 1);
+      mover &= mover - 1;
+    }
+  }
+  __syncthreads();                                          // the positions are listed
+  // the moved weights, and the cache rows of the moves
+  const int* table = p.block_table + (size_t)b * p.max_pages;
+  auto cache_row = [&](int j) {
+    const int pg = j / p.page_size, e = __ldg(table + pg);
+    return (unsigned)e < (unsigned)p.num_pages
+               ? (uint32_t)e * (uint32_t)p.page_size + (uint32_t)(j - pg * p.page_size)
+               : kNoRow;
+  };
+  for (int i = tid; i < holes; i += kThreads) {
+    const uint2 m = moves[i];
+    mass_out[m.y] = __ldg(mass + m.x);
+    uint2 r = make_uint2(cache_row((int)m.x), cache_row((int)m.y));
+    if (r.x == kNoRow || r.y == kNoRow) {
+      atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+      r.x = kNoRow;
+    }
+    moves[i] = r;
+  }
+  if (tid == 0) p.counts[row] = holes;
+}
+
+__global__ void __launch_bounds__(kMoveThreads)
+attn_sink_evict_move_kernel(const __grid_constant__ EvictParams p) {
+  grid_dependency_wait();
+  const int half = threadIdx.x & 15, c = half & 7;
+  uint4* cache = half < 8 ? p.k_cache : p.v_cache;
+  const size_t rows = (size_t)p.batch * p.heads_kv;
+  for (size_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const uint2* moves = p.moves + row * p.max_moves;
+    const int h = (int)(row % (unsigned)p.heads_kv), n = __ldcg(p.counts + row);
+    const int step = gridDim.x * (kMoveThreads / 16);
+    for (int i = blockIdx.x * (kMoveThreads / 16) + (threadIdx.x >> 4); i < n; i += 4 * step) {
+      uint2 m[4];
+      uint4 v[4];
+      #pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        m[u] = make_uint2(kNoRow, 0);
+        if (i + u * step < n) m[u] = __ldcg(moves + i + u * step);
+      }
+      #pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (m[u].x != kNoRow) v[u] = __ldcg(cache + ((size_t)m[u].x * p.heads_kv + h) * 8 + c);
+      #pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (m[u].x != kNoRow) cache[((size_t)m[u].y * p.heads_kv + h) * 8 + c] = v[u];
+    }
+  }
+  // no page behind the freed ones
+  const unsigned tid = (blockIdx.y * gridDim.x + blockIdx.x) * kMoveThreads + threadIdx.x;
+  const unsigned threads = gridDim.x * gridDim.y * kMoveThreads;
+  for (size_t i = (size_t)max(__ldcg(p.num_freed), 0) + tid; i < (size_t)p.max_freed; i += threads)
+    p.freed[i] = -1;
+}
+
+}  // namespace attn_sink

@@ -1,5 +1,6 @@
 // Native side of the conveniences of attn_sink_step.h (page_plan, qkv_rope,
-// qkv_rope_backward, extend): checks the arguments, allocates the outputs and the
+// qkv_rope_backward, extend) and attn_sink_cache.h (decode_shared, page_bounds,
+// select_pages, decode_pages, key_mass, evict): checks the arguments, allocates the outputs and the
 // workspace on the current stream and calls the C entry point.  A small call's
 // kernels take 3 to 10 us; with these steps in Python (ctypes, torch.empty) the
 // host took longer than they did.  A call, host and device, Python -> native:
@@ -27,6 +28,7 @@
 #include <cstring>
 #include <initializer_list>
 
+#include "attn_sink_cache.h"
 #include "attn_sink_step.h"
 
 namespace {
@@ -38,6 +40,16 @@ decltype(&attn_sink_qkv_rope_bwd_workspace_size) f_rope_ws;
 decltype(&attn_sink_qkv_rope_bwd) f_rope_bwd;
 decltype(&attn_sink_extend_workspace_size) f_extend_ws;
 decltype(&attn_sink_extend) f_extend;
+decltype(&attn_sink_decode_shared_workspace_size) f_shared_ws;
+decltype(&attn_sink_decode_shared) f_shared;
+decltype(&attn_sink_page_bounds) f_bounds;
+decltype(&attn_sink_select_pages_workspace_size) f_select_ws;
+decltype(&attn_sink_select_pages) f_select;
+decltype(&attn_sink_decode_pages_workspace_size) f_pages_ws;
+decltype(&attn_sink_decode_pages) f_pages;
+decltype(&attn_sink_key_mass) f_mass;
+decltype(&attn_sink_evict_workspace_size) f_evict_ws;
+decltype(&attn_sink_evict) f_evict;
 
 // A tensor argument; null for None or anything else.
 const at::Tensor* tensor(PyObject* o) {
@@ -381,14 +393,229 @@ PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// init(addresses of the six entry points, in the order of their declaration above)
+// A paged cache and its tables: k_cache and (null: none) v_cache [pages, page size, kv
+// heads, 64], block_table [B, columns], seq_lens [B]; fills the fields all params have.
+template <typename P>
+bool paged(const at::Tensor* kc, const at::Tensor* vc, bool values, const at::Tensor* table,
+           const at::Tensor* lens, P* p) {
+  if (!here(kc)) return false;
+  const c10::Device dev = kc->device();
+  if (!fits(kc, at::kBFloat16, dev, {-1, -1, -1, 64}) ||
+      (values && !fits(vc, at::kBFloat16, dev, {kc->size(0), kc->size(1), kc->size(2), 64})) ||
+      !fits(lens, at::kInt, dev, {-1}) || !fits(table, at::kInt, dev, {lens->size(0), -1}))
+    return false;
+  p->batch = (int)lens->size(0);
+  p->heads_kv = (int)kc->size(2);
+  p->head_dim = 64;
+  p->page_size = (int)kc->size(1);
+  p->num_pages = (int)kc->size(0);
+  p->max_pages = (int)table->size(1);
+  return true;
+}
+
+// The caller's own out and lse (null: none), if they are what q's call writes.
+bool results(PyObject* o, PyObject* l, const at::Tensor& q, const at::Tensor** out,
+             const at::Tensor** lse) {
+  *out = tensor(o);
+  *lse = tensor(l);
+  return (o == Py_None || fits(*out, at::kBFloat16, q.device(), {q.size(0), q.size(1), 64})) &&
+         (l == Py_None || fits(*lse, at::kFloat, q.device(), {q.size(1), q.size(0)}));
+}
+
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  attn_sink_shared_params p;
+  std::memset(&p, 0, sizeof(p));
+  const at::Tensor *q, *kc, *vc, *table, *lens, *cu, *prefix, *sink, *given_out, *given_lse;
+  if (n != 11 || !paged(kc = tensor(a[1]), vc = tensor(a[2]), true, table = tensor(a[3]),
+                        lens = tensor(a[4]), &p) ||
+      !real(a[8], &p.softmax_scale))
+    return none();
+  const c10::Device dev = kc->device();
+  if (!fits(q = tensor(a[0]), at::kBFloat16, dev, {p.batch, -1, 64}) ||
+      !fits(prefix = tensor(a[6]), at::kInt, dev, {-1}) ||
+      !fits(cu = tensor(a[5]), at::kInt, dev, {prefix->size(0) + 1}) ||
+      !fits(sink = tensor(a[7]), at::kFloat, dev, {q->size(1)}) ||
+      !results(a[9], a[10], *q, &given_out, &given_lse))
+    return none();
+  p.num_groups = (int)prefix->size(0);
+  p.heads_q = (int)q->size(1);
+  at::Tensor out, lse;
+  int st;
+  {
+    const Unlocked unlocked;
+    out = given_out ? *given_out : make(*q, at::kBFloat16, {p.batch, p.heads_q, 64});
+    lse = given_lse ? *given_lse : make(*q, at::kFloat, {p.heads_q, p.batch});
+    const size_t bytes = f_shared_ws(&p);
+    const at::Tensor ws = make(*q, at::kByte, {(int64_t)bytes});
+    st = f_shared(&p, data(q), data(kc), data(vc), data_as<int>(table), data_as<int>(lens),
+                  data_as<int>(cu), data_as<int>(prefix), data_as<float>(sink), out.data_ptr(),
+                  data_as<float>(&lse), ws.data_ptr(), bytes, current_stream(*q));
+  }
+  if (st != 0) return PyLong_FromLong(st);
+  return tuple({&out, &lse});
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  attn_sink_bounds_params p;
+  const at::Tensor *kc, *table, *cached, *lens, *bounds;
+  if (n != 5 || !paged(kc = tensor(a[0]), nullptr, false, table = tensor(a[1]),
+                       lens = tensor(a[3]), &p))
+    return none();
+  const c10::Device dev = kc->device();
+  if (!fits(cached = tensor(a[2]), at::kInt, dev, {p.batch}) ||
+      !fits(bounds = tensor(a[4]), at::kBFloat16, dev, {p.num_pages, p.heads_kv, 2, 64}))
+    return none();
+  int st;
+  {
+    const Unlocked unlocked;
+    st = f_bounds(&p, data(kc), data_as<int>(table), data_as<int>(cached), data_as<int>(lens),
+                  data(bounds), current_stream(*kc));
+  }
+  return PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  attn_sink_select_params p;
+  const at::Tensor *q, *bounds, *table, *lens;
+  if (n != 8 || !here(q = tensor(a[0])) || !integer(a[4], &p.count) || p.count < 1 ||
+      !integer(a[5], &p.page_size) || !integer(a[6], &p.keep_first) ||
+      !integer(a[7], &p.keep_last))
+    return none();
+  const c10::Device dev = q->device();
+  if (!fits(lens = tensor(a[3]), at::kInt, dev, {-1}) ||
+      !fits(q, at::kBFloat16, dev, {lens->size(0), -1, 64}) ||
+      !fits(bounds = tensor(a[1]), at::kBFloat16, dev, {-1, -1, 2, 64}) ||
+      !fits(table = tensor(a[2]), at::kInt, dev, {lens->size(0), -1}))
+    return none();
+  p.batch = (int)lens->size(0);
+  p.heads_q = (int)q->size(1);
+  p.heads_kv = (int)bounds->size(1);
+  p.head_dim = 64;
+  p.num_pages = (int)bounds->size(0);
+  p.max_pages = (int)table->size(1);
+  at::Tensor selected;
+  int st;
+  {
+    const Unlocked unlocked;
+    selected = make(*q, at::kInt, {p.batch, p.heads_kv, p.count});
+    const size_t bytes = f_select_ws(&p);
+    const at::Tensor ws = make(*q, at::kByte, {(int64_t)bytes});
+    st = f_select(&p, data(q), data(bounds), data_as<int>(table), data_as<int>(lens),
+                  data_as<int>(&selected), ws.data_ptr(), bytes, current_stream(*q));
+  }
+  if (st != 0) return PyLong_FromLong(st);
+  return THPVariable_Wrap(selected);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* decode_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  attn_sink_pages_params p;
+  const at::Tensor *q, *kc, *vc, *table, *lens, *selected, *sink, *given_out, *given_lse;
+  if (n != 10 || !paged(kc = tensor(a[1]), vc = tensor(a[2]), true, table = tensor(a[3]),
+                        lens = tensor(a[4]), &p) ||
+      !real(a[7], &p.softmax_scale))
+    return none();
+  const c10::Device dev = kc->device();
+  if (!fits(q = tensor(a[0]), at::kBFloat16, dev, {p.batch, -1, 64}) ||
+      !fits(selected = tensor(a[5]), at::kInt, dev, {p.batch, p.heads_kv, -1}) ||
+      !fits(sink = tensor(a[6]), at::kFloat, dev, {q->size(1)}) ||
+      !results(a[8], a[9], *q, &given_out, &given_lse))
+    return none();
+  p.heads_q = (int)q->size(1);
+  p.count = (int)selected->size(2);
+  at::Tensor out, lse;
+  int st;
+  {
+    const Unlocked unlocked;
+    out = given_out ? *given_out : make(*q, at::kBFloat16, {p.batch, p.heads_q, 64});
+    lse = given_lse ? *given_lse : make(*q, at::kFloat, {p.heads_q, p.batch});
+    const size_t bytes = f_pages_ws(&p);
+    const at::Tensor ws = make(*q, at::kByte, {(int64_t)bytes});
+    st = f_pages(&p, data(q), data(kc), data(vc), data_as<int>(table), data_as<int>(lens),
+                 data_as<int>(selected), data_as<float>(sink), out.data_ptr(),
+                 data_as<float>(&lse), ws.data_ptr(), bytes, current_stream(*q));
+  }
+  if (st != 0) return PyLong_FromLong(st);
+  return tuple({&out, &lse});
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* key_mass(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  attn_sink_mass_params p;
+  const at::Tensor *q, *kc, *table, *lens, *cu, *lse, *mass;
+  if (n != 9 || !paged(kc = tensor(a[1]), nullptr, false, table = tensor(a[2]),
+                       lens = tensor(a[3]), &p) ||
+      !truth(a[7], &p.accumulate) || !real(a[8], &p.softmax_scale))
+    return none();
+  const c10::Device dev = kc->device();
+  if (!fits(q = tensor(a[0]), at::kBFloat16, dev, {-1, -1, 64}) ||
+      !fits(cu = tensor(a[4]), at::kInt, dev, {p.batch + 1ll}) ||
+      !fits(lse = tensor(a[5]), at::kFloat, dev, {q->size(1), q->size(0)}) ||
+      !fits(mass = tensor(a[6]), at::kFloat, dev, {p.batch, p.heads_kv, -1}))
+    return none();
+  p.total_q = (int)q->size(0);
+  p.heads_q = (int)q->size(1);
+  p.max_keys = (int)mass->size(2);
+  int st;
+  {
+    const Unlocked unlocked;
+    st = f_mass(&p, data(q), data(kc), data_as<int>(table), data_as<int>(lens),
+                data_as<int>(cu), data_as<float>(lse), data_as<float>(mass), current_stream(*q));
+  }
+  return PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  attn_sink_evict_params p;
+  const at::Tensor *kc, *vc, *table, *lens, *mass;
+  if (n != 8 || !paged(kc = tensor(a[0]), vc = tensor(a[1]), true, table = tensor(a[2]),
+                       lens = tensor(a[3]), &p) ||
+      !integer(a[5], &p.budget) || !integer(a[6], &p.keep_first) || !integer(a[7], &p.keep_last) ||
+      !fits(mass = tensor(a[4]), at::kFloat, kc->device(), {p.batch, p.heads_kv, -1}) ||
+      table->numel() > INT_MAX)
+    return none();
+  p.max_keys = (int)mass->size(2);
+  p.max_freed = (int)table->numel();
+  at::Tensor left, fewer, freed, count;
+  int st;
+  {
+    const Unlocked unlocked;
+    left = make(*mass, at::kFloat, mass->sizes());
+    const int64_t at1 = padded(4ll * p.max_freed), at2 = at1 + padded(4ll * p.batch);
+    const at::Tensor all = make(*kc, at::kByte, {at2 + 4});
+    freed = part(all, 0, at::kInt, {p.max_freed});
+    fewer = part(all, at1, at::kInt, {p.batch});
+    count = part(all, at2, at::kInt, {1});
+    const size_t bytes = f_evict_ws(&p);
+    const at::Tensor ws = make(*kc, at::kByte, {(int64_t)bytes});
+    st = f_evict(&p, data(kc), data(vc), data_as<int>(table), data_as<int>(lens),
+                 data_as<float>(mass), data_as<float>(&left), data_as<int>(&fewer),
+                 data_as<int>(&freed), data_as<int>(&count), ws.data_ptr(), bytes,
+                 current_stream(*kc));
+  }
+  if (st != 0) return PyLong_FromLong(st);
+  return tuple({&fewer, &left, &freed, &count});
+  END_HANDLE_TH_ERRORS
+}
+
+// init(addresses of the entry points, in the order of their declaration above)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* f[6];
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "init takes six addresses");
+  constexpr int kCalls = 16;
+  void* f[kCalls];
+  if (n != kCalls) {
+    PyErr_SetString(PyExc_TypeError, "init takes sixteen addresses");
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i)
+  for (int i = 0; i < kCalls; ++i)
     if ((f[i] = PyLong_AsVoidPtr(a[i])) == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
       return nullptr;
@@ -399,12 +626,24 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   f_rope_bwd = reinterpret_cast<decltype(f_rope_bwd)>(f[3]);
   f_extend_ws = reinterpret_cast<decltype(f_extend_ws)>(f[4]);
   f_extend = reinterpret_cast<decltype(f_extend)>(f[5]);
+  f_shared_ws = reinterpret_cast<decltype(f_shared_ws)>(f[6]);
+  f_shared = reinterpret_cast<decltype(f_shared)>(f[7]);
+  f_bounds = reinterpret_cast<decltype(f_bounds)>(f[8]);
+  f_select_ws = reinterpret_cast<decltype(f_select_ws)>(f[9]);
+  f_select = reinterpret_cast<decltype(f_select)>(f[10]);
+  f_pages_ws = reinterpret_cast<decltype(f_pages_ws)>(f[11]);
+  f_pages = reinterpret_cast<decltype(f_pages)>(f[12]);
+  f_mass = reinterpret_cast<decltype(f_mass)>(f[13]);
+  f_evict_ws = reinterpret_cast<decltype(f_evict_ws)>(f[14]);
+  f_evict = reinterpret_cast<decltype(f_evict)>(f[15]);
   return none();
 }
 
 #define FAST(name) {#name, (PyCFunction)(void*)name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init),     FAST(page_plan), FAST(qkv_rope), FAST(qkv_rope_backward),
-                         FAST(extend), {nullptr, nullptr, 0, nullptr}};
+                         FAST(extend),   FAST(decode_shared), FAST(page_bounds),
+                         FAST(select_pages), FAST(decode_pages), FAST(key_mass), FAST(evict),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "attn_sink_fast", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

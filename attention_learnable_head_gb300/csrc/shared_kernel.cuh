@@ -1,0 +1,133 @@
+// The prefix of groups of sequences in a decode step, sm_103a: the keys that a
+// group's sequences share are read once for all of them.
+//
+// A tile is T = floor(128 / G) consecutive sequences of a group times the G query
+// heads of one kv head: their new tokens' rows lie next to each other in q, so the
+// tile is a tile of attn_sink_extend_kernel whose tokens all see the whole prefix,
+// and that kernel computes it: it leaves each part's maximum, sum and unnormalised
+// output in the workspace.  The keys behind the prefix are each sequence's own; the
+// decode kernel reads them (kDecShared) and joins everything with the sink.
+//
+// This schedule kernel of one CTA lists the tiles' parts.  Groups of one sequence and
+// short prefixes have none (see shared_own): their sequences read all keys themselves.
+#pragma once
+#include "decode_kernel.cuh"
+#include "extend_kernel.cuh"
+
+namespace attn_sink {
+
+static_assert(kDecTileRows == kBlockM, "a tile of the extend kernel");
+
+constexpr int kSharedWarps = 32;
+
+struct SharedPlan {
+  ExtParams e;                             // batch, heads, cache, items, slots
+  const int* cu_groups;                    // [num_groups + 1]
+  const int* prefix_lens;                  // [num_groups]
+  SharedRef* refs;                         // [B]
+  int num_groups;
+};
+
+__global__ void __launch_bounds__(32 * kSharedWarps, 1)
+attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
+  __shared__ int s_scan[32];
+  __shared__ unsigned long long s_work;
+  grid_launch_dependents();
+  const ExtParams& e = p.e;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cap = e.max_pages * e.page_size;
+  if (tid == 0) s_work = 0;
+  __syncthreads();
+  bool bad = false;
+  // The keys that group i reads together, and its sequences [c0, c1); by a whole warp.
+  auto group = [&](int i, int* c0, int* c1) {
+    const int a0 = __ldg(p.cu_groups + i), a1 = __ldg(p.cu_groups + i + 1);
+    const int keys = __ldg(p.prefix_lens + i);
+    *c0 = max(0, a0);
+    *c1 = min(e.batch, a1);
+    bad |= a0 < 0 || a1 > e.batch || a1 < a0 || keys < 0 || (i == 0 && a0 != 0) ||
+           (i == p.num_groups - 1 && a1 != e.batch);
+    int least = INT_MAX;
+    for (int b = *c0 + lane; b < *c1; b += 32) {
+      const int len = __ldg(e.seq_lens + b);
+      bad |= len < 0 || len > cap;
+      least = min(least, max(0, min(len, cap)));
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    const int shared = min(keys, least);
+    return *c1 - *c0 >= kSharedMinSeqs && shared >= kSharedMinKeys ? shared : 0;
+  };
+  // all tiles' blocks of keys: what a slot's share is
+  unsigned long long work = 0;
+  for (int i = warp; i < p.num_groups; i += kSharedWarps) {
+    int c0, c1;
+    const int keys = group(i, &c0, &c1);
+    if (keys > 0)
+      work += (unsigned long long)((c1 - c0 + e.tokens - 1) / e.tokens) *
+              (unsigned)((keys + kBlockN - 1) / kBlockN);
+  }
+  if (lane == 0 && work > 0) atomicAdd(&s_work, work);      // whole numbers: any order
+  if (bad) atomicCAS(e.err, 0, DEVERR_DECODE_INPUT);
+  __syncthreads();
+  const unsigned long long all = s_work * (unsigned)e.heads_kv;
+  const int chunk = (int)min(max((all + (unsigned)e.slots - 1) / (unsigned)e.slots,
+                                 (unsigned long long)kExtMinBlocks), 1ull << 24);
+  // the items of 32 groups at a time, one group a warp
+  int listed = 0;
+  bool over = false;                       // more than the workspace holds: no valid cu_groups
+  for (int i0 = 0; i0 < p.num_groups; i0 += kSharedWarps) {
+    const int i = i0 + warp;
+    int c0 = 0, c1 = 0, keys = 0;
+    if (i < p.num_groups) keys = group(i, &c0, &c1);
+    const int blocks = (keys + kBlockN - 1) / kBlockN;
+    const int tiles = keys > 0 ? (c1 - c0 + e.tokens - 1) / e.tokens : 0;
+    const int parts = keys > 0 ? ext_parts(blocks, chunk) : 0;
+    __syncthreads();                       // the last round's counts have been read
+    if (lane == 0) s_scan[warp] = tiles * parts;
+    __syncthreads();
+    const int mine = s_scan[lane];
+    int upto = mine;
+    #pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    const int first = listed + __shfl_sync(0xffffffffu, upto - mine, warp);
+    listed += __shfl_sync(0xffffffffu, upto, 31);           // 32 groups: below 2^31
+    over = listed > e.n_items;             // never where cu_groups ascends: recorded
+    if (over) break;
+    for (int x = lane; x < tiles * parts; x += 32) {
+      const int tile = x / parts, part = x - tile * parts;
+      const int per = (blocks + parts - 1) / parts, skip = min(blocks, part * per);
+      ExtItem it;
+      it.num = min(per, blocks - skip);
+      it.blk0 = skip;
+      it.seq = c0;                         // whose block-table row the keys are read through
+      it.row0 = c0 + tile * e.tokens;
+      it.lo = 0;
+      it.hi = keys;
+      it.mlo = 0;
+      it.mhi = keys / kBlockN - skip;      // the last block may hold keys behind the prefix
+      it.rows = min(e.tokens, c1 - it.row0) * e.group;
+      it.at0 = 1 << 30;                    // every row sees them all
+      it.split = part << 16 | max(parts, 2);   // one part, too, leaves its sums
+      it.first = first + tile * parts;
+      const uint4* src = reinterpret_cast<const uint4*>(&it);
+      uint4* dst = reinterpret_cast<uint4*>(e.items + first + x);
+      dst[0] = src[0];
+      dst[1] = src[1];
+      dst[2] = src[2];
+    }
+    for (int b = c0 + lane; b < c1; b += 32)
+      p.refs[b] = keys > 0 ? SharedRef{first + (b - c0) / e.tokens * parts, parts}
+                           : SharedRef{0, 0};
+  }
+  if (over) {                              // the same for every thread
+    __syncthreads();
+    for (int b = tid; b < e.batch; b += 32 * kSharedWarps) p.refs[b] = SharedRef{0, 0};
+  }
+  for (int x = (over ? 0 : listed) + tid; x < e.n_items; x += 32 * kSharedWarps)
+    e.items[x].num = -1;
+}
+
+}  // namespace attn_sink
