@@ -17,7 +17,7 @@
 // the 16 for lane t of four, loaded straight into registers.
 //
 // Selection: one CTA for each (sequence, kv head) finds the score of the last page it
-// takes bit by bit (topk.cuh).  The scores come from fp32 sums, so every page within
+// takes (topk.cuh).  The scores come from fp32 sums, so every page within
 // twice their error of that one is computed again in 64 bits, where any are left out
 // (a fraction of a page a row, on average).  What is selected goes through a bitmap to
 // ascending order.
@@ -235,15 +235,15 @@ __device__ __forceinline__ unsigned long long page_score_exact(const SelectParam
 }
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ uint32_t s_score[];                     // [min(max_pages, kSelectStage)]
-  __shared__ int s_sum[2][kThreads / 32];
+  __shared__ NthShared<kThreads> s_nth;
   __shared__ uint32_t s_sure[kThreads], s_tie[kThreads];    // bitmaps of 32 kThreads pages
   __shared__ unsigned long long s_key[kSelectBand];
   __shared__ int s_at[kSelectBand];
   __shared__ int s_many;
-  __shared__ unsigned s_low, s_peak;
+  __shared__ unsigned s_peak;
   const int tid = threadIdx.x, lane = tid & 31;
   const int b = (int)(blockIdx.x / (unsigned)p.heads_kv);
   const int h = (int)(blockIdx.x - (unsigned)b * (unsigned)p.heads_kv);
@@ -277,7 +277,6 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   }
   if (tid == 0) {
     s_many = 0;
-    s_low = 0xFFFFFFFFu;
     s_peak = 0;
   }
   grid_dependency_wait();                                   // the scores
@@ -293,26 +292,17 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   if (lane == 0) atomicMax(&s_peak, peak);
   auto at = [&](int i) { return staged ? s_score[i] : ordered(__ldcg(scores + i)); };
   int turn = 0;
-  bool split;
-  const uint32_t bound = block_nth_largest<kThreads, uint32_t>(
+  int above;
+  const uint32_t low = block_nth<kThreads>(
       need, [&](auto&& take) {
         for (int i = tid; i < n; i += kThreads) take(at(i));
-      }, s_sum, &turn, &split);
-  // the smallest score that is taken
-  uint32_t low = 0xFFFFFFFFu;
-  for (int i = tid; i < n; i += kThreads) {
-    const uint32_t v = at(i);
-    if (v >= bound) low = min(low, v);
-  }
-  low = __reduce_min_sync(0xffffffffu, low);
-  if (lane == 0) atomicMin(&s_low, low);
-  __syncthreads();
+      }, &s_nth, &turn, &above);           // the smallest score that is taken
   // No score is further off than the rounding of its sums: 8 products of 16 terms, each
   // sum cut below 2^-23 of what the terms' sizes add up to at most.
   const float most = norm * __uint_as_float(s_peak << 16);
   const float off = most * 0x1p-15f;                        // twice that, for both sides
-  const float last = unordered(s_low);
-  uint32_t from = s_low, upto = s_low;                      // the border, both ends inside
+  const float last = unordered(low);
+  uint32_t from = low, upto = low;                      // the border, both ends inside
   if (!(most < 1e37f)) {                                    // infinities, NaN
     from = 0;
     upto = 0xFFFFFFFFu;
@@ -326,8 +316,8 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     sure += v > upto;
     border += v >= from && v <= upto;
   }
-  sure = block_sum<kThreads>(sure, s_sum, &turn);
-  border = block_sum<kThreads>(border, s_sum, &turn);
+  sure = block_sum<kThreads>(sure, s_nth.sum, &turn);
+  border = block_sum<kThreads>(border, s_nth.sum, &turn);
   const int left = need - sure;                             // of the border, <= border
   // which of the border: all, by their ranks in shared memory, or by a 64-bit bound
   const bool again = left < border && (off > 0.0f || !(most < 1e37f));
@@ -357,13 +347,13 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     __syncthreads();
     if (!ranked) {
       bool whole;
-      bound64 = block_nth_largest<kThreads, unsigned long long>(
+      bound64 = block_nth64<kThreads>(
           left, [&](auto&& take) {
             for (int i = tid; i < n; i += kThreads) {
               const uint32_t v = at(i);
               if (v >= from && v <= upto) take(exact[i]);
             }
-          }, s_sum, &turn, &whole);
+          }, s_nth.sum, &turn, &whole);
       if (whole && bound64 > 0) --bound64;                  // all at or above it: none is a tie
     }
   }
@@ -391,7 +381,7 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
       const uint32_t v = at(i);
       above += v >= from && v <= upto && exact[i] > bound64;
     }
-    ties = left - block_sum<kThreads>(above, s_sum, &turn);
+    ties = left - block_sum<kThreads>(above, s_nth.sum, &turn);
   }
   if (left == border) ties = 0;
   int done = p.keep_first;
@@ -413,13 +403,13 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     __syncthreads();
     uint32_t word = s_sure[tid], equal = s_tie[tid];
     int all;
-    const int before = block_scan<kThreads>(__popc(equal), s_sum, &turn, &all);
+    const int before = block_scan<kThreads>(__popc(equal), s_nth.sum, &turn, &all);
     for (int k = min(__popc(equal), ties - before); k > 0; --k) {
       word |= equal & (0u - equal);
       equal &= equal - 1;
     }
     ties = max(0, ties - all);
-    int place = done + block_scan<kThreads>(__popc(word), s_sum, &turn, &all);
+    int place = done + block_scan<kThreads>(__popc(word), s_nth.sum, &turn, &all);
     done += all;
     while (word != 0) {
       out[place++] = p.keep_first + base + 32 * tid + __ffs(word) - 1;

@@ -169,11 +169,11 @@ int select_layout(const attn_sink_select_params* p, SelectLayout* L) {
   return ATTN_SINK_OK;
 }
 
-// CTAs of the selection and the eviction: few threads for short rows, of which there
-// tend to be many, many for long ones.
-constexpr int kRowThreadsFew = 256;
-constexpr int kRowThreadsMany = 1024;
-constexpr int kRowLong = 4096;
+// Rows of q a sequence, on average, up to which warps keep them in registers.
+constexpr int kMassFewRows = 32;
+
+// Threads of a selection's or an eviction's CTA, for rows of so many values.
+int row_threads(int row) { return row <= 2048 ? 256 : row <= 8192 ? 512 : 1024; }
 
 // ----------------------------------------------------------------------------- eviction
 struct EvictLayout {
@@ -198,6 +198,17 @@ int evict_layout(const attn_sink_evict_params* p, EvictLayout* L) {
   return ATTN_SINK_OK;
 }
 
+auto select_kernel(int threads) -> void (*)(SelectParams) {
+  return threads == 256   ? attn_sink_select_kernel<256>
+         : threads == 512 ? attn_sink_select_kernel<512>
+                          : attn_sink_select_kernel<1024>;
+}
+auto evict_kernel(int threads) -> void (*)(EvictParams) {
+  return threads == 256   ? attn_sink_evict_kernel<256>
+         : threads == 512 ? attn_sink_evict_kernel<512>
+                          : attn_sink_evict_kernel<1024>;
+}
+
 bool g_cache_attr_set[kMaxDevices] = {false};
 
 // The shared memory limits of the kernels that keep a row in it, once per device.
@@ -207,18 +218,15 @@ int cache_attributes() {
     return ATTN_SINK_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if (!g_cache_attr_set[dev]) {
-    if (cudaFuncSetAttribute(attn_sink_evict_kernel<kRowThreadsFew>,
+    for (int threads : {256, 512, 1024})
+      if (cudaFuncSetAttribute(evict_kernel(threads), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               4 * kEvictStage) != cudaSuccess ||
+          cudaFuncSetAttribute(select_kernel(threads), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               4 * kSelectStage) != cudaSuccess)
+        return ATTN_SINK_ERR_CUDA;
+    if (cudaFuncSetAttribute(attn_sink_key_mass_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kEvictStage) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_sink_evict_kernel<kRowThreadsMany>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kEvictStage) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_sink_select_kernel<kRowThreadsFew>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kSelectStage) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_sink_select_kernel<kRowThreadsMany>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kSelectStage) != cudaSuccess)
+                             kMassSmemBytes) != cudaSuccess)
       return ATTN_SINK_ERR_CUDA;
     g_cache_attr_set[dev] = true;
   }
@@ -425,14 +433,12 @@ int attn_sink_select_pages(const attn_sink_select_params* params, const void* q,
   if (x >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;
   attn_sink_page_scores_kernel<<<dim3((unsigned)x, params->batch), kScoreThreads, 0, s>>>(sp);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
-  const bool many = params->max_pages > kRowLong;
+  const int threads = row_threads(params->max_pages);
   const size_t smem = 4 * (size_t)std::min(std::max(params->max_pages, 1), kSelectStage);
   const unsigned rows = (unsigned)params->batch * (unsigned)params->heads_kv;
-  const bool ok = many ? launch_dependent(attn_sink_select_kernel<kRowThreadsMany>, rows,
-                                          kRowThreadsMany, smem, s, sp)
-                       : launch_dependent(attn_sink_select_kernel<kRowThreadsFew>, rows,
-                                          kRowThreadsFew, smem, s, sp);
-  return ok ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+  return launch_dependent(select_kernel(threads), rows, threads, smem, s, sp)
+             ? ATTN_SINK_OK
+             : ATTN_SINK_ERR_CUDA;
 }
 
 namespace {
@@ -518,7 +524,9 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
   int sms = 0;
   int* err = nullptr;
   if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
+  if ((st = cache_attributes()) != ATTN_SINK_OK) return st;
   MassParams mp;
+  std::memset(&mp, 0, sizeof(mp));
   mp.q = static_cast<const __nv_bfloat16*>(q);
   mp.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
   mp.block_table = block_table;
@@ -538,12 +546,28 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
   mp.max_keys = params->max_keys;
   mp.accumulate = params->accumulate;
   mp.scale_log2 = params->softmax_scale * kLog2e;
-  // blocks of keys, up to a few rounds of the CTAs that the GPU holds at once
-  const long long pairs = (long long)params->batch * params->heads_kv;
-  const int blocks = (params->max_keys + kMassKeys - 1) / kMassKeys;
-  const int x = (int)std::max<long long>(1, std::min<long long>(blocks, (24ll * sms + pairs - 1) / pairs));
-  attn_sink_key_mass_kernel<<<dim3(x, params->heads_kv, params->batch), kMassThreads, 0,
-                              static_cast<cudaStream_t>(stream)>>>(mp);
+  mp.tokens = kBlockM / mp.group;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long rows = (long long)params->total_q * mp.group;
+  if (rows > (long long)kMassFewRows * params->batch) {
+    if ((st = encode_rows(&mp.tm_q, q, params->total_q, params->heads_q,
+                          CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mp.tokens, mp.group)) != ATTN_SINK_OK)
+      return st;
+    const dim3 grid((params->max_keys + kBlockM - 1) / kBlockM, params->heads_kv, params->batch);
+    attn_sink_key_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, s>>>(mp);
+    return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+  }
+  // a warp for each (32 keys, kv head), up to three rounds of the CTAs that fit at once
+  constexpr int kWarps = kMassFewThreads / 32;
+  const long long warps = (params->max_keys + 31ll) / 32 * params->heads_kv;
+  const long long least = (params->heads_kv + kWarps - 1) / kWarps;      // a warp a head
+  const long long x = std::max(least, std::min((warps + kWarps - 1) / kWarps,
+                                               6ll * sms / params->batch));
+  const dim3 grid((unsigned)x, params->batch);
+  if (rows <= 8ll * params->batch)
+    attn_sink_key_mass_few_kernel<1><<<grid, kMassFewThreads, 0, s>>>(mp);
+  else
+    attn_sink_key_mass_few_kernel<4><<<grid, kMassFewThreads, 0, s>>>(mp);
   return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 
@@ -612,10 +636,8 @@ int attn_sink_evict(const attn_sink_evict_params* params, void* k_cache, void* v
   ep.stage = std::min(params->max_keys, kEvictStage);
   const unsigned rows = (unsigned)params->batch * (unsigned)params->heads_kv;
   const size_t smem = 4 * (size_t)std::max(ep.stage, 1);
-  if (params->max_keys > kRowLong)
-    attn_sink_evict_kernel<kRowThreadsMany><<<rows + 1, kRowThreadsMany, smem, s>>>(ep);
-  else
-    attn_sink_evict_kernel<kRowThreadsFew><<<rows + 1, kRowThreadsFew, smem, s>>>(ep);
+  const int threads = row_threads(params->max_keys);
+  evict_kernel(threads)<<<rows + 1, threads, smem, s>>>(ep);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   // about eight CTAs an SM, over the rows and the moves of each, 64 a CTA at a time
   const unsigned y = std::min(rows, 8u * (unsigned)sms);

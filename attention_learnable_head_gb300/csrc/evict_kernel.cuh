@@ -1,8 +1,7 @@
 // Eviction from a paged cache by accumulated attention weight, sm_103a.
 //
-// One CTA for each (sequence, kv head) finds the weight of the last key that stays bit by
-// bit (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th
-// kept key at or behind the budget goes to the n-th hole below it.  Only as many rows
+// One CTA for each (sequence, kv head) finds the weight of the last key that stays
+// (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th kept key at or behind the budget goes to the n-th hole below it.  Only as many rows
 // move as there are holes, and no row is both read and written, so that a second kernel
 // can copy them in any order, 16 lanes a move (8 for the key, 8 for the value).  One more
 // CTA of the first kernel scans the sequences for the pages that become free.
@@ -79,16 +78,16 @@ __device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[k
 }
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_mass[];                      // [stage]
-  __shared__ int s_sum[2][kThreads / 32];
+  __shared__ NthShared<kThreads> s_nth;
   __shared__ uint32_t s_kept[kThreads], s_tie[kThreads];    // bitmaps of 32 kThreads keys
   __shared__ int s_list[kThreads];
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   if (blockIdx.x == gridDim.x - 1) {
-    evict_pages<kThreads>(p, s_sum, reinterpret_cast<int*>(s_kept), reinterpret_cast<int*>(s_tie),
+    evict_pages<kThreads>(p, s_nth.sum, reinterpret_cast<int*>(s_kept), reinterpret_cast<int*>(s_tie),
                           s_list);
     return;
   }
@@ -114,18 +113,15 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
   auto at = [&](int j) { return staged ? s_mass[j] : ordered(__ldg(mass + j)); };
   const int lo = p.keep_first, hi = len - p.keep_last;      // the keys that compete
   const int need = p.budget - p.keep_first - p.keep_last;   // < hi - lo
-  int turn = 0, ties = 0;
+  int turn = 0, ties = 0;                                   // equal ones that stay
   uint32_t bound = 0xFFFFFFFFu;
-  bool exact = need == 0;
-  if (need > 0)
-    bound = block_nth_largest<kThreads, uint32_t>(
+  if (need > 0) {
+    int above;
+    bound = block_nth<kThreads>(
         need, [&](auto&& take) {
           for (int j = lo + tid; j < hi; j += kThreads) take(at(j));
-        }, s_sum, &turn, &exact);
-  if (!exact) {
-    int above = 0;
-    for (int j = lo + tid; j < hi; j += kThreads) above += at(j) > bound;
-    ties = need - block_sum<kThreads>(above, s_sum, &turn);
+        }, &s_nth, &turn, &above);
+    ties = need - above;
   }
   // bitmaps of 32 kThreads keys at a time, a word a thread
   uint2* moves = p.moves + row * p.max_moves;               // positions first: x from, y to
@@ -142,8 +138,8 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
             kept = true;
           } else if (need > 0) {
             const uint32_t v = at(j);
-            kept = v > bound || (exact && v == bound);
-            tie = !exact && v == bound;
+            kept = v > bound;
+            tie = v == bound;
           }
         }
         k = __ballot_sync(0xffffffffu, kept);
@@ -157,7 +153,7 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
     __syncthreads();
     uint32_t kept = s_kept[tid], equal = s_tie[tid];
     int all;
-    const int before = block_scan<kThreads>(__popc(equal), s_sum, &turn, &all);
+    const int before = block_scan<kThreads>(__popc(equal), s_nth.sum, &turn, &all);
     for (int k = min(__popc(equal), ties - before); k > 0; --k) {
       kept |= equal & (0u - equal);
       equal &= equal - 1;
@@ -167,13 +163,13 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
     const int j0 = base + 32 * tid;
     const uint32_t below = fewer - j0 >= 32 ? 0xFFFFFFFFu : fewer <= j0 ? 0u : (1u << (fewer - j0)) - 1u;
     uint32_t hole = ~kept & below, mover = kept & ~below;
-    int place = holes + block_scan<kThreads>(__popc(hole), s_sum, &turn, &all);
+    int place = holes + block_scan<kThreads>(__popc(hole), s_nth.sum, &turn, &all);
     holes += all;
     while (hole != 0) {
       moves[place++].y = (uint32_t)(j0 + __ffs(hole) - 1);
       hole &= hole - 1;
     }
-    place = movers + block_scan<kThreads>(__popc(mover), s_sum, &turn, &all);
+    place = movers + block_scan<kThreads>(__popc(mover), s_nth.sum, &turn, &all);
     movers += all;
     while (mover != 0) {
       moves[place++].x = (uint32_t)(j0 + __ffs(mover) - 1);

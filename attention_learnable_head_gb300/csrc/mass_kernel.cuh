@@ -5,24 +5,28 @@
 // With the lse at hand nothing has to be known of the other keys: a weight needs its
 // score alone, and values are not read.  The keys are the rows of the product, the
 // (token, head) rows of q its columns, so that a thread sums the weights of its own keys
-// and nothing is exchanged before the end.  Warp-level products m16n8k16 hold 32 keys
-// of a warp in registers for as long as q passes by; as a dot product does not care for
-// the order of its terms, the k index is permuted so that a lane's fragments are whole
-// 16-byte chunks (chunks t and 4 + t for lane t of four): keys go from their pages
-// straight into registers, q comes from shared memory 16 bytes a lane.
+// and nothing is exchanged before the end.
 //
-// One new token a sequence: the keys' bytes bound it.  Prompts: an exponential a score.
+// Few rows of q a sequence (one new token): the keys' bytes bound it.  Every warp walks
+// through keys of one head by itself, 32 at a time with the next 32 on their way, with
+// all rows of q in registers, and multiplies with m16n8k16 (a tcgen05 product has 64 rows
+// of keys at least, which would have to go through shared memory).  As a dot product does
+// not care for the order of its terms, the k index is permuted so that a lane's
+// fragments are whole 16-byte chunks (chunks t and 4 + t for lane t of four): keys go from
+// their pages straight into registers.
+//
+// Many rows (prompts): an exponential a score bounds it.  A CTA holds 128 keys and q passes
+// by in tiles of 128 rows through a TMA ring; S = K Q^T goes to TMEM (tcgen05), two tiles
+// at a time, and two warpgroups take turns: a thread has one key, a tile's 128 scores of
+// it in 128 columns, and the rows' lse comes from shared memory, the same for all.
 #pragma once
 #include <cuda_bf16.h>
-#include "sm103_ptx.cuh"
+#include "fwd_kernel.cuh"
 
 namespace attn_sink {
 
-constexpr int kMassThreads = 256;
-constexpr int kMassKeys = 256;           // of a CTA at a time: 32 a warp
-constexpr int kMassRows = 64;            // rows of q in shared memory at a time, two buffers
-
 struct MassParams {
+  CUtensorMap tm_q;               // [T][H_q][64] bf16, box 64 x G x tokens per tile
   const __nv_bfloat16* q;         // [T][H_q][64]
   const __nv_bfloat16* k_cache;   // [num_pages][page_size][H_kv][64]
   const int* block_table;         // [B][max_pages]
@@ -31,162 +35,443 @@ struct MassParams {
   const float* lse;               // [H_q][T]
   float* mass;                    // [B][H_kv][max_keys]
   int* err;
-  int batch, total_q, heads_q, heads_kv, group;
+  int batch, total_q, heads_q, heads_kv, group, tokens;
   int page_size, num_pages, max_pages, max_keys, accumulate;
   float scale_log2;
 };
 
-// 16-byte chunk c of row r of q in shared memory: rows of 128 bytes, whose two halves
-// are exchanged in every other row, so that 8 lanes that read 4 chunks of 2 rows
-// touch every bank once.
-__device__ __forceinline__ uint32_t mass_q_at(int r, int c) {
-  return (uint32_t)r * 128u + (uint32_t)((c ^ ((r & 1) << 2)) << 4);
+// A sequence: its new tokens [q0, q0 + n) of q, its keys, and those with an entry.
+struct MassSeq {
+  int q0, n, len, keys;
+};
+__device__ __forceinline__ MassSeq mass_seq(const MassParams& p, int b, bool* bad) {
+  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), l0 = __ldg(p.seq_lens + b);
+  MassSeq s;
+  s.q0 = min(max(c0, 0), p.total_q);
+  s.n = max(0, min(c1, p.total_q) - s.q0);
+  s.len = max(0, min(l0, p.max_pages * p.page_size));
+  s.keys = min(s.len, p.max_keys);
+  *bad = s.q0 != c0 || s.q0 + s.n != c1 || s.len != l0 || s.keys != s.len;
+  return s;
 }
 
-__global__ void __launch_bounds__(kMassThreads, 3)
-attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
-  __shared__ __align__(128) uint8_t s_q[2][kMassRows * 128];
-  __shared__ float s_lse[2][kMassRows];    // times log2(e)
-  __shared__ int s_at[2][kMassRows];       // last key the row sees; -1: no weight at all
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), l0 = __ldg(p.seq_lens + b);
-  const int q0 = min(max(c0, 0), p.total_q), n = max(0, min(c1, p.total_q) - q0);
-  const int cap = p.max_pages * p.page_size;
-  const int len = max(0, min(l0, cap)), keys = min(len, p.max_keys);
-  if (tid == 0 && blockIdx.x == 0 && h == 0 &&
-      (q0 != c0 || q0 + n != c1 || len != l0 || keys != len))
+constexpr uint32_t kMassNoRow = 0xFFFFFFFFu;
+
+// The row of key j in the cache, in units of a head's 128 bytes; kMassNoRow (and
+// recorded) without a page.
+__device__ __forceinline__ uint32_t mass_row(const MassParams& p, const int* table, int h, int j) {
+  const int pg = j / p.page_size, e = __ldg(table + pg);
+  if ((unsigned)e >= (unsigned)p.num_pages) {
     atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-  const long long rows = (long long)n * p.group;
-  const int at0 = len - n;                 // key position of token 0
+    return kMassNoRow;
+  }
+  return ((uint32_t)e * (uint32_t)p.page_size + (uint32_t)(j - pg * p.page_size)) *
+             (uint32_t)p.heads_kv + (uint32_t)h;
+}
+
+// ----------------------------------------------------------------------------- few rows
+constexpr int kMassFewThreads = 256;
+
+// Sequences of up to 8 kTiles rows of q; those with more take them in turns.
+template <int kTiles>
+__global__ void __launch_bounds__(kMassFewThreads, 2)
+attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const unsigned id = blockIdx.x * (kMassFewThreads / 32) + warp;
+  const unsigned step = gridDim.x * (kMassFewThreads / 32) / (unsigned)p.heads_kv;
+  const unsigned first = id / (unsigned)p.heads_kv;
+  const int h = (int)(id - first * (unsigned)p.heads_kv);
+  const int b = blockIdx.y;
+  bool bad;
+  const MassSeq s = mass_seq(p, b, &bad);
+  if (bad && id == 0 && lane == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  if (first >= step) return;
   float* mass = p.mass + ((size_t)b * p.heads_kv + h) * p.max_keys;
   const int* table = p.block_table + (size_t)b * p.max_pages;
-  // what of C there is to write
-  const int end = p.accumulate ? (n > 0 ? keys : 0) : p.max_keys;
-  for (int j0 = blockIdx.x * kMassKeys; j0 < end; j0 += gridDim.x * kMassKeys) {
-    if (j0 >= keys || n == 0) {
-      if (j0 + tid < end) mass[j0 + tid] = 0.0f;
-      continue;
-    }
-    // A: this warp's 32 keys, two fragments of 16: rows g and g + 8 of each
-    uint4 a[4][2];
-    bool has[4];
+  if (!p.accumulate)
+    for (long long j = (s.n > 0 ? s.keys : 0) + 32ll * first + lane; j < p.max_keys; j += 32ll * step)
+      mass[j] = 0.0f;
+  const long long rows = (long long)s.n * p.group;
+  const int at0 = s.len - s.n;             // key position of token 0
+  const uint4* cache = reinterpret_cast<const uint4*>(p.k_cache) + t;
+  for (long long r0 = 0; r0 < rows; r0 += 8 * kTiles) {
+    // B: row g of every tile, the dimensions of this lane's chunks; lse and the last key
+    // seen of the two rows 2 t, 2 t + 1 whose scores it gets (-1: none, no weight)
+    uint32_t bq[kTiles][8];
+    float z[kTiles][2];
+    int at[kTiles][2];
+    int least = INT_MAX;
     #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int j = j0 + 32 * warp + 8 * r + g;
-      has[r] = false;
-      size_t row = 0;
-      if (j < keys) {
-        const int pg = j / p.page_size, e = __ldg(table + pg);
-        has[r] = (unsigned)e < (unsigned)p.num_pages;
-        row = ((size_t)e * p.page_size + (j - pg * p.page_size)) * p.heads_kv + h;
-        if (!has[r] && t == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-      }
-      const uint4* src = reinterpret_cast<const uint4*>(p.k_cache) + row * 8 + t;
+    for (int i = 0; i < kTiles; ++i) {
       #pragma unroll
-      for (int u = 0; u < 2; ++u) a[r][u] = has[r] ? __ldg(src + 4 * u) : make_uint4(0, 0, 0, 0);
-    }
-    // rows of q from the first token that sees a key of this block
-    const long long first = (long long)max(0, j0 - at0) * p.group / kMassRows * kMassRows;
-    const int last = min(j0 + kMassKeys, keys) - 1;        // last key of the block
-    const int chunks = (int)((rows - first + kMassRows - 1) / kMassRows);
-    auto load = [&](int chunk) {
-      const long long r0 = first + (long long)chunk * kMassRows;
-      const int buf = chunk & 1;
-      #pragma unroll
-      for (int x = tid; x < kMassRows * 8; x += kMassThreads) {
-        const int r = x >> 3;
-        const bool in = r0 + r < rows;
-        const int tok = in ? (int)((r0 + r) / p.group) : 0;
-        const int hd = in ? (int)(r0 + r - (long long)tok * p.group) : 0;
-        cp_async_16_zfill(smem_u32(s_q[buf]) + mass_q_at(r, x & 7),
-                          p.q + ((size_t)(q0 + tok) * p.heads_q + h * p.group + hd) * 64 +
-                              8 * (x & 7),
-                          in ? 16 : 0);
-      }
-      cp_async_commit();
-      if (tid < kMassRows) {
-        const bool in = r0 + tid < rows;
-        float z = 0.0f;
-        int at = -1;
-        if (in) {
-          const int tok = (int)((r0 + tid) / p.group);
-          const int hd = (int)(r0 + tid - (long long)tok * p.group);
-          z = __ldg(p.lse + (size_t)(h * p.group + hd) * p.total_q + q0 + tok);
-          if (!isinf(z)) at = at0 + tok;
+      for (int u = 0; u < 2; ++u) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        const long long r = r0 + 8 * i + g;
+        if (r < rows) {
+          const int tok = (int)(r / p.group), hd = (int)(r - (long long)tok * p.group);
+          v = __ldg(reinterpret_cast<const uint4*>(p.q) +
+                    ((size_t)(s.q0 + tok) * p.heads_q + h * p.group + hd) * 8 + 4 * u + t);
         }
-        s_lse[buf][tid] = z * kLog2e;
-        s_at[buf][tid] = at;
-      }
-    };
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    load(0);
-    for (int chunk = 0; chunk < chunks; ++chunk) {
-      const int buf = chunk & 1;
-      if (chunk + 1 < chunks) {
-        load(chunk + 1);
-        cp_async_wait<1>();
-      } else {
-        cp_async_wait<0>();
-      }
-      __syncthreads();
-      const long long left = rows - first - (long long)chunk * kMassRows;
-      const int tiles = (int)((min((long long)kMassRows, left) + 7) / 8);
-      const bool clear = __all_sync(0xffffffffu, min(s_at[buf][lane], s_at[buf][lane + 32]) >= last);
-      const uint32_t base = smem_u32(s_q[buf]);
-      for (int i = 0; i < tiles; ++i) {
-        uint32_t bq[2][4];
-        #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          ld_shared_v4(base + mass_q_at(8 * i + g, 4 * u + t), bq[u]);
-        const float2 z = *reinterpret_cast<const float2*>(&s_lse[buf][8 * i + 2 * t]);
-        float c[2][4];
-        #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          #pragma unroll
-          for (int e = 0; e < 4; ++e) c[s][e] = 0.0f;
-          #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            mma_16816_bf16(c[s], a[2 * s][u].x, a[2 * s + 1][u].x, a[2 * s][u].y,
-                           a[2 * s + 1][u].y, bq[u][0], bq[u][1]);
-            mma_16816_bf16(c[s], a[2 * s][u].z, a[2 * s + 1][u].z, a[2 * s][u].w,
-                           a[2 * s + 1][u].w, bq[u][2], bq[u][3]);
+        bq[i][4 * u] = v.x;
+        bq[i][4 * u + 1] = v.y;
+        bq[i][4 * u + 2] = v.z;
+        bq[i][4 * u + 3] = v.w;
+        const long long c = r0 + 8 * i + 2 * t + u;
+        z[i][u] = 0.0f;
+        at[i][u] = -1;
+        if (c < rows) {
+          const int tok = (int)(c / p.group), hd = (int)(c - (long long)tok * p.group);
+          const float x = __ldg(p.lse + (size_t)(h * p.group + hd) * p.total_q + s.q0 + tok);
+          if (!isinf(x)) {
+            z[i][u] = -x * kLog2e;
+            at[i][u] = at0 + tok;
           }
         }
-        if (clear) {
+        least = min(least, at[i][u]);
+      }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    const bool add = p.accumulate || r0 > 0;
+    // this lane's key of a group of 32, whose row the others get from it
+    auto row_of = [&](unsigned grp) {
+      const int j = 32 * (int)grp + lane;
+      return j < s.keys ? mass_row(p, table, h, j) : kMassNoRow;
+    };
+    auto load = [&](uint32_t mine, uint4 (*a)[2]) {
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t row = __shfl_sync(0xffffffffu, mine, 8 * r + g);
+        #pragma unroll
+        for (int u = 0; u < 2; ++u)
+          a[r][u] = row != kMassNoRow ? __ldg(cache + (size_t)row * 8 + 4 * u)
+                                      : make_uint4(0, 0, 0, 0);
+      }
+    };
+    const unsigned groups = (unsigned)(s.keys + 31) / 32;
+    auto use = [&](unsigned grp, uint32_t mine, const uint4 (*a)[2], float old) {
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int j0 = 32 * (int)grp;
+      #pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        #pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           #pragma unroll
-          for (int s = 0; s < 2; ++s)
-            #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              sum[2 * s + r] += ex2_approx(fmaf(c[s][2 * r], p.scale_log2, -z.x)) +
-                                ex2_approx(fmaf(c[s][2 * r + 1], p.scale_log2, -z.y));
-        } else {
-          const int2 at = *reinterpret_cast<const int2*>(&s_at[buf][8 * i + 2 * t]);
+          for (int u = 0; u < 2; ++u) {
+            mma_16816_bf16(c, a[2 * m][u].x, a[2 * m + 1][u].x, a[2 * m][u].y, a[2 * m + 1][u].y,
+                           bq[i][4 * u], bq[i][4 * u + 1]);
+            mma_16816_bf16(c, a[2 * m][u].z, a[2 * m + 1][u].z, a[2 * m][u].w, a[2 * m + 1][u].w,
+                           bq[i][4 * u + 2], bq[i][4 * u + 3]);
+          }
           #pragma unroll
-          for (int s = 0; s < 2; ++s)
-            #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int j = j0 + 32 * warp + 16 * s + 8 * r + g;
-              const float w0 = ex2_approx(fmaf(c[s][2 * r], p.scale_log2, -z.x));
-              const float w1 = ex2_approx(fmaf(c[s][2 * r + 1], p.scale_log2, -z.y));
-              sum[2 * s + r] += (j <= at.x ? w0 : 0.0f) + (j <= at.y ? w1 : 0.0f);
+          for (int r = 0; r < 2; ++r) {
+            float w0 = ex2_approx(fmaf(c[2 * r], p.scale_log2, z[i][0]));
+            float w1 = ex2_approx(fmaf(c[2 * r + 1], p.scale_log2, z[i][1]));
+            if (j0 + 31 > least) {         // the same for the whole warp
+              const int j = j0 + 16 * m + 8 * r + g;
+              w0 = j <= at[i][0] ? w0 : 0.0f;
+              w1 = j <= at[i][1] ? w1 : 0.0f;
             }
+            sum[2 * m + r] += w0 + w1;
+          }
         }
       }
-      __syncthreads();                     // the buffer is filled again
+      #pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+      }
+      // lane t of four has key 8 t + g
+      const float w = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
+      const bool has = __shfl_sync(0xffffffffu, mine, 8 * t + g) != kMassNoRow;
+      const int j = j0 + 8 * t + g;
+      if (j < s.keys) mass[j] = old + (has ? w : 0.0f);
+    };
+    auto before = [&](unsigned grp) {
+      const int j = 32 * (int)grp + 8 * t + g;
+      return add && j < s.keys ? mass[j] : 0.0f;
+    };
+    if constexpr (kTiles > 1) {            // the registers hold one group's keys
+      uint4 a[4][2];
+      uint32_t next = first < groups ? row_of(first) : kMassNoRow;
+      for (unsigned now = first; now < groups; now += step) {
+        const uint32_t mine = next;
+        load(mine, a);
+        const float old = before(now);
+        if (now + step < groups) next = row_of(now + step);
+        use(now, mine, a, old);
+      }
+      continue;
     }
+    // rows two groups ahead, keys one
+    uint4 a[2][4][2];
+    float old[2] = {0.0f, 0.0f};
+    uint32_t mine = first < groups ? row_of(first) : kMassNoRow;
+    uint32_t next = first + step < groups ? row_of(first + step) : kMassNoRow;
+    if (first < groups) {
+      load(mine, a[0]);
+      old[0] = before(first);
+    }
+    for (unsigned grp = first; grp < groups; grp += 2 * step) {
+      #pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const unsigned now = grp + k * step;
+        if (now < groups) {
+          if (now + step < groups) {
+            load(next, a[k ^ 1]);
+            old[k ^ 1] = before(now + step);
+          }
+          const uint32_t far = now + 2 * step < groups ? row_of(now + 2 * step) : kMassNoRow;
+          use(now, mine, a[k], old[k]);
+          mine = next;
+          next = far;
+        }
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- many rows
+constexpr int kMassThreads = 320;        // 8 warps of weights, copy warp, MMA warp
+constexpr int kMassStages = 3;
+constexpr uint32_t kMassTmemCols = 256;  // two tiles of 128 fp32 columns
+constexpr int kMassSmemBytes = 1024 + (int)kTileBytes * (1 + kMassStages);
+
+__global__ void __maxnreg__(96)
+attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t q_full[kMassStages], q_empty[kMassStages];
+  __shared__ __align__(8) uint64_t d_full[2], d_empty[2], mma_drained;
+  __shared__ __align__(16) float s_z[kMassStages][kBlockM];   // -lse log2(e); -inf: no row
+  __shared__ __align__(16) int s_at[kMassStages][kBlockM];    // last key the row sees; -1: none
+  __shared__ int s_clear[kMassStages];     // no weight of the tile is masked
+  __shared__ float s_part[kBlockM];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int j0 = blockIdx.x * kBlockM;
+  bool bad;
+  const MassSeq s = mass_seq(p, b, &bad);
+  if (bad && tid == 0 && blockIdx.x == 0 && h == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+  float* mass = p.mass + ((size_t)b * p.heads_kv + h) * p.max_keys;
+  const int at0 = s.len - s.n;             // key position of token 0
+  // tiles of q from the first token that sees a key of the block
+  const int t0 = max(0, j0 - at0) / p.tokens * p.tokens;
+  const int tiles = j0 < s.keys && s.n > t0 ? (s.n - t0 + p.tokens - 1) / p.tokens : 0;
+  if (tiles == 0) {                        // the same for the whole CTA
+    const int j = j0 + tid;
+    if (!p.accumulate && tid < kBlockM && j < p.max_keys) mass[j] = 0.0f;
+    return;
+  }
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sK = smem;
+  uint8_t* sQ = smem + kTileBytes;
+  const int rows = p.tokens * p.group;     // of a tile; behind them zeros, with no weight
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kMassStages; ++i) {
+      mbar_init(&q_full[i], 2);            // the copy, and the rows' lse
+      mbar_init(&q_empty[i], 5);           // the product, and four warps that read the lse
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);
+    }
+    mbar_init(&mma_drained, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == kFwdMmaWarp) {
+    tmem_alloc(&tmem_base_sh, kMassTmemCols);
+    tmem_relinquish();
+  }
+  // a thread's key, and the half of it that it copies
+  const int r = tid & 127, c = warp >> 2;
+  bool has = false;
+  if (warp < 8) {
+    const uint32_t row = j0 + r < s.keys
+                             ? mass_row(p, p.block_table + (size_t)b * p.max_pages, h, j0 + r)
+                             : kMassNoRow;
+    has = row != kMassNoRow;
+    const __nv_bfloat16* src = has ? p.k_cache + (size_t)row * 64 : p.q;   // else nothing is read
     #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-      sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-      if (!has[r]) sum[r] = 0.0f;
+    for (int u = 0; u < 4; ++u)
+      cp_async_16_zfill(smem_u32(sK) + sw128_offset((uint32_t)r, (uint32_t)(4 * c + u)),
+                        has ? src + 8 * (4 * c + u) : p.q, has ? 16u : 0u);
+    cp_async_commit();
+    // the rows of a tile that no copy writes
+    for (int x = rows * 8 + tid; x < kBlockM * 8; x += 256)
+      for (int i = 0; i < kMassStages; ++i)
+        st_shared_v4(smem_u32(sQ + i * kTileBytes) + (uint32_t)x * 16u, 0, 0, 0, 0);
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  if (warp == kFwdTmaWarp) {
+    // ---------------------------------------------------------------- q and its lse
+    int tok[4], hd[4];                     // of columns lane, lane + 32, ..
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      tok[u] = (lane + 32 * u) / p.group;
+      hd[u] = lane + 32 * u - tok[u] * p.group;
     }
-    // lane t of four writes key 8 t + g
-    const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
-    const int j = j0 + 32 * warp + 8 * t + g;
-    if (j < keys) mass[j] = p.accumulate ? mass[j] + mine : mine;
-    else if (j < end) mass[j] = 0.0f;
+    float z[4];
+    auto fetch = [&](int i) {
+      #pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = t0 + i * p.tokens + tok[u];
+        z[u] = tok[u] < p.tokens && x < s.n
+                   ? __ldg(p.lse + (size_t)(h * p.group + hd[u]) * p.total_q + s.q0 + x)
+                   : INFINITY;
+      }
+    };
+    const int last = min(j0 + kBlockM, s.keys) - 1;        // of the block
+    const uint32_t bytes = (uint32_t)rows * 128u;
+    if (lane == 0) tma_prefetch_desc(&p.tm_q);
+    fetch(0);
+    int i = 0;
+    for (; i < tiles; ++i) {
+      const int st = i % kMassStages;
+      if (i >= kMassStages && !mbar_wait_warp(&q_empty[st], ((i / kMassStages) & 1) ^ 1, &abort_flag))
+        break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[st], bytes);
+        tma_load_3d(&p.tm_q, &q_full[st], sQ + st * kTileBytes, 0, h * p.group,
+                    s.q0 + t0 + i * p.tokens);
+      }
+      bool clear = true;
+      #pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = at0 + t0 + i * p.tokens + tok[u];
+        const bool weight = !isinf(z[u]);
+        s_z[st][lane + 32 * u] = weight ? -z[u] * kLog2e : -INFINITY;
+        s_at[st][lane + 32 * u] = weight ? at : -1;
+        clear = clear && (tok[u] >= p.tokens || (weight && at >= last));
+      }
+      clear = __all_sync(0xffffffffu, clear);
+      if (lane == 0) s_clear[st] = clear;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[st]);
+      if (i + 1 < tiles) fetch(i + 1);
+    }
+    if (i < tiles) {
+      // given up: the copies in flight land before the CTA releases its shared memory
+      if (lane == 0) {
+        abort_flag = 1;
+        atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 0x10);
+        for (int k = max(0, i - kMassStages); k < i; ++k)
+          mbar_wait(&q_full[k % kMassStages], (k / kMassStages) & 1, nullptr);
+      }
+      __syncwarp();
+    }
+  } else if (warp == kFwdMmaWarp) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc_bf16(kBlockM, kBlockM, false, false);
+      const uint64_t dK = make_sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dQ = make_sdesc_sw128(smem_u32(sQ), 16, 1024);
+      constexpr uint32_t kTileU = kTileBytes >> 4;
+      bool ok = true;
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int st = i % kMassStages, buf = i & 1;
+        ok = mbar_wait(&q_full[st], (i / kMassStages) & 1, &abort_flag) &&
+             (i < 2 || mbar_wait(&d_empty[buf], ((i >> 1) & 1) ^ 1, &abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        #pragma unroll
+        for (int k = 0; k < kHeadDim / 16; ++k)
+          mma_ss(tmem + buf * kBlockM, dK + 2 * k, dQ + st * kTileU + 2 * k, idesc, k > 0);
+        mma_commit(&d_full[buf]);
+        mma_commit(&q_empty[st]);
+      }
+      if (!ok) {
+        abort_flag = 1;
+        atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 0x11);
+      }
+      mma_commit(&mma_drained);            // before TMEM is released
+      mbar_wait(&mma_drained, 0, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- weights
+    // warpgroup c takes the tiles c, c + 2, ..: thread = key = TMEM lane
+    const uint32_t tD = tmem + c * kBlockM + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint64_t scale = f2(p.scale_log2, p.scale_log2);
+    uint64_t sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+    bool ok = true;
+    for (int i = c; i < tiles; i += 2) {
+      const int st = i % kMassStages;
+      ok = mbar_wait_warp(&q_full[st], (i / kMassStages) & 1, &abort_flag) &&
+           mbar_wait_warp(&d_full[c], (i >> 1) & 1, &abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int parts = (min(p.tokens, s.n - t0 - i * p.tokens) * p.group + 31) / 32;
+      const bool clear = s_clear[st] != 0;
+      for (int part = 0; part < parts; ++part) {
+        uint32_t x[32];
+        tmem_ld_x32(tD + 32 * part, x);
+        tmem_ld_wait();
+        const float4* z4 = reinterpret_cast<const float4*>(&s_z[st][32 * part]);
+        if (clear) {
+          #pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 z = z4[e >> 2];
+            #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint64_t y = ffma2(f2(__uint_as_float(x[e + 2 * u]),
+                                          __uint_as_float(x[e + 2 * u + 1])),
+                                       scale, u ? f2(z.z, z.w) : f2(z.x, z.y));
+              sum[u] = fadd2(sum[u], f2(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))));
+            }
+          }
+        } else {
+          const int4* at4 = reinterpret_cast<const int4*>(&s_at[st][32 * part]);
+          const int j = j0 + r;
+          #pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 z = z4[e >> 2];
+            const int4 at = at4[e >> 2];
+            const float w0 = ex2_approx(fmaf(__uint_as_float(x[e]), p.scale_log2, z.x));
+            const float w1 = ex2_approx(fmaf(__uint_as_float(x[e + 1]), p.scale_log2, z.y));
+            const float w2 = ex2_approx(fmaf(__uint_as_float(x[e + 2]), p.scale_log2, z.z));
+            const float w3 = ex2_approx(fmaf(__uint_as_float(x[e + 3]), p.scale_log2, z.w));
+            sum[0] = fadd2(sum[0], f2(j <= at.x ? w0 : 0.0f, j <= at.y ? w1 : 0.0f));
+            sum[1] = fadd2(sum[1], f2(j <= at.z ? w2 : 0.0f, j <= at.w ? w3 : 0.0f));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&d_empty[c]);
+        mbar_arrive(&q_empty[st]);
+      }
+    }
+    const uint64_t both = fadd2(sum[0], sum[1]);
+    const float w = f2_lo(both) + f2_hi(both);
+    if (c == 1) s_part[r] = w;
+    ok = named_barrier_and(1, 256, ok);
+    if (!ok) {
+      abort_flag = 1;
+      atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 0x12);
+    } else if (c == 0) {
+      const int j = j0 + r;
+      const float all = has ? w + s_part[r] : 0.0f;
+      if (j < s.keys) mass[j] = p.accumulate ? mass[j] + all : all;
+      else if (!p.accumulate && j < p.max_keys) mass[j] = 0.0f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kFwdMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kMassTmemCols);
   }
 }
 
