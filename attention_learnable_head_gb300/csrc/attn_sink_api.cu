@@ -18,6 +18,7 @@
 #include "bounds_kernel.cuh"
 #include "bwd_dq_kernel.cuh"
 #include "bwd_kernel.cuh"
+#include "decode_join.cuh"
 #include "decode_kernel.cuh"
 #include "evict_kernel.cuh"
 #include "extend_kernel.cuh"

@@ -100,6 +100,8 @@ attn_sink_page_bounds_kernel(const __grid_constant__ BoundsParams p) {
 
 // ----------------------------------------------------------------------------- scores
 constexpr int kScoreThreads = 256;
+constexpr int kScoreStages = 3;         // groups of 16 pages on their way to a warp
+constexpr int kScoreSmem = kScoreThreads / 32 * kScoreStages * 16 * 256;
 
 struct SelectParams {
   const __nv_bfloat16* q;         // [B][H_q][64]
@@ -156,50 +158,88 @@ attn_sink_page_scores_kernel(const __grid_constant__ SelectParams p) {
   }
   const size_t row = (size_t)b * p.heads_kv + h;
   const int* table = p.block_table + (size_t)b * p.max_pages;
-  const uint4* bounds = reinterpret_cast<const uint4*>(p.bounds) + (size_t)h * 16 + t;
-  const size_t pstep = (size_t)p.heads_kv * 16;
+  extern __shared__ __align__(256) uint8_t score_smem[];
+  const uint32_t ring = smem_u32(score_smem) + (uint32_t)warp * (kScoreStages * 16 * 256);
+  // 16-byte chunk c of page r: every other page has the halves of its 128 bytes exchanged,
+  // so that 8 lanes that read 4 chunks of 2 pages touch each bank once
+  auto place = [](int r, int c) { return (uint32_t)r * 256u + (uint32_t)((c ^ ((r & 1) << 2)) << 4); };
+  const unsigned tiles = (unsigned)(have + 15) / 16;
   auto entry = [&](unsigned tile) {                         // of page 16 tile + lane % 16
     const int c = 16 * (int)tile + (lane & 15);
-    return c < have ? __ldg(table + c) : -1;
-  };
-  const unsigned tiles = (unsigned)(have + 15) / 16;
-  int next = first < tiles ? entry(first) : -1;
-  for (unsigned tile = first; tile < tiles; tile += step) {
-    const int e0 = __shfl_sync(0xffffffffu, next, g), e1 = __shfl_sync(0xffffffffu, next, g + 8);
-    if (tile + step < tiles) next = entry(tile + step);
-    const bool in0 = (unsigned)e0 < (unsigned)p.num_pages, in1 = (unsigned)e1 < (unsigned)p.num_pages;
-    uint4 v[2][4];
-    #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      v[0][u] = in0 ? __ldg(bounds + e0 * pstep + 4 * u) : make_uint4(0, 0, 0, 0);
-      v[1][u] = in1 ? __ldg(bounds + e1 * pstep + 4 * u) : make_uint4(0, 0, 0, 0);
-    }
-    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t peak = 0;
-    #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      mma_16816_bf16(c, v[0][u].x, v[1][u].x, v[0][u].y, v[1][u].y, qb[4 * u], qb[4 * u + 1]);
-      mma_16816_bf16(c, v[0][u].z, v[1][u].z, v[0][u].w, v[1][u].w, qb[4 * u + 2], qb[4 * u + 3]);
-      #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        peak = __vmaxu2(peak, __vmaxu2(v[r][u].x & 0x7fff7fffu, v[r][u].y & 0x7fff7fffu));
-        peak = __vmaxu2(peak, __vmaxu2(v[r][u].z & 0x7fff7fffu, v[r][u].w & 0x7fff7fffu));
+    int e = -1;
+    if (tile < tiles && c < have) {
+      e = __ldg(table + c);
+      if ((unsigned)e >= (unsigned)p.num_pages) {
+        atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+        e = -1;
       }
     }
-    // the largest head's score (a NaN among them counts: the row's peak says so too)
+    return e;
+  };
+  auto issue = [&](int mine, int st) {
     #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float m = 2 * t < p.group ? c[2 * r] : -INFINITY;
-      if (2 * t + 1 < p.group) m = fmaxf(m, c[2 * r + 1]);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int at = 16 * (int)tile + g + 8 * r;
-      if (t == 0 && at < have) p.scores[row * p.max_pages + at] = (r ? in1 : in0) ? m : -INFINITY;
+    for (int u = 0; u < 8; ++u) {
+      const int r = 2 * u + (lane >> 4);
+      const int e = __shfl_sync(0xffffffffu, mine, r);      // -1: nothing is read, 0 written
+      cp_async_16_zfill(ring + st * (16 * 256) + place(r, lane & 15),
+                        e >= 0 ? p.bounds + ((size_t)e * p.heads_kv + h) * 128 + 8 * (lane & 15) : p.q,
+                        e >= 0 ? 16 : 0);
     }
-    if (t == 0 && ((16 * (int)tile + g < have && !in0) || (16 * (int)tile + g + 8 < have && !in1)))
-      atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-    peak = __reduce_max_sync(0xffffffffu, max(peak & 0xffffu, peak >> 16));
-    if (lane == 0) p.peak[row * p.tiles + tile] = peak;
+  };
+  int mine[kScoreStages];
+  #pragma unroll
+  for (int st = 0; st < kScoreStages; ++st) mine[st] = entry(first + st * step);
+  #pragma unroll
+  for (int st = 0; st < kScoreStages; ++st) {
+    if (first + st * step < tiles) issue(mine[st], st);
+    cp_async_commit();
+  }
+  int next = entry(first + kScoreStages * step);
+  for (unsigned base = first; base < tiles; base += kScoreStages * step) {
+    #pragma unroll
+    for (int st = 0; st < kScoreStages; ++st) {
+      const unsigned tile = base + st * step, ahead = tile + kScoreStages * step;
+      if (tile >= tiles) continue;                          // the same for the whole warp
+      cp_async_wait<kScoreStages - 1>();
+      __syncwarp();
+      uint32_t v[2][4][4];
+      #pragma unroll
+      for (int r = 0; r < 2; ++r)
+        #pragma unroll
+        for (int u = 0; u < 4; ++u)
+          ld_shared_v4(ring + st * (16 * 256) + place(8 * r + g, 4 * u + t), v[r][u]);
+      const bool in0 = __shfl_sync(0xffffffffu, mine[st], g) >= 0;
+      const bool in1 = __shfl_sync(0xffffffffu, mine[st], g + 8) >= 0;
+      __syncwarp();                                         // every lane has read the stage
+      mine[st] = next;
+      if (ahead < tiles) issue(next, st);
+      cp_async_commit();
+      next = entry(ahead + step);
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      uint32_t peak = 0;
+      #pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        mma_16816_bf16(c, v[0][u][0], v[1][u][0], v[0][u][1], v[1][u][1], qb[4 * u], qb[4 * u + 1]);
+        mma_16816_bf16(c, v[0][u][2], v[1][u][2], v[0][u][3], v[1][u][3], qb[4 * u + 2],
+                       qb[4 * u + 3]);
+        #pragma unroll
+        for (int r = 0; r < 2; ++r)
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) peak = __vmaxu2(peak, v[r][u][e] & 0x7fff7fffu);
+      }
+      // the largest head's score (a NaN among them counts: the row's peak says so too)
+      #pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float m = 2 * t < p.group ? c[2 * r] : -INFINITY;
+        if (2 * t + 1 < p.group) m = fmaxf(m, c[2 * r + 1]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int at = 16 * (int)tile + g + 8 * r;
+        if (t == 0 && at < have) p.scores[row * p.max_pages + at] = (r ? in1 : in0) ? m : -INFINITY;
+      }
+      peak = __reduce_max_sync(0xffffffffu, max(peak & 0xffffu, peak >> 16));
+      if (lane == 0) p.peak[row * p.tiles + tile] = peak;
+    }
   }
 }
 
@@ -207,28 +247,56 @@ attn_sink_page_scores_kernel(const __grid_constant__ SelectParams p) {
 constexpr int kSelectStage = 12288;     // scores that a CTA keeps in shared memory
 constexpr int kSelectBand = 256;        // pages at the border that it ranks there
 
-// The 64-bit score of a page, by a whole warp.
+// The 64-bit score of a page, by a whole warp: lanes 4 i .. 4 i + 3 have head i, 16
+// dimensions each.  Products of two bf16 are exact in fp32 where they do not leave its
+// range (kWide: they may; then all is done in fp64, of which the GPU has little), and the
+// rounding of each sum is carried on in a second one: 48 bits and more.
+template <bool kWide>
 __device__ __forceinline__ unsigned long long page_score_exact(const SelectParams& p, int b, int h,
                                                                int col) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, i = lane >> 2, t = lane & 3;
   const int page = __ldg(p.block_table + (size_t)b * p.max_pages + col);
   if ((unsigned)page >= (unsigned)p.num_pages) return ordered(-(double)INFINITY);
-  const uint32_t* src =
-      reinterpret_cast<const uint32_t*>(p.bounds) + ((size_t)page * p.heads_kv + h) * 64 + lane;
-  const uint32_t lo = __ldg(src), hi = __ldg(src + 32);
-  unsigned long long best = 0;
-  for (int i = 0; i < p.group; ++i) {
-    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(p.q) +
-                             ((size_t)b * p.heads_q + h * p.group + i) * 32 + lane);
-    const float q0 = bf16_lo(q), q1 = bf16_hi(q);
-    // products of two bf16 are exact in fp64, and with usual exponents the sums are too
-    const float p0 = q0 > 0.0f || q0 != q0 ? q0 : 0.0f, n0 = q0 < 0.0f || q0 != q0 ? q0 : 0.0f;
-    const float p1 = q1 > 0.0f || q1 != q1 ? q1 : 0.0f, n1 = q1 < 0.0f || q1 != q1 ? q1 : 0.0f;
-    double s = (double)p0 * bf16_lo(hi) + (double)n0 * bf16_lo(lo);
-    s += (double)p1 * bf16_hi(hi) + (double)n1 * bf16_hi(lo);
+  const uint4* src =
+      reinterpret_cast<const uint4*>(p.bounds) + ((size_t)page * p.heads_kv + h) * 16 + 2 * t;
+  const uint4* query = reinterpret_cast<const uint4*>(p.q) +
+                       ((size_t)b * p.heads_q + h * p.group + (i < p.group ? i : 0)) * 8 + 2 * t;
+  double wide = 0.0;
+  float s[2] = {0.0f, 0.0f}, low[2] = {0.0f, 0.0f};
+  #pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint4 q4 = __ldg(query + u), lo4 = __ldg(src + u), hi4 = __ldg(src + 8 + u);
+    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+    const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
     #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const unsigned long long o = ordered(s);
+    for (int e = 0; e < 4; ++e)
+      #pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float x = k ? bf16_hi(q[e]) : bf16_lo(q[e]);
+        const float y[2] = {k ? bf16_hi(hi[e]) : bf16_lo(hi[e]), k ? bf16_hi(lo[e]) : bf16_lo(lo[e])};
+        const float z[2] = {x < 0.0f ? 0.0f : x, x > 0.0f ? 0.0f : x};    // NaN: both
+        #pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          if constexpr (kWide) {
+            wide = fma((double)z[d], (double)y[d], wide);
+          } else {
+            // two-sum: next + (what its rounding lost) = s + the product
+            const float v = __fmul_rn(z[d], y[d]);
+            const float next = __fadd_rn(s[d], v), part = __fsub_rn(next, s[d]);
+            low[d] = __fadd_rn(low[d], __fadd_rn(__fsub_rn(s[d], __fsub_rn(next, part)),
+                                                 __fsub_rn(v, part)));
+            s[d] = next;
+          }
+        }
+      }
+  }
+  double all = kWide ? wide : ((double)s[0] + (double)s[1]) + ((double)low[0] + (double)low[1]);
+  all += __shfl_xor_sync(0xffffffffu, all, 1);
+  all += __shfl_xor_sync(0xffffffffu, all, 2);
+  unsigned long long best = i < p.group ? ordered(all) : 0;
+  #pragma unroll
+  for (int d = 4; d < 32; d <<= 1) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, d);
     best = o > best ? o : best;
   }
   return best;
@@ -242,6 +310,8 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ uint32_t s_sure[kThreads], s_tie[kThreads];    // bitmaps of 32 kThreads pages
   __shared__ unsigned long long s_key[kSelectBand];
   __shared__ int s_at[kSelectBand];
+  __shared__ uint8_t s_take[kSelectBand];
+  __shared__ int s_side[2];
   __shared__ int s_many;
   __shared__ unsigned s_peak;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -265,18 +335,25 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     grid_dependency_wait();
     return;
   }
-  // the largest sum of |q| of a head
+  // the largest sum of |q| of a head, lanes 4 i .. 4 i + 3 have head i (a NaN is the
+  // largest as an integer, too)
   float norm = 0.0f;
-  for (int i = 0; i < p.group; ++i) {
-    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(p.q) +
-                             ((size_t)b * p.heads_q + h * p.group + i) * 32 + lane);
-    float a = fabsf(bf16_lo(q)) + fabsf(bf16_hi(q));
+  if ((lane >> 2) < p.group) {
+    const uint4* query = reinterpret_cast<const uint4*>(p.q) +
+                         ((size_t)b * p.heads_q + h * p.group + (lane >> 2)) * 8 + 2 * (lane & 3);
     #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-    norm = a > norm || a != a ? a : norm;
+    for (int u = 0; u < 2; ++u) {
+      const uint4 v = __ldg(query + u);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      #pragma unroll
+      for (int e = 0; e < 4; ++e) norm += fabsf(bf16_lo(w[e])) + fabsf(bf16_hi(w[e]));
+    }
   }
+  norm += __shfl_xor_sync(0xffffffffu, norm, 1);
+  norm += __shfl_xor_sync(0xffffffffu, norm, 2);
+  norm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(norm) & 0x7fffffffu));
   if (tid == 0) {
-    s_many = 0;
+    s_many = s_side[0] = s_side[1] = 0;
     s_peak = 0;
   }
   grid_dependency_wait();                                   // the scores
@@ -316,8 +393,13 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     sure += v > upto;
     border += v >= from && v <= upto;
   }
-  sure = block_sum<kThreads>(sure, s_nth.sum, &turn);
-  border = block_sum<kThreads>(border, s_nth.sum, &turn);
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  border = __reduce_add_sync(0xffffffffu, border);
+  if (lane == 0 && sure != 0) atomicAdd(&s_side[0], sure);  // whole numbers: any order
+  if (lane == 0 && border != 0) atomicAdd(&s_side[1], border);
+  __syncthreads();
+  sure = s_side[0];
+  border = s_side[1];
   const int left = need - sure;                             // of the border, <= border
   // which of the border: all, by their ranks in shared memory, or by a 64-bit bound
   const bool again = left < border && (off > 0.0f || !(most < 1e37f));
@@ -332,7 +414,9 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
       while (todo != 0) {
         const int j = i0 + __ffs(todo) - 1;
         todo &= todo - 1;
-        const unsigned long long key = page_score_exact(p, b, h, p.keep_first + j);
+        const unsigned long long key = most < 1e37f
+                                           ? page_score_exact<false>(p, b, h, p.keep_first + j)
+                                           : page_score_exact<true>(p, b, h, p.keep_first + j);
         if (lane != 0) continue;
         if (ranked) {
           const int x = atomicAdd(&s_many, 1);              // their order does not matter
@@ -345,7 +429,15 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
       __syncwarp();
     }
     __syncthreads();
-    if (!ranked) {
+    if (ranked) {
+      if (tid < border) {
+        int before = 0;
+        for (int y = 0; y < border; ++y)
+          before += s_key[y] > s_key[tid] || (s_key[y] == s_key[tid] && s_at[y] < s_at[tid]);
+        s_take[tid] = before < left;
+      }
+      __syncthreads();
+    } else {
       bool whole;
       bound64 = block_nth64<kThreads>(
           left, [&](auto&& take) {
@@ -357,23 +449,6 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
       if (whole && bound64 > 0) --bound64;                  // all at or above it: none is a tie
     }
   }
-  // Taken for sure, or one of equals of which the first ones are taken?
-  auto kind = [&](int i) {
-    const uint32_t v = at(i);
-    if (v > upto) return 2;
-    if (v < from) return 0;
-    if (left == border) return 2;
-    if (!again) return 1;
-    if (ranked) {
-      int x = 0;
-      while (s_at[x] != i) ++x;
-      int before = 0;
-      for (int y = 0; y < border; ++y)
-        before += s_key[y] > s_key[x] || (s_key[y] == s_key[x] && s_at[y] < i);
-      return before < left ? 2 : 0;
-    }
-    return exact[i] > bound64 ? 2 : exact[i] == bound64 ? 1 : 0;
-  };
   int ties = !again ? left : 0;                             // equals that are taken
   if (again && !ranked) {
     int above = 0;
@@ -387,28 +462,45 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   int done = p.keep_first;
   for (int base = 0; base < n; base += 32 * kThreads) {
     __syncthreads();                                        // the last round's words are read
-    for (int w = tid >> 5; w < kThreads; w += kThreads / 32) {
-      uint32_t s = 0, e = 0;
-      if (base + 32 * w < n) {
-        const int i = base + 32 * w + lane;
-        const int k = i < n ? kind(i) : 0;
-        s = __ballot_sync(0xffffffffu, k == 2);
-        e = __ballot_sync(0xffffffffu, k == 1);
+    const int words = min(kThreads, (n - base + 31) / 32);
+    if (tid >= words) s_sure[tid] = s_tie[tid] = 0;
+    for (int w = tid >> 5; w < words; w += kThreads / 32) {
+      const int i = base + 32 * w + lane;
+      const uint32_t v = i < n ? at(i) : 0;
+      bool take = i < n && v > upto, tie = false;
+      const bool edge = i < n && v >= from && v <= upto;
+      if (__any_sync(0xffffffffu, edge) && edge) {          // few: of whom some may be taken
+        if (left == border) {
+          take = true;
+        } else if (!again) {
+          tie = true;                                       // the first ones of equals
+        } else if (ranked) {
+          int x = 0;
+          while (s_at[x] != i) ++x;
+          take = s_take[x] != 0;
+        } else {
+          take = exact[i] > bound64;
+          tie = exact[i] == bound64;
+        }
       }
+      const uint32_t s = __ballot_sync(0xffffffffu, take), e = __ballot_sync(0xffffffffu, tie);
       if (lane == 0) {
         s_sure[w] = s;
         s_tie[w] = e;
       }
     }
     __syncthreads();
-    uint32_t word = s_sure[tid], equal = s_tie[tid];
+    uint32_t word = s_sure[tid];
     int all;
-    const int before = block_scan<kThreads>(__popc(equal), s_nth.sum, &turn, &all);
-    for (int k = min(__popc(equal), ties - before); k > 0; --k) {
-      word |= equal & (0u - equal);
-      equal &= equal - 1;
+    if (ties > 0) {                                         // the same for the whole CTA
+      uint32_t equal = s_tie[tid];
+      const int before = block_scan<kThreads>(__popc(equal), s_nth.sum, &turn, &all);
+      for (int k = min(__popc(equal), ties - before); k > 0; --k) {
+        word |= equal & (0u - equal);
+        equal &= equal - 1;
+      }
+      ties = max(0, ties - all);
     }
-    ties = max(0, ties - all);
     int place = done + block_scan<kThreads>(__popc(word), s_nth.sum, &turn, &all);
     done += all;
     while (word != 0) {

@@ -21,6 +21,7 @@ int cache_validate(const P* p, int most_batch) {
 template <typename P>
 int group_validate(const P* p) {
   if (p->heads_q < 1 || p->heads_q % p->heads_kv != 0) return ATTN_SINK_ERR_INVALID_ARG;
+  if ((long long)p->batch * p->heads_q >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;
   return decode_group_ok(p->heads_q / p->heads_kv) ? ATTN_SINK_OK : ATTN_SINK_ERR_UNSUPPORTED;
 }
 
@@ -31,33 +32,32 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 }
 
 // ----------------------------------------------------------------------------- decode
-// Partial results and counters of the decode kernel for `splits` key ranges.
-struct DecodeParts {
+// The slices of a sequence's keys in the decode kernel, and what they leave.
+struct DecodeSlices {
   int splits;
-  size_t off_lo, off_lse, off_done, total;
+  size_t off_ml, total;
 };
-DecodeParts decode_parts(int splits, int batch, int heads_q, int heads_kv) {
-  DecodeParts d;
+DecodeSlices decode_slices(int splits, int batch, int heads_q) {
+  DecodeSlices d;
   d.splits = splits;
-  const size_t o = (size_t)splits * batch * heads_q * kHeadDim * 2;      // bf16
-  d.off_lo = align256(o);
-  d.off_lse = d.off_lo + align256(o);
-  d.off_done = d.off_lse + align256((size_t)splits * heads_q * batch * sizeof(float));
-  d.total = d.off_done + align256((size_t)batch * heads_kv * sizeof(int));
+  const size_t rows = (size_t)splits * batch * heads_q;
+  d.off_ml = align256(rows * kHeadDim * sizeof(float));
+  d.total = d.off_ml + align256(rows * sizeof(float2));
   return d;
 }
 
-// Key ranges of a sequence: see decode_layout.
+constexpr int kDecCtasPerSm = 5;
+
+// As many slices of at least kDecKeys keys as the GPU holds at once.
 int decode_splits(int batch, int heads_kv, long long keys, int sms) {
   const long long ctas = std::max(1ll, (long long)batch * heads_kv);
-  long long s = std::max<long long>(1, (40ll * sms + ctas - 1) / ctas);
-  s = std::min<long long>(s, std::max<long long>(1, (keys + 255) / 256));
-  return (int)std::min<long long>(s, 64);
+  const long long most = std::min(64ll, (keys + kDecKeys - 1) / kDecKeys);
+  return (int)std::max(1ll, std::min(most, kDecCtasPerSm * (long long)sms / ctas));
 }
 
 // The fields of DecodeParams that every mode has; *tma: which copies are taken.
 template <typename P>
-int decode_params(const P* p, const DecodeParts& L, const void* q, const void* k_cache,
+int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* k_cache,
                   const void* v_cache, const int* block_table, const int* seq_lens,
                   const float* sink, void* out, float* lse, uint8_t* ws, int* err,
                   DecodeParams* dp, bool* tma) {
@@ -67,10 +67,8 @@ int decode_params(const P* p, const DecodeParts& L, const void* q, const void* k
   dp->v_cache = static_cast<const __nv_bfloat16*>(v_cache);
   dp->block_table = block_table;
   dp->seq_lens = seq_lens;
-  dp->o_part = reinterpret_cast<__nv_bfloat16*>(ws);
-  dp->o_part_lo = reinterpret_cast<__nv_bfloat16*>(ws + L.off_lo);
-  dp->lse_part = reinterpret_cast<float*>(ws + L.off_lse);
-  dp->done = reinterpret_cast<int*>(ws + L.off_done);
+  dp->slice_o = reinterpret_cast<float*>(ws);
+  dp->slice_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   dp->sink = sink;
   dp->out = static_cast<__nv_bfloat16*>(out);
   dp->lse = lse;
@@ -110,9 +108,17 @@ auto decode_kernel(int group, bool tma) -> void (*)(DecodeParams) {
   }
 }
 
+template <bool kShared>
+bool launch_join(const DecodeParams& dp, cudaStream_t s) {
+  constexpr int kRows = kDecJoinThreads / 32;
+  const long long rows = (long long)dp.batch * dp.heads_q;
+  return launch_dependent(attn_sink_decode_join_kernel<kShared>,
+                          dim3((unsigned)((rows + kRows - 1) / kRows)), kDecJoinThreads, 0, s, dp);
+}
+
 // ----------------------------------------------------------------------------- shared prefixes
 struct SharedLayout {
-  DecodeParts own;
+  DecodeSlices own;
   int tokens, n_items, slots;
   size_t off_items, off_refs, off_ml, off_o, total;
 };
@@ -132,8 +138,7 @@ int shared_layout(const attn_sink_shared_params* p, int sms, SharedLayout* L) {
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
   L->n_items = (int)items;
   const long long cap = (long long)p->max_pages * p->page_size;
-  L->own = decode_parts(decode_splits(p->batch, p->heads_kv, cap, sms), p->batch, p->heads_q,
-                        p->heads_kv);
+  L->own = decode_slices(decode_splits(p->batch, p->heads_kv, cap, sms), p->batch, p->heads_q);
   size_t off = L->own.total;
   L->off_items = off;
   off += align256((size_t)L->n_items * sizeof(ExtItem));
@@ -226,7 +231,16 @@ int cache_attributes() {
         return ATTN_SINK_ERR_CUDA;
     if (cudaFuncSetAttribute(attn_sink_key_mass_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMassSmemBytes) != cudaSuccess)
+                             kMassSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_sink_key_mass_few_kernel<1>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMassFewSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_sink_key_mass_few_kernel<4>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMassFewSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_sink_page_scores_kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kScoreSmem) != cudaSuccess)
       return ATTN_SINK_ERR_CUDA;
     g_cache_attr_set[dev] = true;
   }
@@ -324,9 +338,6 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
   sp.prefix_lens = prefix_lens;
   sp.num_groups = params->num_groups;
   sp.refs = reinterpret_cast<SharedRef*>(ws + L.off_refs);
-  if (cudaMemsetAsync(dp.done, 0, (size_t)params->batch * params->heads_kv * sizeof(int), s) !=
-      cudaSuccess)
-    return ATTN_SINK_ERR_CUDA;
   attn_sink_shared_plan_kernel<<<1, 32 * kSharedWarps, 0, s>>>(sp);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   const auto tiles = tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>;
@@ -335,7 +346,8 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
     return ATTN_SINK_ERR_CUDA;
   const dim3 grid(L.own.splits, params->heads_kv, params->batch);
   return launch_dependent(decode_kernel<kDecShared>(ep.group, dec_tma), grid, kDecThreads, 0, s,
-                          dp)
+                          dp) &&
+                 launch_join<true>(dp, s)
              ? ATTN_SINK_OK
              : ATTN_SINK_ERR_CUDA;
 }
@@ -431,7 +443,8 @@ int attn_sink_select_pages(const attn_sink_select_params* params, const void* q,
   const long long x = std::max(least, std::min((warps + kWarps - 1) / kWarps,
                                                8ll * sms / params->batch));
   if (x >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;
-  attn_sink_page_scores_kernel<<<dim3((unsigned)x, params->batch), kScoreThreads, 0, s>>>(sp);
+  attn_sink_page_scores_kernel<<<dim3((unsigned)x, params->batch), kScoreThreads, kScoreSmem, s>>>(
+      sp);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   const int threads = row_threads(params->max_pages);
   const size_t smem = 4 * (size_t)std::min(std::max(params->max_pages, 1), kSelectStage);
@@ -443,7 +456,7 @@ int attn_sink_select_pages(const attn_sink_select_params* params, const void* q,
 
 namespace {
 
-int pages_layout(const attn_sink_pages_params* p, int sms, DecodeParts* L) {
+int pages_layout(const attn_sink_pages_params* p, int sms, DecodeSlices* L) {
   int st = cache_validate(p, 65535);
   if (st != ATTN_SINK_OK || (st = group_validate(p)) != ATTN_SINK_OK) return st;
   if (!scale_ok(p->softmax_scale) || p->count < 0 ||
@@ -451,15 +464,14 @@ int pages_layout(const attn_sink_pages_params* p, int sms, DecodeParts* L) {
     return ATTN_SINK_ERR_INVALID_ARG;
   if (p->heads_kv > 65535) return ATTN_SINK_ERR_UNSUPPORTED;
   const long long keys = (long long)std::min(p->count, p->max_pages) * p->page_size;
-  *L = decode_parts(decode_splits(p->batch, p->heads_kv, keys, sms), p->batch, p->heads_q,
-                    p->heads_kv);
+  *L = decode_slices(decode_splits(p->batch, p->heads_kv, keys, sms), p->batch, p->heads_q);
   return ATTN_SINK_OK;
 }
 
 }  // namespace
 
 size_t attn_sink_decode_pages_workspace_size(const attn_sink_pages_params* params) {
-  DecodeParts L;
+  DecodeSlices L;
   if (pages_layout(params, sm_count_or_default(), &L) != ATTN_SINK_OK || params->batch == 0)
     return 0;
   return L.total;
@@ -470,7 +482,7 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
                            const int* seq_lens, const int* selected, const float* sink, void* out,
                            float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   NvtxRange range("attn_sink_decode_pages");
-  DecodeParts L;
+  DecodeSlices L;
   int st = pages_layout(params, sm_count_or_default(), &L);
   if (st != ATTN_SINK_OK) return st;
   if (params->batch == 0) return ATTN_SINK_OK;
@@ -493,13 +505,11 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
     return st;
   dp.selected = selected;
   dp.count = params->count;
-  if (cudaMemsetAsync(dp.done, 0, (size_t)params->batch * params->heads_kv * sizeof(int), s) !=
-      cudaSuccess)
-    return ATTN_SINK_ERR_CUDA;
   const dim3 grid(L.splits, params->heads_kv, params->batch);
   decode_kernel<kDecPages>(params->heads_q / params->heads_kv, tma)<<<grid, kDecThreads, 0, s>>>(
       dp);
-  return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
+  if (!launched()) return ATTN_SINK_ERR_CUDA;
+  return L.splits == 1 || launch_join<false>(dp, s) ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 
 int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const void* k_cache,
@@ -546,14 +556,14 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
   mp.max_keys = params->max_keys;
   mp.accumulate = params->accumulate;
   mp.scale_log2 = params->softmax_scale * kLog2e;
-  mp.tokens = kBlockM / mp.group;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = (long long)params->total_q * mp.group;
-  if (rows > (long long)kMassFewRows * params->batch) {
+  if (rows > (long long)kMassFewRows * params->batch && mp.group <= kMassMaxGroup) {
+    mp.tokens = kMassRows / mp.group;
     if ((st = encode_rows(&mp.tm_q, q, params->total_q, params->heads_q,
                           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mp.tokens, mp.group)) != ATTN_SINK_OK)
       return st;
-    const dim3 grid((params->max_keys + kBlockM - 1) / kBlockM, params->heads_kv, params->batch);
+    const dim3 grid((params->max_keys + kMassKeys - 1) / kMassKeys, params->heads_kv, params->batch);
     attn_sink_key_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, s>>>(mp);
     return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
   }
@@ -565,9 +575,9 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
                                                6ll * sms / params->batch));
   const dim3 grid((unsigned)x, params->batch);
   if (rows <= 8ll * params->batch)
-    attn_sink_key_mass_few_kernel<1><<<grid, kMassFewThreads, 0, s>>>(mp);
+    attn_sink_key_mass_few_kernel<1><<<grid, kMassFewThreads, kMassFewSmem, s>>>(mp);
   else
-    attn_sink_key_mass_few_kernel<4><<<grid, kMassFewThreads, 0, s>>>(mp);
+    attn_sink_key_mass_few_kernel<4><<<grid, kMassFewThreads, kMassFewSmem, s>>>(mp);
   return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
 

@@ -40,19 +40,22 @@ constexpr int kDecMaxGroup = 8;        // query heads per kv head
 constexpr int kDecKeys = 64;           // keys per stage: 16 per warp
 constexpr int kDecStages = 2;
 constexpr float kLn2Dec = 0.6931471805599453f;
+constexpr float kLog2eDec = 1.4426950408889634f;
 constexpr int kDecTileRows = 128;      // kDecShared: rows of a prefix tile's partial results
 constexpr int kDecNoKey = INT_MIN;     // kDecPages: no entry of the list, or behind the last key
 constexpr int kSharedMinSeqs = 2;      // kDecShared: smaller groups and shorter prefixes are read
 constexpr int kSharedMinKeys = 64;     //   by each sequence for itself
 
 // What a decode step reads: every cached key (or a window), the pages selected for
-// each kv head, or the keys behind the prefix a group of sequences shares, whose
-// results the merge then joins (shared_kernel.cuh).
+// each kv head, or the keys behind the prefix a group of sequences shares
+// (shared_kernel.cuh).  The last two leave a slice's sums to a kernel that joins them
+// (decode_join.cuh), where there is more than one slice.
 enum DecodeMode { kDecAll, kDecPages, kDecShared };
 
 // The prefix of a sequence in decode_shared: its tile's partial results.
-struct SharedRef {
+struct alignas(16) SharedRef {
   int first, parts;               // of [partial][kv head][128 rows]; 0 parts: no prefix
+  int place, pad;                 // the sequence's place in the tile
 };
 
 struct DecodeParams {
@@ -82,10 +85,12 @@ struct DecodeParams {
   int count;
   const int* cu_groups;           // kDecShared: [num_groups + 1] first sequences
   const int* prefix_lens;         // [num_groups]
-  const SharedRef* refs;          // [B], behind grid_dependency_wait
+  const SharedRef* refs;          // [B]
   const float* prefix_o;          // [partial][H_kv][128 rows][64] sums
   const float2* prefix_ml;        // [partial][H_kv][128 rows]: maximum (log2 units), sum
   int num_groups;
+  float* slice_o;                 // kDecPages, kDecShared: [B][H_q][splits][64] sums
+  float2* slice_ml;               // [B][H_q][splits]: maximum (log2 units), sum
 };
 
 // Page sizes the TMA path copies whole: a multiple of 8 keys (whole 128-byte
@@ -94,13 +99,6 @@ __host__ __device__ constexpr bool decode_tma_page(int page_size) {
   return page_size >= 8 && (page_size & (page_size - 1)) == 0;
 }
 
-// The group of sequence b: its first sequence, how many it has (0: none) and the keys
-// of the prefix that are read once for all of them: none in a group of one, and
-// no more than its shortest sequence has.  Called by a whole CTA of `threads`
-// threads; every thread gets the answer.
-struct SharedGroup {
-  int first, size, prefix;
-};
 __device__ __forceinline__ int shared_seq_len(const int* seq_lens, int b, int cap) {
   return max(0, min(__ldg(seq_lens + b), cap));
 }
@@ -156,7 +154,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   // The slices start on 64-key block boundaries (so the TMA path copies whole
   // pages into a block); keys before the window start are masked.
   int lo = p.window > 0 ? max(0, L - p.window) : 0;
-  int seq_first = 0;                 // kDecShared: the group's first sequence
+  if constexpr (kMode != kDecAll) grid_launch_dependents();
   if constexpr (kMode == kDecShared) {
     __shared__ int s_min[kDecWarps];
     const int gp = shared_find(p.cu_groups, p.num_groups, b);
@@ -175,10 +173,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     for (int w = 0; w < kDecWarps; ++w) least = min(least, s_min[w]);
     if (c0 <= b && b < c1 && c1 - c0 >= kSharedMinSeqs) {
       const int shared = min(keys, least);
-      if (shared >= kSharedMinKeys) {
-        lo = shared;
-        seq_first = c0;
-      }
+      if (shared >= kSharedMinKeys) lo = shared;
     }
   }
   // kDecPages: the sequence's pages; L from here on counts the keys of the listed ones,
@@ -195,6 +190,20 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   const int k1 = min(L, k0 + per);
   const int nblk = k1 > k0 ? (k1 - k0 + kDecKeys - 1) / kDecKeys : 0;
   const size_t row_stride = (size_t)p.heads_kv * 64;     // one key of the cache
+  // kDecShared: the kernel in front computes the prefix at the same time.  This one has
+  // ended only when that one has: one CTA waits for it.
+  auto leave = [&] {
+    if (kMode == kDecShared && split == 0 && g == 0 && b == 0) grid_dependency_wait();
+  };
+  if constexpr (kMode != kDecAll) {
+    if (nblk == 0 && p.splits + (kMode == kDecShared) > 1) {   // an empty slice
+      if (tid < G)
+        p.slice_ml[((size_t)b * p.heads_q + g * G + tid) * p.splits + split] =
+            make_float2(-INFINITY, 0.0f);
+      leave();
+      return;
+    }
+  }
 
   // Q as the A operand (rows >= G are zero): a0 = dims 16 kk + 2 t4 .. + 1,
   // a2 = the same + 8, of head row gr; a1 = a3 = 0 (rows 8..15).
@@ -504,6 +513,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       for (int j = max(0, issued - kDecStages); j < issued; ++j)
         mbar_wait(&kv_full[j % kDecStages], (j / kDecStages) & 1, nullptr);
     }
+    leave();
     return;
   }
   // a value that rounded to fp16 infinity (or a NaN) lies outside the fp16 range
@@ -527,6 +537,42 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   // thread t: head t / 16, dims 4 (t % 16) .. + 4
   const int h = tid >> 4;
   const int d0 = 4 * (tid & 15);
+  if constexpr (kMode != kDecAll) {
+    if (h < G) {
+      float mm = -INFINITY;
+      #pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
+      const int hq = g * G + h;
+      const size_t row = (size_t)b * p.heads_q + hq;
+      const bool whole = kMode == kDecPages && p.splits == 1;   // then the sink joins here
+      const float s2 = whole ? __ldg(p.sink + hq) * kLog2eDec : -INFINITY;
+      const float mf = fmaxf(mm, s2);
+      const float mb = mf == -INFINITY ? 0.0f : mf;
+      float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      #pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float wt = ex2_approx(s_m[w][h] - mb);           // NaN sums reach the result
+        z = fmaf(wt, s_l[w][h], z);
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaf(wt, s_o[w][h][d0 + e], acc[e]);
+      }
+      if (whole) {
+        z += s2 == mb ? 1.0f : ex2_approx(s2 - mb);            // 1 where both are inf
+        const float inv = z != 0.0f ? 1.0f / z : 0.0f;
+        *reinterpret_cast<uint2*>(p.out + row * 64 + d0) = make_uint2(
+            pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        if (d0 == 0)
+          p.lse[(size_t)hq * p.batch + b] = z != 0.0f ? (mb + __log2f(z)) * kLn2Dec : -INFINITY;
+      } else {
+        const size_t at = row * p.splits + split;
+        *reinterpret_cast<float4*>(p.slice_o + at * 64 + d0) =
+            make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (d0 == 0) p.slice_ml[at] = make_float2(mf, z);
+      }
+    }
+    leave();
+    return;
+  }
   if (h < G) {
     float mm = -INFINITY;
     for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
@@ -540,8 +586,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
         for (int e = 0; e < 4; ++e) acc[e] = fmaf(wt, s_o[w][h][d0 + e], acc[e]);
       }
     }
-    const bool some = kMode == kDecAll ? ll > 0.0f : ll != 0.0f;   // NaN scores reach the result
-    const float inv = some ? 1.0f / ll : 0.0f;
+    const float inv = (ll > 0.0f) ? 1.0f / ll : 0.0f;
     const int hq = g * G + h;
     const size_t oi = (((size_t)split * p.batch + b) * p.heads_q + hq) * 64 + d0;
     uint32_t hi[2], lo2[2];
@@ -555,7 +600,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     *reinterpret_cast<uint2*>(p.o_part_lo + oi) = make_uint2(lo2[0], lo2[1]);
     if (d0 == 0)
       p.lse_part[((size_t)split * p.heads_q + hq) * p.batch + b] =
-          some ? (mm + __log2f(ll)) * kLn2Dec : -INFINITY;
+          (ll > 0.0f) ? (mm + __log2f(ll)) * kLn2Dec : -INFINITY;
   }
 
   // ---- the last CTA of (b, g) merges the slices with the sink:
@@ -570,30 +615,14 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  SharedRef ref{0, 0};
-  size_t prow = 0;                   // the prefix's first partial result of this row
-  const size_t pstep = (size_t)p.heads_kv * kDecTileRows;
-  if constexpr (kMode == kDecShared) {
-    grid_dependency_wait();
-    if (lo > 0) {
-      const int2 r = __ldcg(reinterpret_cast<const int2*>(p.refs + b));
-      ref = SharedRef{r.x, r.y};
-    }
-    prow = ((size_t)ref.first * p.heads_kv + g) * kDecTileRows +
-           (b - seq_first) % (kDecTileRows / G) * G + h;
-  }
   if (h < G) {
     const int hq = g * G + h;
     const float sk = __ldg(p.sink + hq);
     float m = sk;
-    if constexpr (kMode == kDecShared)
-      for (int c = 0; c < ref.parts; ++c)
-        m = fmaxf(m, __ldcg(p.prefix_ml + prow + c * pstep).x * kLn2Dec);
     for (int c = 0; c < p.splits; ++c)
       m = fmaxf(m, __ldcg(p.lse_part + ((size_t)c * p.heads_q + hq) * p.batch + b));
     const float m_use = (m == -INFINITY) ? 0.0f : m;
     float z = (sk == -INFINITY) ? 0.0f : __expf(sk - m_use);
-    if (kMode != kDecAll && sk == m_use) z = 1.0f;         // where both are inf, too
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int c = 0; c < p.splits; ++c) {
       const float lc = __ldcg(p.lse_part + ((size_t)c * p.heads_q + hq) * p.batch + b);
@@ -608,21 +637,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       acc[2] = fmaf(wc, bf16_lo(o.y) + bf16_lo(r.y), acc[2]);
       acc[3] = fmaf(wc, bf16_hi(o.y) + bf16_hi(r.y), acc[3]);
     }
-    if constexpr (kMode == kDecShared)
-      for (int c = 0; c < ref.parts; ++c) {
-        const float2 ml = __ldcg(p.prefix_ml + prow + c * pstep);
-        if (ml.x == -INFINITY) continue;            // a part without a key stored no sums
-        const float wc = __expf(fmaf(ml.x, kLn2Dec, -m_use));
-        z = fmaf(wc, ml.y, z);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(
-            p.prefix_o + (prow + c * pstep) * 64 + d0));
-        acc[0] = fmaf(wc, o.x, acc[0]);
-        acc[1] = fmaf(wc, o.y, acc[1]);
-        acc[2] = fmaf(wc, o.z, acc[2]);
-        acc[3] = fmaf(wc, o.w, acc[3]);
-      }
-    const bool some = kMode == kDecAll ? z > 0.0f : z != 0.0f;
-    const float inv_z = some ? 1.0f / z : 0.0f;
+    const float inv_z = (z > 0.0f) ? 1.0f / z : 0.0f;
     uint32_t hi[2], lo2[2];
     #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -633,7 +648,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     const size_t oi = ((size_t)b * p.heads_q + hq) * 64 + d0;
     *reinterpret_cast<uint2*>(p.out + oi) = make_uint2(hi[0], hi[1]);
     if (p.out_lo) *reinterpret_cast<uint2*>(p.out_lo + oi) = make_uint2(lo2[0], lo2[1]);
-    if (d0 == 0) p.lse[(size_t)hq * p.batch + b] = some ? m_use + __logf(z) : -INFINITY;
+    if (d0 == 0) p.lse[(size_t)hq * p.batch + b] = (z > 0.0f) ? m_use + __logf(z) : -INFINITY;
   }
 }
 

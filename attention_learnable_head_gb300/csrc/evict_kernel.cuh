@@ -128,37 +128,31 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
   int holes = 0, movers = 0;
   for (int base = 0; base < len; base += 32 * kThreads) {
     __syncthreads();                                        // the last round's words are read
-    for (int w = tid >> 5; w < kThreads; w += kThreads / 32) {
-      uint32_t k = 0, e = 0;
-      if (base + 32 * w < len) {
-        const int j = base + 32 * w + lane;
-        bool kept = false, tie = false;
-        if (j < len) {
-          if (j < lo || j >= hi) {
-            kept = true;
-          } else if (need > 0) {
-            const uint32_t v = at(j);
-            kept = v > bound;
-            tie = v == bound;
-          }
-        }
-        k = __ballot_sync(0xffffffffu, kept);
-        e = __ballot_sync(0xffffffffu, tie);
-      }
+    const int words = min(kThreads, (len - base + 31) / 32);
+    if (tid >= words) s_kept[tid] = s_tie[tid] = 0;
+    for (int w = tid >> 5; w < words; w += kThreads / 32) {
+      const int j = base + 32 * w + lane;
+      const uint32_t v = j < len ? at(j) : 0;
+      const bool inner = j >= lo && j < hi;
+      const uint32_t k = __ballot_sync(0xffffffffu, j < len && (!inner || (need > 0 && v > bound)));
+      const uint32_t e = __ballot_sync(0xffffffffu, inner && v == bound && ties > 0);
       if (lane == 0) {
         s_kept[w] = k;
         s_tie[w] = e;
       }
     }
     __syncthreads();
-    uint32_t kept = s_kept[tid], equal = s_tie[tid];
+    uint32_t kept = s_kept[tid];
     int all;
-    const int before = block_scan<kThreads>(__popc(equal), s_nth.sum, &turn, &all);
-    for (int k = min(__popc(equal), ties - before); k > 0; --k) {
-      kept |= equal & (0u - equal);
-      equal &= equal - 1;
+    if (ties > 0) {                                         // the same for the whole CTA
+      uint32_t equal = s_tie[tid];
+      const int before = block_scan<kThreads>(__popc(equal), s_nth.sum, &turn, &all);
+      for (int k = min(__popc(equal), ties - before); k > 0; --k) {
+        kept |= equal & (0u - equal);
+        equal &= equal - 1;
+      }
+      ties = max(0, ties - all);
     }
-    ties = max(0, ties - all);
     // bits of the word below the budget, and of keys that there are
     const int j0 = base + 32 * tid;
     const uint32_t below = fewer - j0 >= 32 ? 0xFFFFFFFFu : fewer <= j0 ? 0u : (1u << (fewer - j0)) - 1u;

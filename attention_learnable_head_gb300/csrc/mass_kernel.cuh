@@ -15,10 +15,11 @@
 // fragments are whole 16-byte chunks (chunks t and 4 + t for lane t of four): keys go from
 // their pages straight into registers.
 //
-// Many rows (prompts): an exponential a score bounds it.  A CTA holds 128 keys and q passes
-// by in tiles of 128 rows through a TMA ring; S = K Q^T goes to TMEM (tcgen05), two tiles
-// at a time, and two warpgroups take turns: a thread has one key, a tile's 128 scores of
-// it in 128 columns, and the rows' lse comes from shared memory, the same for all.
+// Many rows (prompts): an exponential a score bounds it, and next to it shared memory.  A
+// CTA holds 256 keys in TMEM, as the A operands of two products (from shared memory they
+// would be read again for every tile), and q passes by in tiles of 96 rows through a TMA
+// ring.  A thread has two keys and 16 rows of a half tile: the rows' lse, the same for all
+// threads, comes from shared memory once for both.
 #pragma once
 #include <cuda_bf16.h>
 #include "fwd_kernel.cuh"
@@ -71,11 +72,20 @@ __device__ __forceinline__ uint32_t mass_row(const MassParams& p, const int* tab
 
 // ----------------------------------------------------------------------------- few rows
 constexpr int kMassFewThreads = 256;
+constexpr int kMassFewStages = 3;        // groups of 32 keys on their way to a warp
+constexpr int kMassFewSmem = kMassFewThreads / 32 * kMassFewStages * 32 * 128;
+
+// 16-byte chunk c of row r of a warp's stage: the halves of every 128 bytes are exchanged
+// in every other row, so that 8 lanes that read 4 chunks of 2 rows touch each bank once.
+__device__ __forceinline__ uint32_t mass_few_at(int r, int c) {
+  return (uint32_t)r * 128u + (uint32_t)((c ^ ((r & 1) << 2)) << 4);
+}
 
 // Sequences of up to 8 kTiles rows of q; those with more take them in turns.
 template <int kTiles>
 __global__ void __launch_bounds__(kMassFewThreads, 2)
 attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
+  extern __shared__ __align__(128) uint8_t few_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const unsigned id = blockIdx.x * (kMassFewThreads / 32) + warp;
@@ -94,7 +104,7 @@ attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
       mass[j] = 0.0f;
   const long long rows = (long long)s.n * p.group;
   const int at0 = s.len - s.n;             // key position of token 0
-  const uint4* cache = reinterpret_cast<const uint4*>(p.k_cache) + t;
+  const uint32_t ring = smem_u32(few_smem) + (uint32_t)warp * (kMassFewStages * 32 * 128);
   for (long long r0 = 0; r0 < rows; r0 += 8 * kTiles) {
     // B: row g of every tile, the dimensions of this lane's chunks; lse and the last key
     // seen of the two rows 2 t, 2 t + 1 whose scores it gets (-1: none, no weight)
@@ -138,18 +148,18 @@ attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
       const int j = 32 * (int)grp + lane;
       return j < s.keys ? mass_row(p, table, h, j) : kMassNoRow;
     };
-    auto load = [&](uint32_t mine, uint4 (*a)[2]) {
+    auto issue = [&](uint32_t mine, int st) {
       #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t row = __shfl_sync(0xffffffffu, mine, 8 * r + g);
-        #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          a[r][u] = row != kMassNoRow ? __ldg(cache + (size_t)row * 8 + 4 * u)
-                                      : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < 8; ++u) {
+        const int r = 4 * u + (lane >> 3);
+        const uint32_t row = __shfl_sync(0xffffffffu, mine, r);
+        const bool in = row != kMassNoRow;                  // else nothing is read, 0 written
+        cp_async_16_zfill(ring + st * (32 * 128) + mass_few_at(r, lane & 7),
+                          in ? p.k_cache + (size_t)row * 64 + 8 * (lane & 7) : p.q, in ? 16 : 0);
       }
     };
     const unsigned groups = (unsigned)(s.keys + 31) / 32;
-    auto use = [&](unsigned grp, uint32_t mine, const uint4 (*a)[2], float old) {
+    auto use = [&](unsigned grp, uint32_t mine, const uint32_t (*a)[2][4], float old) {
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       const int j0 = 32 * (int)grp;
       #pragma unroll
@@ -159,10 +169,10 @@ attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
           float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            mma_16816_bf16(c, a[2 * m][u].x, a[2 * m + 1][u].x, a[2 * m][u].y, a[2 * m + 1][u].y,
-                           bq[i][4 * u], bq[i][4 * u + 1]);
-            mma_16816_bf16(c, a[2 * m][u].z, a[2 * m + 1][u].z, a[2 * m][u].w, a[2 * m + 1][u].w,
-                           bq[i][4 * u + 2], bq[i][4 * u + 3]);
+            mma_16816_bf16(c, a[2 * m][u][0], a[2 * m + 1][u][0], a[2 * m][u][1],
+                           a[2 * m + 1][u][1], bq[i][4 * u], bq[i][4 * u + 1]);
+            mma_16816_bf16(c, a[2 * m][u][2], a[2 * m + 1][u][2], a[2 * m][u][3],
+                           a[2 * m + 1][u][3], bq[i][4 * u + 2], bq[i][4 * u + 3]);
           }
           #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -192,66 +202,97 @@ attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
       const int j = 32 * (int)grp + 8 * t + g;
       return add && j < s.keys ? mass[j] : 0.0f;
     };
-    if constexpr (kTiles > 1) {            // the registers hold one group's keys
-      uint4 a[4][2];
-      uint32_t next = first < groups ? row_of(first) : kMassNoRow;
-      for (unsigned now = first; now < groups; now += step) {
-        const uint32_t mine = next;
-        load(mine, a);
-        const float old = before(now);
-        if (now + step < groups) next = row_of(now + step);
-        use(now, mine, a, old);
-      }
-      continue;
+    // the table one group ahead of the copies, those kMassFewStages ahead of their use
+    uint32_t mine[kMassFewStages];
+    float old[kMassFewStages];
+    #pragma unroll
+    for (int st = 0; st < kMassFewStages; ++st) {
+      const unsigned grp = first + st * step;
+      mine[st] = grp < groups ? row_of(grp) : kMassNoRow;
     }
-    // rows two groups ahead, keys one
-    uint4 a[2][4][2];
-    float old[2] = {0.0f, 0.0f};
-    uint32_t mine = first < groups ? row_of(first) : kMassNoRow;
-    uint32_t next = first + step < groups ? row_of(first + step) : kMassNoRow;
-    if (first < groups) {
-      load(mine, a[0]);
-      old[0] = before(first);
+    #pragma unroll
+    for (int st = 0; st < kMassFewStages; ++st) {
+      const unsigned grp = first + st * step;
+      if (grp < groups) issue(mine[st], st);
+      cp_async_commit();
+      old[st] = grp < groups ? before(grp) : 0.0f;
     }
-    for (unsigned grp = first; grp < groups; grp += 2 * step) {
+    uint32_t next = first + kMassFewStages * step < groups ? row_of(first + kMassFewStages * step)
+                                                           : kMassNoRow;
+    for (unsigned base = first; base < groups; base += kMassFewStages * step) {
       #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const unsigned now = grp + k * step;
-        if (now < groups) {
-          if (now + step < groups) {
-            load(next, a[k ^ 1]);
-            old[k ^ 1] = before(now + step);
+      for (int st = 0; st < kMassFewStages; ++st) {
+        const unsigned now = base + st * step, ahead = now + kMassFewStages * step;
+        if (now < groups) {                // the same for the whole warp
+          cp_async_wait<kMassFewStages - 1>();
+          __syncwarp();
+          uint32_t a[4][2][4];
+          #pragma unroll
+          for (int r = 0; r < 4; ++r)
+            #pragma unroll
+            for (int u = 0; u < 2; ++u)
+              ld_shared_v4(ring + st * (32 * 128) + mass_few_at(8 * r + g, 4 * u + t), a[r][u]);
+          const uint32_t rows_now = mine[st];
+          const float was = old[st];
+          __syncwarp();                    // every lane has read the stage
+          mine[st] = next;
+          if (ahead < groups) {
+            issue(next, st);
+            old[st] = before(ahead);
           }
-          const uint32_t far = now + 2 * step < groups ? row_of(now + 2 * step) : kMassNoRow;
-          use(now, mine, a[k], old[k]);
-          mine = next;
-          next = far;
+          cp_async_commit();
+          next = ahead + step < groups ? row_of(ahead + step) : kMassNoRow;
+          use(now, rows_now, a, was);
         }
       }
     }
+    cp_async_wait<0>();
+    __syncwarp();
   }
 }
 
 // ----------------------------------------------------------------------------- many rows
-constexpr int kMassThreads = 320;        // 8 warps of weights, copy warp, MMA warp
-constexpr int kMassStages = 3;
-constexpr uint32_t kMassTmemCols = 256;  // two tiles of 128 fp32 columns
-constexpr int kMassSmemBytes = 1024 + (int)kTileBytes * (1 + kMassStages);
+constexpr int kMassKeys = 256;           // of a CTA: two for each TMEM lane
+constexpr int kMassRows = 96;            // of a tile of q
+constexpr int kMassMaxGroup = kMassRows;
+constexpr int kMassWarps = 12;           // of weights
+constexpr int kMassCopyWarp = 12;
+constexpr int kMassMmaWarp = 13;
+constexpr int kMassThreads = 32 * 14;
+constexpr int kMassStages = 4;
+constexpr uint32_t kMassTileBytes = kMassRows * 128;
+constexpr int kMassHalf = kMassRows / 2; // of a product
+constexpr uint32_t kMassTmemCols = 256;  // keys: 2 x 32 columns of bf16 pairs, scores: 4 x 48
+constexpr uint32_t kMassColS = 64;
+constexpr int kMassSmemBytes = 1024 + (int)kMassTileBytes * kMassStages;
 
-__global__ void __maxnreg__(96)
+// mbar_wait_warp for the inner loop, where it mostly need not wait: what follows a first
+// try is a call.
+__device__ __noinline__ bool mass_wait_more(uint64_t* bar, uint32_t parity,
+                                            volatile int* abort_flag) {
+  return mbar_wait_warp(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool mass_wait(uint64_t* bar, uint32_t parity,
+                                          volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity)) ||
+         mass_wait_more(bar, parity, abort_flag);
+}
+
+__global__ void __launch_bounds__(kMassThreads, 2)
 attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full[kMassStages], q_empty[kMassStages];
-  __shared__ __align__(8) uint64_t d_full[2], d_empty[2], mma_drained;
-  __shared__ __align__(16) float s_z[kMassStages][kBlockM];   // -lse log2(e); -inf: no row
-  __shared__ __align__(16) int s_at[kMassStages][kBlockM];    // last key the row sees; -1: none
+  __shared__ __align__(8) uint64_t s_full[2], s_empty[2], mma_drained;
+  __shared__ __align__(16) float s_z[kMassStages][kMassRows];   // -lse log2(e); -inf: no row
+  __shared__ __align__(16) int s_at[kMassStages][kMassRows];    // last key the row sees; -1: none
   __shared__ int s_clear[kMassStages];     // no weight of the tile is masked
-  __shared__ float s_part[kBlockM];
+  __shared__ float s_part[2][kMassKeys];
+  __shared__ uint8_t s_has[kMassKeys];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, b = blockIdx.z;
-  const int j0 = blockIdx.x * kBlockM;
+  const int j0 = blockIdx.x * kMassKeys;
   bool bad;
   const MassSeq s = mass_seq(p, b, &bad);
   if (bad && tid == 0 && blockIdx.x == 0 && h == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
@@ -262,92 +303,107 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   const int tiles = j0 < s.keys && s.n > t0 ? (s.n - t0 + p.tokens - 1) / p.tokens : 0;
   if (tiles == 0) {                        // the same for the whole CTA
     const int j = j0 + tid;
-    if (!p.accumulate && tid < kBlockM && j < p.max_keys) mass[j] = 0.0f;
+    if (!p.accumulate && tid < kMassKeys && j < p.max_keys) mass[j] = 0.0f;
     return;
   }
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sK = smem;
-  uint8_t* sQ = smem + kTileBytes;
+  uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
   const int rows = p.tokens * p.group;     // of a tile; behind them zeros, with no weight
+  // a thread's key goes from its page into TMEM
+  const int c = warp >> 2, r = tid & 127;
+  uint32_t key[32];
+  bool has = false;
+  if (warp < 8) {
+    const int j = j0 + tid;
+    const uint32_t row = j < s.keys
+                             ? mass_row(p, p.block_table + (size_t)b * p.max_pages, h, j)
+                             : kMassNoRow;
+    has = row != kMassNoRow;
+    #pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint4 v = has ? __ldg(reinterpret_cast<const uint4*>(p.k_cache) + (size_t)row * 8 + u)
+                          : make_uint4(0, 0, 0, 0);
+      key[4 * u] = v.x;
+      key[4 * u + 1] = v.y;
+      key[4 * u + 2] = v.z;
+      key[4 * u + 3] = v.w;
+    }
+    s_has[tid] = has;
+  }
   if (tid == 0) {
     abort_flag = 0;
     for (int i = 0; i < kMassStages; ++i) {
       mbar_init(&q_full[i], 2);            // the copy, and the rows' lse
-      mbar_init(&q_empty[i], 5);           // the product, and four warps that read the lse
+      mbar_init(&q_empty[i], 1 + kMassWarps);   // the product, and the warps that read the lse
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kMassWarps);
     }
     mbar_init(&mma_drained, 1);
     fence_mbarrier_init();
   }
-  if (warp == kFwdMmaWarp) {
+  if (warp == kMassMmaWarp) {
     tmem_alloc(&tmem_base_sh, kMassTmemCols);
     tmem_relinquish();
   }
-  // a thread's key, and the half of it that it copies
-  const int r = tid & 127, c = warp >> 2;
-  bool has = false;
-  if (warp < 8) {
-    const uint32_t row = j0 + r < s.keys
-                             ? mass_row(p, p.block_table + (size_t)b * p.max_pages, h, j0 + r)
-                             : kMassNoRow;
-    has = row != kMassNoRow;
-    const __nv_bfloat16* src = has ? p.k_cache + (size_t)row * 64 : p.q;   // else nothing is read
-    #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      cp_async_16_zfill(smem_u32(sK) + sw128_offset((uint32_t)r, (uint32_t)(4 * c + u)),
-                        has ? src + 8 * (4 * c + u) : p.q, has ? 16u : 0u);
-    cp_async_commit();
-    // the rows of a tile that no copy writes
-    for (int x = rows * 8 + tid; x < kBlockM * 8; x += 256)
-      for (int i = 0; i < kMassStages; ++i)
-        st_shared_v4(smem_u32(sQ + i * kTileBytes) + (uint32_t)x * 16u, 0, 0, 0, 0);
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-  }
+  // the rows of a tile that no copy writes
+  for (int x = rows * 8 + tid; x < kMassRows * 8; x += kMassThreads)
+    for (int i = 0; i < kMassStages; ++i)
+      st_shared_v4(smem_u32(sQ + i * kMassTileBytes) + (uint32_t)x * 16u, 0, 0, 0, 0);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+  if (warp < 8) {
+    tmem_st_x32(tmem + 32 * c + lane_base, key);
+    tmem_st_wait();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
 
-  if (warp == kFwdTmaWarp) {
+  if (warp == kMassCopyWarp) {
     // ---------------------------------------------------------------- q and its lse
-    int tok[4], hd[4];                     // of columns lane, lane + 32, ..
+    constexpr int kCols = kMassRows / 32;
+    int tok[kCols], hd[kCols];             // of columns lane, lane + 32, ..
     #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kCols; ++u) {
       tok[u] = (lane + 32 * u) / p.group;
       hd[u] = lane + 32 * u - tok[u] * p.group;
     }
-    float z[4];
-    auto fetch = [&](int i) {
+    // the lse of the next kAhead tiles is on its way: a load takes as long as a tile
+    constexpr int kAhead = 4;
+    float z[kAhead][kCols];
+    auto fetch = [&](int i, float* z) {
       #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kCols; ++u) {
         const int x = t0 + i * p.tokens + tok[u];
         z[u] = tok[u] < p.tokens && x < s.n
                    ? __ldg(p.lse + (size_t)(h * p.group + hd[u]) * p.total_q + s.q0 + x)
                    : INFINITY;
       }
     };
-    const int last = min(j0 + kBlockM, s.keys) - 1;        // of the block
+    const int last = min(j0 + kMassKeys, s.keys) - 1;      // of the block
     const uint32_t bytes = (uint32_t)rows * 128u;
     if (lane == 0) tma_prefetch_desc(&p.tm_q);
-    fetch(0);
+    #pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(k, z[k]);
     int i = 0;
-    for (; i < tiles; ++i) {
+    auto tile = [&](float* z) {
       const int st = i % kMassStages;
       if (i >= kMassStages && !mbar_wait_warp(&q_empty[st], ((i / kMassStages) & 1) ^ 1, &abort_flag))
-        break;
+        return false;
       if (lane == 0) {
         mbar_arrive_expect_tx(&q_full[st], bytes);
-        tma_load_3d(&p.tm_q, &q_full[st], sQ + st * kTileBytes, 0, h * p.group,
+        tma_load_3d(&p.tm_q, &q_full[st], sQ + st * kMassTileBytes, 0, h * p.group,
                     s.q0 + t0 + i * p.tokens);
       }
       bool clear = true;
       #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kCols; ++u) {
         const int at = at0 + t0 + i * p.tokens + tok[u];
         const bool weight = !isinf(z[u]);
         s_z[st][lane + 32 * u] = weight ? -z[u] * kLog2e : -INFINITY;
@@ -358,9 +414,16 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       if (lane == 0) s_clear[st] = clear;
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[st]);
-      if (i + 1 < tiles) fetch(i + 1);
-    }
-    if (i < tiles) {
+      fetch(i + kAhead, z);
+      ++i;
+      return true;
+    };
+    bool ok = true;
+    while (ok && i < tiles)
+      #pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (ok && i < tiles) ok = tile(z[k]);
+    if (!ok) {
       // given up: the copies in flight land before the CTA releases its shared memory
       if (lane == 0) {
         abort_flag = 1;
@@ -370,25 +433,30 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       }
       __syncwarp();
     }
-  } else if (warp == kFwdMmaWarp) {
+  } else if (warp == kMassMmaWarp) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {
-      const uint32_t idesc = make_idesc_bf16(kBlockM, kBlockM, false, false);
-      const uint64_t dK = make_sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint32_t idesc = make_idesc_bf16(kBlockM, kMassHalf, false, false);
       const uint64_t dQ = make_sdesc_sw128(smem_u32(sQ), 16, 1024);
-      constexpr uint32_t kTileU = kTileBytes >> 4;
+      constexpr uint32_t kTileU = kMassTileBytes >> 4;
       bool ok = true;
       for (int i = 0; ok && i < tiles; ++i) {
-        const int st = i % kMassStages, buf = i & 1;
-        ok = mbar_wait(&q_full[st], (i / kMassStages) & 1, &abort_flag) &&
-             (i < 2 || mbar_wait(&d_empty[buf], ((i >> 1) & 1) ^ 1, &abort_flag));
-        if (!ok) break;
-        tc_fence_after();
+        const int st = i % kMassStages;
+        ok = mbar_wait(&q_full[st], (i / kMassStages) & 1, &abort_flag);
         #pragma unroll
-        for (int k = 0; k < kHeadDim / 16; ++k)
-          mma_ss(tmem + buf * kBlockM, dK + 2 * k, dQ + st * kTileU + 2 * k, idesc, k > 0);
-        mma_commit(&d_full[buf]);
-        mma_commit(&q_empty[st]);
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && (i < 1 || mbar_wait(&s_empty[half], (i & 1) ^ 1, &abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          #pragma unroll
+          for (int k = 0; k < kHeadDim / 16; ++k)
+            #pragma unroll
+            for (int e = 0; e < 2; ++e)
+              mma_ts(tmem + kMassColS + kMassHalf * (2 * half + e), tmem + 32 * e + 8 * k,
+                     dQ + st * kTileU + half * (kMassHalf * 128 >> 4) + 2 * k, idesc, k > 0);
+          mma_commit(&s_full[half]);
+        }
+        if (ok) mma_commit(&q_empty[st]);
       }
       if (!ok) {
         abort_flag = 1;
@@ -400,76 +468,93 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- weights
-    // warpgroup c takes the tiles c, c + 2, ..: thread = key = TMEM lane
-    const uint32_t tD = tmem + c * kBlockM + ((uint32_t)((warp & 3) * 32) << 16);
+    // warpgroup c has columns 16 c .. 16 c + 15 of every half tile; thread = TMEM lane = keys
+    // r and r + 128
+    const uint32_t tS = tmem + kMassColS + 16 * c + lane_base;
     const uint64_t scale = f2(p.scale_log2, p.scale_log2);
-    uint64_t sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+    uint64_t sum[2][2] = {{f2(0.0f, 0.0f), f2(0.0f, 0.0f)}, {f2(0.0f, 0.0f), f2(0.0f, 0.0f)}};
+    const int last_cols = (s.n - t0 - (tiles - 1) * p.tokens) * p.group - 16 * c;
     bool ok = true;
-    for (int i = c; i < tiles; i += 2) {
+    for (int i = 0; i < tiles; ++i) {
       const int st = i % kMassStages;
-      ok = mbar_wait_warp(&q_full[st], (i / kMassStages) & 1, &abort_flag) &&
-           mbar_wait_warp(&d_full[c], (i >> 1) & 1, &abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const int parts = (min(p.tokens, s.n - t0 - i * p.tokens) * p.group + 31) / 32;
+      ok = mass_wait(&q_full[st], (i / kMassStages) & 1, &abort_flag);
+      const int cols = i + 1 < tiles ? kMassRows : last_cols;
       const bool clear = s_clear[st] != 0;
-      for (int part = 0; part < parts; ++part) {
-        uint32_t x[32];
-        tmem_ld_x32(tD + 32 * part, x);
+      #pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && mass_wait(&s_full[half], i & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[2][16];
+        tmem_ld_x16(tS + 2 * kMassHalf * half, x[0]);
+        tmem_ld_x16(tS + 2 * kMassHalf * half + kMassHalf, x[1]);
         tmem_ld_wait();
-        const float4* z4 = reinterpret_cast<const float4*>(&s_z[st][32 * part]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[half]);         // the next product may begin
+        if (cols <= kMassHalf * half) continue;             // the same for the whole warp
+        const float4* z4 = reinterpret_cast<const float4*>(&s_z[st][kMassHalf * half + 16 * c]);
         if (clear) {
           #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
+          for (int e = 0; e < 16; e += 4) {
             const float4 z = z4[e >> 2];
             #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint64_t y = ffma2(f2(__uint_as_float(x[e + 2 * u]),
-                                          __uint_as_float(x[e + 2 * u + 1])),
-                                       scale, u ? f2(z.z, z.w) : f2(z.x, z.y));
-              sum[u] = fadd2(sum[u], f2(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))));
-            }
+            for (int k = 0; k < 2; ++k)
+              #pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const uint64_t v = ffma2(f2(__uint_as_float(x[k][e + 2 * u]),
+                                            __uint_as_float(x[k][e + 2 * u + 1])),
+                                         scale, u ? f2(z.z, z.w) : f2(z.x, z.y));
+                sum[k][u] = fadd2(sum[k][u], f2(ex2_approx(f2_lo(v)), ex2_approx(f2_hi(v))));
+              }
           }
         } else {
-          const int4* at4 = reinterpret_cast<const int4*>(&s_at[st][32 * part]);
-          const int j = j0 + r;
+          const int4* at4 = reinterpret_cast<const int4*>(&s_at[st][kMassHalf * half + 16 * c]);
           #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
+          for (int e = 0; e < 16; e += 4) {
             const float4 z = z4[e >> 2];
             const int4 at = at4[e >> 2];
-            const float w0 = ex2_approx(fmaf(__uint_as_float(x[e]), p.scale_log2, z.x));
-            const float w1 = ex2_approx(fmaf(__uint_as_float(x[e + 1]), p.scale_log2, z.y));
-            const float w2 = ex2_approx(fmaf(__uint_as_float(x[e + 2]), p.scale_log2, z.z));
-            const float w3 = ex2_approx(fmaf(__uint_as_float(x[e + 3]), p.scale_log2, z.w));
-            sum[0] = fadd2(sum[0], f2(j <= at.x ? w0 : 0.0f, j <= at.y ? w1 : 0.0f));
-            sum[1] = fadd2(sum[1], f2(j <= at.z ? w2 : 0.0f, j <= at.w ? w3 : 0.0f));
+            #pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = j0 + 128 * k + r;
+              const float w0 = ex2_approx(fmaf(__uint_as_float(x[k][e]), p.scale_log2, z.x));
+              const float w1 = ex2_approx(fmaf(__uint_as_float(x[k][e + 1]), p.scale_log2, z.y));
+              const float w2 = ex2_approx(fmaf(__uint_as_float(x[k][e + 2]), p.scale_log2, z.z));
+              const float w3 = ex2_approx(fmaf(__uint_as_float(x[k][e + 3]), p.scale_log2, z.w));
+              sum[k][0] = fadd2(sum[k][0], f2(j <= at.x ? w0 : 0.0f, j <= at.y ? w1 : 0.0f));
+              sum[k][1] = fadd2(sum[k][1], f2(j <= at.z ? w2 : 0.0f, j <= at.w ? w3 : 0.0f));
+            }
           }
         }
       }
-      tc_fence_before();
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&d_empty[c]);
-        mbar_arrive(&q_empty[st]);
-      }
+      if (lane == 0) mbar_arrive(&q_empty[st]);
     }
-    const uint64_t both = fadd2(sum[0], sum[1]);
-    const float w = f2_lo(both) + f2_hi(both);
-    if (c == 1) s_part[r] = w;
-    ok = named_barrier_and(1, 256, ok);
+    float w[2];
+    #pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint64_t both = fadd2(sum[k][0], sum[k][1]);
+      w[k] = f2_lo(both) + f2_hi(both);
+      if (c > 0) s_part[c - 1][128 * k + r] = w[k];
+    }
+    ok = named_barrier_and(1, 32 * kMassWarps, ok);
     if (!ok) {
       abort_flag = 1;
       atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 0x12);
     } else if (c == 0) {
-      const int j = j0 + r;
-      const float all = has ? w + s_part[r] : 0.0f;
-      if (j < s.keys) mass[j] = p.accumulate ? mass[j] + all : all;
-      else if (!p.accumulate && j < p.max_keys) mass[j] = 0.0f;
+      #pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int x = 128 * k + r, j = j0 + x;
+        const float all = s_has[x] ? w[k] + (s_part[0][x] + s_part[1][x]) : 0.0f;
+        if (j < s.keys) mass[j] = p.accumulate ? mass[j] + all : all;
+        else if (!p.accumulate && j < p.max_keys) mass[j] = 0.0f;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kFwdMmaWarp) {
+  if (warp == kMassMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kMassTmemCols);
   }

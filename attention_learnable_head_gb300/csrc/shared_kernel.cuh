@@ -6,7 +6,8 @@
 // tile is a tile of attn_sink_extend_kernel whose tokens all see the whole prefix,
 // and that kernel computes it: it leaves each part's maximum, sum and unnormalised
 // output in the workspace.  The keys behind the prefix are each sequence's own; the
-// decode kernel reads them (kDecShared) and joins everything with the sink.
+// decode kernel reads them (kDecShared), at the same time, and a last one joins
+// everything with the sink (decode_join.cuh).
 //
 // This schedule kernel of one CTA lists the tiles' parts.  Groups of one sequence and
 // short prefixes have none (see shared_own): their sequences read all keys themselves.
@@ -119,12 +120,13 @@ attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
       dst[2] = src[2];
     }
     for (int b = c0 + lane; b < c1; b += 32)
-      p.refs[b] = keys > 0 ? SharedRef{first + (b - c0) / e.tokens * parts, parts}
-                           : SharedRef{0, 0};
+      p.refs[b] = keys > 0 ? SharedRef{first + (b - c0) / e.tokens * parts, parts,
+                                       (b - c0) % e.tokens, 0}
+                           : SharedRef{0, 0, 0, 0};
   }
   if (over) {                              // the same for every thread
     __syncthreads();
-    for (int b = tid; b < e.batch; b += 32 * kSharedWarps) p.refs[b] = SharedRef{0, 0};
+    for (int b = tid; b < e.batch; b += 32 * kSharedWarps) p.refs[b] = SharedRef{0, 0, 0, 0};
   }
   for (int x = (over ? 0 : listed) + tid; x < e.n_items; x += 32 * kSharedWarps)
     e.items[x].num = -1;

@@ -66,11 +66,11 @@ __device__ __forceinline__ int block_scan(int x, int (*s)[kThreads / 32], int* t
 }
 
 // What block_nth keeps in shared memory.
-constexpr int kNthBins = 2048;
+constexpr int kNthEach = 2;              // bins a thread
 template <int kThreads>
 struct NthShared {
   int sum[2][kThreads / 32];
-  unsigned bins[kNthBins];
+  unsigned bins[kNthEach * kThreads];
   uint32_t list[kThreads];
   uint32_t low, high, value;
   int count, bin, before;
@@ -82,6 +82,9 @@ struct NthShared {
 template <int kThreads, typename Each>
 __device__ __forceinline__ uint32_t block_nth(int n, Each each, NthShared<kThreads>* s, int* turn,
                                               int* above) {
+  constexpr int kNthBins = kNthEach * kThreads;
+  constexpr int kBits = kThreads == 256 ? 9 : kThreads == 512 ? 10 : 11;
+  static_assert(1 << kBits == kNthBins, "a power of two");
   const int tid = threadIdx.x, lane = tid & 31;
   uint32_t low = 0xFFFFFFFFu, high = 0;
   each([&](uint32_t v) {
@@ -103,7 +106,7 @@ __device__ __forceinline__ uint32_t block_nth(int n, Each each, NthShared<kThrea
   uint32_t base = s->low, span = s->high - s->low;
   int left = n;                            // rank within the range
   while (true) {
-    const int shift = max(0, 32 - __clz(span) - 11);        // span >> shift < kNthBins
+    const int shift = max(0, 32 - __clz(span) - kBits);        // span >> shift < kNthBins
     for (int i = tid; i < kNthBins; i += kThreads) s->bins[i] = 0;
     if (tid == 0) s->count = 0;
     __syncthreads();
@@ -111,20 +114,19 @@ __device__ __forceinline__ uint32_t block_nth(int n, Each each, NthShared<kThrea
       if (v - base <= span) atomicAdd(&s->bins[(v - base) >> shift], 1u);
     });
     __syncthreads();
-    // the bin in which the rank lies, from the top: kNthBins / kThreads bins a thread
-    constexpr int kEach = kNthBins / kThreads;
-    int mine[kEach], sum = 0;
+    // the bin in which the rank lies, from the top
+    int mine[kNthEach], sum = 0;
     #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      mine[i] = (int)s->bins[kNthBins - 1 - (tid * kEach + i)];
+    for (int i = 0; i < kNthEach; ++i) {
+      mine[i] = (int)s->bins[kNthBins - 1 - (tid * kNthEach + i)];
       sum += mine[i];
     }
     int all;
     int upto = block_scan<kThreads>(sum, s->sum, turn, &all);
     #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < kNthEach; ++i) {
       if (upto < left && left <= upto + mine[i]) {
-        s->bin = kNthBins - 1 - (tid * kEach + i);
+        s->bin = kNthBins - 1 - (tid * kNthEach + i);
         s->before = upto;
       }
       upto += mine[i];
