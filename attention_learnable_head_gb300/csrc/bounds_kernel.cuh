@@ -313,7 +313,7 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ uint8_t s_take[kSelectBand];
   __shared__ int s_side[2];
   __shared__ int s_many;
-  __shared__ unsigned s_peak;
+  __shared__ unsigned s_peak[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int b = (int)(blockIdx.x / (unsigned)p.heads_kv);
   const int h = (int)(blockIdx.x - (unsigned)b * (unsigned)p.heads_kv);
@@ -354,29 +354,32 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   norm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(norm) & 0x7fffffffu));
   if (tid == 0) {
     s_many = s_side[0] = s_side[1] = 0;
-    s_peak = 0;
   }
   grid_dependency_wait();                                   // the scores
   const float* scores = p.scores + row * p.max_pages + p.keep_first;
   const bool staged = n <= kSelectStage;
-  if (staged)
-    for (int i = tid; i < n; i += kThreads) s_score[i] = ordered(__ldcg(scores + i));
+  uint32_t least = 0xFFFFFFFFu, largest = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint32_t v = ordered(__ldcg(scores + i));
+    least = min(least, v);
+    largest = max(largest, v);
+    if (staged) s_score[i] = v;
+  }
   unsigned peak = 0;
   for (int i = tid; i < (have + 15) / 16; i += kThreads)
     peak = max(peak, __ldcg(p.peak + row * p.tiles + i));
   peak = __reduce_max_sync(0xffffffffu, peak);
-  __syncthreads();
-  if (lane == 0) atomicMax(&s_peak, peak);
+  if (lane == 0) s_peak[tid >> 5] = peak;
   auto at = [&](int i) { return staged ? s_score[i] : ordered(__ldcg(scores + i)); };
   int turn = 0;
-  int above;
   const uint32_t low = block_nth<kThreads>(
-      need, [&](auto&& take) {
+      need, least, largest, [&](auto&& take) {
         for (int i = tid; i < n; i += kThreads) take(at(i));
-      }, &s_nth, &turn, &above);           // the smallest score that is taken
+      }, &s_nth, &turn).value;             // the smallest score that is taken
   // No score is further off than the rounding of its sums: 8 products of 16 terms, each
   // sum cut below 2^-23 of what the terms' sizes add up to at most.
-  const float most = norm * __uint_as_float(s_peak << 16);
+  peak = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? s_peak[lane] : 0u);
+  const float most = norm * __uint_as_float(peak << 16);
   const float off = most * 0x1p-15f;                        // twice that, for both sides
   const float last = unordered(low);
   uint32_t from = low, upto = low;                      // the border, both ends inside

@@ -46,13 +46,11 @@ DecodeSlices decode_slices(int splits, int batch, int heads_q) {
   return d;
 }
 
-constexpr int kDecCtasPerSm = 5;
-
 // As many slices of at least kDecKeys keys as the GPU holds at once.
 int decode_splits(int batch, int heads_kv, long long keys, int sms) {
   const long long ctas = std::max(1ll, (long long)batch * heads_kv);
   const long long most = std::min(64ll, (keys + kDecKeys - 1) / kDecKeys);
-  return (int)std::max(1ll, std::min(most, kDecCtasPerSm * (long long)sms / ctas));
+  return (int)std::max(1ll, std::min(most, dec_ctas(kDecPages) * (long long)sms / ctas));
 }
 
 // The fields of DecodeParams that every mode has; *tma: which copies are taken.
@@ -107,6 +105,8 @@ auto decode_kernel(int group, bool tma) -> void (*)(DecodeParams) {
     default: return attn_sink_decode_kernel<8, true, kMode>;
   }
 }
+
+constexpr int kDecSliceSmem = 1024 + dec_stages(kDecPages) * 2 * kDecKeys * 128;
 
 template <bool kShared>
 bool launch_join(const DecodeParams& dp, cudaStream_t s) {
@@ -183,7 +183,7 @@ int row_threads(int row) { return row <= 2048 ? 256 : row <= 8192 ? 512 : 1024; 
 // ----------------------------------------------------------------------------- eviction
 struct EvictLayout {
   int max_moves;
-  size_t off_moves, total;
+  size_t off_moves, off_from, total;
 };
 
 int evict_layout(const attn_sink_evict_params* p, EvictLayout* L) {
@@ -199,7 +199,8 @@ int evict_layout(const attn_sink_evict_params* p, EvictLayout* L) {
   L->max_moves = std::min(p->budget, behind);
   const size_t rows = (size_t)p->batch * p->heads_kv;
   L->off_moves = align256(rows * sizeof(int));
-  L->total = L->off_moves + align256(rows * L->max_moves * sizeof(uint2));
+  L->off_from = L->off_moves + align256(rows * L->max_moves * sizeof(int));
+  L->total = L->off_from + align256(rows * L->max_moves * sizeof(int));
   return ATTN_SINK_OK;
 }
 
@@ -223,6 +224,15 @@ int cache_attributes() {
     return ATTN_SINK_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if (!g_cache_attr_set[dev]) {
+    for (int group : {1, 2, 4, 8})
+      for (bool tma : {false, true})
+        if (cudaFuncSetAttribute(decode_kernel<kDecPages>(group, tma),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kDecSliceSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(decode_kernel<kDecShared>(group, tma),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kDecSliceSmem) != cudaSuccess)
+          return ATTN_SINK_ERR_CUDA;
     for (int threads : {256, 512, 1024})
       if (cudaFuncSetAttribute(evict_kernel(threads), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                4 * kEvictStage) != cudaSuccess ||
@@ -279,7 +289,8 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
   int sms = 0;
   int* err = nullptr;
   if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
-  if ((st = extend_attributes()) != ATTN_SINK_OK) return st;
+  if ((st = extend_attributes()) != ATTN_SINK_OK || (st = cache_attributes()) != ATTN_SINK_OK)
+    return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeParams dp;
@@ -345,8 +356,8 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
                         kFwdSmemBytes, s, ep))
     return ATTN_SINK_ERR_CUDA;
   const dim3 grid(L.own.splits, params->heads_kv, params->batch);
-  return launch_dependent(decode_kernel<kDecShared>(ep.group, dec_tma), grid, kDecThreads, 0, s,
-                          dp) &&
+  return launch_dependent(decode_kernel<kDecShared>(ep.group, dec_tma), grid, kDecThreads,
+                          kDecSliceSmem, s, dp) &&
                  launch_join<true>(dp, s)
              ? ATTN_SINK_OK
              : ATTN_SINK_ERR_CUDA;
@@ -497,6 +508,7 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
   int sms = 0;
   int* err = nullptr;
   if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
+  if ((st = cache_attributes()) != ATTN_SINK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   DecodeParams dp;
   bool tma;
@@ -506,8 +518,8 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
   dp.selected = selected;
   dp.count = params->count;
   const dim3 grid(L.splits, params->heads_kv, params->batch);
-  decode_kernel<kDecPages>(params->heads_q / params->heads_kv, tma)<<<grid, kDecThreads, 0, s>>>(
-      dp);
+  decode_kernel<kDecPages>(params->heads_q / params->heads_kv,
+                           tma)<<<grid, kDecThreads, kDecSliceSmem, s>>>(dp);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   return L.splits == 1 || launch_join<false>(dp, s) ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }
@@ -630,7 +642,8 @@ int attn_sink_evict(const attn_sink_evict_params* params, void* k_cache, void* v
   ep.freed = freed_pages;
   ep.num_freed = num_freed;
   ep.counts = reinterpret_cast<int*>(ws);
-  ep.moves = reinterpret_cast<uint2*>(ws + L.off_moves);
+  ep.to = reinterpret_cast<int*>(ws + L.off_moves);
+  ep.from = reinterpret_cast<int*>(ws + L.off_from);
   ep.err = err;
   ep.batch = params->batch;
   ep.heads_kv = params->heads_kv;
@@ -647,8 +660,10 @@ int attn_sink_evict(const attn_sink_evict_params* params, void* k_cache, void* v
   const unsigned rows = (unsigned)params->batch * (unsigned)params->heads_kv;
   const size_t smem = 4 * (size_t)std::max(ep.stage, 1);
   const int threads = row_threads(params->max_keys);
+  ep.here = rows >= (unsigned)sms;         // enough CTAs to move the rows themselves
   evict_kernel(threads)<<<rows + 1, threads, smem, s>>>(ep);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
+  if (ep.here) return ATTN_SINK_OK;
   // about eight CTAs an SM, over the rows and the moves of each, 64 a CTA at a time
   const unsigned y = std::min(rows, 8u * (unsigned)sms);
   const unsigned x = (unsigned)std::max(

@@ -39,6 +39,9 @@ constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecMaxGroup = 8;        // query heads per kv head
 constexpr int kDecKeys = 64;           // keys per stage: 16 per warp
 constexpr int kDecStages = 2;
+// Stages and CTAs per SM by what is read: see the kernel.
+__host__ __device__ constexpr int dec_stages(int mode) { return mode == 0 ? kDecStages : 3; }
+__host__ __device__ constexpr int dec_ctas(int mode) { return mode == 0 ? 5 : 4; }
 constexpr float kLn2Dec = 0.6931471805599453f;
 constexpr float kLog2eDec = 1.4426950408889634f;
 constexpr int kDecTileRows = 128;      // kDecShared: rows of a prefix tile's partial results
@@ -121,19 +124,27 @@ __device__ __forceinline__ int shared_find(const int* cu, int groups, int b) {
 // copied by TMA (one thread issues them; page sizes of decode_tma_page),
 // otherwise by every thread with 16-byte cp.async.
 template <int G, bool kTma, DecodeMode kMode = kDecAll>
-__global__ void __launch_bounds__(kDecThreads, 5)
+__global__ void __launch_bounds__(kDecThreads, dec_ctas(kMode))
 attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ __align__(1024) uint8_t s_kv[kDecStages][2][kDecKeys * 128];   // K, V blocks
-  __shared__ uint8_t s_valid[kDecStages][kDecKeys];    // key inside the slice, page in range
-  __shared__ uint8_t s_pageok[kDecStages][8];          // TMA path: copy i of the block is a page
+  constexpr int kStages = dec_stages(kMode);
+  constexpr bool kAll = kMode == kDecAll;
+  extern __shared__ uint8_t dec_smem[];
+  __shared__ __align__(1024) uint8_t s_fixed[kAll ? kStages * 2 * kDecKeys * 128 : 16];
+  // K, V blocks (more than two stages do not fit static shared memory)
+  uint8_t (*s_kv)[2][kDecKeys * 128] = reinterpret_cast<uint8_t (*)[2][kDecKeys * 128]>(
+      kAll ? s_fixed
+           : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dec_smem) + 1023) &
+                                        ~static_cast<uintptr_t>(1023)));
+  __shared__ uint8_t s_valid[kStages][kDecKeys];       // key inside the slice, page in range
+  __shared__ uint8_t s_pageok[kStages][8];             // TMA path: copy i of the block is a page
                                                        //   (kDecPages: how many of its keys are seen)
-  __shared__ __align__(8) uint64_t kv_full[kDecStages];   // TMA path: the stage's copies landed
+  __shared__ __align__(8) uint64_t kv_full[kStages];   // TMA path: the stage's copies landed
   __shared__ float s_m[kDecWarps][kDecMaxGroup];
   __shared__ float s_l[kDecWarps][kDecMaxGroup];
   __shared__ int s_last;
   // the warps' O rows for the final merge reuse the K/V stages (free by then)
   float (*s_o)[kDecMaxGroup][64] = reinterpret_cast<float (*)[kDecMaxGroup][64]>(&s_kv[0][0][0]);
-  static_assert(sizeof(float) * kDecWarps * kDecMaxGroup * 64 <= sizeof(s_kv),
+  static_assert(sizeof(float) * kDecWarps * kDecMaxGroup * 64 <= kStages * 2 * kDecKeys * 128,
                 "merge buffer larger than the K/V stages");
 
   const int split = blockIdx.x;
@@ -290,26 +301,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   const int log2_box = kTma ? min(p.log2_page, 6) : 0;
   const int box = 1 << log2_box;
   const int npg = kTma ? kDecKeys >> log2_box : 0;      // copies per block and tensor
-  // (kDecPages: through the list, and seen[i] = how many of the copy's keys the
-  // sequence has.)
-  auto tma_fetch = [&](int blk, int* pe, int* seen) {
-    if constexpr (kMode == kDecPages) {
-      int col[8];
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = k0 + blk * kDecKeys + i * box;
-        col[i] = i < npg && blk < nblk && j < k1 ? __ldg(listed + (j >> p.log2_page)) : -1;
-      }
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = k0 + blk * kDecKeys + i * box;
-        const bool in = col[i] >= 0 && col[i] < have;      // one behind the sequence's: reported
-        seen[i] = in ? min(max(len - col[i] * p.page_size - (j & (p.page_size - 1)), 0), box) : 0;
-        pe[i] = in ? max(-1, __ldg(p.block_table + (size_t)b * p.max_pages + col[i]))
-                   : col[i] < 0 ? kDecNoKey : -1;
-      }
-      return;
-    }
+  auto tma_fetch = [&](int blk, int* pe) {
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int j = k0 + blk * kDecKeys + i * box;       // first key of copy i
@@ -318,19 +310,18 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
                   : -1;
     }
   };
-  auto tma_issue = [&](int blk, int st, const int* pe, const int* seen) {
+  auto tma_issue = [&](int blk, int st, const int* pe) {
     const int base = k0 + blk * kDecKeys;
     const int oob = p.num_pages * p.page_size;           // first row past the cache
     int row[8];
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int j = base + i * box;
-      const bool needed = i < npg && j < k1 && j + box > lo &&
-                          (kMode != kDecPages || pe[i] != kDecNoKey);
+      const bool needed = i < npg && j < k1 && j + box > lo;
       const bool ok = pe[i] >= 0 && pe[i] < p.num_pages;
       if (needed && !ok) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
       row[i] = ok ? pe[i] * p.page_size + (j & (p.page_size - 1)) : oob;
-      if (i < npg) s_pageok[st][i] = !ok ? 0 : kMode == kDecPages ? seen[i] : 1;
+      if (i < npg) s_pageok[st][i] = ok ? 1 : 0;
     }
     mbar_arrive_expect_tx(&kv_full[st], 2 * kDecKeys * 128);
     #pragma unroll
@@ -341,10 +332,45 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       }
     }
   };
+  // The other modes: lane i of the first warp has copy i, and the loads are further
+  // ahead: list entries (kDecPages) two blocks, table entries one block in front of the
+  // copies, which so wait for neither.
+  struct Copy {
+    int entry, seen;                 // of the table; keys that the sequence has there
+  };
+  auto lane_list = [&](int blk) {    // the column of the block table; -1: none
+    const int j = k0 + blk * kDecKeys + lane * box;
+    if (lane >= npg || blk >= nblk || j >= k1) return -1;
+    return kMode == kDecPages ? __ldg(listed + (j >> p.log2_page)) : j >> p.log2_page;
+  };
+  auto lane_entry = [&](int blk, int col) {
+    const int j = k0 + blk * kDecKeys + lane * box;
+    if (col < 0) return Copy{kDecNoKey, 0};
+    if (col >= have) return Copy{-1, 0};                    // behind the sequence: reported
+    return Copy{max(-1, __ldg(p.block_table + (size_t)b * p.max_pages + col)),
+                kMode == kDecPages
+                    ? min(max(len - col * p.page_size - (j & (p.page_size - 1)), 0), box)
+                    : 1};
+  };
+  auto lane_issue = [&](int blk, int st, const Copy& e) {   // by the whole warp
+    const int j = k0 + blk * kDecKeys + lane * box;
+    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], 2 * kDecKeys * 128);
+    __syncwarp();
+    if (lane < npg) {
+      const bool ok = e.entry >= 0 && e.entry < p.num_pages;
+      if (!ok && e.entry != kDecNoKey && j < k1 && j + box > lo)
+        atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+      const int row = ok ? e.entry * p.page_size + (j & (p.page_size - 1))
+                         : p.num_pages * p.page_size;       // past the cache: zeros
+      s_pageok[st][lane] = ok ? e.seen : 0;
+      tma_load_3d(&p.tm_k, &kv_full[st], &s_kv[st][0][lane * box * 128], 0, g, row);
+      tma_load_3d(&p.tm_v, &kv_full[st], &s_kv[st][1][lane * box * 128], 0, g, row);
+    }
+  };
   int issued = 0;                                         // TMA path: blocks issued
   if (kTma) {
     if (tid == 0) {
-      for (int st = 0; st < kDecStages; ++st) mbar_init(&kv_full[st], 1);
+      for (int st = 0; st < kStages; ++st) mbar_init(&kv_full[st], 1);
       fence_mbarrier_init();
     }
     __syncthreads();
@@ -353,16 +379,33 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   // two-stage ring: block blk + 1 is in flight while blk is used (five CTAs per
   // SM keep ten blocks in flight; measured better than three stages at four
   // CTAs per SM)
-  int pg[8], pg_next[8], seen[8], seen_next[8];
+  int pg[8], pg_next[8];
+  Copy next{kDecNoKey, 0};
+  int col_next = -1;
   bool ok = true;
-  if (kTma) {
+  if (kTma && !kAll) {
+    if (warp == 0) {
+      int col[kStages + 2];
+      Copy c[kStages + 1];
+      #pragma unroll
+      for (int i = 0; i < kStages + 2; ++i) col[i] = lane_list(i);
+      #pragma unroll
+      for (int i = 0; i < kStages + 1; ++i) c[i] = lane_entry(i, col[i]);
+      #pragma unroll
+      for (int i = 0; i < kStages; ++i)
+        if (i < nblk) lane_issue(i, i, c[i]);
+      issued = min(nblk, kStages);
+      next = c[kStages];
+      col_next = col[kStages + 1];
+    }
+  } else if (kTma) {
     if (tid == 0) {
-      tma_fetch(0, pg, seen);
-      if (nblk > 0) tma_issue(0, 0, pg, seen);
-      tma_fetch(1, pg, seen);
-      if (nblk > 1) tma_issue(1, 1, pg, seen);
+      tma_fetch(0, pg);
+      if (nblk > 0) tma_issue(0, 0, pg);
+      tma_fetch(1, pg);
+      if (nblk > 1) tma_issue(1, 1, pg);
       issued = min(nblk, 2);
-      tma_fetch(2, pg_next, seen_next);
+      tma_fetch(2, pg_next);
     }
   } else {
     fetch_pages(0, pg);
@@ -370,10 +413,10 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     fetch_pages(1, pg_next);
   }
   for (int blk = 0; blk < nblk; ++blk) {
-    const int st = blk % kDecStages;
+    const int st = blk % kStages;
     if (kTma) {
       // bounded wait; the whole CTA agrees on the outcome
-      const bool landed = mbar_wait_warp(&kv_full[st], (blk / kDecStages) & 1, nullptr);
+      const bool landed = mbar_wait_warp(&kv_full[st], (blk / kStages) & 1, nullptr);
       if (!__syncthreads_and(landed)) {
         ok = false;
         break;
@@ -383,7 +426,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
         #pragma unroll
         for (int u = 0; u < 4; ++u) pg[u] = pg_next[u];
         fetch_pages(blk + 2, pg_next);
-        load_block(blk + 1, (blk + 1) % kDecStages, pg);
+        load_block(blk + 1, (blk + 1) % kStages, pg);
         cp_async_wait<1>();
       } else {
         cp_async_wait<0>();
@@ -493,14 +536,18 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       mma_16816_f16(oacc[2 * u + 1], pa0, 0u, pa2, 0u, h2, h3);
     }
     __syncthreads();   // every warp is done with stage st before it is refilled
-    if (kTma && tid == 0 && blk + 2 < nblk) {
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        pg[i] = pg_next[i];
-        if constexpr (kMode == kDecPages) seen[i] = seen_next[i];
+    if (kTma && !kAll) {
+      if (warp == 0 && blk + kStages < nblk) {
+        lane_issue(blk + kStages, st, next);
+        issued = blk + kStages + 1;
+        next = lane_entry(blk + kStages + 1, col_next);
+        col_next = lane_list(blk + kStages + 2);
       }
-      tma_fetch(blk + 3, pg_next, seen_next);
-      tma_issue(blk + 2, st, pg, seen);
+    } else if (kTma && tid == 0 && blk + 2 < nblk) {
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) pg[i] = pg_next[i];
+      tma_fetch(blk + 3, pg_next);
+      tma_issue(blk + 2, st, pg);
       issued = blk + 3;
     }
   }
@@ -510,8 +557,8 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     // land before the CTA releases its shared memory, and write nothing
     if (tid == 0) {
       atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 5);
-      for (int j = max(0, issued - kDecStages); j < issued; ++j)
-        mbar_wait(&kv_full[j % kDecStages], (j / kDecStages) & 1, nullptr);
+      for (int j = max(0, issued - kStages); j < issued; ++j)
+        mbar_wait(&kv_full[j % kStages], (j / kStages) & 1, nullptr);
     }
     leave();
     return;

@@ -2,9 +2,10 @@
 //
 // One CTA for each (sequence, kv head) finds the weight of the last key that stays
 // (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th kept key at or behind the budget goes to the n-th hole below it.  Only as many rows
-// move as there are holes, and no row is both read and written, so that a second kernel
-// can copy them in any order, 16 lanes a move (8 for the key, 8 for the value).  One more
-// CTA of the first kernel scans the sequences for the pages that become free.
+// move as there are holes, and no row is both read and written, so that they can be copied
+// in any order, 16 lanes a move (8 for the key, 8 for the value): by the same CTA where
+// there are enough of them to fill the GPU, by a second kernel where there are few.  One
+// more CTA of the first kernel scans the sequences for the pages that become free.
 #pragma once
 #include <climits>
 #include <cuda_bf16.h>
@@ -27,10 +28,11 @@ struct EvictParams {
   int* freed;                     // [max_freed]
   int* num_freed;                 // [1]
   int* counts;                    // [B][H_kv] moves
-  uint2* moves;                   // [B][H_kv][max_moves] cache rows (of all heads): from, to
+  int* to;                        // [B][H_kv][max_moves] holes, in order
+  int* from;                      // [B][H_kv][max_moves] keys that move there, from the last
   int* err;
   int batch, heads_kv, page_size, num_pages, max_pages, max_keys;
-  int budget, keep_first, keep_last, max_freed, max_moves, stage;
+  int budget, keep_first, keep_last, max_freed, max_moves, stage, here;   // here: one kernel
 };
 
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
@@ -39,6 +41,49 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool* bad)
   const int len = __ldg(p.seq_lens + b), cap = min(p.max_pages * p.page_size, p.max_keys);
   *bad |= len < 0 || len > cap;
   return max(0, min(len, cap));
+}
+
+// The moves first, first + step, .. of row (b, h), by 16 lanes each.
+__device__ __forceinline__ void evict_move(const EvictParams& p, int b, int h, int moves, int first,
+                                           int step) {
+  const int lane16 = threadIdx.x & 15, c = lane16 & 7;
+  uint4* cache = (lane16 < 8 ? p.k_cache : p.v_cache) + h * 8 + c;
+  const size_t row = (size_t)b * p.heads_kv + h;
+  const int* to = p.to + row * p.max_moves;
+  const int* from = p.from + row * p.max_moves;
+  const int* table = p.block_table + (size_t)b * p.max_pages;
+  auto cache_row = [&](int j) {
+    const int pg = j / p.page_size, e = __ldg(table + pg);
+    return (unsigned)e < (unsigned)p.num_pages
+               ? (uint32_t)e * (uint32_t)p.page_size + (uint32_t)(j - pg * p.page_size)
+               : kNoRow;
+  };
+  constexpr int kAtOnce = 4;
+  for (int i = first; i < moves; i += kAtOnce * step) {
+    int a[kAtOnce], z[kAtOnce];
+    uint32_t src[kAtOnce], dst[kAtOnce];
+    uint4 v[kAtOnce];
+    #pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int m = i + u * step;
+      a[u] = m < moves ? __ldcg(from + moves - 1 - m) : -1;
+      z[u] = m < moves ? __ldcg(to + m) : -1;
+    }
+    #pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      src[u] = a[u] >= 0 ? cache_row(a[u]) : kNoRow;
+      dst[u] = a[u] >= 0 ? cache_row(z[u]) : kNoRow;
+      if (a[u] >= 0 && lane16 == 0 && (src[u] == kNoRow || dst[u] == kNoRow))
+        atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+      if (dst[u] == kNoRow) src[u] = kNoRow;
+    }
+    #pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (src[u] != kNoRow) v[u] = __ldcg(cache + (size_t)src[u] * p.heads_kv * 8);
+    #pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (src[u] != kNoRow) cache[(size_t)dst[u] * p.heads_kv * 8] = v[u];
+  }
 }
 
 // The pages that become free, and the new lengths.
@@ -75,6 +120,8 @@ __device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[k
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
   if (tid == 0) *p.num_freed = done;
+  if (p.here)                             // no page behind the freed ones
+    for (int i = done + tid; i < p.max_freed; i += kThreads) p.freed[i] = -1;
 }
 
 template <int kThreads>
@@ -104,28 +151,41 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
     return;
   }
   const bool staged = len <= p.stage;
-  for (int j = tid; j < p.max_keys; j += kThreads) {
-    const float m = j < len ? __ldg(mass + j) : 0.0f;
-    if (staged && j < len) s_mass[j] = ordered(m);
-    mass_out[j] = j < fewer ? m : 0.0f;
-  }
-  __syncthreads();
-  auto at = [&](int j) { return staged ? s_mass[j] : ordered(__ldg(mass + j)); };
   const int lo = p.keep_first, hi = len - p.keep_last;      // the keys that compete
   const int need = p.budget - p.keep_first - p.keep_last;   // < hi - lo
-  int turn = 0, ties = 0;                                   // equal ones that stay
-  uint32_t bound = 0xFFFFFFFFu;
-  if (need > 0) {
-    int above;
-    bound = block_nth<kThreads>(
-        need, [&](auto&& take) {
-          for (int j = lo + tid; j < hi; j += kThreads) take(at(j));
-        }, &s_nth, &turn, &above);
-    ties = need - above;
+  uint32_t least = 0xFFFFFFFFu, largest = 0;
+  for (int j = tid; j < p.max_keys; j += kThreads) {
+    const float m = j < len ? __ldg(mass + j) : 0.0f;
+    mass_out[j] = j < fewer ? m : 0.0f;
+    if (j >= len) continue;
+    const uint32_t v = ordered(m);
+    if (staged) s_mass[j] = v;
+    if (j >= lo && j < hi) {
+      least = min(least, v);
+      largest = max(largest, v);
+    }
   }
-  // bitmaps of 32 kThreads keys at a time, a word a thread
-  uint2* moves = p.moves + row * p.max_moves;               // positions first: x from, y to
-  int holes = 0, movers = 0;
+  auto at = [&](int j) { return staged ? s_mass[j] : ordered(__ldg(mass + j)); };
+  int turn = 0, ties = 0;                                   // some of the equal ones stay
+  uint32_t bound = 0;
+  bool whole = true;                                        // or all of them
+  if (need > 0) {
+    // a thread reads what it stored itself: j = tid modulo kThreads
+    const Nth nth = block_nth<kThreads>(
+        need, least, largest, [&](auto&& take) {
+          for (int j = tid; j < hi; j += kThreads)
+            if (j >= lo) take(at(j));
+        }, &s_nth, &turn);
+    bound = nth.value;
+    whole = need - nth.above == nth.same;
+    if (!whole) ties = need - nth.above;
+  }
+  // Bitmaps of 32 kThreads keys at a time, a word a thread.  With s kept keys in front of j,
+  // a hole at j is number j - s, and a kept key at j >= budget is number budget - 1 - s
+  // from the last.
+  int* to = p.to + row * p.max_moves;
+  int* come = p.from + row * p.max_moves;
+  int stay = 0, holes = 0;
   for (int base = 0; base < len; base += 32 * kThreads) {
     __syncthreads();                                        // the last round's words are read
     const int words = min(kThreads, (len - base + 31) / 32);
@@ -134,8 +194,9 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
       const int j = base + 32 * w + lane;
       const uint32_t v = j < len ? at(j) : 0;
       const bool inner = j >= lo && j < hi;
-      const uint32_t k = __ballot_sync(0xffffffffu, j < len && (!inner || (need > 0 && v > bound)));
-      const uint32_t e = __ballot_sync(0xffffffffu, inner && v == bound && ties > 0);
+      const bool chosen = need > 0 && (v > bound || (whole && v == bound));
+      const uint32_t k = __ballot_sync(0xffffffffu, j < len && (!inner || chosen));
+      const uint32_t e = __ballot_sync(0xffffffffu, inner && !whole && v == bound);
       if (lane == 0) {
         s_kept[w] = k;
         s_tie[w] = e;
@@ -153,70 +214,47 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
       }
       ties = max(0, ties - all);
     }
-    // bits of the word below the budget, and of keys that there are
     const int j0 = base + 32 * tid;
+    const int first = stay + block_scan<kThreads>(__popc(kept), s_nth.sum, &turn, &all);
+    stay += all;
+    // bits of the word below the budget
     const uint32_t below = fewer - j0 >= 32 ? 0xFFFFFFFFu : fewer <= j0 ? 0u : (1u << (fewer - j0)) - 1u;
     uint32_t hole = ~kept & below, mover = kept & ~below;
-    int place = holes + block_scan<kThreads>(__popc(hole), s_nth.sum, &turn, &all);
-    holes += all;
-    while (hole != 0) {
-      moves[place++].y = (uint32_t)(j0 + __ffs(hole) - 1);
-      hole &= hole - 1;
+    int place = j0 - first;
+    if (j0 < fewer) {
+      while (hole != 0) {
+        to[place++] = j0 + __ffs(hole) - 1;
+        hole &= hole - 1;
+      }
     }
-    place = movers + block_scan<kThreads>(__popc(mover), s_nth.sum, &turn, &all);
-    movers += all;
+    // kept keys of this word below the budget come first
+    place = fewer - 1 - first - __popc(kept & below);
     while (mover != 0) {
-      moves[place++].x = (uint32_t)(j0 + __ffs(mover) - 1);
+      come[place--] = j0 + __ffs(mover) - 1;
       mover &= mover - 1;
     }
+    // holes up to the budget: what is left of it when its kept keys are counted
+    if (j0 < fewer && fewer <= j0 + 32) s_list[0] = fewer - first - __popc(kept & below);
   }
-  __syncthreads();                                          // the positions are listed
-  // the moved weights, and the cache rows of the moves
-  const int* table = p.block_table + (size_t)b * p.max_pages;
-  auto cache_row = [&](int j) {
-    const int pg = j / p.page_size, e = __ldg(table + pg);
-    return (unsigned)e < (unsigned)p.num_pages
-               ? (uint32_t)e * (uint32_t)p.page_size + (uint32_t)(j - pg * p.page_size)
-               : kNoRow;
-  };
-  for (int i = tid; i < holes; i += kThreads) {
-    const uint2 m = moves[i];
-    mass_out[m.y] = __ldg(mass + m.x);
-    uint2 r = make_uint2(cache_row((int)m.x), cache_row((int)m.y));
-    if (r.x == kNoRow || r.y == kNoRow) {
-      atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-      r.x = kNoRow;
-    }
-    moves[i] = r;
-  }
-  if (tid == 0) p.counts[row] = holes;
+  __syncthreads();                                          // the moves are listed
+  holes = fewer > 0 ? s_list[0] : 0;
+  for (int i = tid; i < holes; i += kThreads)
+    mass_out[__ldcg(to + i)] = __ldg(mass + __ldcg(come + holes - 1 - i));
+  if (p.here)
+    evict_move(p, b, (int)(row - (size_t)b * p.heads_kv), holes, tid >> 4, kThreads / 16);
+  else if (tid == 0)
+    p.counts[row] = holes;
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
 attn_sink_evict_move_kernel(const __grid_constant__ EvictParams p) {
   grid_dependency_wait();
-  const int half = threadIdx.x & 15, c = half & 7;
-  uint4* cache = half < 8 ? p.k_cache : p.v_cache;
   const size_t rows = (size_t)p.batch * p.heads_kv;
   for (size_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    const uint2* moves = p.moves + row * p.max_moves;
-    const int h = (int)(row % (unsigned)p.heads_kv), n = __ldcg(p.counts + row);
-    const int step = gridDim.x * (kMoveThreads / 16);
-    for (int i = blockIdx.x * (kMoveThreads / 16) + (threadIdx.x >> 4); i < n; i += 4 * step) {
-      uint2 m[4];
-      uint4 v[4];
-      #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        m[u] = make_uint2(kNoRow, 0);
-        if (i + u * step < n) m[u] = __ldcg(moves + i + u * step);
-      }
-      #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (m[u].x != kNoRow) v[u] = __ldcg(cache + ((size_t)m[u].x * p.heads_kv + h) * 8 + c);
-      #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (m[u].x != kNoRow) cache[((size_t)m[u].y * p.heads_kv + h) * 8 + c] = v[u];
-    }
+    const int b = (int)(row / (unsigned)p.heads_kv);
+    evict_move(p, b, (int)(row - (size_t)b * p.heads_kv), __ldcg(p.counts + row),
+               blockIdx.x * (kMoveThreads / 16) + (threadIdx.x >> 4),
+               gridDim.x * (kMoveThreads / 16));
   }
   // no page behind the freed ones
   const unsigned tid = (blockIdx.y * gridDim.x + blockIdx.x) * kMoveThreads + threadIdx.x;

@@ -72,44 +72,44 @@ struct NthShared {
   int sum[2][kThreads / 32];
   unsigned bins[kNthEach * kThreads];
   uint32_t list[kThreads];
-  uint32_t low, high, value;
-  int count, bin, before;
+  uint32_t low[kThreads / 32], high[kThreads / 32], value;
+  int count, bin, before, same;
 };
 
-// The value of rank n, 1 <= n <= count, from the top over the values that `each` passes
-// to its argument, shared out over the threads: T with count(v > T) < n <= count(v >=
-// T).  *above: count(v > T).  *turn as in block_sum.
+// What block_nth says of the value of a rank.
+struct Nth {
+  uint32_t value;
+  int above, same;                         // how many are larger, and equal
+};
+
+// The value T of rank n from the top, 1 <= n <= count: count(v > T) < n <= count(v >= T),
+// over the values that `each` passes to its argument, shared out over the threads.  low
+// and high: the smallest and the largest of this thread's (0xFFFFFFFF and 0 of none).
+// What `each` reads need not be visible to other threads yet.  *turn as in block_sum.
 template <int kThreads, typename Each>
-__device__ __forceinline__ uint32_t block_nth(int n, Each each, NthShared<kThreads>* s, int* turn,
-                                              int* above) {
+__device__ __forceinline__ Nth block_nth(int n, uint32_t low, uint32_t high, Each each,
+                                         NthShared<kThreads>* s, int* turn) {
   constexpr int kNthBins = kNthEach * kThreads;
   constexpr int kBits = kThreads == 256 ? 9 : kThreads == 512 ? 10 : 11;
+  constexpr int kWarps = kThreads / 32;
   static_assert(1 << kBits == kNthBins, "a power of two");
   const int tid = threadIdx.x, lane = tid & 31;
-  uint32_t low = 0xFFFFFFFFu, high = 0;
-  each([&](uint32_t v) {
-    low = min(low, v);
-    high = max(high, v);
-  });
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
-  if (tid == 0) {
-    s->low = 0xFFFFFFFFu;
-    s->high = 0;
-  }
-  __syncthreads();
   if (lane == 0) {
-    atomicMin(&s->low, low);
-    atomicMax(&s->high, high);
+    s->low[tid >> 5] = low;
+    s->high[tid >> 5] = high;
   }
+  #pragma unroll
+  for (int i = 0; i < kNthEach; ++i) s->bins[tid + i * kThreads] = 0;
+  if (tid == 0) s->count = 0;
   __syncthreads();
-  uint32_t base = s->low, span = s->high - s->low;
+  low = __reduce_min_sync(0xffffffffu, lane < kWarps ? s->low[lane] : 0xFFFFFFFFu);
+  high = __reduce_max_sync(0xffffffffu, lane < kWarps ? s->high[lane] : 0u);
+  uint32_t base = low, span = high - low;
   int left = n;                            // rank within the range
   while (true) {
     const int shift = max(0, 32 - __clz(span) - kBits);        // span >> shift < kNthBins
-    for (int i = tid; i < kNthBins; i += kThreads) s->bins[i] = 0;
-    if (tid == 0) s->count = 0;
-    __syncthreads();
     each([&](uint32_t v) {
       if (v - base <= span) atomicAdd(&s->bins[(v - base) >> shift], 1u);
     });
@@ -137,10 +137,7 @@ __device__ __forceinline__ uint32_t block_nth(int n, Each each, NthShared<kThrea
     left -= s->before;
     base += bin << shift;
     span = shift > 0 ? min(span - (bin << shift), (1u << shift) - 1u) : 0u;
-    if (shift == 0) {                      // one value
-      *above = n - left;
-      return base;
-    }
+    if (shift == 0) return Nth{base, n - left, many};       // one value
     if (many <= kThreads) {
       each([&](uint32_t v) {
         if (v - base <= span) s->list[atomicAdd(&s->count, 1)] = v;   // in any order
@@ -156,13 +153,16 @@ __device__ __forceinline__ uint32_t block_nth(int n, Each each, NthShared<kThrea
         if (more < left && left <= more + same) {           // equal ones say the same
           s->value = v;
           s->before = more;
+          s->same = same;
         }
       }
       __syncthreads();
-      *above = n - left + s->before;
-      return s->value;
+      return Nth{s->value, n - left + s->before, s->same};
     }
     __syncthreads();                       // the bins have been read
+    #pragma unroll
+    for (int i = 0; i < kNthEach; ++i) s->bins[tid + i * kThreads] = 0;
+    __syncthreads();
   }
 }
 
