@@ -18,7 +18,6 @@
 #include "bounds_kernel.cuh"
 #include "bwd_dq_kernel.cuh"
 #include "bwd_kernel.cuh"
-#include "decode_join.cuh"
 #include "decode_kernel.cuh"
 #include "evict_kernel.cuh"
 #include "extend_kernel.cuh"
@@ -31,6 +30,7 @@
 #include "rope_kernel.cuh"
 #include "schedule_kernel.cuh"
 #include "shared_kernel.cuh"
+#include "slice_kernel.cuh"
 
 // Device word a kernel sets when it gives up on a bounded wait.
 __device__ int g_attn_sink_device_error = 0;
@@ -245,7 +245,8 @@ int validate(const attn_sink_params* p, const int* cu_q, const int* cu_k, Geomet
 // box_rows box and 128-byte swizzle: 64 columns of a 16-bit type, or 32 of fp32.
 int encode_rows(CUtensorMap* m, const void* ptr, long long tokens, int heads,
                 CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                int box_rows = kBlockM, int box_heads = 1) {
+                int box_rows = kBlockM, int box_heads = 1,
+                CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   if (!load_encode()) return ATTN_SINK_ERR_CUDA;
   const cuuint64_t esize = dtype == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)tokens};
@@ -254,7 +255,7 @@ int encode_rows(CUtensorMap* m, const void* ptr, long long tokens, int heads,
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = g_encode(m, dtype, 3, const_cast<void*>(ptr), dims,
                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }

@@ -32,7 +32,7 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 }
 
 // ----------------------------------------------------------------------------- decode
-// The slices of a sequence's keys in the decode kernel, and what they leave.
+// The slices of a sequence's keys, and what they leave.
 struct DecodeSlices {
   int splits;
   size_t off_ml, total;
@@ -46,19 +46,25 @@ DecodeSlices decode_slices(int splits, int batch, int heads_q) {
   return d;
 }
 
-// As many slices of at least kDecKeys keys as the GPU holds at once.
-int decode_splits(int batch, int heads_kv, long long keys, int sms) {
+// Slices of a sequence of up to `keys` keys: four rounds of the CTAs that the GPU holds at
+// once, so that a last, partly filled one matters less, of kSliceLong keys or more; or, of
+// few sequences, as many as it holds, of `least` keys or more.
+constexpr int kSliceLong = 512;
+constexpr int kSliceRounds = 4;
+int decode_splits(int batch, int heads_kv, long long keys, int least, int sms) {
   const long long ctas = std::max(1ll, (long long)batch * heads_kv);
-  const long long most = std::min(64ll, (keys + kDecKeys - 1) / kDecKeys);
-  return (int)std::max(1ll, std::min(most, dec_ctas(kDecPages) * (long long)sms / ctas));
+  const long long slots = kSliceCtas * (long long)sms;
+  const long long rounds = std::min((kSliceRounds * slots + ctas - 1) / ctas, keys / kSliceLong);
+  const long long fill = std::min(slots / ctas, (keys + least - 1) / least);
+  return (int)std::max(1ll, std::min((long long)kSliceMax, std::max(rounds, fill)));
 }
 
-// The fields of DecodeParams that every mode has; *tma: which copies are taken.
+// The fields of SliceParams that both uses have; *tma: which copies are taken.
 template <typename P>
 int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* k_cache,
                   const void* v_cache, const int* block_table, const int* seq_lens,
                   const float* sink, void* out, float* lse, uint8_t* ws, int* err,
-                  DecodeParams* dp, bool* tma) {
+                  SliceParams* dp, bool* tma) {
   std::memset(dp, 0, sizeof(*dp));
   dp->q = static_cast<const __nv_bfloat16*>(q);
   dp->k_cache = static_cast<const __nv_bfloat16*>(k_cache);
@@ -80,48 +86,59 @@ int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* 
   dp->splits = L.splits;
   dp->scale_log2 = p->softmax_scale * kLog2e;
   const long long rows = (long long)p->num_pages * p->page_size;
-  *tma = decode_tma_page(p->page_size) && rows > 0 && rows < (1ll << 31);
+  *tma = slice_tma_page(p->page_size) && rows > 0 && rows < (1ll << 31);
   while ((1 << dp->log2_page) < p->page_size) ++dp->log2_page;
   if (!*tma) return ATTN_SINK_OK;
-  const int box = std::min(p->page_size, kDecKeys);
+  const int box = std::min(p->page_size, kSliceKeys);
+  // No more than a head's 128 bytes into L2: with pages of its own for each head, its
+  // neighbour's are not wanted (64 sequences x 2048 keys read 375 MB of 269 and took 67
+  // us, not 55, where L2 fetched 256 bytes)
+  constexpr CUtensorMapL2promotion kOneHead = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   int st;
   if ((st = encode_rows(&dp->tm_k, k_cache, rows, p->heads_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        box)) != ATTN_SINK_OK)
+                        box, 1, kOneHead)) != ATTN_SINK_OK)
     return st;
   return encode_rows(&dp->tm_v, v_cache, rows, p->heads_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     box);
+                     box, 1, kOneHead);
 }
 
-template <DecodeMode kMode>
-auto decode_kernel(int group, bool tma) -> void (*)(DecodeParams) {
+template <bool kShared>
+auto slice_kernel(int group, bool tma) -> void (*)(SliceParams) {
   switch (group * 2 + (tma ? 1 : 0)) {
-    case 2: return attn_sink_decode_kernel<1, false, kMode>;
-    case 3: return attn_sink_decode_kernel<1, true, kMode>;
-    case 4: return attn_sink_decode_kernel<2, false, kMode>;
-    case 5: return attn_sink_decode_kernel<2, true, kMode>;
-    case 8: return attn_sink_decode_kernel<4, false, kMode>;
-    case 9: return attn_sink_decode_kernel<4, true, kMode>;
-    case 16: return attn_sink_decode_kernel<8, false, kMode>;
-    default: return attn_sink_decode_kernel<8, true, kMode>;
+    case 2: return attn_sink_slice_kernel<1, false, kShared>;
+    case 3: return attn_sink_slice_kernel<1, true, kShared>;
+    case 4: return attn_sink_slice_kernel<2, false, kShared>;
+    case 5: return attn_sink_slice_kernel<2, true, kShared>;
+    case 8: return attn_sink_slice_kernel<4, false, kShared>;
+    case 9: return attn_sink_slice_kernel<4, true, kShared>;
+    case 16: return attn_sink_slice_kernel<8, false, kShared>;
+    default: return attn_sink_slice_kernel<8, true, kShared>;
   }
 }
 
-constexpr int kDecSliceSmem = 1024 + dec_stages(kDecPages) * 2 * kDecKeys * 128;
-
 template <bool kShared>
-bool launch_join(const DecodeParams& dp, cudaStream_t s) {
-  constexpr int kRows = kDecJoinThreads / 32;
+bool launch_join(const SliceParams& dp, cudaStream_t s) {
+  constexpr int kRows = kJoinThreads / 32;
   const long long rows = (long long)dp.batch * dp.heads_q;
-  return launch_dependent(attn_sink_decode_join_kernel<kShared>,
-                          dim3((unsigned)((rows + kRows - 1) / kRows)), kDecJoinThreads, 0, s, dp);
+  return launch_dependent(attn_sink_join_kernel<kShared>,
+                          dim3((unsigned)((rows + kRows - 1) / kRows)), kJoinThreads, 0, s, dp);
 }
 
 // ----------------------------------------------------------------------------- shared prefixes
+constexpr int kSharedWhole = 4096;
 struct SharedLayout {
   DecodeSlices own;
   int tokens, n_items, slots;
   size_t off_items, off_refs, off_ml, off_o, total;
 };
+
+// Slices of the keys behind the prefix, of which the host only knows that they are not
+// more than the table holds: one, which joins the prefix itself and needs no kernel for
+// that, where the CTAs fill half of the GPU or the table is short.
+int shared_splits(int batch, int heads_kv, long long cap, int sms) {
+  if (2ll * batch * heads_kv >= kSliceCtas * (long long)sms || cap <= kSharedWhole) return 1;
+  return decode_splits(batch, heads_kv, cap, kSliceLong, sms);
+}
 
 int shared_layout(const attn_sink_shared_params* p, int sms, SharedLayout* L) {
   int st = cache_validate(p, 65535);
@@ -138,7 +155,7 @@ int shared_layout(const attn_sink_shared_params* p, int sms, SharedLayout* L) {
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
   L->n_items = (int)items;
   const long long cap = (long long)p->max_pages * p->page_size;
-  L->own = decode_slices(decode_splits(p->batch, p->heads_kv, cap, sms), p->batch, p->heads_q);
+  L->own = decode_slices(shared_splits(p->batch, p->heads_kv, cap, sms), p->batch, p->heads_q);
   size_t off = L->own.total;
   L->off_items = off;
   off += align256((size_t)L->n_items * sizeof(ExtItem));
@@ -226,12 +243,12 @@ int cache_attributes() {
   if (!g_cache_attr_set[dev]) {
     for (int group : {1, 2, 4, 8})
       for (bool tma : {false, true})
-        if (cudaFuncSetAttribute(decode_kernel<kDecPages>(group, tma),
+        if (cudaFuncSetAttribute(slice_kernel<false>(group, tma),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kDecSliceSmem) != cudaSuccess ||
-            cudaFuncSetAttribute(decode_kernel<kDecShared>(group, tma),
+                                 kSliceSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(slice_kernel<true>(group, tma),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kDecSliceSmem) != cudaSuccess)
+                                 kSliceSmem) != cudaSuccess)
           return ATTN_SINK_ERR_CUDA;
     for (int threads : {256, 512, 1024})
       if (cudaFuncSetAttribute(evict_kernel(threads), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -293,7 +310,7 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  DecodeParams dp;
+  SliceParams dp;
   bool dec_tma;
   if ((st = decode_params(params, L.own, q, k_cache, v_cache, block_table, seq_lens, sink, out,
                           lse, ws, err, &dp, &dec_tma)) != ATTN_SINK_OK)
@@ -356,9 +373,9 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
                         kFwdSmemBytes, s, ep))
     return ATTN_SINK_ERR_CUDA;
   const dim3 grid(L.own.splits, params->heads_kv, params->batch);
-  return launch_dependent(decode_kernel<kDecShared>(ep.group, dec_tma), grid, kDecThreads,
-                          kDecSliceSmem, s, dp) &&
-                 launch_join<true>(dp, s)
+  return launch_dependent(slice_kernel<true>(ep.group, dec_tma), grid, kSliceThreads,
+                          kSliceSmem, s, dp) &&
+                 (L.own.splits == 1 || launch_join<true>(dp, s))
              ? ATTN_SINK_OK
              : ATTN_SINK_ERR_CUDA;
 }
@@ -475,7 +492,8 @@ int pages_layout(const attn_sink_pages_params* p, int sms, DecodeSlices* L) {
     return ATTN_SINK_ERR_INVALID_ARG;
   if (p->heads_kv > 65535) return ATTN_SINK_ERR_UNSUPPORTED;
   const long long keys = (long long)std::min(p->count, p->max_pages) * p->page_size;
-  *L = decode_slices(decode_splits(p->batch, p->heads_kv, keys, sms), p->batch, p->heads_q);
+  *L = decode_slices(decode_splits(p->batch, p->heads_kv, keys, kSliceThreads, sms), p->batch,
+                     p->heads_q);
   return ATTN_SINK_OK;
 }
 
@@ -510,7 +528,7 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
   if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
   if ((st = cache_attributes()) != ATTN_SINK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  DecodeParams dp;
+  SliceParams dp;
   bool tma;
   if ((st = decode_params(params, L, q, k_cache, v_cache, block_table, seq_lens, sink, out, lse,
                           static_cast<uint8_t*>(workspace), err, &dp, &tma)) != ATTN_SINK_OK)
@@ -518,8 +536,7 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
   dp.selected = selected;
   dp.count = params->count;
   const dim3 grid(L.splits, params->heads_kv, params->batch);
-  decode_kernel<kDecPages>(params->heads_q / params->heads_kv,
-                           tma)<<<grid, kDecThreads, kDecSliceSmem, s>>>(dp);
+  slice_kernel<false>(params->heads_q / params->heads_kv, tma)<<<grid, kSliceThreads, kSliceSmem, s>>>(dp);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   return L.splits == 1 || launch_join<false>(dp, s) ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
 }

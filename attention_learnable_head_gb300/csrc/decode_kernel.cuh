@@ -28,7 +28,6 @@
 //                read with a transposing ldmatrix and converted from bf16)
 // The 4 warps' (m, l, O) states are merged through shared memory at the end.
 #pragma once
-#include <climits>
 #include <cuda_bf16.h>
 #include "sm103_ptx.cuh"
 
@@ -39,27 +38,7 @@ constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecMaxGroup = 8;        // query heads per kv head
 constexpr int kDecKeys = 64;           // keys per stage: 16 per warp
 constexpr int kDecStages = 2;
-// Stages and CTAs per SM by what is read: see the kernel.
-__host__ __device__ constexpr int dec_stages(int mode) { return mode == 0 ? kDecStages : 3; }
-__host__ __device__ constexpr int dec_ctas(int mode) { return mode == 0 ? 5 : 4; }
 constexpr float kLn2Dec = 0.6931471805599453f;
-constexpr float kLog2eDec = 1.4426950408889634f;
-constexpr int kDecTileRows = 128;      // kDecShared: rows of a prefix tile's partial results
-constexpr int kDecNoKey = INT_MIN;     // kDecPages: no entry of the list, or behind the last key
-constexpr int kSharedMinSeqs = 2;      // kDecShared: smaller groups and shorter prefixes are read
-constexpr int kSharedMinKeys = 64;     //   by each sequence for itself
-
-// What a decode step reads: every cached key (or a window), the pages selected for
-// each kv head, or the keys behind the prefix a group of sequences shares
-// (shared_kernel.cuh).  The last two leave a slice's sums to a kernel that joins them
-// (decode_join.cuh), where there is more than one slice.
-enum DecodeMode { kDecAll, kDecPages, kDecShared };
-
-// The prefix of a sequence in decode_shared: its tile's partial results.
-struct alignas(16) SharedRef {
-  int first, parts;               // of [partial][kv head][128 rows]; 0 parts: no prefix
-  int place, pad;                 // the sequence's place in the tile
-};
 
 struct DecodeParams {
   CUtensorMap tm_k;               // k_cache as [num_pages * page_size][H_kv][64], box
@@ -84,16 +63,6 @@ struct DecodeParams {
   int splits;
   int log2_page;                  // TMA path: log2(page_size)
   float scale_log2;               // softmax_scale * log2(e)
-  const int* selected;            // kDecPages: [B][H_kv][count] columns of the block table
-  int count;
-  const int* cu_groups;           // kDecShared: [num_groups + 1] first sequences
-  const int* prefix_lens;         // [num_groups]
-  const SharedRef* refs;          // [B]
-  const float* prefix_o;          // [partial][H_kv][128 rows][64] sums
-  const float2* prefix_ml;        // [partial][H_kv][128 rows]: maximum (log2 units), sum
-  int num_groups;
-  float* slice_o;                 // kDecPages, kDecShared: [B][H_q][splits][64] sums
-  float2* slice_ml;               // [B][H_q][splits]: maximum (log2 units), sum
 };
 
 // Page sizes the TMA path copies whole: a multiple of 8 keys (whole 128-byte
@@ -102,49 +71,22 @@ __host__ __device__ constexpr bool decode_tma_page(int page_size) {
   return page_size >= 8 && (page_size & (page_size - 1)) == 0;
 }
 
-__device__ __forceinline__ int shared_seq_len(const int* seq_lens, int b, int cap) {
-  return max(0, min(__ldg(seq_lens + b), cap));
-}
-// The last p in [0, groups] with cu[p] <= b; every lane of the warp gets it.
-__device__ __forceinline__ int shared_find(const int* cu, int groups, int b) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, span = groups + 1;             // the answer lies in [lo, lo + span)
-  while (span > 1) {
-    const int step = (span + 31) / 32;
-    const int at = lo + lane * step;
-    const bool le = lane * step < span && (lane == 0 || __ldg(cu + at) <= b);
-    const int i = 31 - __clz(__ballot_sync(0xffffffffu, le));
-    lo += i * step;
-    span = min(step, span - i * step);
-  }
-  return lo;
-}
-
 // G = query heads per kv head (1, 2, 4 or 8).  kTma: the blocks' pages are
 // copied by TMA (one thread issues them; page sizes of decode_tma_page),
 // otherwise by every thread with 16-byte cp.async.
-template <int G, bool kTma, DecodeMode kMode = kDecAll>
-__global__ void __launch_bounds__(kDecThreads, dec_ctas(kMode))
+template <int G, bool kTma>
+__global__ void __launch_bounds__(kDecThreads, 5)
 attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kStages = dec_stages(kMode);
-  constexpr bool kAll = kMode == kDecAll;
-  extern __shared__ uint8_t dec_smem[];
-  __shared__ __align__(1024) uint8_t s_fixed[kAll ? kStages * 2 * kDecKeys * 128 : 16];
-  // K, V blocks (more than two stages do not fit static shared memory)
-  uint8_t (*s_kv)[2][kDecKeys * 128] = reinterpret_cast<uint8_t (*)[2][kDecKeys * 128]>(
-      kAll ? s_fixed
-           : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dec_smem) + 1023) &
-                                        ~static_cast<uintptr_t>(1023)));
-  __shared__ uint8_t s_valid[kStages][kDecKeys];       // key inside the slice, page in range
-  __shared__ uint8_t s_pageok[kStages][8];             // TMA path: copy i of the block is a page
-                                                       //   (kDecPages: how many of its keys are seen)
-  __shared__ __align__(8) uint64_t kv_full[kStages];   // TMA path: the stage's copies landed
+  __shared__ __align__(1024) uint8_t s_kv[kDecStages][2][kDecKeys * 128];   // K, V blocks
+  __shared__ uint8_t s_valid[kDecStages][kDecKeys];    // key inside the slice, page in range
+  __shared__ uint8_t s_pageok[kDecStages][8];          // TMA path: copy i of the block is a page
+  __shared__ __align__(8) uint64_t kv_full[kDecStages];   // TMA path: the stage's copies landed
   __shared__ float s_m[kDecWarps][kDecMaxGroup];
   __shared__ float s_l[kDecWarps][kDecMaxGroup];
   __shared__ int s_last;
   // the warps' O rows for the final merge reuse the K/V stages (free by then)
   float (*s_o)[kDecMaxGroup][64] = reinterpret_cast<float (*)[kDecMaxGroup][64]>(&s_kv[0][0][0]);
-  static_assert(sizeof(float) * kDecWarps * kDecMaxGroup * 64 <= kStages * 2 * kDecKeys * 128,
+  static_assert(sizeof(float) * kDecWarps * kDecMaxGroup * 64 <= sizeof(s_kv),
                 "merge buffer larger than the K/V stages");
 
   const int split = blockIdx.x;
@@ -164,57 +106,13 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   }
   // The slices start on 64-key block boundaries (so the TMA path copies whole
   // pages into a block); keys before the window start are masked.
-  int lo = p.window > 0 ? max(0, L - p.window) : 0;
-  if constexpr (kMode != kDecAll) grid_launch_dependents();
-  if constexpr (kMode == kDecShared) {
-    __shared__ int s_min[kDecWarps];
-    const int gp = shared_find(p.cu_groups, p.num_groups, b);
-    int c0 = 0, c1 = 0, keys = 0;
-    if (gp < p.num_groups) {
-      c0 = max(0, __ldg(p.cu_groups + gp));
-      c1 = min(p.batch, __ldg(p.cu_groups + gp + 1));
-      keys = __ldg(p.prefix_lens + gp);
-    }
-    int least = INT_MAX;
-    for (int i = c0 + tid; i < c1; i += kDecThreads)
-      least = min(least, shared_seq_len(p.seq_lens, i, cap));
-    least = __reduce_min_sync(0xffffffffu, least);
-    if (lane == 0) s_min[warp] = least;
-    __syncthreads();
-    for (int w = 0; w < kDecWarps; ++w) least = min(least, s_min[w]);
-    if (c0 <= b && b < c1 && c1 - c0 >= kSharedMinSeqs) {
-      const int shared = min(keys, least);
-      if (shared >= kSharedMinKeys) lo = shared;
-    }
-  }
-  // kDecPages: the sequence's pages; L from here on counts the keys of the listed ones,
-  // in the order of the list
-  const int len = L, have = (L + p.page_size - 1) / p.page_size;
-  const int* listed = nullptr;
-  if constexpr (kMode == kDecPages) {
-    listed = p.selected + ((size_t)b * p.heads_kv + g) * p.count;
-    L = min(p.count, have) * p.page_size;
-  }
+  const int lo = p.window > 0 ? max(0, L - p.window) : 0;
   const int lo_blk = lo & ~(kDecKeys - 1);
   const int per = ((L - lo_blk + p.splits - 1) / p.splits + kDecKeys - 1) & ~(kDecKeys - 1);
   const int k0 = lo_blk + split * per;
   const int k1 = min(L, k0 + per);
   const int nblk = k1 > k0 ? (k1 - k0 + kDecKeys - 1) / kDecKeys : 0;
   const size_t row_stride = (size_t)p.heads_kv * 64;     // one key of the cache
-  // kDecShared: the kernel in front computes the prefix at the same time.  This one has
-  // ended only when that one has: one CTA waits for it.
-  auto leave = [&] {
-    if (kMode == kDecShared && split == 0 && g == 0 && b == 0) grid_dependency_wait();
-  };
-  if constexpr (kMode != kDecAll) {
-    if (nblk == 0 && p.splits + (kMode == kDecShared) > 1) {   // an empty slice
-      if (tid < G)
-        p.slice_ml[((size_t)b * p.heads_q + g * G + tid) * p.splits + split] =
-            make_float2(-INFINITY, 0.0f);
-      leave();
-      return;
-    }
-  }
 
   // Q as the A operand (rows >= G are zero): a0 = dims 16 kk + 2 t4 .. + 1,
   // a2 = the same + 8, of head row gr; a1 = a3 = 0 (rows 8..15).
@@ -239,20 +137,9 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = k0 + blk * kDecKeys + (((tid >> 3) + 16 * u) & (kDecKeys - 1));
-      if constexpr (kMode == kDecPages) {
-        pg[u] = kDecNoKey;
-        if (blk < nblk && j < k1) {
-          const int at = j / p.page_size, col = __ldg(listed + at);
-          if (col >= have)
-            pg[u] = -1;                      // reported, as a bad table entry is
-          else if (col >= 0 && col * p.page_size + (j - at * p.page_size) < len)
-            pg[u] = max(-1, __ldg(p.block_table + (size_t)b * p.max_pages + col));
-        }
-      } else {
-        pg[u] = (blk < nblk && j < k1)
-                    ? __ldg(p.block_table + (size_t)b * p.max_pages + j / p.page_size)
-                    : -1;
-      }
+      pg[u] = (blk < nblk && j < k1)
+                  ? __ldg(p.block_table + (size_t)b * p.max_pages + j / p.page_size)
+                  : -1;
     }
   };
   // Block `blk` of the slice into stage `st`, with the table entries pg of its
@@ -265,7 +152,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     for (int u = 0; u < 4; ++u) {
       const int key = ((tid >> 3) + 16 * u) & (kDecKeys - 1);
       const int j = base + key;
-      const bool inside = j >= lo && j < k1 && (kMode != kDecPages || pg[u] != kDecNoKey);
+      const bool inside = j >= lo && j < k1;
       const bool valid = inside && pg[u] >= 0 && pg[u] < p.num_pages;
       if (inside && !valid && c == 0) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
       if (c == 0) s_valid[st][key] = valid ? 1 : 0;
@@ -332,45 +219,10 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       }
     }
   };
-  // The other modes: lane i of the first warp has copy i, and the loads are further
-  // ahead: list entries (kDecPages) two blocks, table entries one block in front of the
-  // copies, which so wait for neither.
-  struct Copy {
-    int entry, seen;                 // of the table; keys that the sequence has there
-  };
-  auto lane_list = [&](int blk) {    // the column of the block table; -1: none
-    const int j = k0 + blk * kDecKeys + lane * box;
-    if (lane >= npg || blk >= nblk || j >= k1) return -1;
-    return kMode == kDecPages ? __ldg(listed + (j >> p.log2_page)) : j >> p.log2_page;
-  };
-  auto lane_entry = [&](int blk, int col) {
-    const int j = k0 + blk * kDecKeys + lane * box;
-    if (col < 0) return Copy{kDecNoKey, 0};
-    if (col >= have) return Copy{-1, 0};                    // behind the sequence: reported
-    return Copy{max(-1, __ldg(p.block_table + (size_t)b * p.max_pages + col)),
-                kMode == kDecPages
-                    ? min(max(len - col * p.page_size - (j & (p.page_size - 1)), 0), box)
-                    : 1};
-  };
-  auto lane_issue = [&](int blk, int st, const Copy& e) {   // by the whole warp
-    const int j = k0 + blk * kDecKeys + lane * box;
-    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], 2 * kDecKeys * 128);
-    __syncwarp();
-    if (lane < npg) {
-      const bool ok = e.entry >= 0 && e.entry < p.num_pages;
-      if (!ok && e.entry != kDecNoKey && j < k1 && j + box > lo)
-        atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-      const int row = ok ? e.entry * p.page_size + (j & (p.page_size - 1))
-                         : p.num_pages * p.page_size;       // past the cache: zeros
-      s_pageok[st][lane] = ok ? e.seen : 0;
-      tma_load_3d(&p.tm_k, &kv_full[st], &s_kv[st][0][lane * box * 128], 0, g, row);
-      tma_load_3d(&p.tm_v, &kv_full[st], &s_kv[st][1][lane * box * 128], 0, g, row);
-    }
-  };
   int issued = 0;                                         // TMA path: blocks issued
   if (kTma) {
     if (tid == 0) {
-      for (int st = 0; st < kStages; ++st) mbar_init(&kv_full[st], 1);
+      for (int st = 0; st < kDecStages; ++st) mbar_init(&kv_full[st], 1);
       fence_mbarrier_init();
     }
     __syncthreads();
@@ -380,25 +232,8 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   // SM keep ten blocks in flight; measured better than three stages at four
   // CTAs per SM)
   int pg[8], pg_next[8];
-  Copy next{kDecNoKey, 0};
-  int col_next = -1;
   bool ok = true;
-  if (kTma && !kAll) {
-    if (warp == 0) {
-      int col[kStages + 2];
-      Copy c[kStages + 1];
-      #pragma unroll
-      for (int i = 0; i < kStages + 2; ++i) col[i] = lane_list(i);
-      #pragma unroll
-      for (int i = 0; i < kStages + 1; ++i) c[i] = lane_entry(i, col[i]);
-      #pragma unroll
-      for (int i = 0; i < kStages; ++i)
-        if (i < nblk) lane_issue(i, i, c[i]);
-      issued = min(nblk, kStages);
-      next = c[kStages];
-      col_next = col[kStages + 1];
-    }
-  } else if (kTma) {
+  if (kTma) {
     if (tid == 0) {
       tma_fetch(0, pg);
       if (nblk > 0) tma_issue(0, 0, pg);
@@ -413,10 +248,10 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     fetch_pages(1, pg_next);
   }
   for (int blk = 0; blk < nblk; ++blk) {
-    const int st = blk % kStages;
+    const int st = blk % kDecStages;
     if (kTma) {
       // bounded wait; the whole CTA agrees on the outcome
-      const bool landed = mbar_wait_warp(&kv_full[st], (blk / kStages) & 1, nullptr);
+      const bool landed = mbar_wait_warp(&kv_full[st], (blk / kDecStages) & 1, nullptr);
       if (!__syncthreads_and(landed)) {
         ok = false;
         break;
@@ -426,7 +261,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
         #pragma unroll
         for (int u = 0; u < 4; ++u) pg[u] = pg_next[u];
         fetch_pages(blk + 2, pg_next);
-        load_block(blk + 1, (blk + 1) % kStages, pg);
+        load_block(blk + 1, (blk + 1) % kDecStages, pg);
         cp_async_wait<1>();
       } else {
         cp_async_wait<0>();
@@ -436,18 +271,10 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     // TMA copies whole pages: value rows outside [lo, k1) may hold anything (cache
     // rows that no token was written to), and 0 * inf is not 0.
     const int base = k0 + blk * kDecKeys;
-    bool edge = base < lo || base + kDecKeys > k1;             // same for the whole CTA
-    if constexpr (kTma && kMode == kDecPages) {                // a page that is partly filled
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) edge |= i < npg && s_pageok[st][i] < box;
-    }
-    if (kTma && edge) {
+    if (kTma && (base < lo || base + kDecKeys > k1)) {         // same for the whole CTA
       for (int c = tid; c < kDecKeys * 8; c += kDecThreads) {
         const int j = base + (c >> 3);
-        bool gone = j < lo || j >= k1;
-        if constexpr (kMode == kDecPages)
-          gone = gone || ((c >> 3) & (box - 1)) >= s_pageok[st][(c >> 3) >> log2_box];
-        if (gone)
+        if (j < lo || j >= k1)
           *reinterpret_cast<uint4*>(&s_kv[st][1][c * 16]) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();     // the stage's next copy comes through the async proxy
@@ -484,10 +311,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
         bool valid;
         if (kTma) {
           const int j = k0 + blk * kDecKeys + key;
-          if constexpr (kMode == kDecPages)
-            valid = (key & (box - 1)) < s_pageok[st][key >> log2_box] && j < k1;
-          else
-            valid = s_pageok[st][key >> log2_box] != 0 && j >= lo && j < k1;
+          valid = s_pageok[st][key >> log2_box] != 0 && j >= lo && j < k1;
         } else {
           valid = s_valid[st][key] != 0;
         }
@@ -536,14 +360,7 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
       mma_16816_f16(oacc[2 * u + 1], pa0, 0u, pa2, 0u, h2, h3);
     }
     __syncthreads();   // every warp is done with stage st before it is refilled
-    if (kTma && !kAll) {
-      if (warp == 0 && blk + kStages < nblk) {
-        lane_issue(blk + kStages, st, next);
-        issued = blk + kStages + 1;
-        next = lane_entry(blk + kStages + 1, col_next);
-        col_next = lane_list(blk + kStages + 2);
-      }
-    } else if (kTma && tid == 0 && blk + 2 < nblk) {
+    if (kTma && tid == 0 && blk + 2 < nblk) {
       #pragma unroll
       for (int i = 0; i < 8; ++i) pg[i] = pg_next[i];
       tma_fetch(blk + 3, pg_next);
@@ -557,10 +374,9 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
     // land before the CTA releases its shared memory, and write nothing
     if (tid == 0) {
       atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 5);
-      for (int j = max(0, issued - kStages); j < issued; ++j)
-        mbar_wait(&kv_full[j % kStages], (j / kStages) & 1, nullptr);
+      for (int j = max(0, issued - kDecStages); j < issued; ++j)
+        mbar_wait(&kv_full[j % kDecStages], (j / kDecStages) & 1, nullptr);
     }
-    leave();
     return;
   }
   // a value that rounded to fp16 infinity (or a NaN) lies outside the fp16 range
@@ -584,42 +400,6 @@ attn_sink_decode_kernel(const __grid_constant__ DecodeParams p) {
   // thread t: head t / 16, dims 4 (t % 16) .. + 4
   const int h = tid >> 4;
   const int d0 = 4 * (tid & 15);
-  if constexpr (kMode != kDecAll) {
-    if (h < G) {
-      float mm = -INFINITY;
-      #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
-      const int hq = g * G + h;
-      const size_t row = (size_t)b * p.heads_q + hq;
-      const bool whole = kMode == kDecPages && p.splits == 1;   // then the sink joins here
-      const float s2 = whole ? __ldg(p.sink + hq) * kLog2eDec : -INFINITY;
-      const float mf = fmaxf(mm, s2);
-      const float mb = mf == -INFINITY ? 0.0f : mf;
-      float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float wt = ex2_approx(s_m[w][h] - mb);           // NaN sums reach the result
-        z = fmaf(wt, s_l[w][h], z);
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fmaf(wt, s_o[w][h][d0 + e], acc[e]);
-      }
-      if (whole) {
-        z += s2 == mb ? 1.0f : ex2_approx(s2 - mb);            // 1 where both are inf
-        const float inv = z != 0.0f ? 1.0f / z : 0.0f;
-        *reinterpret_cast<uint2*>(p.out + row * 64 + d0) = make_uint2(
-            pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        if (d0 == 0)
-          p.lse[(size_t)hq * p.batch + b] = z != 0.0f ? (mb + __log2f(z)) * kLn2Dec : -INFINITY;
-      } else {
-        const size_t at = row * p.splits + split;
-        *reinterpret_cast<float4*>(p.slice_o + at * 64 + d0) =
-            make_float4(acc[0], acc[1], acc[2], acc[3]);
-        if (d0 == 0) p.slice_ml[at] = make_float2(mf, z);
-      }
-    }
-    leave();
-    return;
-  }
   if (h < G) {
     float mm = -INFINITY;
     for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, s_m[w][h]);

@@ -5,21 +5,25 @@
 // heads of one kv head: their new tokens' rows lie next to each other in q, so the
 // tile is a tile of attn_sink_extend_kernel whose tokens all see the whole prefix,
 // and that kernel computes it: it leaves each part's maximum, sum and unnormalised
-// output in the workspace.  The keys behind the prefix are each sequence's own; the
-// decode kernel reads them (kDecShared), at the same time, and a last one joins
-// everything with the sink (decode_join.cuh).
+// output in the workspace.  The keys behind the prefix are each sequence's own;
+// attn_sink_slice_kernel reads them, at the same time, and a last kernel joins
+// everything with the sink (slice_kernel.cuh).
 //
-// This schedule kernel of one CTA lists the tiles' parts.  Groups of one sequence and
-// short prefixes have none (see shared_own): their sequences read all keys themselves.
+// This schedule kernel of one CTA lists the tiles' parts.  Their keys are cut so that
+// rounds of CTAs times what the longest takes is least, over chunks of kSharedTries sizes
+// from an even share of all blocks on (three prompts of 4096 to 8192 keys, 192 samples:
+// cut by the even share itself, 1.2 rounds, 52 us).  Groups of one sequence and
+// short prefixes have none (kSharedMinSeqs, kSharedMinKeys): their sequences read all keys themselves.
 #pragma once
-#include "decode_kernel.cuh"
 #include "extend_kernel.cuh"
+#include "slice_kernel.cuh"
 
 namespace attn_sink {
 
-static_assert(kDecTileRows == kBlockM, "a tile of the extend kernel");
-
 constexpr int kSharedWarps = 32;
+constexpr int kSharedTries = 32;
+constexpr int kSharedListed = 1024;      // groups up to which sizes are tried
+constexpr int kSharedMinBlocks = 2;      // key blocks of a part
 
 struct SharedPlan {
   ExtParams e;                             // batch, heads, cache, items, slots
@@ -32,12 +36,16 @@ struct SharedPlan {
 __global__ void __launch_bounds__(32 * kSharedWarps, 1)
 attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
   __shared__ int s_scan[32];
-  __shared__ unsigned long long s_work;
+  __shared__ unsigned long long s_work, s_best;
+  __shared__ int s_tiles[kSharedListed], s_blocks[kSharedListed];
   grid_launch_dependents();
   const ExtParams& e = p.e;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = e.max_pages * e.page_size;
-  if (tid == 0) s_work = 0;
+  if (tid == 0) {
+    s_work = 0;
+    s_best = ~0ull;
+  }
   __syncthreads();
   bool bad = false;
   // The keys that group i reads together, and its sequences [c0, c1); by a whole warp.
@@ -63,16 +71,39 @@ attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
   for (int i = warp; i < p.num_groups; i += kSharedWarps) {
     int c0, c1;
     const int keys = group(i, &c0, &c1);
-    if (keys > 0)
-      work += (unsigned long long)((c1 - c0 + e.tokens - 1) / e.tokens) *
-              (unsigned)((keys + kBlockN - 1) / kBlockN);
+    const int tiles = keys > 0 ? (c1 - c0 + e.tokens - 1) / e.tokens : 0;
+    const int blocks = (keys + kBlockN - 1) / kBlockN;
+    work += (unsigned long long)tiles * (unsigned)blocks;
+    if (lane == 0 && i < kSharedListed) {
+      s_tiles[i] = tiles;
+      s_blocks[i] = blocks;
+    }
   }
   if (lane == 0 && work > 0) atomicAdd(&s_work, work);      // whole numbers: any order
   if (bad) atomicCAS(e.err, 0, DEVERR_DECODE_INPUT);
   __syncthreads();
   const unsigned long long all = s_work * (unsigned)e.heads_kv;
-  const int chunk = (int)min(max((all + (unsigned)e.slots - 1) / (unsigned)e.slots,
-                                 (unsigned long long)kExtMinBlocks), 1ull << 24);
+  const unsigned long long share = (all + (unsigned)e.slots - 1) / (unsigned)e.slots;
+  int chunk = (int)min(max(share, (unsigned long long)kSharedMinBlocks), 1ull << 20);
+  if (p.num_groups <= kSharedListed) {
+    // warp i tries the share times (16 + i) / 16
+    const int c = max(chunk, (int)min((share * (16 + warp) + 15) / 16, 1ull << 20));
+    unsigned ctas = 0;
+    int longest = 0;
+    for (int i = lane; i < p.num_groups; i += 32)
+      if (s_tiles[i] > 0) {
+        const int parts = ext_parts(s_blocks[i], c);
+        ctas += (unsigned)s_tiles[i] * (unsigned)parts;
+        longest = max(longest, (s_blocks[i] + parts - 1) / parts);
+      }
+    ctas = __reduce_add_sync(0xffffffffu, ctas) * (unsigned)e.heads_kv;   // a launch grid
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const unsigned long long rounds = (ctas + (unsigned)e.slots - 1) / (unsigned)e.slots;
+    if (lane == 0)
+      atomicMin(&s_best, rounds * (unsigned)(longest + kExtOver) << 21 | (unsigned)c);
+    __syncthreads();
+    chunk = (int)(s_best & ((1u << 21) - 1));
+  }
   // the items of 32 groups at a time, one group a warp
   int listed = 0;
   bool over = false;                       // more than the workspace holds: no valid cu_groups

@@ -67,9 +67,8 @@ size_t attn_sink_decode_shared_workspace_size(const attn_sink_shared_params* par
  * [0, B], and a negative prefix_lens, are clamped and recorded as 0x800.
  * q, out [B, heads_q, 64] bf16, lse [heads_q, B] fp32, sink [heads_q] fp32.
  * Scores multiply the bf16 inputs exactly with fp32 sums and the softmax is fp32; in
- * O = P v the prefix's probabilities are rounded to bf16 next to the bf16 values, and
- * the others to fp16 next to fp16 values, as in attn_sink_extend and
- * attn_sink_decode (own values outside the fp16 range are recorded as 0x400).
+ * O = P v the values enter as they are, the prefix's probabilities rounded to bf16, as
+ * in attn_sink_extend, the others as the sum of two bf16 (17 bits).
  */
 int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q,
                             const void* k_cache, const void* v_cache, const int* block_table,
@@ -159,8 +158,8 @@ size_t attn_sink_decode_pages_workspace_size(const attn_sink_pages_params* param
  * (columns of the block table, as attn_sink_select_pages writes them).  Entries are
  * distinct, in any order; at most the first N = ceil(seq_lens[b] / page_size) of a
  * list are read.  A negative entry is no page, one of N or more is skipped and
- * recorded as 0x800.  A head that sees no key gets out = 0, lse = sink.  Layouts and
- * arithmetic as attn_sink_decode.
+ * recorded as 0x800.  A head that sees no key gets out = 0, lse = sink.  Layouts as
+ * attn_sink_decode, arithmetic as the own keys of attn_sink_decode_shared.
  */
 int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
                            const void* k_cache, const void* v_cache, const int* block_table,
