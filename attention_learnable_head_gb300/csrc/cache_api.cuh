@@ -64,7 +64,7 @@ template <typename P>
 int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* k_cache,
                   const void* v_cache, const int* block_table, const int* seq_lens,
                   const float* sink, void* out, float* lse, uint8_t* ws, int* err,
-                  SliceParams* dp, bool* tma) {
+                  bool own_pages, SliceParams* dp, bool* tma) {
   std::memset(dp, 0, sizeof(*dp));
   dp->q = static_cast<const __nv_bfloat16*>(q);
   dp->k_cache = static_cast<const __nv_bfloat16*>(k_cache);
@@ -84,22 +84,24 @@ int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* 
   dp->num_pages = p->num_pages;
   dp->max_pages = p->max_pages;
   dp->splits = L.splits;
+  dp->whole = L.splits == 1;
   dp->scale_log2 = p->softmax_scale * kLog2e;
   const long long rows = (long long)p->num_pages * p->page_size;
   *tma = slice_tma_page(p->page_size) && rows > 0 && rows < (1ll << 31);
   while ((1 << dp->log2_page) < p->page_size) ++dp->log2_page;
   if (!*tma) return ATTN_SINK_OK;
   const int box = std::min(p->page_size, kSliceKeys);
-  // No more than a head's 128 bytes into L2: with pages of its own for each head, its
+  // With pages of its own for each head no more than its 128 bytes into L2: its
   // neighbour's are not wanted (64 sequences x 2048 keys read 375 MB of 269 and took 67
   // us, not 55, where L2 fetched 256 bytes)
-  constexpr CUtensorMapL2promotion kOneHead = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  const CUtensorMapL2promotion promotion =
+      own_pages ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   int st;
   if ((st = encode_rows(&dp->tm_k, k_cache, rows, p->heads_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        box, 1, kOneHead)) != ATTN_SINK_OK)
+                        box, 1, promotion)) != ATTN_SINK_OK)
     return st;
   return encode_rows(&dp->tm_v, v_cache, rows, p->heads_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     box, 1, kOneHead);
+                     box, 1, promotion);
 }
 
 template <bool kShared>
@@ -313,7 +315,7 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
   SliceParams dp;
   bool dec_tma;
   if ((st = decode_params(params, L.own, q, k_cache, v_cache, block_table, seq_lens, sink, out,
-                          lse, ws, err, &dp, &dec_tma)) != ATTN_SINK_OK)
+                          lse, ws, err, false, &dp, &dec_tma)) != ATTN_SINK_OK)
     return st;
   dp.cu_groups = cu_groups;
   dp.prefix_lens = prefix_lens;
@@ -375,7 +377,7 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
   const dim3 grid(L.own.splits, params->heads_kv, params->batch);
   return launch_dependent(slice_kernel<true>(ep.group, dec_tma), grid, kSliceThreads,
                           kSliceSmem, s, dp) &&
-                 (L.own.splits == 1 || launch_join<true>(dp, s))
+                 (dp.whole || launch_join<true>(dp, s))
              ? ATTN_SINK_OK
              : ATTN_SINK_ERR_CUDA;
 }
@@ -531,7 +533,7 @@ int attn_sink_decode_pages(const attn_sink_pages_params* params, const void* q,
   SliceParams dp;
   bool tma;
   if ((st = decode_params(params, L, q, k_cache, v_cache, block_table, seq_lens, sink, out, lse,
-                          static_cast<uint8_t*>(workspace), err, &dp, &tma)) != ATTN_SINK_OK)
+                          static_cast<uint8_t*>(workspace), err, true, &dp, &tma)) != ATTN_SINK_OK)
     return st;
   dp.selected = selected;
   dp.count = params->count;

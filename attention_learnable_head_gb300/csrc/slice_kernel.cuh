@@ -67,6 +67,7 @@ struct SliceParams {
   int batch, heads_q, heads_kv;
   int page_size, num_pages, max_pages, count, num_groups;
   int splits;
+  int whole;                      // a single slice, joined where it is computed
   int log2_page;                  // TMA path: log2(page_size)
   float scale_log2;               // softmax_scale * log2(e)
 };
@@ -81,19 +82,26 @@ __device__ __forceinline__ int slice_seq_len(const int* seq_lens, int b, int cap
   return max(0, min(__ldg(seq_lens + b), cap));
 }
 
-// The last p in [0, groups] with cu[p] <= b; every lane of the warp gets it.
-__device__ __forceinline__ int shared_find(const int* cu, int groups, int b) {
+// The group of sequence b among [cu[p], cu[p + 1]), p < groups: p (groups: none), and its
+// bounds; by a whole warp, of which every lane gets the answer.
+struct SharedGroup {
+  int at, first, end;
+};
+__device__ __forceinline__ SharedGroup shared_find(const int* cu, int groups, int b) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, span = groups + 1;             // the answer lies in [lo, lo + span)
-  while (span > 1) {
-    const int step = (span + 31) / 32;
-    const int at = lo + lane * step;
-    const bool le = lane * step < span && (lane == 0 || __ldg(cu + at) <= b);
-    const int i = 31 - __clz(__ballot_sync(0xffffffffu, le));
+  int lo = 0, span = groups + 1;             // the last p with cu[p] <= b is in [lo, lo + span)
+  while (true) {
+    const int step = (span + 30) / 31;       // 31 places, and one behind
+    const int at = min(lo + lane * step, groups);
+    const int v = __ldg(cu + at);
+    const int i = max(0, 31 - __clz(__ballot_sync(0xffffffffu, lane * step < span && v <= b)));
+    if (step == 1) {
+      const int first = __shfl_sync(0xffffffffu, v, i), end = __shfl_sync(0xffffffffu, v, i + 1);
+      return SharedGroup{lo + i, first, lo + i < groups ? end : first};
+    }
     lo += i * step;
     span = min(step, span - i * step);
   }
-  return lo;
 }
 
 // Keys that the group of sequence b reads together (see attn_sink_shared_plan_kernel);
@@ -101,13 +109,9 @@ __device__ __forceinline__ int shared_find(const int* cu, int groups, int b) {
 __device__ __forceinline__ int shared_prefix(const SliceParams& p, int b, int cap) {
   __shared__ int s_min[kSliceWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int at = shared_find(p.cu_groups, p.num_groups, b);
-  int c0 = 0, c1 = 0, keys = 0;
-  if (at < p.num_groups) {
-    c0 = max(0, __ldg(p.cu_groups + at));
-    c1 = min(p.batch, __ldg(p.cu_groups + at + 1));
-    keys = __ldg(p.prefix_lens + at);
-  }
+  const SharedGroup group = shared_find(p.cu_groups, p.num_groups, b);
+  const int c0 = max(0, group.first), c1 = min(p.batch, group.end);
+  const int keys = group.at < p.num_groups ? __ldg(p.prefix_lens + group.at) : 0;
   int least = INT_MAX;
   for (int i = c0 + (int)threadIdx.x; i < c1; i += kSliceThreads)
     least = min(least, slice_seq_len(p.seq_lens, i, cap));
@@ -161,7 +165,7 @@ attn_sink_slice_kernel(const __grid_constant__ SliceParams p) {
   auto leave = [&] {
     if (kShared && split == 0 && g == 0 && b == 0) grid_dependency_wait();
   };
-  if (blocks == 0 && p.splits > 1) {                        // an empty slice
+  if (blocks == 0 && !p.whole) {                            // an empty slice
     if (tid < G)
       p.slice_ml[((size_t)b * p.heads_q + g * G + tid) * p.splits + split] =
           make_float2(-INFINITY, 0.0f);
@@ -408,7 +412,7 @@ attn_sink_slice_kernel(const __grid_constant__ SliceParams p) {
   // thread t: head t / 16, dims 4 (t % 16) .. + 4
   const int h = tid >> 4;
   const int d0 = 4 * (tid & 15);
-  const bool whole = p.splits == 1;                         // then all is joined here
+  const bool whole = p.whole != 0;
   if (kShared && whole) grid_dependency_wait();             // the prefix
   if (h < G) {
     float mm = -INFINITY;
