@@ -359,11 +359,19 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   const float* scores = p.scores + row * p.max_pages + p.keep_first;
   const bool staged = n <= kSelectStage;
   uint32_t least = 0xFFFFFFFFu, largest = 0;
-  for (int i = tid; i < n; i += kThreads) {
-    const uint32_t v = ordered(__ldcg(scores + i));
-    least = min(least, v);
-    largest = max(largest, v);
-    if (staged) s_score[i] = v;
+  for (int i0 = tid; i0 < n; i0 += 8 * kThreads) {
+    float x[8];                                             // on their way together
+    #pragma unroll
+    for (int u = 0; u < 8; ++u)
+      x[u] = i0 + u * kThreads < n ? __ldcg(scores + i0 + u * kThreads) : 0.0f;
+    #pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (i0 + u * kThreads >= n) break;
+      const uint32_t v = ordered(x[u]);
+      least = min(least, v);
+      largest = max(largest, v);
+      if (staged) s_score[i0 + u * kThreads] = v;
+    }
   }
   unsigned peak = 0;
   for (int i = tid; i < (have + 15) / 16; i += kThreads)
@@ -374,7 +382,14 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   int turn = 0;
   const uint32_t low = block_nth<kThreads>(
       need, least, largest, [&](auto&& take) {
-        for (int i = tid; i < n; i += kThreads) take(at(i));
+        for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+          uint32_t v[4];
+          #pragma unroll
+          for (int u = 0; u < 4; ++u) v[u] = i0 + u * kThreads < n ? at(i0 + u * kThreads) : 0u;
+          #pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (i0 + u * kThreads < n) take(v[u]);
+        }
       }, &s_nth, &turn).value;             // the smallest score that is taken
   // No score is further off than the rounding of its sums: 8 products of 16 terms, each
   // sum cut below 2^-23 of what the terms' sizes add up to at most.

@@ -200,6 +200,8 @@ constexpr int kMassFewRows = 32;
 int row_threads(int row) { return row <= 2048 ? 256 : row <= 8192 ? 512 : 1024; }
 
 // ----------------------------------------------------------------------------- eviction
+// Shared memory up to which a row's moves are listed there: four CTAs of 512 threads an SM.
+constexpr size_t kEvictLists = 40 * 1024;
 struct EvictLayout {
   int max_moves;
   size_t off_moves, off_from, total;
@@ -677,9 +679,12 @@ int attn_sink_evict(const attn_sink_evict_params* params, void* k_cache, void* v
   ep.max_moves = L.max_moves;
   ep.stage = std::min(params->max_keys, kEvictStage);
   const unsigned rows = (unsigned)params->batch * (unsigned)params->heads_kv;
-  const size_t smem = 4 * (size_t)std::max(ep.stage, 1);
+  const size_t lists = 8 * (size_t)L.max_moves;
+  size_t smem = 4 * (size_t)std::max(ep.stage, 1);
   const int threads = row_threads(params->max_keys);
   ep.here = rows >= (unsigned)sms;         // enough CTAs to move the rows themselves
+  ep.lists = ep.here && smem + lists <= kEvictLists;
+  if (ep.lists) smem += lists;
   evict_kernel(threads)<<<rows + 1, threads, smem, s>>>(ep);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
   if (ep.here) return ATTN_SINK_OK;

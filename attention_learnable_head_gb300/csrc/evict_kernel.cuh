@@ -3,9 +3,9 @@
 // One CTA for each (sequence, kv head) finds the weight of the last key that stays
 // (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th kept key at or behind the budget goes to the n-th hole below it.  Only as many rows
 // move as there are holes, and no row is both read and written, so that they can be copied
-// in any order, 16 lanes a move (8 for the key, 8 for the value): by the same CTA where
-// there are enough of them to fill the GPU, by a second kernel where there are few.  One
-// more CTA of the first kernel scans the sequences for the pages that become free.
+// in any order, 8 lanes a move: by the same CTA where there are enough of them to fill
+// the GPU, by a second kernel where there are few.  One more CTA of the first kernel scans
+// the sequences for the pages that become free.
 #pragma once
 #include <climits>
 #include <cuda_bf16.h>
@@ -32,10 +32,13 @@ struct EvictParams {
   int* from;                      // [B][H_kv][max_moves] keys that move there, from the last
   int* err;
   int batch, heads_kv, page_size, num_pages, max_pages, max_keys;
-  int budget, keep_first, keep_last, max_freed, max_moves, stage, here;   // here: one kernel
+  int budget, keep_first, keep_last, max_freed, max_moves, stage;
+  int here;                       // one kernel: the CTA of a row moves it
+  int lists;                      // the moves are listed in shared memory, behind the weights
 };
 
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+constexpr uint32_t kStays = 0xFFFFFFFFu;   // in the place of a weight: no competition
 
 __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool* bad) {
   const int len = __ldg(p.seq_lens + b), cap = min(p.max_pages * p.page_size, p.max_keys);
@@ -43,14 +46,11 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool* bad)
   return max(0, min(len, cap));
 }
 
-// The moves first, first + step, .. of row (b, h), by 16 lanes each.
-__device__ __forceinline__ void evict_move(const EvictParams& p, int b, int h, int moves, int first,
-                                           int step) {
-  const int lane16 = threadIdx.x & 15, c = lane16 & 7;
-  uint4* cache = (lane16 < 8 ? p.k_cache : p.v_cache) + h * 8 + c;
-  const size_t row = (size_t)b * p.heads_kv + h;
-  const int* to = p.to + row * p.max_moves;
-  const int* from = p.from + row * p.max_moves;
+// The moves first, first + step, .. of sequence b and kv head h, by 8 lanes each; `from` is
+// listed from the last.
+__device__ __forceinline__ void evict_move(const EvictParams& p, int b, int h, const int* to,
+                                           const int* from, int moves, int first, int step) {
+  const int c = threadIdx.x & 7;
   const int* table = p.block_table + (size_t)b * p.max_pages;
   auto cache_row = [&](int j) {
     const int pg = j / p.page_size, e = __ldg(table + pg);
@@ -58,31 +58,37 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int b, int h, i
                ? (uint32_t)e * (uint32_t)p.page_size + (uint32_t)(j - pg * p.page_size)
                : kNoRow;
   };
-  constexpr int kAtOnce = 4;
+  constexpr int kAtOnce = 4;               // chains of four loads
   for (int i = first; i < moves; i += kAtOnce * step) {
-    int a[kAtOnce], z[kAtOnce];
     uint32_t src[kAtOnce], dst[kAtOnce];
-    uint4 v[kAtOnce];
     #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int m = i + u * step;
-      a[u] = m < moves ? __ldcg(from + moves - 1 - m) : -1;
-      z[u] = m < moves ? __ldcg(to + m) : -1;
+      src[u] = dst[u] = kNoRow;
+      if (m < moves) {
+        src[u] = cache_row(from[moves - 1 - m]);
+        dst[u] = cache_row(to[m]);
+        if (src[u] == kNoRow || dst[u] == kNoRow) {
+          atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
+          src[u] = kNoRow;
+        }
+      }
     }
-    #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      src[u] = a[u] >= 0 ? cache_row(a[u]) : kNoRow;
-      dst[u] = a[u] >= 0 ? cache_row(z[u]) : kNoRow;
-      if (a[u] >= 0 && lane16 == 0 && (src[u] == kNoRow || dst[u] == kNoRow))
-        atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
-      if (dst[u] == kNoRow) src[u] = kNoRow;
-    }
+    uint4 k[kAtOnce], v[kAtOnce];
     #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
-      if (src[u] != kNoRow) v[u] = __ldcg(cache + (size_t)src[u] * p.heads_kv * 8);
+      if (src[u] != kNoRow) {
+        const size_t at = ((size_t)src[u] * p.heads_kv + h) * 8 + c;
+        k[u] = __ldcg(p.k_cache + at);
+        v[u] = __ldcg(p.v_cache + at);
+      }
     #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
-      if (src[u] != kNoRow) cache[(size_t)dst[u] * p.heads_kv * 8] = v[u];
+      if (src[u] != kNoRow) {
+        const size_t at = ((size_t)dst[u] * p.heads_kv + h) * 8 + c;
+        p.k_cache[at] = k[u];
+        p.v_cache[at] = v[u];
+      }
   }
 }
 
@@ -154,37 +160,55 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
   const int lo = p.keep_first, hi = len - p.keep_last;      // the keys that compete
   const int need = p.budget - p.keep_first - p.keep_last;   // < hi - lo
   uint32_t least = 0xFFFFFFFFu, largest = 0;
-  for (int j = tid; j < p.max_keys; j += kThreads) {
-    const float m = j < len ? __ldg(mass + j) : 0.0f;
-    mass_out[j] = j < fewer ? m : 0.0f;
-    if (j >= len) continue;
-    const uint32_t v = ordered(m);
-    if (staged) s_mass[j] = v;
-    if (j >= lo && j < hi) {
-      least = min(least, v);
-      largest = max(largest, v);
+  for (int j0 = tid; j0 < p.max_keys; j0 += 8 * kThreads) {
+    float m[8];                            // on their way together
+    #pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u * kThreads;
+      m[u] = j < len ? __ldg(mass + j) : 0.0f;
+    }
+    #pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u * kThreads;
+      if (j < p.max_keys) mass_out[j] = j < fewer ? m[u] : 0.0f;
+      if (j >= len) continue;
+      const bool competes = j >= lo && j < hi;
+      const uint32_t v = competes ? ordered(m[u]) : kStays;
+      if (staged) s_mass[j] = v;
+      if (competes) {
+        least = min(least, v);
+        largest = max(largest, v);
+      }
     }
   }
-  auto at = [&](int j) { return staged ? s_mass[j] : ordered(__ldg(mass + j)); };
+  auto at = [&](int j) {
+    return staged ? s_mass[j] : j >= lo && j < hi ? ordered(__ldg(mass + j)) : kStays;
+  };
   int turn = 0, ties = 0;                                   // some of the equal ones stay
-  uint32_t bound = 0;
-  bool whole = true;                                        // or all of them
+  uint32_t bound = 0, cut = kStays;                         // from `cut` on all stay
   if (need > 0) {
     // a thread reads what it stored itself: j = tid modulo kThreads
     const Nth nth = block_nth<kThreads>(
         need, least, largest, [&](auto&& take) {
-          for (int j = tid; j < hi; j += kThreads)
-            if (j >= lo) take(at(j));
+          for (int j0 = tid; j0 < hi; j0 += 4 * kThreads) {
+            uint32_t v[4];
+            #pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = j0 + u * kThreads < hi ? at(j0 + u * kThreads) : kStays;
+            #pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (v[u] != kStays) take(v[u]);
+          }
         }, &s_nth, &turn);
     bound = nth.value;
-    whole = need - nth.above == nth.same;
-    if (!whole) ties = need - nth.above;
+    if (need - nth.above < nth.same) ties = need - nth.above;
+    cut = ties > 0 ? bound + 1 : bound;
   }
   // Bitmaps of 32 kThreads keys at a time, a word a thread.  With s kept keys in front of j,
   // a hole at j is number j - s, and a kept key at j >= budget is number budget - 1 - s
   // from the last.
-  int* to = p.to + row * p.max_moves;
-  int* come = p.from + row * p.max_moves;
+  int* const lists = reinterpret_cast<int*>(s_mass + p.stage);
+  int* const to = p.lists ? lists : p.to + row * p.max_moves;
+  int* const come = p.lists ? lists + p.max_moves : p.from + row * p.max_moves;
   int stay = 0, holes = 0;
   for (int base = 0; base < len; base += 32 * kThreads) {
     __syncthreads();                                        // the last round's words are read
@@ -192,14 +216,12 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
     if (tid >= words) s_kept[tid] = s_tie[tid] = 0;
     for (int w = tid >> 5; w < words; w += kThreads / 32) {
       const int j = base + 32 * w + lane;
-      const uint32_t v = j < len ? at(j) : 0;
-      const bool inner = j >= lo && j < hi;
-      const bool chosen = need > 0 && (v > bound || (whole && v == bound));
-      const uint32_t k = __ballot_sync(0xffffffffu, j < len && (!inner || chosen));
-      const uint32_t e = __ballot_sync(0xffffffffu, inner && !whole && v == bound);
-      if (lane == 0) {
-        s_kept[w] = k;
-        s_tie[w] = e;
+      const uint32_t v = j < len ? at(j) : 0;               // 0: no value
+      const uint32_t k = __ballot_sync(0xffffffffu, v >= cut);
+      if (lane == 0) s_kept[w] = k;
+      if (ties > 0) {                                       // the same for the whole CTA
+        const uint32_t e = __ballot_sync(0xffffffffu, v == bound);
+        if (lane == 0) s_tie[w] = e;
       }
     }
     __syncthreads();
@@ -239,9 +261,9 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
   __syncthreads();                                          // the moves are listed
   holes = fewer > 0 ? s_list[0] : 0;
   for (int i = tid; i < holes; i += kThreads)
-    mass_out[__ldcg(to + i)] = __ldg(mass + __ldcg(come + holes - 1 - i));
+    mass_out[to[i]] = __ldg(mass + come[holes - 1 - i]);
   if (p.here)
-    evict_move(p, b, (int)(row - (size_t)b * p.heads_kv), holes, tid >> 4, kThreads / 16);
+    evict_move(p, b, (int)(row - (size_t)b * p.heads_kv), to, come, holes, tid >> 3, kThreads / 8);
   else if (tid == 0)
     p.counts[row] = holes;
 }
@@ -252,9 +274,10 @@ attn_sink_evict_move_kernel(const __grid_constant__ EvictParams p) {
   const size_t rows = (size_t)p.batch * p.heads_kv;
   for (size_t row = blockIdx.y; row < rows; row += gridDim.y) {
     const int b = (int)(row / (unsigned)p.heads_kv);
-    evict_move(p, b, (int)(row - (size_t)b * p.heads_kv), __ldcg(p.counts + row),
-               blockIdx.x * (kMoveThreads / 16) + (threadIdx.x >> 4),
-               gridDim.x * (kMoveThreads / 16));
+    evict_move(p, b, (int)(row - (size_t)b * p.heads_kv), p.to + row * p.max_moves,
+               p.from + row * p.max_moves, __ldcg(p.counts + row),
+               blockIdx.x * (kMoveThreads / 8) + (threadIdx.x >> 3),
+               gridDim.x * (kMoveThreads / 8));
   }
   // no page behind the freed ones
   const unsigned tid = (blockIdx.y * gridDim.x + blockIdx.x) * kMoveThreads + threadIdx.x;

@@ -1,5 +1,5 @@
 // The n-th largest of a row of values by one CTA.  Values are mapped to unsigned
-// integers of the same order first (a NaN counts as the largest).  A histogram of
+// integers of the same order first (a NaN counts as the largest; 0xFFFFFFFF is free).  A histogram of
 // their range, as it is, says which bin the n-th is in; a bin of few values is ranked
 // value by value, one of many has a histogram of its own.  Floats as integers are about
 // their logarithms, so that attention weights spread over the bins and few additions
@@ -12,7 +12,7 @@ namespace attn_sink {
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);   // -0 equals 0
-  if (x != x) return 0xFFFFFFFFu;
+  if (x != x) return 0xFFFFFFFEu;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
