@@ -311,8 +311,7 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ unsigned long long s_key[kSelectBand];
   __shared__ int s_at[kSelectBand];
   __shared__ uint8_t s_take[kSelectBand];
-  __shared__ int s_side[2];
-  __shared__ int s_many;
+  __shared__ int s_many, s_side;   // pages at the border, and above it
   __shared__ unsigned s_peak[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int b = (int)(blockIdx.x / (unsigned)p.heads_kv);
@@ -353,7 +352,7 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   norm += __shfl_xor_sync(0xffffffffu, norm, 2);
   norm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(norm) & 0x7fffffffu));
   if (tid == 0) {
-    s_many = s_side[0] = s_side[1] = 0;
+    s_many = s_side = 0;
   }
   grid_dependency_wait();                                   // the scores
   const float* scores = p.scores + row * p.max_pages + p.keep_first;
@@ -405,46 +404,49 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     from = ordered(__fsub_rd(last, off));
     upto = ordered(__fadd_ru(last, off));
   }
-  int sure = 0, border = 0;
-  for (int i = tid; i < n; i += kThreads) {
-    const uint32_t v = at(i);
-    sure += v > upto;
-    border += v >= from && v <= upto;
+  int sure = 0;
+  for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+    uint32_t v[4];
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i0 + u * kThreads < n ? at(i0 + u * kThreads) : 0u;
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      sure += v[u] > upto;
+      if (v[u] < from || v[u] > upto || i0 + u * kThreads >= n) continue;
+      const int x = atomicAdd(&s_many, 1);                  // their order does not matter
+      if (x < kSelectBand) s_at[x] = i0 + u * kThreads;
+    }
   }
   sure = __reduce_add_sync(0xffffffffu, sure);
-  border = __reduce_add_sync(0xffffffffu, border);
-  if (lane == 0 && sure != 0) atomicAdd(&s_side[0], sure);  // whole numbers: any order
-  if (lane == 0 && border != 0) atomicAdd(&s_side[1], border);
+  if (lane == 0 && sure != 0) atomicAdd(&s_side, sure);     // whole numbers: any order
   __syncthreads();
-  sure = s_side[0];
-  border = s_side[1];
-  const int left = need - sure;                             // of the border, <= border
+  const int left = need - s_side, border = s_many;          // of the border, left <= border
   // which of the border: all, by their ranks in shared memory, or by a 64-bit bound
-  const bool again = left < border && (off > 0.0f || !(most < 1e37f));
+  const bool every = left == border;
+  const bool again = !every && (off > 0.0f || !(most < 1e37f));
   const bool ranked = again && border <= kSelectBand;
   const unsigned long long* exact = p.exact + row * p.max_pages;
   unsigned long long bound64 = 0;
   if (again) {
-    for (int i0 = tid - lane; i0 < n; i0 += kThreads) {
-      const int i = i0 + lane;
-      const uint32_t v = i < n ? at(i) : 0;
-      unsigned todo = __ballot_sync(0xffffffffu, i < n && v >= from && v <= upto);
-      while (todo != 0) {
-        const int j = i0 + __ffs(todo) - 1;
-        todo &= todo - 1;
-        const unsigned long long key = most < 1e37f
-                                           ? page_score_exact<false>(p, b, h, p.keep_first + j)
-                                           : page_score_exact<true>(p, b, h, p.keep_first + j);
-        if (lane != 0) continue;
-        if (ranked) {
-          const int x = atomicAdd(&s_many, 1);              // their order does not matter
-          s_key[x] = key;
-          s_at[x] = j;
-        } else {
-          p.exact[row * p.max_pages + j] = key;
+    auto score = [&](int i) {
+      return most < 1e37f ? page_score_exact<false>(p, b, h, p.keep_first + i)
+                          : page_score_exact<true>(p, b, h, p.keep_first + i);
+    };
+    if (ranked) {
+      for (int x = tid >> 5; x < border; x += kThreads / 32) {
+        const unsigned long long key = score(s_at[x]);
+        if (lane == 0) s_key[x] = key;
+      }
+    } else {
+      for (int i0 = tid - lane; i0 < n; i0 += kThreads) {
+        const uint32_t v = i0 + lane < n ? at(i0 + lane) : 0;
+        unsigned todo = __ballot_sync(0xffffffffu, i0 + lane < n && v >= from && v <= upto);
+        for (; todo != 0; todo &= todo - 1) {
+          const int i = i0 + __ffs(todo) - 1;
+          const unsigned long long key = score(i);
+          if (lane == 0) p.exact[row * p.max_pages + i] = key;
         }
       }
-      __syncwarp();
     }
     __syncthreads();
     if (ranked) {
@@ -476,7 +478,7 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     }
     ties = left - block_sum<kThreads>(above, s_nth.sum, &turn);
   }
-  if (left == border) ties = 0;
+  if (every) ties = 0;
   int done = p.keep_first;
   for (int base = 0; base < n; base += 32 * kThreads) {
     __syncthreads();                                        // the last round's words are read
@@ -484,13 +486,10 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
     if (tid >= words) s_sure[tid] = s_tie[tid] = 0;
     for (int w = tid >> 5; w < words; w += kThreads / 32) {
       const int i = base + 32 * w + lane;
-      const uint32_t v = i < n ? at(i) : 0;
-      bool take = i < n && v > upto, tie = false;
-      const bool edge = i < n && v >= from && v <= upto;
-      if (__any_sync(0xffffffffu, edge) && edge) {          // few: of whom some may be taken
-        if (left == border) {
-          take = true;
-        } else if (!again) {
+      const uint32_t v = i < n ? at(i) : 0;                 // 0: no score
+      bool take = v > upto || (every && v >= from && i < n), tie = false;
+      if (!every && i < n && v >= from && v <= upto) {      // few: of whom some may be taken
+        if (!again) {
           tie = true;                                       // the first ones of equals
         } else if (ranked) {
           int x = 0;

@@ -243,6 +243,10 @@ def test_select_pages_long_rows():
     """A row that does not fit shared memory, against the definition on all pages at once."""
     c = Paged(32, [20011, 13000], hq=8, hkv=1, page=1)
     select_both(c, c.q(), random_bounds(c), 4000, 1, 1)
+    c = Paged(37, [40000], hq=1, hkv=1, page=1)               # more than a bitmap's pages, too
+    select_both(c, c.q(), random_bounds(c), 9000, 1, 1)
+    b = random_bounds(c)[:3].repeat(c.pages // 3 + 1, 1, 1, 1)[:c.pages].contiguous()
+    select_both(c, c.q(), b, 9000, 1, 1)
 
 
 @pytest.mark.parametrize("page", [1, 16])
