@@ -100,7 +100,7 @@ attn_sink_page_bounds_kernel(const __grid_constant__ BoundsParams p) {
 
 // ----------------------------------------------------------------------------- scores
 constexpr int kScoreThreads = 256;
-constexpr int kScoreStages = 3;         // groups of 16 pages on their way to a warp
+constexpr int kScoreStages = 2;         // groups of 16 pages on their way to a warp
 constexpr int kScoreSmem = kScoreThreads / 32 * kScoreStages * 16 * 256;
 
 struct SelectParams {
@@ -123,7 +123,7 @@ __device__ __forceinline__ int select_len(const SelectParams& p, int b, bool* ba
   return max(0, min(len, cap));
 }
 
-__global__ void __launch_bounds__(kScoreThreads)
+__global__ void __launch_bounds__(kScoreThreads, 3)
 attn_sink_page_scores_kernel(const __grid_constant__ SelectParams p) {
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

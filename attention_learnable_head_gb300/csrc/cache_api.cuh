@@ -589,9 +589,11 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
   mp.max_keys = params->max_keys;
   mp.accumulate = params->accumulate;
   mp.scale_log2 = params->softmax_scale * kLog2e;
+  mp.inv_scale = 1.0f / params->softmax_scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = (long long)params->total_q * mp.group;
-  if (rows > (long long)kMassFewRows * params->batch && mp.group <= kMassMaxGroup) {
+  if (rows > (long long)kMassFewRows * params->batch && mp.group <= kMassMaxGroup &&
+      params->softmax_scale >= kMassLeastScale && params->softmax_scale <= kMassMostScale) {
     mp.tokens = kMassRows / mp.group;
     if ((st = encode_rows(&mp.tm_q, q, params->total_q, params->heads_q,
                           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mp.tokens, mp.group)) != ATTN_SINK_OK)
@@ -600,12 +602,13 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
     attn_sink_key_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, s>>>(mp);
     return launched() ? ATTN_SINK_OK : ATTN_SINK_ERR_CUDA;
   }
-  // a warp for each (32 keys, kv head), up to three rounds of the CTAs that fit at once
+  // a warp for each (32 keys, kv head), up to two rounds of the CTAs that fit at once (32 x 8192
+  // keys: one 43.6 us, two 42.6, three 44.2)
   constexpr int kWarps = kMassFewThreads / 32;
   const long long warps = (params->max_keys + 31ll) / 32 * params->heads_kv;
   const long long least = (params->heads_kv + kWarps - 1) / kWarps;      // a warp a head
   const long long x = std::max(least, std::min((warps + kWarps - 1) / kWarps,
-                                               6ll * sms / params->batch));
+                                               4ll * sms / params->batch));
   const dim3 grid((unsigned)x, params->batch);
   if (rows <= 8ll * params->batch)
     attn_sink_key_mass_few_kernel<1><<<grid, kMassFewThreads, kMassFewSmem, s>>>(mp);

@@ -15,11 +15,13 @@
 // fragments are whole 16-byte chunks (chunks t and 4 + t for lane t of four): keys go from
 // their pages straight into registers.
 //
-// Many rows (prompts): an exponential a score bounds it, and next to it shared memory.  A
-// CTA holds 256 keys in TMEM, as the A operands of two products (from shared memory they
-// would be read again for every tile), and q passes by in tiles of 96 rows through a TMA
-// ring.  A thread has two keys and 16 rows of a half tile: the rows' lse, the same for all
-// threads, comes from shared memory once for both.
+// Many rows (prompts): an exponential a score bounds it.  A CTA holds 256 keys in TMEM, as the
+// A operands of two products (from shared memory they would be read again for every tile),
+// and q passes by in tiles of 96 rows through a TMA ring.  The rows' lse is part of the
+// product: 16 more terms, of which three are ones on the keys' side and -(lse - c) /
+// softmax_scale in three bf16 (24 bits) on the rows', with c a constant of the tile, so that
+// a thread, with two keys and 32 of the rows, has one fma and one exponential for each
+// score and reads nothing but TMEM.
 #pragma once
 #include <cuda_bf16.h>
 #include "fwd_kernel.cuh"
@@ -38,7 +40,7 @@ struct MassParams {
   int* err;
   int batch, total_q, heads_q, heads_kv, group, tokens;
   int page_size, num_pages, max_pages, max_keys, accumulate;
-  float scale_log2;
+  float scale_log2, inv_scale;    // softmax_scale log2(e), 1 / softmax_scale
 };
 
 // A sequence: its new tokens [q0, q0 + n) of q, its keys, and those with an entry.
@@ -252,7 +254,7 @@ attn_sink_key_mass_few_kernel(const __grid_constant__ MassParams p) {
 }
 
 // ----------------------------------------------------------------------------- many rows
-constexpr int kMassKeys = 256;           // of a CTA: two for each TMEM lane
+constexpr int kMassKeys = 256;           // of a CTA: two products of 128
 constexpr int kMassRows = 96;            // of a tile of q
 constexpr int kMassMaxGroup = kMassRows;
 constexpr int kMassWarps = 12;           // of weights
@@ -261,10 +263,26 @@ constexpr int kMassMmaWarp = 13;
 constexpr int kMassThreads = 32 * 14;
 constexpr int kMassStages = 4;
 constexpr uint32_t kMassTileBytes = kMassRows * 128;
-constexpr int kMassHalf = kMassRows / 2; // of a product
-constexpr uint32_t kMassTmemCols = 256;  // keys: 2 x 32 columns of bf16 pairs, scores: 4 x 48
+constexpr uint32_t kMassLseBytes = kMassRows * 32;    // of a stage: 16 bf16 a row
+constexpr uint32_t kMassOneBytes = kBlockM * 32;      // the keys' side
+constexpr uint32_t kMassTmemCols = 256;  // keys: 2 x 32 columns of bf16 pairs, scores: 2 x 96
 constexpr uint32_t kMassColS = 64;
-constexpr int kMassSmemBytes = 1024 + (int)kMassTileBytes * kMassStages;
+constexpr int kMassSmemBytes =
+    1024 + (int)((kMassTileBytes + kMassLseBytes) * kMassStages + kMassOneBytes);
+// softmax_scale for which (lse - c) / softmax_scale is an ordinary number
+constexpr float kMassLeastScale = 0x1p-10f, kMassMostScale = 0x1p10f;
+
+// Byte offset of 16-byte chunk c (0, 1) of row r of the 16 more terms: core matrices of 8 rows
+// x 16 bytes, the two of 8 rows next to each other.
+__device__ __forceinline__ uint32_t mass_more_at(int r, int c) {
+  return (uint32_t)(r >> 3) * 256u + (uint32_t)c * 128u + (uint32_t)(r & 7) * 16u;
+}
+// Its descriptor: no swizzle, 128 bytes from core matrix to core matrix along the terms, 256
+// along the rows.
+__device__ __forceinline__ uint64_t mass_more_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 |
+         (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46;
+}
 
 // mbar_wait_warp for the inner loop, where it mostly need not wait: what follows a first
 // try is a call.
@@ -283,8 +301,8 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full[kMassStages], q_empty[kMassStages];
   __shared__ __align__(8) uint64_t s_full[2], s_empty[2], mma_drained;
-  __shared__ __align__(16) float s_z[kMassStages][kMassRows];   // -lse log2(e); -inf: no row
   __shared__ __align__(16) int s_at[kMassStages][kMassRows];    // last key the row sees; -1: none
+  __shared__ float s_base[kMassStages];    // -c log2(e) of the tile
   __shared__ int s_clear[kMassStages];     // no weight of the tile is masked
   __shared__ float s_part[2][kMassKeys];
   __shared__ uint8_t s_has[kMassKeys];
@@ -308,6 +326,8 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   }
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
+  uint8_t* sLse = sQ + kMassStages * kMassTileBytes;
+  uint8_t* sOne = sLse + kMassStages * kMassLseBytes;
   const int rows = p.tokens * p.group;     // of a tile; behind them zeros, with no weight
   // a thread's key goes from its page into TMEM
   const int c = warp >> 2, r = tid & 127;
@@ -334,7 +354,7 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
     abort_flag = 0;
     for (int i = 0; i < kMassStages; ++i) {
       mbar_init(&q_full[i], 2);            // the copy, and the rows' lse
-      mbar_init(&q_empty[i], 1 + kMassWarps);   // the product, and the warps that read the lse
+      mbar_init(&q_empty[i], 1 + kMassWarps);   // the product, and the warps that read the tile's
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -347,10 +367,17 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
     tmem_alloc(&tmem_base_sh, kMassTmemCols);
     tmem_relinquish();
   }
-  // the rows of a tile that no copy writes
+  // the rows of a tile that no copy writes; three ones for each key, and zeros
   for (int x = rows * 8 + tid; x < kMassRows * 8; x += kMassThreads)
     for (int i = 0; i < kMassStages; ++i)
       st_shared_v4(smem_u32(sQ + i * kMassTileBytes) + (uint32_t)x * 16u, 0, 0, 0, 0);
+  for (int x = tid; x < kMassRows * kMassStages; x += kMassThreads)
+    st_shared_v4(smem_u32(sLse + (x / kMassRows) * kMassLseBytes) + mass_more_at(x % kMassRows, 1), 0,
+                 0, 0, 0);
+  for (int x = tid; x < kBlockM; x += kMassThreads) {
+    st_shared_v4(smem_u32(sOne) + mass_more_at(x, 0), 0x3F803F80u, 0x00003F80u, 0, 0);
+    st_shared_v4(smem_u32(sOne) + mass_more_at(x, 1), 0, 0, 0, 0);
+  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -368,7 +395,7 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   if (warp == kMassCopyWarp) {
     // ---------------------------------------------------------------- q and its lse
     constexpr int kCols = kMassRows / 32;
-    int tok[kCols], hd[kCols];             // of columns lane, lane + 32, ..
+    int tok[kCols], hd[kCols];             // of rows lane, lane + 32, ..
     #pragma unroll
     for (int u = 0; u < kCols; ++u) {
       tok[u] = (lane + 32 * u) / p.group;
@@ -401,17 +428,30 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
         tma_load_3d(&p.tm_q, &q_full[st], sQ + st * kMassTileBytes, 0, h * p.group,
                     s.q0 + t0 + i * p.tokens);
       }
+      // c: the first row's lse, where it is a number
+      const float first = __shfl_sync(0xffffffffu, z[0], 0);
+      const float base = fabsf(first) < 1e30f ? first : 0.0f;
       bool clear = true;
       #pragma unroll
       for (int u = 0; u < kCols; ++u) {
         const int at = at0 + t0 + i * p.tokens + tok[u];
         const bool weight = !isinf(z[u]);
-        s_z[st][lane + 32 * u] = weight ? -z[u] * kLog2e : -INFINITY;
+        const float y = weight ? (base - z[u]) * p.inv_scale : -1e30f;
+        const uint32_t hi = pack_bf16x2(y, 0.0f) & 0xFFFFu;
+        const float y1 = y - bf16_lo(hi);
+        const uint32_t mid = pack_bf16x2(y1, 0.0f) & 0xFFFFu;
+        const uint32_t low = pack_bf16x2(y1 - bf16_lo(mid), 0.0f) & 0xFFFFu;
+        st_shared_v4(smem_u32(sLse + st * kMassLseBytes) + mass_more_at(lane + 32 * u, 0),
+                     hi | mid << 16, weight ? low : 0u, 0, 0);
         s_at[st][lane + 32 * u] = weight ? at : -1;
         clear = clear && (tok[u] >= p.tokens || (weight && at >= last));
       }
       clear = __all_sync(0xffffffffu, clear);
-      if (lane == 0) s_clear[st] = clear;
+      if (lane == 0) {
+        s_clear[st] = clear;
+        s_base[st] = -base * kLog2e;
+      }
+      fence_proxy_async_smem();            // the product reads the lse
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[st]);
       fetch(i + kAhead, z);
@@ -436,25 +476,24 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   } else if (warp == kMassMmaWarp) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {
-      const uint32_t idesc = make_idesc_bf16(kBlockM, kMassHalf, false, false);
+      const uint32_t idesc = make_idesc_bf16(kBlockM, kMassRows, false, false);
       const uint64_t dQ = make_sdesc_sw128(smem_u32(sQ), 16, 1024);
-      constexpr uint32_t kTileU = kMassTileBytes >> 4;
+      const uint64_t dLse = mass_more_desc(smem_u32(sLse)), dOne = mass_more_desc(smem_u32(sOne));
       bool ok = true;
       for (int i = 0; ok && i < tiles; ++i) {
         const int st = i % kMassStages;
         ok = mbar_wait(&q_full[st], (i / kMassStages) & 1, &abort_flag);
         #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && (i < 1 || mbar_wait(&s_empty[half], (i & 1) ^ 1, &abort_flag));
+        for (int e = 0; e < 2; ++e) {
+          ok = ok && (i < 1 || mbar_wait(&s_empty[e], (i & 1) ^ 1, &abort_flag));
           if (!ok) break;
           tc_fence_after();
+          const uint32_t d = tmem + kMassColS + kMassRows * e;
           #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k)
-            #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              mma_ts(tmem + kMassColS + kMassHalf * (2 * half + e), tmem + 32 * e + 8 * k,
-                     dQ + st * kTileU + half * (kMassHalf * 128 >> 4) + 2 * k, idesc, k > 0);
-          mma_commit(&s_full[half]);
+            mma_ts(d, tmem + 32 * e + 8 * k, dQ + st * (kMassTileBytes >> 4) + 2 * k, idesc, k > 0);
+          mma_ss(d, dOne, dLse + st * (kMassLseBytes >> 4), idesc, 1);
+          mma_commit(&s_full[e]);
         }
         if (ok) mma_commit(&q_empty[st]);
       }
@@ -468,62 +507,50 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- weights
-    // warpgroup c has columns 16 c .. 16 c + 15 of every half tile; thread = TMEM lane = keys
-    // r and r + 128
-    const uint32_t tS = tmem + kMassColS + 16 * c + lane_base;
+    // warpgroup c has rows 32 c .. 32 c + 31 of every tile; thread = TMEM lane = keys r and
+    // r + 128
+    const uint32_t tS = tmem + kMassColS + 32 * c + lane_base;
     const uint64_t scale = f2(p.scale_log2, p.scale_log2);
     uint64_t sum[2][2] = {{f2(0.0f, 0.0f), f2(0.0f, 0.0f)}, {f2(0.0f, 0.0f), f2(0.0f, 0.0f)}};
-    const int last_cols = (s.n - t0 - (tiles - 1) * p.tokens) * p.group - 16 * c;
+    const int last_cols = (s.n - t0 - (tiles - 1) * p.tokens) * p.group - 32 * c;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
       const int st = i % kMassStages;
       ok = mass_wait(&q_full[st], (i / kMassStages) & 1, &abort_flag);
-      const int cols = i + 1 < tiles ? kMassRows : last_cols;
+      const bool some = i + 1 < tiles || last_cols > 0;     // a row with a token
       const bool clear = s_clear[st] != 0;
+      const uint64_t off = f2(s_base[st], s_base[st]);
       #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        ok = ok && mass_wait(&s_full[half], i & 1, &abort_flag);
+      for (int e = 0; e < 2; ++e) {
+        ok = ok && mass_wait(&s_full[e], i & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
-        uint32_t x[2][16];
-        tmem_ld_x16(tS + 2 * kMassHalf * half, x[0]);
-        tmem_ld_x16(tS + 2 * kMassHalf * half + kMassHalf, x[1]);
+        uint32_t x[32];
+        tmem_ld_x32(tS + kMassRows * e, x);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[half]);         // the next product may begin
-        if (cols <= kMassHalf * half) continue;             // the same for the whole warp
-        const float4* z4 = reinterpret_cast<const float4*>(&s_z[st][kMassHalf * half + 16 * c]);
+        if (lane == 0) mbar_arrive(&s_empty[e]);            // the next product may begin
+        if (!some) continue;                                // the same for the whole warp
         if (clear) {
           #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 z = z4[e >> 2];
-            #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint64_t v = ffma2(f2(__uint_as_float(x[k][e + 2 * u]),
-                                            __uint_as_float(x[k][e + 2 * u + 1])),
-                                         scale, u ? f2(z.z, z.w) : f2(z.x, z.y));
-                sum[k][u] = fadd2(sum[k][u], f2(ex2_approx(f2_lo(v)), ex2_approx(f2_hi(v))));
-              }
+          for (int k = 0; k < 32; k += 2) {
+            const uint64_t v =
+                ffma2(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale, off);
+            sum[e][(k >> 1) & 1] =
+                fadd2(sum[e][(k >> 1) & 1], f2(ex2_approx(f2_lo(v)), ex2_approx(f2_hi(v))));
           }
         } else {
-          const int4* at4 = reinterpret_cast<const int4*>(&s_at[st][kMassHalf * half + 16 * c]);
+          const int2* at2 = reinterpret_cast<const int2*>(&s_at[st][32 * c]);
+          const int j = j0 + 128 * e + r;
           #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 z = z4[e >> 2];
-            const int4 at = at4[e >> 2];
-            #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int j = j0 + 128 * k + r;
-              const float w0 = ex2_approx(fmaf(__uint_as_float(x[k][e]), p.scale_log2, z.x));
-              const float w1 = ex2_approx(fmaf(__uint_as_float(x[k][e + 1]), p.scale_log2, z.y));
-              const float w2 = ex2_approx(fmaf(__uint_as_float(x[k][e + 2]), p.scale_log2, z.z));
-              const float w3 = ex2_approx(fmaf(__uint_as_float(x[k][e + 3]), p.scale_log2, z.w));
-              sum[k][0] = fadd2(sum[k][0], f2(j <= at.x ? w0 : 0.0f, j <= at.y ? w1 : 0.0f));
-              sum[k][1] = fadd2(sum[k][1], f2(j <= at.z ? w2 : 0.0f, j <= at.w ? w3 : 0.0f));
-            }
+          for (int k = 0; k < 32; k += 2) {
+            const int2 at = at2[k >> 1];
+            const uint64_t v =
+                ffma2(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale, off);
+            const float w0 = ex2_approx(f2_lo(v)), w1 = ex2_approx(f2_hi(v));
+            sum[e][(k >> 1) & 1] =
+                fadd2(sum[e][(k >> 1) & 1], f2(j <= at.x ? w0 : 0.0f, j <= at.y ? w1 : 0.0f));
           }
         }
       }
