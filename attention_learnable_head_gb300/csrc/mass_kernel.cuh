@@ -389,8 +389,10 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
     tmem_st_wait();
     tc_fence_before();
   }
-  __syncthreads();
-  tc_fence_after();
+  if (warp != kMassCopyWarp) {             // which need not wait for the keys
+    named_barrier_sync(2, kMassThreads - 32);
+    tc_fence_after();
+  }
 
   if (warp == kMassCopyWarp) {
     // ---------------------------------------------------------------- q and its lse

@@ -23,7 +23,7 @@ namespace attn_sink {
 constexpr int kSharedWarps = 32;
 constexpr int kSharedTries = 32;
 constexpr int kSharedListed = 1024;      // groups up to which sizes are tried
-constexpr int kSharedMinBlocks = 2;      // key blocks of a part
+constexpr int kSharedMinBlocks = 1;      // key blocks of a part
 
 struct SharedPlan {
   ExtParams e;                             // batch, heads, cache, items, slots
@@ -38,6 +38,7 @@ attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
   __shared__ int s_scan[32];
   __shared__ unsigned long long s_work, s_best;
   __shared__ int s_tiles[kSharedListed], s_blocks[kSharedListed];
+  __shared__ int s_first[kSharedListed], s_end[kSharedListed], s_keys[kSharedListed];
   grid_launch_dependents();
   const ExtParams& e = p.e;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -77,6 +78,9 @@ attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
     if (lane == 0 && i < kSharedListed) {
       s_tiles[i] = tiles;
       s_blocks[i] = blocks;
+      s_first[i] = c0;
+      s_end[i] = c1;
+      s_keys[i] = keys;
     }
   }
   if (lane == 0 && work > 0) atomicAdd(&s_work, work);      // whole numbers: any order
@@ -110,7 +114,13 @@ attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
   for (int i0 = 0; i0 < p.num_groups; i0 += kSharedWarps) {
     const int i = i0 + warp;
     int c0 = 0, c1 = 0, keys = 0;
-    if (i < p.num_groups) keys = group(i, &c0, &c1);
+    if (i < p.num_groups && p.num_groups > kSharedListed) {
+      keys = group(i, &c0, &c1);
+    } else if (i < p.num_groups) {
+      c0 = s_first[i];
+      c1 = s_end[i];
+      keys = s_keys[i];
+    }
     const int blocks = (keys + kBlockN - 1) / kBlockN;
     const int tiles = keys > 0 ? (c1 - c0 + e.tokens - 1) / e.tokens : 0;
     const int parts = keys > 0 ? ext_parts(blocks, chunk) : 0;

@@ -89,6 +89,7 @@ def all_keys(c):
     ([(5000, [5001] * 33)], dict(hq=8, hkv=1, page=8)),
     ([(640, [700] * 130)], dict(hq=1, hkv=1)),               # more than a tile of one head
     ([(70, [71] * 3)] * 40, dict(hq=2, hkv=1)),              # more groups than the plan has warps
+    ([(64, [65, 66])] * 1100, dict(hq=1, hkv=1, page=64)),   # more than it keeps at hand
     ([(64, [1]), (10 ** 9, [2, 2])], {}),
 ])
 def test_decode_shared(groups, kw):
