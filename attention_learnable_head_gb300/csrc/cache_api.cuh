@@ -127,7 +127,6 @@ bool launch_join(const SliceParams& dp, cudaStream_t s) {
 }
 
 // ----------------------------------------------------------------------------- shared prefixes
-constexpr int kSharedWhole = 4096;
 struct SharedLayout {
   DecodeSlices own;
   int tokens, n_items, slots;
@@ -136,10 +135,13 @@ struct SharedLayout {
 
 // Slices of the keys behind the prefix, of which the host only knows that they are not
 // more than the table holds: one, which joins the prefix itself and needs no kernel for
-// that, where the CTAs fill half of the GPU or the table is short.
+// that (4 us), where the CTAs fill half of the GPU or the table is short; else of
+// kSharedLong keys or more.  A block of keys takes a warp of a CTA by itself about 1 us.
+constexpr int kSharedWhole = 2048;
+constexpr int kSharedLong = 256;
 int shared_splits(int batch, int heads_kv, long long cap, int sms) {
   if (2ll * batch * heads_kv >= kSliceCtas * (long long)sms || cap <= kSharedWhole) return 1;
-  return decode_splits(batch, heads_kv, cap, kSliceLong, sms);
+  return decode_splits(batch, heads_kv, cap, kSharedLong, sms);
 }
 
 int shared_layout(const attn_sink_shared_params* p, int sms, SharedLayout* L) {

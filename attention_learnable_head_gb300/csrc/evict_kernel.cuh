@@ -95,8 +95,8 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int b, int h, c
 // The pages that become free, and the new lengths.
 template <int kThreads>
 __device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[kThreads / 32],
-                                            int* s_count, int* s_from, int* s_first) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+                                            int* s_from, int* s_first) {
+  const int tid = threadIdx.x;
   int turn = 0, done = 0;
   bool bad = false;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
@@ -111,17 +111,19 @@ __device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[k
     int all;
     const int before = block_scan<kThreads>(count, s_sum, &turn, &all);
     __syncthreads();                      // the last round's have been used
-    s_count[tid] = count;
     s_from[tid] = from;
-    s_first[tid] = done + before;
+    s_first[tid] = before;
     __syncthreads();
-    const int most = min(kThreads, p.batch - b0);
-    for (int i = warp; i < most; i += kThreads / 32)
-      for (int x = lane; x < s_count[i]; x += 32) {
-        const int to = s_first[i] + x;
-        if (to < p.max_freed)
-          p.freed[to] = __ldg(p.block_table + (size_t)(b0 + i) * p.max_pages + s_from[i] + x);
-      }
+    // entry by entry over the CTA; whose it is by bisection (few pages of many sequences, or
+    // many of few: 10000 of two took 24 us with a warp a sequence)
+    for (int x = tid; x < all && done + x < p.max_freed; x += kThreads) {
+      int i = 0;                          // the last sequence that starts at or before x
+      #pragma unroll
+      for (int d = kThreads / 2; d > 0; d >>= 1)
+        if (s_first[i + d] <= x) i += d;
+      p.freed[done + x] =
+          __ldg(p.block_table + (size_t)(b0 + i) * p.max_pages + s_from[i] + x - s_first[i]);
+    }
     done += all;
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
@@ -136,12 +138,12 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_mass[];                      // [stage]
   __shared__ NthShared<kThreads> s_nth;
   __shared__ uint32_t s_kept[kThreads], s_tie[kThreads];    // bitmaps of 32 kThreads keys
-  __shared__ int s_list[kThreads];
+  __shared__ int s_holes;
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   if (blockIdx.x == gridDim.x - 1) {
-    evict_pages<kThreads>(p, s_nth.sum, reinterpret_cast<int*>(s_kept), reinterpret_cast<int*>(s_tie),
-                          s_list);
+    evict_pages<kThreads>(p, s_nth.sum, reinterpret_cast<int*>(s_kept),
+                          reinterpret_cast<int*>(s_tie));
     return;
   }
   const int b = (int)(blockIdx.x / (unsigned)p.heads_kv);
@@ -256,10 +258,10 @@ attn_sink_evict_kernel(const __grid_constant__ EvictParams p) {
       mover &= mover - 1;
     }
     // holes up to the budget: what is left of it when its kept keys are counted
-    if (j0 < fewer && fewer <= j0 + 32) s_list[0] = fewer - first - __popc(kept & below);
+    if (j0 < fewer && fewer <= j0 + 32) s_holes = fewer - first - __popc(kept & below);
   }
   __syncthreads();                                          // the moves are listed
-  holes = fewer > 0 ? s_list[0] : 0;
+  holes = fewer > 0 ? s_holes : 0;
   for (int i = tid; i < holes; i += kThreads)
     mass_out[to[i]] = __ldg(mass + come[holes - 1 - i]);
   if (p.here)

@@ -481,6 +481,7 @@ def random_mass(c, keys=None):
     ([300, 20, 0, 301], dict(page=1, hkv=3, hq=3), 36, 4, 32),     # nothing left to choose
     ([300, 20, 100, 101], dict(page=24), 100, 0, 0),
     ([300, 290], dict(page=64), 0, 0, 0),                          # everything goes
+    ([5000, 7, 6000, 30], dict(page=1, hkv=1, hq=1), 20, 1, 1),    # many pages of few sequences
     ([300, 290], dict(page=64), 1, 0, 0),
     ([300, 290], dict(page=64), 299, 0, 1),
     ([300, 290], {}, 1000, 4, 4),                                  # nothing does
