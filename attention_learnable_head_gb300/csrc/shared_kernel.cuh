@@ -47,6 +47,8 @@ attn_sink_shared_plan_kernel(const __grid_constant__ SharedPlan p) {
     s_work = 0;
     s_best = ~0ull;
   }
+  // a sequence that no group has keeps this
+  for (int b = tid; b < e.batch; b += 32 * kSharedWarps) p.refs[b] = SharedRef{0, 0, 0, 0};
   __syncthreads();
   bool bad = false;
   // The keys that group i reads together, and its sequences [c0, c1); by a whole warp.
