@@ -85,6 +85,9 @@ int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* 
   dp->max_pages = p->max_pages;
   dp->splits = L.splits;
   dp->whole = L.splits == 1;
+#ifdef ATTN_SINK_TEST_HOOKS
+  dp->skip_k_tile = g_test_skip_k_tile.load();
+#endif
   dp->scale_log2 = p->softmax_scale * kLog2e;
   const long long rows = (long long)p->num_pages * p->page_size;
   *tma = slice_tma_page(p->page_size) && rows > 0 && rows < (1ll << 31);
@@ -592,6 +595,9 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
   mp.accumulate = params->accumulate;
   mp.scale_log2 = params->softmax_scale * kLog2e;
   mp.inv_scale = 1.0f / params->softmax_scale;
+#ifdef ATTN_SINK_TEST_HOOKS
+  mp.skip_k_tile = g_test_skip_k_tile.load();
+#endif
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = (long long)params->total_q * mp.group;
   if (rows > (long long)kMassFewRows * params->batch && mp.group <= kMassMaxGroup &&

@@ -41,6 +41,9 @@ struct MassParams {
   int batch, total_q, heads_q, heads_kv, group, tokens;
   int page_size, num_pages, max_pages, max_keys, accumulate;
   float scale_log2, inv_scale;    // softmax_scale log2(e), 1 / softmax_scale
+#ifdef ATTN_SINK_TEST_HOOKS
+  int skip_k_tile;
+#endif
 };
 
 // A sequence: its new tokens [q0, q0 + n) of q, its keys, and those with an entry.
@@ -303,7 +306,7 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
   __shared__ __align__(8) uint64_t s_full[2], s_empty[2], mma_drained;
   __shared__ __align__(16) int s_at[kMassStages][kMassRows];    // last key the row sees; -1: none
   __shared__ float s_base[kMassStages];    // -c log2(e) of the tile
-  __shared__ int s_clear[kMassStages];     // no weight of the tile is masked
+  __shared__ int s_clear[kMassStages];     // all 96 rows have a token that sees every key
   __shared__ float s_part[2][kMassKeys];
   __shared__ uint8_t s_has[kMassKeys];
   __shared__ uint32_t tmem_base_sh;
@@ -425,7 +428,7 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       const int st = i % kMassStages;
       if (i >= kMassStages && !mbar_wait_warp(&q_empty[st], ((i / kMassStages) & 1) ^ 1, &abort_flag))
         return false;
-      if (lane == 0) {
+      if (lane == 0 && TEST_HOOK_FWD_ISSUE_K(i)) {
         mbar_arrive_expect_tx(&q_full[st], bytes);
         tma_load_3d(&p.tm_q, &q_full[st], sQ + st * kMassTileBytes, 0, h * p.group,
                     s.q0 + t0 + i * p.tokens);
@@ -446,7 +449,7 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
         st_shared_v4(smem_u32(sLse + st * kMassLseBytes) + mass_more_at(lane + 32 * u, 0),
                      hi | mid << 16, weight ? low : 0u, 0, 0);
         s_at[st][lane + 32 * u] = weight ? at : -1;
-        clear = clear && (tok[u] >= p.tokens || (weight && at >= last));
+        clear = clear && weight && at >= last;
       }
       clear = __all_sync(0xffffffffu, clear);
       if (lane == 0) {
@@ -465,16 +468,17 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (ok && i < tiles) ok = tile(z[k]);
-    if (!ok) {
-      // given up: the copies in flight land before the CTA releases its shared memory
-      if (lane == 0) {
+    if (lane == 0) {
+      if (!ok) {
         abort_flag = 1;
         atomicCAS(p.err, 0, DEVERR_TIMEOUT_FWD + 0x10);
-        for (int k = max(0, i - kMassStages); k < i; ++k)
-          mbar_wait(&q_full[k % kMassStages], (k / kMassStages) & 1, nullptr);
       }
-      __syncwarp();
+      // the copies in flight land before the CTA releases its shared memory, also where the
+      // other warps have given up
+      for (int k = max(0, i - kMassStages); k < i; ++k)
+        mbar_wait(&q_full[k % kMassStages], (k / kMassStages) & 1, nullptr);
     }
+    __syncwarp();
   } else if (warp == kMassMmaWarp) {
     // ---------------------------------------------------------------- products
     if (lane == 0) {

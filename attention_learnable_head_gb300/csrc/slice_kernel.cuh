@@ -70,6 +70,9 @@ struct SliceParams {
   int whole;                      // a single slice, joined where it is computed
   int log2_page;                  // TMA path: log2(page_size)
   float scale_log2;               // softmax_scale * log2(e)
+#ifdef ATTN_SINK_TEST_HOOKS
+  int skip_k_tile;
+#endif
 };
 
 // Page sizes that are copied by TMA: whole 128-byte swizzle atoms of 8 keys, and blocks
@@ -226,9 +229,10 @@ attn_sink_slice_kernel(const __grid_constant__ SliceParams p) {
     uint8_t* const dst = ring + st * kSliceStageBytes;
     const int off = j - page_of(j) * p.page_size;
     if (kTma) {
-      if (lane == 0) mbar_arrive_expect_tx(&full[warp][st], kSliceStageBytes);
+      const bool send = TEST_HOOK_FWD_ISSUE_K(i);
+      if (lane == 0 && send) mbar_arrive_expect_tx(&full[warp][st], kSliceStageBytes);
       __syncwarp();
-      if (mine) {
+      if (mine && send) {
         const int row = ok ? e.entry * p.page_size + off : p.num_pages * p.page_size;   // zeros
         tma_load_3d(&p.tm_k, &full[warp][st], dst + (lane << log2_box) * 128, 0, g, row);
         tma_load_3d(&p.tm_v, &full[warp][st], dst + kSliceKeys * 128 + (lane << log2_box) * 128, 0, g,

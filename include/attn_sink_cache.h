@@ -38,7 +38,7 @@ extern "C" {
 #endif
 
 typedef struct attn_sink_shared_params {
-  int batch;          /* 0 <= B <= 65535 sequences */
+  int batch;          /* 0 <= B <= 65535 sequences; B * heads_q < 2^31 */
   int num_groups;     /* 0 <= P <= B (0 only with B = 0) */
   int heads_q;        /* G * heads_kv with G in {1, 2, 4, 8} */
   int heads_kv;       /* 1 .. 65535 */
@@ -102,7 +102,7 @@ int attn_sink_page_bounds(const attn_sink_bounds_params* params, const void* k_c
                           void* bounds, void* stream);
 
 typedef struct attn_sink_select_params {
-  int batch;          /* 0 <= B <= 65535 sequences */
+  int batch;          /* 0 <= B <= 65535 sequences; B * heads_q < 2^31 */
   int heads_q;        /* G * heads_kv with G in {1, 2, 4, 8} */
   int heads_kv;       /* >= 1; B * heads_kv < 2^31 */
   int head_dim;       /* must be 64 */
@@ -137,7 +137,7 @@ int attn_sink_select_pages(const attn_sink_select_params* params, const void* q,
                            int* selected, void* workspace, size_t workspace_bytes, void* stream);
 
 typedef struct attn_sink_pages_params {
-  int batch;          /* 0 <= B <= 65535 sequences */
+  int batch;          /* 0 <= B <= 65535 sequences; B * heads_q < 2^31 */
   int heads_q;        /* G * heads_kv with G in {1, 2, 4, 8} */
   int heads_kv;       /* 1 .. 65535 */
   int head_dim;       /* must be 64 */
@@ -175,7 +175,7 @@ typedef struct attn_sink_mass_params {
   int page_size;      /* keys per page, >= 1 */
   int num_pages;      /* num_pages * page_size * heads_kv < 2^32 */
   int max_pages;      /* columns of block_table; max_pages * page_size <= 2^30 */
-  int max_keys;       /* C >= 0: keys a row of mass has room for */
+  int max_keys;       /* 0 <= C <= 2^30: keys a row of mass has room for */
   int accumulate;     /* 1: added to mass; 0: mass is overwritten */
   float softmax_scale;/* finite and > 0 */
 } attn_sink_mass_params;
@@ -193,7 +193,8 @@ typedef struct attn_sink_mass_params {
  * 0 overwrites them and sets those behind to zero.  A sequence without new tokens
  * adds nothing.  Keys without a page get no weight.  seq_lens above C are clamped to C
  * for mass and recorded as 0x800: keys behind have no entry.  Scores multiply the bf16
- * inputs exactly; all sums are fp32 in a fixed order.  No workspace; one launch.
+ * inputs exactly; all sums are fp32 in a fixed order (of many tokens, the score's takes
+ * the lse in as well).  No workspace; one launch.
  */
 int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const void* k_cache,
                        const int* block_table, const int* seq_lens, const int* cu_seqlens_q,
@@ -201,12 +202,12 @@ int attn_sink_key_mass(const attn_sink_mass_params* params, const void* q, const
 
 typedef struct attn_sink_evict_params {
   int batch;          /* 0 <= B <= 65535 sequences */
-  int heads_kv;       /* >= 1; B * heads_kv < 2^31 */
+  int heads_kv;       /* >= 1; B * heads_kv < 2^31 - 1 */
   int head_dim;       /* must be 64 */
   int page_size;      /* keys per page, >= 1 */
   int num_pages;      /* num_pages * page_size * heads_kv < 2^32 */
-  int max_pages;      /* columns of block_table; max_pages * page_size <= 2^30 */
-  int max_keys;       /* C >= 0: keys a row of mass has room for */
+  int max_pages;      /* columns of block_table; max_pages * page_size <= 2^30, B * max_pages < 2^31 */
+  int max_keys;       /* 0 <= C <= 2^30: keys a row of mass has room for */
   int budget;         /* keys that a sequence keeps at most, >= 0 */
   int keep_first;     /* first and last keys of a sequence that always stay: */
   int keep_last;      /*   >= 0, keep_first + keep_last <= budget */
