@@ -7,20 +7,23 @@
 // hi).  A page of 16 keys is so judged by 1/16 of what its keys and values weigh.
 //
 // Bounds: eight lanes of 16 bytes read a head's key, a warp four heads of a page, key
-// by key, all of a page's loads on their way at once up to 16.
+// by key, all of a page's loads on their way at once up to 16.  Bounded by the keys' bytes: 16
+// prompts of 500 to 2047 new keys, 29 MB, 7.4 us with the launch; one page each of 128
+// sequences 4.1 us.
 //
 // Scores: pages are the 16 rows, the group's heads the 8 columns of warp-level
 // products m16n8k16 (a tcgen05 product has 64 rows of one operand at least, and its
 // operands would go through shared memory: this is bound by the bounds' bytes).  As a
 // dot product does not care for the order of its terms, the k index is permuted so
 // that a lane's fragments are whole 16-byte chunks of a page's bounds: chunk 4 u + t of
-// the 16 for lane t of four, loaded straight into registers.
+// the 16 for lane t of four.  64 sequences x 8 heads x 1024 pages: 101 MB in 21 us.
 //
 // Selection: one CTA for each (sequence, kv head) finds the score of the last page it
 // takes (topk.cuh).  The scores come from fp32 sums, so every page within
-// twice their error of that one is computed again in 64 bits, where any are left out
-// (a fraction of a page a row, on average).  What is selected goes through a bitmap to
-// ascending order.
+// twice their error of that one is computed again with the sums' rounding carried on, where
+// any are left out (a fraction of a page a row, on average).  What is selected goes through a bitmap to
+// ascending order.  Bounded by the latency of these passes: 128 pages for 64 x 8 rows
+// of 1024 10 us, 256 for 8 rows of 8192 12 us.
 #pragma once
 #include <climits>
 #include <cuda_bf16.h>

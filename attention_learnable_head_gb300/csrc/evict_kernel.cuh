@@ -1,11 +1,16 @@
 // Eviction from a paged cache by accumulated attention weight, sm_103a.
 //
 // One CTA for each (sequence, kv head) finds the weight of the last key that stays
-// (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th kept key at or behind the budget goes to the n-th hole below it.  Only as many rows
-// move as there are holes, and no row is both read and written, so that they can be copied
-// in any order, 8 lanes a move: by the same CTA where there are enough of them to fill
-// the GPU, by a second kernel where there are few.  One more CTA of the first kernel scans
-// the sequences for the pages that become free.
+// (topk.cuh), its row of weights in shared memory, and lists what moves: the n-th kept key
+// at or behind the budget goes to the n-th hole below it.  Only as many rows move as there
+// are holes, and no row is both read and written, so that they can be copied in any order,
+// 8 lanes a move: by the same CTA where there are enough of them to fill the GPU, by a second
+// kernel where there are few.  One more CTA of the first kernel scans the sequences for the
+// pages that become free.
+//
+// 4 sequences x 8 heads, 16384 keys to 2048: 22 us, of which 15 are the chain of one CTA a
+// row (load, rank, list) on 33 of 152 SMs and the rest the moves; 64 sequences x 8 heads, 4351
+// keys to 4096: 12 us, that chain alone.  Their bytes would take 5 and 3.
 #pragma once
 #include <climits>
 #include <cuda_bf16.h>

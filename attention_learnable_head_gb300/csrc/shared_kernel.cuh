@@ -11,9 +11,13 @@
 //
 // This schedule kernel of one CTA lists the tiles' parts.  Their keys are cut so that
 // rounds of CTAs times what the longest takes is least, over chunks of kSharedTries sizes
-// from an even share of all blocks on (three prompts of 4096 to 8192 keys, 192 samples:
-// cut by the even share itself, 1.2 rounds, 52 us).  Groups of one sequence and
-// short prefixes have none (kSharedMinSeqs, kSharedMinKeys): their sequences read all keys themselves.
+// from an even share of all blocks on (three prompts of 4096 to 8192 keys, 192 samples, 64
+// heads on 8: 38 us, 620 TFLOP/s, bound by the chain of a tile's softmax; cut by the even
+// share itself, 1.2 rounds, 52 us).  With 512 to 1024 own keys each the call takes 99 us: own
+// keys and prefix share the SMs, whose registers hold two CTAs of the one or three of the
+// other.  8 sequences of 200 own keys behind 1024: 13 us, three dependent kernels.  Groups of
+// one sequence and short prefixes have none (kSharedMinSeqs, kSharedMinKeys): their
+// sequences read all keys themselves.
 #pragma once
 #include "extend_kernel.cuh"
 #include "slice_kernel.cuh"

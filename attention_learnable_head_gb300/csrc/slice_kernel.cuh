@@ -19,6 +19,11 @@
 // at least).  The G <= 8 query heads fill half of the 16 rows: S = Q K^T uses the others
 // for nothing, O = P V for the lower halves of the probabilities: P = hi + lo in two bf16
 // (17 bits), rows 0-7 and 8-15, so that bf16 values enter as they are.
+//
+// Bounded by the keys' and values' bytes: 64 sequences x 8 heads x 2048 selected keys 56 us
+// (269 MB, 4.9 TB/s: rows of 128 bytes, each head of pages of its own), 192 sequences x 512 to
+// 1024 own keys 57 us (5.3 TB/s).  One sequence of 4096 selected keys: 6 us, the chain
+// of the two kernels.
 #pragma once
 #include <climits>
 #include <cuda_bf16.h>
