@@ -458,7 +458,8 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       for (int u = 0; u < kCols; ++u) {
         const int at = at0 + t0 + i * p.tokens + tok[u];
         const bool weight = !isinf(z[u]);
-        const float y = weight ? (base - z[u]) * p.inv_scale : -1e30f;
+        float y = weight ? (base - z[u]) * p.inv_scale : -1e30f;
+        if (fabsf(y) > 1e37f) y = copysignf(1e37f, y);      // its three parts stay finite
         const uint32_t hi = pack_bf16x2(y, 0.0f) & 0xFFFFu;
         const float y1 = y - bf16_lo(hi);
         const uint32_t mid = pack_bf16x2(y1, 0.0f) & 0xFFFFu;
@@ -571,7 +572,7 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       } else {
         const float off = s_base[info];
         const int x0 = t0 + i * p.tokens, at_i = at0 + x0;
-        const int rows_i = min(rows, (s.n - x0) * p.group);
+        const int rows_i = min(p.tokens, s.n - x0) * p.group;
         #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
           ok = ok && (e == 0 || mass_wait(&s_full[e], i & 1, &abort_flag));

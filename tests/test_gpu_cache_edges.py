@@ -147,6 +147,22 @@ def test_key_mass_large_lse(new):
     assert ((mass.double().cpu() - want).abs() <= 40 * SCORE * want + 1e-30).all()
 
 
+@pytest.mark.parametrize("new", [[1, 1], [40, 70]])
+def test_key_mass_lse_at_the_ends_of_fp32(new):
+    """The largest lse gives no weight, the smallest an infinite one, NaN NaN."""
+    for end, at in ((3.3e38, 1), (3.3e38, 0), (-3.3e38, 1), (math.nan, 2)):
+        c, cu, q, lse = mass_case(90, new, [300, 513])
+        lse[at, 0] = end                                      # of the first sequence, head 0
+        k, _, table, lens = c.gpu()
+        mass = torch.zeros(2, 2, c.cols * c.page, device="cuda")
+        binding.key_mass(q.cuda(), k, table, lens, ints(cu), lse.cuda(), mass)
+        want = oracle_mass(q, c.k, c.table, c.lens, cu, lse, torch.zeros(mass.shape), scale=0.125)
+        got = mass.double().cpu()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        fine = torch.isfinite(want)
+        assert ((got - want)[fine].abs() <= (2 * SCORE + 60 * 2 ** -24) * want[fine] + 1e-30).all()
+
+
 def test_key_mass_nan_and_infinite_scores():
     """A NaN key has NaN weight; an infinite one infinite or no weight; others are as before."""
     for new in ([1, 1], [40, 70]):
