@@ -241,6 +241,10 @@ auto evict_kernel(int threads) -> void (*)(EvictParams) {
                           : attn_sink_evict_kernel<1024>;
 }
 
+auto prefix_kernel(bool tma) -> void (*)(ExtParams) {
+  return tma ? attn_sink_extend_kernel<true, true> : attn_sink_extend_kernel<false, true>;
+}
+
 bool g_cache_attr_set[kMaxDevices] = {false};
 
 // The shared memory limits of the kernels that keep a row in it, once per device.
@@ -259,6 +263,10 @@ int cache_attributes() {
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSliceSmem) != cudaSuccess)
           return ATTN_SINK_ERR_CUDA;
+    for (bool tma : {false, true})
+      if (cudaFuncSetAttribute(prefix_kernel(tma), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kFwdSmemBytes) != cudaSuccess)
+        return ATTN_SINK_ERR_CUDA;
     for (int threads : {256, 512, 1024})
       if (cudaFuncSetAttribute(evict_kernel(threads), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                4 * kEvictStage) != cudaSuccess ||
@@ -315,8 +323,7 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
   int sms = 0;
   int* err = nullptr;
   if ((st = device_state(&sms, &err)) != ATTN_SINK_OK) return st;
-  if ((st = extend_attributes()) != ATTN_SINK_OK || (st = cache_attributes()) != ATTN_SINK_OK)
-    return st;
+  if ((st = cache_attributes()) != ATTN_SINK_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   SliceParams dp;
@@ -377,7 +384,7 @@ int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q
   sp.refs = reinterpret_cast<SharedRef*>(ws + L.off_refs);
   attn_sink_shared_plan_kernel<<<1, 32 * kSharedWarps, 0, s>>>(sp);
   if (!launched()) return ATTN_SINK_ERR_CUDA;
-  const auto tiles = tma ? attn_sink_extend_kernel<true> : attn_sink_extend_kernel<false>;
+  const auto tiles = prefix_kernel(tma);
   if (!launch_dependent(tiles, (unsigned)L.n_items * (unsigned)params->heads_kv, kExtThreads,
                         kFwdSmemBytes, s, ep))
     return ATTN_SINK_ERR_CUDA;

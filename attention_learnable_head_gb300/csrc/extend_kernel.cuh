@@ -450,14 +450,28 @@ __device__ __forceinline__ uint32_t ext_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-template <bool kTma>
+// Two bf16 each whose sums are p0 and p1 to 2^-14 of them: 8 bits of a little less than p, cut
+// off, and the rest.  Both are above zero where p is, so that an infinite value stays one
+// (what a rounded first one leaves may be zero or less: 0 * inf is not 0).
+__device__ __forceinline__ void ext_split(float p0, float p1, uint32_t* first, uint32_t* second) {
+  const uint64_t p = f2(p0, p1), w = fmul2(p, f2(1.0f - 0x1p-9f, 1.0f - 0x1p-9f));
+  *first = __byte_perm(__float_as_uint(f2_lo(w)), __float_as_uint(f2_hi(w)), 0x7632);
+  const uint64_t rest = fsub2(p, f2(bf16_lo(*first), bf16_hi(*first)));
+  *second = pack_bf16x2(f2_lo(rest), f2_hi(rest));
+}
+
+// kTwo: P as the sum of two bf16 (ext_split), the second in the columns of the scores, which
+// the threads have read: O += P_2 v comes first, then the next block's scores, then O += P_1 v.
+// A CTA waits longer for its scores, which the tiles of shared prefixes take on
+// (shared_kernel.cuh): one token a sequence is asked for as exactly as by attn_sink_decode.
+template <bool kTma, bool kTwo = false>
 __global__ void __maxnreg__(96)
 attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full, mma_drained;
   __shared__ __align__(8) uint64_t k_full[kFwdKStages], k_empty[kFwdKStages];
   __shared__ __align__(8) uint64_t v_full[kFwdVStages], v_empty[kFwdVStages];
-  __shared__ __align__(8) uint64_t s_full, s_free, p_full, pv_done;
+  __shared__ __align__(8) uint64_t s_full, s_free, p_full, pv_done, low_done;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
   __shared__ float s_mx[2][2][kBlockM];
@@ -531,6 +545,7 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
       mbar_init(&s_free, 64 * row_warps);
       mbar_init(&p_full, 64 * row_warps);
       mbar_init(&pv_done, 1);
+      if (kTwo) mbar_init(&low_done, 1);
       fence_mbarrier_init();
       s_lo = lo;
       s_hi = hi;
@@ -748,7 +763,7 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
         };
         bool ok = mbar_wait(&q_full, 0, &abort_flag) && issue_s(0);
         for (int n = 0; ok && n < num; ++n) {
-          if (n + 1 < num) {
+          if (!kTwo && n + 1 < num) {
             if (!mbar_wait(&s_free, n & 1, &abort_flag) || !issue_s(n + 1)) {
               ok = false;
               break;
@@ -761,10 +776,21 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
             break;
           }
           tc_fence_after();
+          if constexpr (kTwo) {
+            #pragma unroll
+            for (int k = 0; k < kBlockN / 16; ++k)
+              mma_ts(tmem + kFwdColO, tmem + kFwdColS + 64 * (k >> 2) + 8 * (k & 3),
+                     dV0 + sv * kTileU + 128 * k, idesc_o, (n > 0 || k > 0));
+            mma_commit(&low_done);
+            if (n + 1 < num && (!mbar_wait(&low_done, n & 1, &abort_flag) || !issue_s(n + 1))) {
+              ok = false;
+              break;
+            }
+          }
           #pragma unroll
           for (int k = 0; k < kBlockN / 16; ++k)
             mma_ts(tmem + kFwdColO, tmem + kFwdColP + 8 * k, dV0 + sv * kTileU + 128 * k, idesc_o,
-                   (n > 0 || k > 0));
+                   (kTwo || n > 0 || k > 0));
           mma_commit(&pv_done);
           mma_commit(&v_empty[sv]);
         }
@@ -898,30 +924,39 @@ attn_sink_extend_kernel(const __grid_constant__ ExtParams p) {
         const uint64_t negm2 = f2(-m_use, -m_use);
         uint64_t rs = f2(0.0f, 0.0f);
         uint32_t pk[16];
-        #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const uint64_t x =
-              ffma2(f2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])), sl2x2, negm2);
-          const float e0 = ex2_approx(f2_lo(x));
-          const float e1 = ex2_approx(f2_hi(x));
-          rs = fadd2(rs, f2(e0, e1));
-          pk[e >> 1] = pack_bf16x2(e0, e1);
-        }
-        // PV(it - 1) has read the P columns and updated O
-        if (it > 0 && !mbar_wait_warp(&pv_done, (it - 1) & 1, &abort_flag)) ok = false;
-        if (ok) {
-          tc_fence_after();
-          tmem_st_x16(tP, pk);
+        uint32_t low[8];                                    // kTwo: what pk leaves of P
+        auto exponentials = [&](int at, int n) {            // of columns at .. at + n - 1
           #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t x =
-                ffma2(f2(__uint_as_float(a[32 + e]), __uint_as_float(a[33 + e])), sl2x2, negm2);
+          for (int e = 0; e < n; e += 2) {
+            const uint64_t x = ffma2(f2(__uint_as_float(a[at + e]), __uint_as_float(a[at + e + 1])),
+                                     sl2x2, negm2);
             const float e0 = ex2_approx(f2_lo(x));
             const float e1 = ex2_approx(f2_hi(x));
             rs = fadd2(rs, f2(e0, e1));
-            pk[e >> 1] = pack_bf16x2(e0, e1);
+            if constexpr (kTwo) ext_split(e0, e1, &pk[e >> 1], &low[(e >> 1) & 7]);
+            else pk[e >> 1] = pack_bf16x2(e0, e1);
           }
-          tmem_st_x16(tP + 16, pk);
+        };
+        // PV(it - 1) has read the P columns and updated O
+        auto pv_read = [&] {
+          if (it > 0 && !mbar_wait_warp(&pv_done, (it - 1) & 1, &abort_flag)) ok = false;
+        };
+        if (!kTwo) exponentials(0, 32);
+        pv_read();
+        if (ok) {
+          tc_fence_after();
+          if constexpr (kTwo) {
+            #pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              exponentials(16 * u, 16);
+              tmem_st_x8(tP + 8 * u, pk);
+              tmem_st_x8(tS + 8 * u, low);
+            }
+          } else {
+            tmem_st_x16(tP, pk);
+            exponentials(32, 32);
+            tmem_st_x16(tP + 16, pk);
+          }
           l = l * alpha + (f2_lo(rs) + f2_hi(rs));
           if (it > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
             #pragma unroll

@@ -67,8 +67,8 @@ size_t attn_sink_decode_shared_workspace_size(const attn_sink_shared_params* par
  * [0, B], and a negative prefix_lens, are clamped and recorded as 0x800.
  * q, out [B, heads_q, 64] bf16, lse [heads_q, B] fp32, sink [heads_q] fp32.
  * Scores multiply the bf16 inputs exactly with fp32 sums and the softmax is fp32; in
- * O = P v the values enter as they are, the prefix's probabilities rounded to bf16, as
- * in attn_sink_extend, the others as the sum of two bf16 (17 bits).
+ * O = P v the values enter as they are, probabilities as the sum of two bf16, off by
+ * 2^-16 of their size at most, in the prefix by 2^-14.
  */
 int attn_sink_decode_shared(const attn_sink_shared_params* params, const void* q,
                             const void* k_cache, const void* v_cache, const int* block_table,
