@@ -413,10 +413,13 @@ attn_sink_slice_kernel(const __grid_constant__ SliceParams p) {
     s_m[warp][gr] = m_r;
     s_l[warp][gr] = l_r;
   }
+  // hi is above zero where P is, lo of any sign: an infinite value is infinite in hi's sum,
+  // and may be NaN or the other infinity in lo's
+  auto both = [](float hi, float lo) { return isinf(hi) ? hi : hi + lo; };
   #pragma unroll
   for (int nd = 0; nd < 8; ++nd)
     *reinterpret_cast<float2*>(&s_o[warp][gr][8 * nd + 2 * t4]) =
-        make_float2(oacc[nd][0] + oacc[nd][2], oacc[nd][1] + oacc[nd][3]);
+        make_float2(both(oacc[nd][0], oacc[nd][2]), both(oacc[nd][1], oacc[nd][3]));
   __syncthreads();
   // thread t: head t / 16, dims 4 (t % 16) .. + 4
   const int h = tid >> 4;

@@ -122,17 +122,44 @@ def test_pages_norm():
     norm(out, want)
 
 
+def infinite(out, lse, want, rows, heads):
+    """Dimension 3 infinite, 9 minus infinite and 20 NaN in these rows and heads, nothing else."""
+    o, z, spread = want
+    out, fine = out.double().cpu(), torch.isfinite(o)
+    assert (out[rows, heads, 3] == math.inf).all() and (out[rows, heads, 9] == -math.inf).all()
+    assert out[rows, heads, 20].isnan().all()
+    assert (~fine).sum() == 3 * out[rows, heads, 0].numel() and not lse.isnan().any()
+    near(torch.where(fine, out, 0.0), (torch.where(fine, o, 0.0), z, torch.where(fine, spread, 0.0)))
+
+
+def put_infinite(c, b, h, keys):
+    for j, d, x in zip(keys, (3, 9, 20, 20), (math.inf, -math.inf, math.inf, -math.inf)):
+        c.v[int(c.table[b, j // c.page]), j % c.page, h, d] = x
+
+
 def test_shared_infinite_values():
     """An infinite value of the prefix makes the outputs of its dimension infinite, two of
     opposite signs NaN, and no other."""
     c, cu, prefix = shared_case(95, [(320, [330, 400, 325]), (200, [200, 230])], hq=16, hkv=2)
-    group, q = c.hq // c.hkv, c.q()
-    for j, d, x in ((5, 3, math.inf), (130, 9, -math.inf), (7, 20, math.inf), (300, 20, -math.inf)):
-        c.v[int(c.table[0, j // c.page]), j % c.page, 1, d] = x
+    q = c.q()
+    put_infinite(c, 0, 1, [5, 130, 7, 300])
     out, lse = decode_shared(c, q, cu, prefix)
-    o, z, spread = oracle_attend(q, c.k, c.v, c.table, all_keys(c), c.sink, scale=0.125)
-    out, fine = out.double().cpu(), torch.isfinite(o)
-    assert (out[:3, group:, 3] == math.inf).all() and (out[:3, group:, 9] == -math.inf).all()
-    assert out[:3, group:, 20].isnan().all()
-    assert fine.sum() == fine.numel() - 3 * group * 3 and not lse.isnan().any()
-    near(torch.where(fine, out, 0.0), (torch.where(fine, o, 0.0), z, torch.where(fine, spread, 0.0)))
+    infinite(out, lse, oracle_attend(q, c.k, c.v, c.table, all_keys(c), c.sink, scale=0.125),
+             slice(0, 3), slice(8, 16))
+
+
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("cols", [30, 600])                   # a slice, several joined
+def test_infinite_values_of_own_keys(page, cols):
+    c = Paged(96, [400, 333, 290], hq=16, hkv=2, page=page, cols=cols)
+    q = c.q()
+    put_infinite(c, 1, 0, [5, 130, 7, 300])
+    want = oracle_attend(q, c.k, c.v, c.table, all_keys(c), c.sink, scale=0.125)
+    out, lse = decode_shared(c, q, [0, 1, 2, 3], [0, 0, 0])
+    infinite(out, lse, want, slice(1, 2), slice(0, 8))
+    k, v, table, lens = c.gpu()
+    sel = torch.arange(cols, dtype=torch.int32).expand(3, 2, cols).contiguous()
+    have = torch.tensor([-(-n // page) for n in c.lens])[:, None, None]
+    sel = torch.where(sel < have, sel, -1).cuda()
+    out, lse = binding.decode_pages(q.cuda(), k, v, table, lens, sel, c.sink.cuda())
+    infinite(out, lse, want, slice(1, 2), slice(0, 8))
