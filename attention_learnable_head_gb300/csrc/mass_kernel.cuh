@@ -450,9 +450,19 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
         tma_load_3d(&p.tm_q, &q_full[st], sQ + st * kMassTileBytes, 0, h * p.group,
                     s.q0 + t0 + i * p.tokens);
       }
-      // c: the first row's lse, where it is a number
-      const float first = __shfl_sync(0xffffffffu, z[0], 0);
-      const float base = fabsf(first) < 1e30f ? first : 0.0f;
+      // c: of the rows' lse the one next to zero (0 if they are out of fp32's middle range).  A
+      // score's sum then is off by the rounding of |lse - c| <= 2 |lse| of its own row: with the
+      // first row's lse for c, a head switched off by a sink of 1e6 took 3 % of the others'
+      // weights with it, one of 1e20 all of them.
+      uint32_t size = 0x7F800000u;
+      #pragma unroll
+      for (int u = 0; u < kCols; ++u) size = min(size, __float_as_uint(z[u]) & 0x7FFFFFFFu);
+      size = __reduce_min_sync(0xffffffffu, size);
+      bool above = false;
+      #pragma unroll
+      for (int u = 0; u < kCols; ++u) above = above || __float_as_uint(z[u]) == size;
+      const float least = __uint_as_float(size);
+      const float base = !(least < 1e30f) ? 0.0f : __any_sync(0xffffffffu, above) ? least : -least;
       bool clear = true;
       #pragma unroll
       for (int u = 0; u < kCols; ++u) {
