@@ -241,6 +241,13 @@ int validate(const attn_sink_params* p, const int* cu_q, const int* cu_k, Geomet
   return ATTN_SINK_OK;
 }
 
+// log2 of a power of two.
+int log2_of(int n) {
+  int k = 0;
+  while ((1 << k) < n) ++k;
+  return k;
+}
+
 // 3-D map over a [tokens][heads][64] tensor with a (128 bytes) x box_heads x
 // box_rows box and 128-byte swizzle: 64 columns of a 16-bit type, or 32 of fp32.
 int encode_rows(CUtensorMap* m, const void* ptr, long long tokens, int heads,
@@ -755,8 +762,7 @@ int attn_sink_decode(const attn_sink_decode_params* params, const void* q, const
   // pool whose rows fit the copy coordinates); per-thread copies otherwise.
   const long long rows = (long long)params->num_pages * params->page_size;
   const bool tma = decode_tma_page(params->page_size) && rows > 0 && rows < (1ll << 31);
-  dp.log2_page = 0;
-  while ((1 << dp.log2_page) < params->page_size) ++dp.log2_page;
+  dp.log2_page = tma ? log2_of(params->page_size) : 0;
   if (tma) {
     const int box = std::min(params->page_size, kDecKeys);
     if ((st = encode_rows(&dp.tm_k, k_cache, rows, params->heads_kv,

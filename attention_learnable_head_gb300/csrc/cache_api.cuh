@@ -91,8 +91,8 @@ int decode_params(const P* p, const DecodeSlices& L, const void* q, const void* 
   dp->scale_log2 = p->softmax_scale * kLog2e;
   const long long rows = (long long)p->num_pages * p->page_size;
   *tma = slice_tma_page(p->page_size) && rows > 0 && rows < (1ll << 31);
-  while ((1 << dp->log2_page) < p->page_size) ++dp->log2_page;
   if (!*tma) return ATTN_SINK_OK;
+  dp->log2_page = log2_of(p->page_size);
   const int box = std::min(p->page_size, kSliceKeys);
   // With pages of its own for each head no more than its 128 bytes into L2: its
   // neighbour's are not wanted (64 sequences x 2048 keys read 375 MB of 269 and took 67
