@@ -97,7 +97,8 @@ __device__ __forceinline__ void evict_move(const EvictParams& p, int b, int h, c
   }
 }
 
-// The pages that become free, and the new lengths.
+// The pages that become free, and the new lengths.  Entries outside the cache are no pages:
+// where a round has any, it is listed again without them.
 template <int kThreads>
 __device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[kThreads / 32],
                                             int* s_from, int* s_first) {
@@ -121,15 +122,32 @@ __device__ __forceinline__ void evict_pages(const EvictParams& p, int (*s_sum)[k
     __syncthreads();
     // entry by entry over the CTA; whose it is by bisection (few pages of many sequences, or
     // many of few: 10000 of two took 24 us with a warp a sequence)
-    for (int x = tid; x < all && done + x < p.max_freed; x += kThreads) {
+    auto entry = [&](int x) {
       int i = 0;                          // the last sequence that starts at or before x
       #pragma unroll
       for (int d = kThreads / 2; d > 0; d >>= 1)
         if (s_first[i + d] <= x) i += d;
-      p.freed[done + x] =
-          __ldg(p.block_table + (size_t)(b0 + i) * p.max_pages + s_from[i] + x - s_first[i]);
+      return __ldg(p.block_table + (size_t)(b0 + i) * p.max_pages + s_from[i] + x - s_first[i]);
+    };
+    bool none = false;
+    for (int x = tid; x < all; x += kThreads) {
+      const int e = entry(x);
+      none |= (unsigned)e >= (unsigned)p.num_pages;
+      if (x < p.max_freed - done) p.freed[done + x] = e;
     }
-    done += all;
+    if (!__syncthreads_or(none)) {
+      done += all;
+      continue;
+    }
+    bad = true;
+    for (int x0 = 0; x0 < all; x0 += kThreads) {
+      const int e = x0 + tid < all ? entry(x0 + tid) : -1;
+      const bool page = (unsigned)e < (unsigned)p.num_pages;
+      int pages;
+      const int at = done + block_scan<kThreads>(page, s_sum, &turn, &pages);
+      if (page && at < p.max_freed) p.freed[at] = e;
+      done += pages;
+    }
   }
   if (bad) atomicCAS(p.err, 0, DEVERR_DECODE_INPUT);
   if (tid == 0) *p.num_freed = done;

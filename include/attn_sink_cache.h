@@ -233,8 +233,9 @@ size_t attn_sink_evict_workspace_size(const attn_sink_evict_params* params);
  * zero behind; new_lens [B] = min(L, budget); freed_pages [max_freed], the
  * block-table entries of pages that hold no key any more, sequence by sequence, in
  * the order of their columns, -1 behind the last (the free pages of
- * attn_sink_page_plan; block_table itself stays as it is); num_freed [1], how many
- * there are (more than max_freed when they do not fit).  Sequences of at most budget
+ * attn_sink_page_plan; block_table itself stays as it is; entries outside the cache
+ * are left out and recorded); num_freed [1], how many there are (more than max_freed
+ * when they do not fit).  Sequences of at most budget
  * keys, and the rows behind a sequence's new length, keep what they hold.  Pages that
  * hold any of a changed sequence's keys must be in no other sequence's row.
  * seq_lens above C are clamped and recorded as 0x800; where the block table has no

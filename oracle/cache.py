@@ -113,7 +113,7 @@ def oracle_evict(k_cache, v_cache, table, lens, mass, *, budget: int, first: int
     for b, n in enumerate(lens):
         keep = min(n, budget)
         fewer.append(keep)
-        freed += [int(x) for x in table[b, -(-keep // page):-(-n // page)]]
+        freed += [int(x) for x in table[b, -(-keep // page):-(-n // page)] if 0 <= x < pages]
         for h in range(hkv):
             if n <= budget:
                 out[b, h, :n] = mass[b, h, :n]
