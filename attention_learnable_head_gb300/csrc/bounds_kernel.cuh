@@ -396,11 +396,15 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   // No score is further off than the rounding of its sums: 8 products of 16 terms, each
   // sum cut below 2^-23 of what the terms' sizes add up to at most.
   peak = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? s_peak[lane] : 0u);
-  const float most = norm * __uint_as_float(peak << 16);
+  const float top = __uint_as_float(peak << 16), most = norm * top;
+  // Infinities, NaN, and scores so small that fp32 loses some of their products: all of them
+  // in fp64.  (None of that where there are only zeros.)
+  const bool wide =
+      !(most < 1e37f) || (most < 0x1p-90f && norm != 0.0f && top != 0.0f);
   const float off = most * 0x1p-15f;                        // twice that, for both sides
   const float last = unordered(low);
   uint32_t from = low, upto = low;                      // the border, both ends inside
-  if (!(most < 1e37f)) {                                    // infinities, NaN
+  if (wide) {
     from = 0;
     upto = 0xFFFFFFFFu;
   } else if (off > 0.0f) {
@@ -426,14 +430,14 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
   const int left = need - s_side, border = s_many;          // of the border, left <= border
   // which of the border: all, by their ranks in shared memory, or by a 64-bit bound
   const bool every = left == border;
-  const bool again = !every && (off > 0.0f || !(most < 1e37f));
+  const bool again = !every && (off > 0.0f || wide);
   const bool ranked = again && border <= kSelectBand;
   const unsigned long long* exact = p.exact + row * p.max_pages;
   unsigned long long bound64 = 0;
   if (again) {
     auto score = [&](int i) {
-      return most < 1e37f ? page_score_exact<false>(p, b, h, p.keep_first + i)
-                          : page_score_exact<true>(p, b, h, p.keep_first + i);
+      return wide ? page_score_exact<true>(p, b, h, p.keep_first + i)
+                  : page_score_exact<false>(p, b, h, p.keep_first + i);
     };
     if (ranked) {
       for (int x = tid >> 5; x < border; x += kThreads / 32) {
