@@ -393,15 +393,16 @@ attn_sink_select_kernel(const __grid_constant__ SelectParams p) {
             if (i0 + u * kThreads < n) take(v[u]);
         }
       }, &s_nth, &turn).value;             // the smallest score that is taken
-  // No score is further off than the rounding of its sums: 8 products of 16 terms, each
-  // sum cut below 2^-23 of what the terms' sizes add up to at most.
+  // No score is further off than the rounding of its sums: 8 products of 16 terms and the sum
+  // so far, each of the 17 cut below 2^-23 of what the terms' sizes add up to at most, 8 * 17 *
+  // 2^-23 = 1.0625 * 2^-16; and 2^-119 where small terms are lost, nothing of 2^-90.
   peak = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? s_peak[lane] : 0u);
   const float top = __uint_as_float(peak << 16), most = norm * top;
   // Infinities, NaN, and scores so small that fp32 loses some of their products: all of them
   // in fp64.  (None of that where there are only zeros.)
   const bool wide =
       !(most < 1e37f) || (most < 0x1p-90f && norm != 0.0f && top != 0.0f);
-  const float off = most * 0x1p-15f;                        // twice that, for both sides
+  const float off = most * 0x1.2p-15f;                      // more than twice that: both sides
   const float last = unordered(low);
   uint32_t from = low, upto = low;                      // the border, both ends inside
   if (wide) {
