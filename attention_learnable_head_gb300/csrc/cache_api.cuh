@@ -156,8 +156,11 @@ int shared_layout(const attn_sink_shared_params* p, int sms, SharedLayout* L) {
   if (p->heads_kv > 65535) return ATTN_SINK_ERR_UNSUPPORTED;
   L->tokens = kBlockM / (p->heads_q / p->heads_kv);
   L->slots = kExtCtasPerSm * sms;
-  // the bounds of attn_sink_shared_plan_kernel: a share's parts and one more a tile
-  const long long tiles = (long long)p->batch / L->tokens + p->num_groups;
+  // the bounds of attn_sink_shared_plan_kernel: a share's parts and one more a tile, of groups of
+  // kSharedMinSeqs sequences or more (4096 sequences each in a group of its own: 702 MB of
+  // workspace, 1256 where those counted too)
+  const long long tiles =
+      (long long)p->batch / L->tokens + std::min(p->num_groups, p->batch / kSharedMinSeqs);
   const long long items = tiles + (L->slots + p->heads_kv - 1) / p->heads_kv;
   if (items * p->heads_kv >= (1ll << 31)) return ATTN_SINK_ERR_UNSUPPORTED;   // launch grid
   L->n_items = (int)items;
