@@ -450,13 +450,15 @@ __device__ __forceinline__ uint32_t ext_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// Two bf16 each whose sums are p0 and p1 to 2^-14 of them: 8 bits of a little less than p, cut
-// off, and the rest.  Both are above zero where p is, so that an infinite value stays one
-// (what a rounded first one leaves may be zero or less: 0 * inf is not 0).
+// Two bf16 each whose sums are p0 and p1 to 2^-14 of them: the upper 8 bits, and the rest of
+// (1 + 2^-17) p.  Both are above zero where p is, so that an infinite value stays one (a rest
+// of p itself may be zero, one of a rounded first negative: 0 * inf is not 0).
 __device__ __forceinline__ void ext_split(float p0, float p1, uint32_t* first, uint32_t* second) {
-  const uint64_t p = f2(p0, p1), w = fmul2(p, f2(1.0f - 0x1p-9f, 1.0f - 0x1p-9f));
-  *first = __byte_perm(__float_as_uint(f2_lo(w)), __float_as_uint(f2_hi(w)), 0x7632);
-  const uint64_t rest = fsub2(p, f2(bf16_lo(*first), bf16_hi(*first)));
+  const uint32_t w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+  *first = __byte_perm(w0, w1, 0x7632);
+  const uint64_t rest = ffma2(f2(p0, p1), f2(1.0f + 0x1p-17f, 1.0f + 0x1p-17f),
+                              f2(__uint_as_float((w0 & 0xFFFF0000u) | 0x80000000u),
+                                 __uint_as_float((w1 & 0xFFFF0000u) | 0x80000000u)));
   *second = pack_bf16x2(f2_lo(rest), f2_hi(rest));
 }
 

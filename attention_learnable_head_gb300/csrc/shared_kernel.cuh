@@ -6,7 +6,7 @@
 // tile is a tile of attn_sink_extend_kernel whose tokens all see the whole prefix,
 // and that kernel computes it, with P as two bf16 (ext_split: with one, as for a prompt's
 // tokens, outputs were off by 0.0023 of their norm, of which 0.0017 is their own rounding; the
-// second costs 18 us of the larger call below, 0.7 of the smaller): it leaves each part's
+// second costs 18 us of the larger call below, 0.4 of the smaller): it leaves each part's
 // maximum, sum and unnormalised output in the workspace.  The keys behind the prefix are
 // each sequence's own; attn_sink_slice_kernel reads them, at the same time, and a last
 // kernel joins everything with the sink (slice_kernel.cuh).
@@ -17,7 +17,7 @@
 // heads on 8, P as one bf16: 38 us, 556 TFLOP/s, bound by the chain of a tile's softmax; cut by
 // the even share itself, 1.2 rounds, 52 us).  With 512 to 1024 own keys each the call takes
 // 118 us: own keys and prefix share the SMs, whose registers hold two CTAs of the one or three
-// of the other.  8 sequences of 200 own keys behind 1024: 14 us, three dependent kernels.
+// of the other.  8 sequences of 200 own keys behind 1024: 13.5 us, three dependent kernels.
 // Groups of one sequence and short prefixes have none (kSharedMinSeqs, kSharedMinKeys): their
 // sequences read all keys themselves.
 #pragma once

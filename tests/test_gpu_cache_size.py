@@ -1,8 +1,8 @@
 """The size of the decode steps' error, which the bounds of test_gpu_cache.py (the worst
 case of one rounding of P to bf16) do not see.
 
-P enters O = P v as the sum of two bf16, at most 2^-16 off (of a shared prefix 2^-14, whose
-first bf16 is cut off from 2^-9 less), and values as they are; scores
+P enters O = P v as the sum of two bf16, at most 2^-16 off (of a shared prefix 2^-14: the
+first bf16 is cut off, and the sum 2^-17 more than P), and values as they are; scores
 are off by SCORE at most (test_gpu_cache.py), which a probability and the sum each feel.  So
 before it is rounded an output is within (2^-14 + 2 SCORE) sum_j P_j |v_j| of the formula's,
 and its rounding to bf16 adds 2^-8 of its size.  A single bf16 P would be off by up to 2^-8
