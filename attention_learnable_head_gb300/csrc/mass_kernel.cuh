@@ -452,8 +452,8 @@ attn_sink_key_mass_kernel(const __grid_constant__ MassParams p) {
       }
       // c: of the rows' lse the one next to zero (0 if they are out of fp32's middle range).  A
       // score's sum then is off by the rounding of |lse - c| <= 2 |lse| of its own row: with the
-      // first row's lse for c, a head switched off by a sink of 1e6 took 3 % of the others'
-      // weights with it, one of 1e20 all of them.
+      // first row's lse for c, weights next to a head switched off by a sink of 1e4, 1e6 and
+      // 1e10 were off by 0.06, 4.7 and 100 %; so by 3e-7.
       uint32_t size = 0x7F800000u;
       #pragma unroll
       for (int u = 0; u < kCols; ++u) size = min(size, __float_as_uint(z[u]) & 0x7FFFFFFFu);
