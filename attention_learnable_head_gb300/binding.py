@@ -1300,7 +1300,8 @@ def key_mass(q, k_cache, block_table, seq_lens, cu_seqlens_q, lse, mass, *,
     and over the query heads of its kv head (attn_sink_key_mass): added to mass [B,
     heads_kv, C] fp32 in place (accumulate False: written, the rest of a row zero).
     q [T, H_q, 64] packed by cu_seqlens_q [B + 1] int32 and lse [H_q, T] as extend,
-    decode and the calls above took and gave them.  Returns mass."""
+    decode and the calls above took and gave them.  Single tokens and chunks of prompts
+    belong in calls of their own (attn_sink_cache.h says why).  Returns mass."""
     if softmax_scale is None:
         softmax_scale = 0.125
     if stream is None:

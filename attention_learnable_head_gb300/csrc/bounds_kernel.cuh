@@ -21,8 +21,8 @@
 // Selection: one CTA for each (sequence, kv head) finds the score of the last page it
 // takes (topk.cuh).  The scores come from fp32 sums, so every page within
 // twice their error of that one is computed again with the sums' rounding carried on, where
-// any are left out (a fraction of a page a row, on average).  What is selected goes through a bitmap to
-// ascending order.  Bounded by the latency of these passes: 128 pages for 64 x 8 rows
+// any are left out (a fraction of a page a row, on average).  What is selected goes through
+// a bitmap to ascending order.  Bounded by the latency of these passes: 128 pages for 64 x 8 rows
 // of 1024 10 us, 256 for 8 rows of 8192 12 us.
 #pragma once
 #include <climits>

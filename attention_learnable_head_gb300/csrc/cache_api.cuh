@@ -137,7 +137,8 @@ struct SharedLayout {
 };
 
 // Slices of the keys behind the prefix, of which the host only knows that they are not
-// more than the table holds: one, which joins the prefix itself and needs no kernel for
+// more than the table holds (right for own keys that are alike: 40 sequences behind a prefix
+// and 24 of 1000 to 100000 own keys take 771 us, attn_sink_decode, which cuts all, 316): one, which joins the prefix itself and needs no kernel for
 // that (4 us), where the CTAs fill half of the GPU or the table is short; else of
 // kSharedLong keys or more.  A block of keys takes a warp of a CTA by itself about 1 us.
 constexpr int kSharedWhole = 2048;
@@ -201,14 +202,18 @@ int select_layout(const attn_sink_select_params* p, SelectLayout* L) {
   return ATTN_SINK_OK;
 }
 
-// Rows of q a sequence, on average, up to which warps keep them in registers.
+// Rows of q a sequence, on average, up to which warps keep them in registers.  The host knows
+// the average alone, so this is right for sequences that are alike: one with many rows among
+// many with few is read once for every 32 of them (255 single tokens on 1024 keys 53 us, a
+// chunk of 512 on 16384 keys 111 us, both together 36 ms).
 constexpr int kMassFewRows = 32;
 
 // Threads of a selection's or an eviction's CTA, for rows of so many values.
 int row_threads(int row) { return row <= 2048 ? 256 : row <= 8192 ? 512 : 1024; }
 
 // ----------------------------------------------------------------------------- eviction
-// Shared memory up to which a row's moves are listed there: four CTAs of 512 threads an SM.
+// Shared memory up to which a row's moves are listed there: that of four CTAs fits an SM, whose
+// registers hold four of 256 threads, two of 512 or one of 1024.
 constexpr size_t kEvictLists = 40 * 1024;
 struct EvictLayout {
   int max_moves;

@@ -8,9 +8,11 @@
 // kernel where there are few.  One more CTA of the first kernel scans the sequences for the
 // pages that become free.
 //
-// 4 sequences x 8 heads, 16384 keys to 2048: 22 us, of which 15 are the chain of one CTA a
-// row (load, rank, list) on 33 of 152 SMs and the rest the moves; 64 sequences x 8 heads, 4351
-// keys to 4096: 12 us, that chain alone.  Their bytes would take 5 and 3.
+// 4 sequences x 8 heads, 8947 to 16384 keys to 2048: 22 us, of which 15 are the chain of one
+// CTA a row (load, rank, list) on 33 of 152 SMs and the rest the moves; 64 sequences x 8 heads
+// of 2183 to 4351 keys, 11 of them past 4096: 12 us, that chain alone.  Their bytes would take
+// 5 and 3.  All 64 of 4351 keys: 26 us, 512 rows in two rounds (64 registers leave two CTAs of
+// 512 threads an SM).
 #pragma once
 #include <climits>
 #include <cuda_bf16.h>

@@ -23,9 +23,9 @@
 // a thread, with two keys and 48 of the rows, has one fma and one exponential for each
 // score and reads nothing but TMEM.  Eight warps of 48 rows wait less often than twelve of
 // 32.  Tiles with masks (the last 256 keys' triangle, rows without a token, lse that are
-// infinite) have a loop of their own: with the masks in the same one all tiles paid for
-// them.  4 sequences of 280 to 512 new tokens on 13.6 to 16.4 k keys, 64 heads on 8:
-// 272 us, of which 168 are exponentials at the unit's rate; about 30 are the blocks'
+// infinite; all tiles where G does not divide 96) have a loop of their own: with the masks in
+// the same one all tiles paid for them.  4 sequences of 280 to 512 new tokens on 13.6 to 16.4 k
+// keys, 64 heads on 8: 275 us, of which 168 are exponentials at the unit's rate; about 30 are the blocks'
 // beginnings and 35 the hand-over of products to weights.
 #pragma once
 #include <cuda_bf16.h>

@@ -13,7 +13,7 @@
 //
 // This schedule kernel of one CTA lists the tiles' parts.  Their keys are cut so that
 // rounds of CTAs times what the longest takes is least, over chunks of kSharedTries sizes
-// from an even share of all blocks on (three prompts of 4096 to 8192 keys, 192 samples, 64
+// from an even share of all blocks on (three prompts of 4608 to 8192 keys, 192 samples, 64
 // heads on 8, P as one bf16: 38 us, 556 TFLOP/s, bound by the chain of a tile's softmax; cut by
 // the even share itself, 1.2 rounds, 52 us).  With 512 to 1024 own keys each the call takes
 // 118 us: own keys and prefix share the SMs, whose registers hold two CTAs of the one or three

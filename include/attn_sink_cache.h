@@ -62,7 +62,11 @@ size_t attn_sink_decode_shared_workspace_size(const attn_sink_shared_params* par
  * all its query rows in one product; the keys behind them are each sequence's own.
  * A group's prefix is clamped to its shortest sequence (the rest is read through
  * each sequence's own row), so that the result is attn_sink_decode's whatever
- * prefix_lens holds, as long as the rows' keys there are the same.  A sequence
+ * prefix_lens holds, as long as the rows' keys there are the same.  A sequence's own
+ * keys are shared out over several CTAs only where batch * heads_kv of them leave
+ * half of the GPU empty: a larger batch in which some sequences have much longer keys
+ * of their own than the others is faster with attn_sink_decode (40 sequences behind
+ * 1024 shared keys and 24 of 1000 to 100000 own ones: 771 us, decode 316 us).  A sequence
  * outside every group has no prefix; a cu_groups that does not ascend or leaves
  * [0, B], and a negative prefix_lens, are clamped and recorded as 0x800.
  * q, out [B, heads_q, 64] bf16, lse [heads_q, B] fp32, sink [heads_q] fp32.
@@ -190,7 +194,13 @@ typedef struct attn_sink_mass_params {
  * attn_sink_extend, attn_sink_decode or any call above gave for these rows (an lse of
  * +-inf: no weight).  mass [B, heads_kv, C] fp32, one row of C keys for each kv head
  * of a row of the block table.  accumulate = 1 changes entries j < seq_lens[b] only;
- * 0 overwrites them and sets those behind to zero.  A sequence without new tokens
+ * 0 overwrites them and sets those behind to zero.  One of two kernels takes the whole
+ * call: where the sequences have 32 rows of q (tokens times heads of a group) or fewer
+ * on average, one that walks through a sequence's keys once for every 32 of its rows,
+ * else one for prompts.  Single tokens and chunks of prompts belong in calls of their
+ * own: 255 tokens on 1024 keys each take 53 us, one chunk of 512 on 16384 keys 111 us,
+ * both in one call 36 ms.  The first kernel also takes prompts of groups of more than
+ * 96 heads and of scales outside 2^-10 .. 2^10.  A sequence without new tokens
  * adds nothing.  Keys without a page get no weight.  seq_lens above C are clamped to C
  * for mass and recorded as 0x800: keys behind have no entry.  Scores multiply the bf16
  * inputs exactly; all sums are fp32 in a fixed order (of many tokens, the score's takes
